@@ -34,8 +34,14 @@ AR_LL_AUTO, AR_LL_GLOBAL, AR_LL_CLUSTER = 0, 1, 2
 AR_HB_STAGING_AUTO, AR_HB_STAGING_TMA, AR_HB_STAGING_DIRECT = 0, 1, 2
 AR_MAX_RANKS = 32
 AR_LL_MAX_BYTES = 64 << 20
+AR_E4M3 = 8                     # enum ar_dtype8
+AR_SCALE_BLOCK = 128
+AR_MOE_MAX_EXPERTS = 1024
+AR_MOE_MAX_CHOICES = 32
+AR_NORM_GRAD_ROWS = 512
 
 DTYPES = {"bf16": AR_BF16, "fp16": AR_FP16, "fp32": AR_FP32}
+DTYPES8 = {**DTYPES, "e4m3": AR_E4M3}
 ALGOS = {"one_shot": AR_ONE_SHOT, "two_shot": AR_TWO_SHOT, "auto": AR_ALGO_AUTO}
 PROTOS = {"ll": AR_LL, "hb": AR_HB, "auto": AR_PROTO_AUTO}
 
@@ -131,6 +137,17 @@ SIGNATURES = {
     "ar_plan_execute": ([_VP, _VPP, _VPP, _VP], _I),
     "ar_plan_stats": ([_VP, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_I)], _I),
     "ar_plan_destroy": ([_VP], _I),
+    "ar_rmsnorm": ([_VP, _SZ, _VP, _SZ, _VP, ctypes.c_float, _VP, _SZ, _VP, _SZ, _VP, _VP, _SZ,
+                    _SZ, _I, _I, _VP], _I),
+    "ar_rmsnorm_grad": ([_VP, _SZ, _VP, _SZ, _VP, _SZ, _VP, _VP, _VP, _SZ, _VP, _VP, _SZ, _SZ,
+                         _SZ, _I, _VP], _I),
+    "ar_moe_route": ([_VP, _I, _SZ, _I, _I, _VP, _VP, _VP, _VP], _I),
+    "ar_moe_dispatch": ([_VP, _SZ, _VP, _VP, _VP, _SZ, _VP, _SZ, _SZ, _I, _SZ, _I, _VP], _I),
+    "ar_moe_return": ([_VP, _SZ, _SZ, _VP, _VP, _VP, _SZ, _SZ, _I, _SZ, _I, _VP], _I),
+    "ar_moe_return_grad": ([_VP, _SZ, _VP, _SZ, _SZ, _VP, _VP, _VP, _SZ, _VP, _SZ, _I, _SZ, _I,
+                            _VP], _I),
+    "ar_matmul8": ([_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _I, _VP, _SZ, _SZ, _SZ, _SZ, _I, _VP,
+                    _VP], _I),
 }
 
 
@@ -388,6 +405,79 @@ def ar_plan_stats(p: int):
 
 def ar_plan_destroy(p: int) -> None:
     _check(load_library().ar_plan_destroy(p), "ar_plan_destroy")
+
+
+def _dtype8(dtype) -> int:
+    return DTYPES8[dtype] if isinstance(dtype, str) else dtype
+
+
+def ar_rmsnorm(x, res, gamma, eps: float, total, y, scale, rstd, T: int, H: int, dtype,
+               out_dtype=None, ldx: int = 0, ldres: int = 0, ldsum: int = 0, ldy: int = 0,
+               stream=None) -> None:
+    """Residual addition and root-mean-square norm of T rows of H elements:
+    ``total = x + res``, ``y = norm(x + res) * gamma`` in ``out_dtype`` (default
+    ``dtype``; ``"e4m3"`` with one ``scale`` per 128 elements).  ``res``,
+    ``gamma``, ``total``, ``scale`` and ``rstd`` may be None."""
+    dt = _dtype8(dtype)
+    _check(load_library().ar_rmsnorm(_ptr(x), ldx, _ptr(res), ldres, _ptr(gamma), eps,
+                                     _ptr(total), ldsum, _ptr(y), ldy, _ptr(scale), _ptr(rstd),
+                                     T, H, dt, dt if out_dtype is None else _dtype8(out_dtype),
+                                     _stream(stream)), "ar_rmsnorm")
+
+
+def ar_rmsnorm_grad(dy, dtotal, total, gamma, rstd, dx, dgamma, work, work_bytes: int, T: int,
+                    H: int, dtype, lddy: int = 0, lddtotal: int = 0, ldtotal: int = 0,
+                    lddx: int = 0, stream=None) -> None:
+    """Gradient of ar_rmsnorm: ``dx`` (of x and of the residual alike) and the
+    binary32 ``dgamma``, joined in ``work`` (min(T, AR_NORM_GRAD_ROWS) * H floats)."""
+    _check(load_library().ar_rmsnorm_grad(_ptr(dy), lddy, _ptr(dtotal), lddtotal, _ptr(total),
+                                          ldtotal, _ptr(gamma), _ptr(rstd), _ptr(dx), lddx,
+                                          _ptr(dgamma), _ptr(work), work_bytes, T, H,
+                                          _dtype8(dtype), _stream(stream)), "ar_rmsnorm_grad")
+
+
+def ar_moe_route(ids, T: int, K: int, E: int, offsets, row_of, src=None, ids_bytes: int = 4,
+                 stream=None) -> None:
+    """Stable order of the T * K (token, choice) pairs by expert; ids outside
+    [0, E) get no row.  ``ids_bytes`` is 4 or 8."""
+    _check(load_library().ar_moe_route(_ptr(ids), ids_bytes, T, K, E, _ptr(offsets),
+                                       _ptr(row_of), _ptr(src), _stream(stream)), "ar_moe_route")
+
+
+def ar_moe_dispatch(x, xscale, row_of, rows, rscale, nrows: int, T: int, K: int, H: int, dtype,
+                    ldx: int = 0, ldrows: int = 0, stream=None) -> None:
+    """The tokens' rows (and their scales) in the experts' order."""
+    _check(load_library().ar_moe_dispatch(_ptr(x), ldx, _ptr(xscale), _ptr(row_of), _ptr(rows),
+                                          ldrows, _ptr(rscale), nrows, T, K, H, _dtype8(dtype),
+                                          _stream(stream)), "ar_moe_dispatch")
+
+
+def ar_moe_return(rows, nrows: int, row_of, w, out, T: int, K: int, H: int, dtype,
+                  ldrows: int = 0, ldout: int = 0, stream=None) -> None:
+    """The experts' rows back at their tokens, weighted (``w`` None: ones)."""
+    _check(load_library().ar_moe_return(_ptr(rows), ldrows, nrows, _ptr(row_of), _ptr(w),
+                                        _ptr(out), ldout, T, K, H, _dtype8(dtype),
+                                        _stream(stream)), "ar_moe_return")
+
+
+def ar_moe_return_grad(dout, rows, nrows: int, row_of, w, drows, dw, T: int, K: int, H: int,
+                       dtype, lddout: int = 0, ldrows: int = 0, lddrows: int = 0,
+                       stream=None) -> None:
+    """Gradient of ar_moe_return: of the rows and of the weights (either None)."""
+    _check(load_library().ar_moe_return_grad(_ptr(dout), lddout, _ptr(rows), ldrows, nrows,
+                                             _ptr(row_of), _ptr(w), _ptr(drows), lddrows,
+                                             _ptr(dw), T, K, H, _dtype8(dtype),
+                                             _stream(stream)), "ar_moe_return_grad")
+
+
+def ar_matmul8(a, sa, b, sb, offsets, E: int, d, M: int, N: int, K: int, out_dtype,
+               lda: int = 0, ldb: int = 0, ldd: int = 0, status=None, stream=None) -> None:
+    """Product of E4M3 rows with E4M3 weights and their scales per block of
+    128, for one matrix (``offsets`` None) or grouped by expert."""
+    _check(load_library().ar_matmul8(_ptr(a), lda, _ptr(sa), _ptr(b), ldb, _ptr(sb),
+                                     _ptr(offsets), E, _ptr(d), ldd, M, N, K,
+                                     _dtype8(out_dtype), _ptr(status), _stream(stream)),
+           "ar_matmul8")
 
 
 class Handle:

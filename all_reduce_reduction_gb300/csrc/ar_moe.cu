@@ -1,0 +1,593 @@
+// Tokens sorted by expert and back, with weights applied, and the gradients.
+//
+//   route:    row(t, k) = offsets[id] + number of earlier pairs with the same id
+//   dispatch: rows[row(t, k)] = x[t]
+//   return:   out[t] = round(fold_k w[t, k] * rows[row(t, k)])
+//   gradient: drows[row(t, k)] = round(w[t, k] * dout[t]),
+//             dw[t, k] = sum_h dout[t][h] * rows[row(t, k)][h]
+//
+// The row movers go by token, not by row: a token's row is read once and
+// written K times (dispatch, gradient), or K rows are read and one is written
+// (return), so each byte crosses memory once whatever the order.
+#include "ar_rows.cuh"
+
+namespace ar {
+
+// ---- the order ---------------------------------------------------------------
+
+struct RouteArgs {
+    const void *ids;
+    int32_t *offsets, *row_of, *src;
+    uint32_t n;               // pairs
+    int E;
+    int wide_ids;             // 8-byte ids
+};
+
+constexpr int kRouteCtas = 8;          // CTAs of the one cluster for larger inputs
+constexpr int kRouteWarps = 32;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t ld_peer_u32(const void *p, uint32_t rank) {
+    const uint32_t local = (uint32_t)__cvta_generic_to_shared(p);
+    uint32_t remote, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+// The expert of pair p, or E for one that is not here.
+__device__ __forceinline__ int expert_of(const RouteArgs &a, uint32_t p) {
+    const int64_t id = a.wide_ids ? reinterpret_cast<const int64_t *>(a.ids)[p]
+                                  : (int64_t) reinterpret_cast<const int32_t *>(a.ids)[p];
+    return id >= 0 && id < a.E ? (int)id : a.E;
+}
+
+// Stable counting sort in one launch: one CTA, or one cluster of kRouteCtas.
+// The pairs are cut into one run per warp, in order.  Each warp counts its
+// run's experts (lanes with the same expert are found by a match, the lowest
+// one adds their number, so the counts need no atomics and their order is
+// fixed); the counts are scanned over a CTA's warps, over the cluster's CTAs
+// and over the experts; then each warp walks its run again and hands out rows.
+// Bound by latency: the input is some hundred KB.
+__global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ RouteArgs a) {
+    extern __shared__ uint32_t route_smem[];
+    const int E1 = a.E + 1;                           // expert E: not here
+    uint32_t *total = route_smem;                     // [E1]: this CTA's counts
+    uint32_t *first = total + E1;                     // [E1]: rows before the expert
+    uint32_t *count = first + E1;                     // [warps][E1]
+    __shared__ uint32_t part[32];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ctas = cluster_size(), rank = cluster_rank();
+    kernel_prologue();
+
+    for (int i = threadIdx.x; i < warps * E1; i += blockDim.x)
+        count[i] = 0u;
+    __syncthreads();
+    const uint32_t runs = ctas * warps;
+    const uint32_t len = ((a.n + runs - 1) / runs + 31) / 32 * 32;
+    const uint64_t lo64 = (uint64_t)(rank * warps + warp) * len;
+    const uint32_t lo = lo64 < a.n ? (uint32_t)lo64 : a.n;
+    const uint32_t hi = a.n - lo < len ? a.n : lo + len;
+    uint32_t *mine = count + warp * E1;
+    for (uint32_t p0 = lo; p0 < hi; p0 += 32) {
+        const uint32_t p = p0 + lane;
+        const int e = p < hi ? expert_of(a, p) : -1;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        if (e >= 0 && lane == __ffs(same) - 1)
+            mine[e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // over the CTA's warps: count[w][e] becomes the number before warp w
+    for (int e = threadIdx.x; e < E1; e += blockDim.x) {
+        uint32_t sum = 0u;
+        for (int w = 0; w < warps; ++w) {
+            const uint32_t c = count[w * E1 + e];
+            count[w * E1 + e] = sum;
+            sum += c;
+        }
+        total[e] = sum;
+    }
+    cluster_barrier();
+    // over the CTAs, then over the experts
+    uint32_t carry = 0u;
+    for (int e0 = 0; e0 < E1; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
+        uint32_t before = 0u, all = 0u;
+        if (e < E1)
+            for (uint32_t c = 0; c < ctas; ++c) {
+                const uint32_t v = ld_peer_u32(total + e, c);
+                before += c < rank ? v : 0u;
+                all += v;
+            }
+        uint32_t scan = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+            scan += lane >= d ? v : 0u;
+        }
+        if (lane == 31)
+            part[warp] = scan;
+        __syncthreads();
+        uint32_t w = lane < warps ? part[lane] : 0u;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, w, d);
+            w += lane >= d ? v : 0u;
+        }
+        const uint32_t lower = __shfl_sync(0xFFFFFFFFu, w, warp > 0 ? warp - 1 : 0);
+        const uint32_t start = carry + (warp > 0 ? lower : 0u) + scan - all;
+        carry += __shfl_sync(0xFFFFFFFFu, w, 31);
+        if (e < E1) {
+            first[e] = start + before;
+            if (rank == 0)
+                a.offsets[e] = (int32_t)start;
+        }
+        __syncthreads();
+    }
+    cluster_barrier();                                // every peer has read `total`
+    for (uint32_t p0 = lo; p0 < hi; p0 += 32) {
+        const uint32_t p = p0 + lane;
+        const int e = p < hi ? expert_of(a, p) : -1;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+        const uint32_t base = e >= 0 ? first[e] + mine[e] : 0u;
+        __syncwarp();
+        if (e >= 0) {
+            const uint32_t row = base + __popc(same & ((1u << lane) - 1u));
+            a.row_of[p] = e < a.E ? (int32_t)row : -1;
+            if (a.src)
+                a.src[row] = e < a.E ? (int32_t)p : -1;
+            if (lane == __ffs(same) - 1)
+                mine[e] += __popc(same);
+        }
+        __syncwarp();
+    }
+}
+
+static cudaError_t launch_route(const RouteArgs &a, cudaStream_t s) {
+    // a warp's run is 32 pairs at least; one CTA up to 1024 pairs
+    const uint32_t groups = (a.n + 31) / 32;
+    const int warps = groups < 1 ? 1 : groups < (uint32_t)kRouteWarps ? (int)groups : kRouteWarps;
+    const int ctas = groups > (uint32_t)kRouteWarps ? kRouteCtas : 1;
+    const size_t smem = (size_t)(warps + 2) * (a.E + 1) * sizeof(uint32_t);
+    // the opt-in holds for every size used: 34 rows of at most 1025 words
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_moe_route, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)((kRouteWarps + 2) * (AR_MOE_MAX_EXPERTS + 1) * sizeof(uint32_t)));
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = ctas;
+    cfg.blockDim = warps * 32;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_moe_route, a);
+}
+
+// ---- rows to their experts -----------------------------------------------------
+
+struct MoveArgs {
+    const uint8_t *x;
+    const float *xscale;
+    const int32_t *row_of;
+    uint8_t *rows;
+    float *rscale;
+    uint64_t sx, srows;       // bytes between rows
+    uint64_t nrows, T;
+    uint64_t bytes;           // of a row
+    uint64_t units;           // of a row, of sizeof(UNIT) bytes
+    uint32_t parts;           // CTAs per token
+    int K, nb;                // nb: scales per row
+};
+
+// CTA b moves part b % parts of token b / parts.  A thread loads PER units of
+// the token's row and stores them to each of its K rows.
+template <typename UNIT, int PER>
+__global__ void __launch_bounds__(256) k_moe_dispatch(const __grid_constant__ MoveArgs a) {
+    kernel_prologue();
+    for (uint64_t job = blockIdx.x; job < a.T * a.parts; job += gridDim.x) {
+        const uint64_t t = job / a.parts;
+        const uint32_t part = (uint32_t)(job - t * a.parts);
+        const UNIT *x = reinterpret_cast<const UNIT *>(a.x + t * a.sx);
+        const int32_t *row_of = a.row_of + t * a.K;
+        const uint64_t u0 = (uint64_t)part * (256 * PER) + threadIdx.x;
+        UNIT v[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (u0 + j * 256 < a.units)
+                v[j] = x[u0 + j * 256];
+        for (int k = 0; k < a.K; ++k) {
+            const int32_t r = row_of[k];
+            if (r < 0 || (uint64_t)r >= a.nrows)
+                continue;
+            uint8_t *row = a.rows + (uint64_t)r * a.srows;
+            UNIT *to = reinterpret_cast<UNIT *>(row);
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (u0 + j * 256 < a.units)
+                    to[u0 + j * 256] = v[j];
+            if (part == 0) {
+                // the bytes past the last whole unit, and the scales
+                for (uint64_t i = a.units * sizeof(UNIT) + threadIdx.x; i < a.bytes; i += 256)
+                    row[i] = reinterpret_cast<const uint8_t *>(x)[i];
+                for (int i = threadIdx.x; i < a.nb; i += 256)
+                    a.rscale[(uint64_t)r * a.nb + i] = a.xscale[t * a.nb + i];
+            }
+        }
+    }
+}
+
+template <typename UNIT> static cudaError_t dispatch_unit(MoveArgs a, cudaStream_t s) {
+    a.units = a.bytes / sizeof(UNIT);
+    auto grid = [&](int per) {
+        const uint64_t parts = (a.units + 256 * per - 1) / (256 * per);
+        a.parts = (uint32_t)(parts < 1 ? 1 : parts);
+        const uint64_t g = a.T * a.parts;
+        return (int)(g < (1u << 30) ? g : (1u << 30));
+    };
+    return launch_kernel(k_moe_dispatch<UNIT, 1>, grid(1), 256, 0, s, true, a);
+}
+
+// ---- rows back at their tokens ---------------------------------------------------
+
+struct ReturnArgs {
+    const uint8_t *rows;
+    const int32_t *row_of;
+    const float *w;
+    uint8_t *out;
+    uint64_t srows, sout;     // bytes between rows
+    uint64_t nrows, T, H;
+    uint32_t parts;           // CTAs per token
+    int K;
+};
+
+// CTA b computes part b % parts of token b / parts, one unit a thread, up to
+// eight rows' loads in flight.
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(256) k_moe_return(const __grid_constant__ ReturnArgs a) {
+    using L = Rows<DT, WIDE>;
+    kernel_prologue();
+    const uint64_t units = L::units(a.H);
+    for (uint64_t job = blockIdx.x; job < a.T * a.parts; job += gridDim.x) {
+        const uint64_t t = job / a.parts;
+        const uint64_t u = (job - t * a.parts) * 256 + threadIdx.x;
+        if (u >= units)
+            continue;
+        const int32_t *row_of = a.row_of + t * a.K;
+        float acc[L::E];
+#pragma unroll
+        for (int i = 0; i < L::E; ++i)
+            acc[i] = 0.0f;
+        bool any = false;
+        for (int k0 = 0; k0 < a.K; k0 += 8) {
+            uint4 p[8];
+            float w[8];
+            bool here[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int32_t r = k0 + j < a.K ? row_of[k0 + j] : -1;
+                here[j] = r >= 0 && (uint64_t)r < a.nrows;
+                if (here[j]) {
+                    p[j] = L::load(a.rows + (uint64_t)r * a.srows, u, a.H);
+                    w[j] = a.w ? a.w[t * a.K + k0 + j] : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (here[j]) {
+                    float v[L::E];
+                    L::widen(p[j], v);
+#pragma unroll
+                    for (int i = 0; i < L::E; ++i) {
+                        const float x = __fmul_rn(w[j], v[i]);
+                        acc[i] = any ? __fadd_rn(acc[i], x) : x;
+                    }
+                    any = true;
+                }
+        }
+        L::store(a.out + t * a.sout, u, a.H, acc);
+    }
+}
+
+// ---- gradient of the return ------------------------------------------------------
+
+struct ReturnGradArgs {
+    const uint8_t *dout, *rows;
+    const int32_t *row_of;
+    const float *w;
+    uint8_t *drows;
+    float *dw;
+    uint64_t sdout, srows, sdrows;    // bytes between rows
+    uint64_t nrows, T, H;
+    int K;
+};
+
+// One CTA per token.  Eight choices at a time: every thread walks its units of
+// dout, writes the weighted unit to each choice's row of drows and adds its
+// product with the choice's row; the eight sums are then joined over the CTA.
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(1024) k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
+    using L = Rows<DT, WIDE>;
+    __shared__ float part[8][32];
+    kernel_prologue();
+    const uint64_t units = L::units(a.H);
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const uint8_t *dout = a.dout + t * a.sdout;
+        for (int k0 = 0; k0 < a.K; k0 += 8) {
+            int32_t r[8];
+            float w[8], dot[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                r[j] = k0 + j < a.K ? a.row_of[t * a.K + k0 + j] : -1;
+                if (r[j] >= 0 && (uint64_t)r[j] >= a.nrows)
+                    r[j] = -1;
+                w[j] = a.w && k0 + j < a.K ? a.w[t * a.K + k0 + j] : 1.0f;
+                dot[j] = 0.0f;
+            }
+            for (uint64_t u = threadIdx.x; u < units; u += blockDim.x) {
+                uint4 p[8];
+                if (a.dw) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (r[j] >= 0)
+                            p[j] = L::load(a.rows + (uint64_t)r[j] * a.srows, u, a.H);
+                }
+                float d[L::E];
+                L::widen(L::load(dout, u, a.H), d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (r[j] < 0)
+                        continue;
+                    if (a.dw) {
+                        float v[L::E];
+                        L::widen(p[j], v);
+#pragma unroll
+                        for (int i = 0; i < L::E; ++i)
+                            dot[j] += d[i] * v[i];
+                    }
+                    if (a.drows) {
+                        float g[L::E];
+#pragma unroll
+                        for (int i = 0; i < L::E; ++i)
+                            g[i] = __fmul_rn(w[j], d[i]);
+                        L::store(a.drows + (uint64_t)r[j] * a.sdrows, u, a.H, g);
+                    }
+                }
+            }
+            if (a.dw) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float v = warp_sum(dot[j]);
+                    if (lane == 0)
+                        part[j][warp] = v;
+                }
+                __syncthreads();
+                // warp w joins choices w, w + warps, ...
+                for (int j = warp; j < 8; j += warps) {
+                    const float v = warp_sum(lane < warps ? part[j][lane] : 0.0f);
+                    if (lane == 0 && k0 + j < a.K)
+                        a.dw[t * a.K + k0 + j] = v;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+template <int DT, bool WIDE>
+static cudaError_t return_grad_launch(const ReturnGradArgs &a, cudaStream_t s) {
+    const uint64_t units = (Rows<DT, WIDE>::units(a.H) + 31) / 32 * 32;
+    const int grid = (int)(a.T < (1u << 30) ? a.T : (1u << 30));
+    const int most = 512;
+    return launch_kernel(k_moe_return_grad<DT, WIDE>, grid, (int)(units < most ? units : most), 0, s,
+                         true, a);
+}
+
+template <int DT, bool WIDE> static cudaError_t return_launch(ReturnArgs a, cudaStream_t s) {
+    const uint64_t parts = (Rows<DT, WIDE>::units(a.H) + 255) / 256;
+    a.parts = (uint32_t)parts;
+    const uint64_t g = a.T * parts;
+    return launch_kernel(k_moe_return<DT, WIDE>, (int)(g < (1u << 30) ? g : (1u << 30)), 256, 0, s,
+                         true, a);
+}
+
+// Sizes every row mover shares: the status code, AR_OK if they hold.
+static int check_moe(size_t T, int K, size_t H) {
+    if (K < 1 || K > AR_MOE_MAX_CHOICES || H < 1)
+        return AR_ERR_INVALID;
+    if (H >= (size_t)1 << 31 || T >= ((size_t)1 << 31) / (size_t)K)
+        return AR_ERR_UNSUPPORTED;
+    return AR_OK;
+}
+
+}  // namespace ar
+
+using namespace ar;
+
+extern "C" {
+
+int ar_moe_route(const void *ids, int ids_bytes, size_t T, int K, int E, int32_t *offsets,
+                 int32_t *row_of, int32_t *src, cudaStream_t stream) {
+    const int rc = check_moe(T, K, 1);
+    if (rc != AR_OK)
+        return rc;
+    if ((ids_bytes != 4 && ids_bytes != 8) || E < 1 || !offsets || (T > 0 && (!ids || !row_of)))
+        return AR_ERR_INVALID;
+    if (E > AR_MOE_MAX_EXPERTS)
+        return AR_ERR_UNSUPPORTED;
+    const size_t n = T * (size_t)K;
+    const Matrix mi = matrix(ids, 0, 1, n, ids_bytes), mo = matrix(offsets, 0, 1, E + 1, 4);
+    const Matrix mr = matrix(row_of, 0, 1, n, 4), ms = matrix(src, 0, 1, n, 4);
+    if (!mi.ok || !mo.ok || !mr.ok || !ms.ok || meet(mi, mo) || meet(mi, mr) || meet(mi, ms) ||
+        meet(mo, mr) || meet(mo, ms) || meet(mr, ms))
+        return AR_ERR_INVALID;
+    RouteArgs a;
+    a.ids = ids;
+    a.offsets = offsets;
+    a.row_of = row_of;
+    a.src = src;
+    a.n = (uint32_t)n;
+    a.E = E;
+    a.wide_ids = ids_bytes == 8;
+    return launched(launch_route(a, stream));
+}
+
+int ar_moe_dispatch(const void *x, size_t ldx, const float *xscale, const int32_t *row_of,
+                    void *rows, size_t ldrows, float *rscale, size_t nrows, size_t T, int K,
+                    size_t H, int dtype, cudaStream_t stream) {
+    const int rc = check_moe(T, K, H);
+    if (rc != AR_OK)
+        return rc;
+    if (!(float_dtype(dtype) || dtype == AR_E4M3) || (xscale != nullptr) != (rscale != nullptr))
+        return AR_ERR_INVALID;
+    if (T == 0 || nrows == 0)
+        return AR_OK;
+    if (!x || !row_of || !rows)
+        return AR_ERR_INVALID;
+    const size_t esz = dtype == AR_E4M3 ? 1 : elem_size(dtype);
+    const size_t nb = xscale ? (H - 1) / AR_SCALE_BLOCK + 1 : 0;
+    const Matrix mx = matrix(x, ldx, T, H, esz), mr = matrix(rows, ldrows, nrows, H, esz);
+    const Matrix mi = matrix(row_of, 0, T, K, 4);
+    const Matrix mc = matrix(xscale, 0, T, nb, 4), md = matrix(rscale, 0, nrows, nb, 4);
+    if (!mx.ok || !mr.ok || !mi.ok || !mc.ok || !md.ok || meet(mr, mx) || meet(mr, mi) ||
+        meet(mr, mc) || meet(mr, md) || meet(md, mx) || meet(md, mi) || meet(md, mc))
+        return AR_ERR_INVALID;
+    MoveArgs a;
+    a.x = static_cast<const uint8_t *>(x);
+    a.xscale = xscale;
+    a.row_of = row_of;
+    a.rows = static_cast<uint8_t *>(rows);
+    a.rscale = rscale;
+    a.sx = mx.stride;
+    a.srows = mr.stride;
+    a.nrows = nrows;
+    a.T = T;
+    a.bytes = H * esz;
+    a.K = K;
+    a.nb = (int)nb;
+    const uintptr_t low = mx.p | mr.p | mx.stride | mr.stride;
+    if (low % 16 == 0)
+        return launched(dispatch_unit<uint4>(a, stream));
+    if (low % 4 == 0)
+        return launched(dispatch_unit<uint32_t>(a, stream));
+    if (low % 2 == 0)
+        return launched(dispatch_unit<uint16_t>(a, stream));
+    return launched(dispatch_unit<uint8_t>(a, stream));
+}
+
+int ar_moe_return(const void *rows, size_t ldrows, size_t nrows, const int32_t *row_of,
+                  const float *w, void *out, size_t ldout, size_t T, int K, size_t H, int dtype,
+                  cudaStream_t stream) {
+    const int rc = check_moe(T, K, H);
+    if (rc != AR_OK)
+        return rc;
+    if (!float_dtype(dtype))
+        return AR_ERR_INVALID;
+    if (T == 0)
+        return AR_OK;
+    if ((!rows && nrows > 0) || !row_of || !out)
+        return AR_ERR_INVALID;
+    const size_t esz = elem_size(dtype);
+    const Matrix mr = matrix(rows, ldrows, nrows, H, esz), mo = matrix(out, ldout, T, H, esz);
+    const Matrix mi = matrix(row_of, 0, T, K, 4), mw = matrix(w, 0, T, K, 4);
+    if (!mr.ok || !mo.ok || !mi.ok || !mw.ok || meet(mo, mr) || meet(mo, mi) || meet(mo, mw))
+        return AR_ERR_INVALID;
+    ReturnArgs a;
+    a.rows = static_cast<const uint8_t *>(rows);
+    a.row_of = row_of;
+    a.w = w;
+    a.out = static_cast<uint8_t *>(out);
+    a.srows = mr.stride;
+    a.sout = mo.stride;
+    a.nrows = nrows;
+    a.T = T;
+    a.H = H;
+    a.K = K;
+    const bool v = wide(mr) && wide(mo);
+    switch (dtype) {
+    case AR_BF16:
+        return launched(v ? return_launch<AR_BF16, true>(a, stream)
+                          : return_launch<AR_BF16, false>(a, stream));
+    case AR_FP16:
+        return launched(v ? return_launch<AR_FP16, true>(a, stream)
+                          : return_launch<AR_FP16, false>(a, stream));
+    default:
+        return launched(v ? return_launch<AR_FP32, true>(a, stream)
+                          : return_launch<AR_FP32, false>(a, stream));
+    }
+}
+
+int ar_moe_return_grad(const void *dout, size_t lddout, const void *rows, size_t ldrows,
+                       size_t nrows, const int32_t *row_of, const float *w, void *drows,
+                       size_t lddrows, float *dw, size_t T, int K, size_t H, int dtype,
+                       cudaStream_t stream) {
+    const int rc = check_moe(T, K, H);
+    if (rc != AR_OK)
+        return rc;
+    if (!float_dtype(dtype) || (!drows && !dw))
+        return AR_ERR_INVALID;
+    if (T == 0)
+        return AR_OK;
+    if (!dout || !row_of || (dw && !rows && nrows > 0))
+        return AR_ERR_INVALID;
+    const size_t esz = elem_size(dtype);
+    const Matrix mo = matrix(dout, lddout, T, H, esz), mr = matrix(rows, ldrows, nrows, H, esz);
+    const Matrix md = matrix(drows, lddrows, nrows, H, esz);
+    const Matrix mi = matrix(row_of, 0, T, K, 4), mw = matrix(w, 0, T, K, 4);
+    const Matrix mg = matrix(dw, 0, T, K, 4);
+    if (!mo.ok || !mr.ok || !md.ok || !mi.ok || !mw.ok || !mg.ok || clash(md, mr) || meet(md, mo) ||
+        meet(md, mi) || meet(md, mw) || meet(md, mg) || meet(mg, mo) || meet(mg, mr) ||
+        meet(mg, mi) || meet(mg, mw))
+        return AR_ERR_INVALID;
+    ReturnGradArgs a;
+    a.dout = static_cast<const uint8_t *>(dout);
+    a.rows = static_cast<const uint8_t *>(rows);
+    a.row_of = row_of;
+    a.w = w;
+    a.drows = static_cast<uint8_t *>(drows);
+    a.dw = dw;
+    a.sdout = mo.stride;
+    a.srows = mr.stride;
+    a.sdrows = md.stride;
+    a.nrows = nrows;
+    a.T = T;
+    a.H = H;
+    a.K = K;
+    const bool v = wide(mo) && (!rows || wide(mr)) && (!drows || wide(md));
+    switch (dtype) {
+    case AR_BF16:
+        return launched(v ? return_grad_launch<AR_BF16, true>(a, stream)
+                          : return_grad_launch<AR_BF16, false>(a, stream));
+    case AR_FP16:
+        return launched(v ? return_grad_launch<AR_FP16, true>(a, stream)
+                          : return_grad_launch<AR_FP16, false>(a, stream));
+    default:
+        return launched(v ? return_grad_launch<AR_FP32, true>(a, stream)
+                          : return_grad_launch<AR_FP32, false>(a, stream));
+    }
+}
+
+}  // extern "C"

@@ -1,0 +1,445 @@
+// Root-mean-square norm with the residual's addition, and its gradient.
+//
+//   v = x + res,  r = 1 / sqrt(mean(v^2) + eps),  y = v * r * gamma
+//   dx = r * (gamma*dy - n * mean(gamma*dy*n)) + dsum,  dgamma = sum_t dy * n,
+//   n = s * r
+//
+// Both are bound by memory: a row is read once, kept in registers across the
+// row's reduction, and written once.  A CTA works on one row at a time; the
+// units beyond what the registers hold (rows past 2048 units, 16384 elements
+// of a two-byte type) are read a second time.
+#include "ar_rows.cuh"
+
+namespace ar {
+
+struct NormArgs {
+    const uint8_t *x, *res;
+    const void *gamma;
+    uint8_t *sum, *y;
+    float *scale, *rstd;
+    uint64_t sx, sres, ssum, sy;      // bytes between rows
+    uint64_t T, H;
+    float eps;
+};
+
+// Two binary32 values to two E4M3 codes, `a` in the low byte; nearest even,
+// saturating, NaN to the NaN code.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+    uint16_t q;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(b), "f"(a));
+    return q;
+}
+
+// A block's largest magnitude counts as at least this, so that neither the
+// scale nor its reciprocal leaves the range of normal numbers.
+constexpr float kLeastBlock = 0x1p-96f;
+constexpr float kTopE4M3 = 448.0f;
+
+// The unit's share of y in 8 bits, and its block's scale.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint64_t u, uint64_t H,
+                                           const float *v) {
+    using L = Rows<DT, WIDE>;
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < L::E; ++i)
+        m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+    for (int d = L::kBlockLanes / 2; d > 0; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const float scale = __fdiv_rn(fmaxf(m, kLeastBlock), kTopE4M3);
+    const float inv = __fdiv_rn(1.0f, scale);
+    if (L::at(u, 0) >= H)
+        return;
+    if (u % L::kBlockLanes == 0)
+        scales[u / L::kBlockLanes] = scale;
+    uint32_t q[(L::E + 3) / 4];
+#pragma unroll
+    for (int i = 0; i < L::E; i += 4)
+        q[i / 4] = e4m3x2(v[i] * inv, v[i + 1] * inv) |
+                   e4m3x2(v[i + 2] * inv, v[i + 3] * inv) << 16;
+    if (WIDE && (u + 1) * L::E <= H) {
+        if (L::E == 8)
+            *reinterpret_cast<uint2 *>(row + u * 8) = make_uint2(q[0], q[L::E / 4 - 1]);
+        else
+            *reinterpret_cast<uint32_t *>(row + u * 4) = q[0];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < L::E; ++i)
+        if (L::at(u, i) < H)
+            row[L::at(u, i)] = (uint8_t)(q[i / 4] >> (8 * (i & 3)));
+}
+
+// One CTA per row.  UNITS units of a thread stay in registers.  Every loop
+// over units has the same trip count in a whole warp (the bound is a multiple
+// of 32), which the shuffles of store_e4m3 need.
+template <int DT, bool WIDE, bool E4M3, int UNITS>
+__global__ void __launch_bounds__(1024) k_rmsnorm(const __grid_constant__ NormArgs a) {
+    using L = Rows<DT, WIDE>;
+    __shared__ float part[32];
+    kernel_prologue();
+    const uint64_t H = a.H, units = (L::units(H) + 31) / 32 * 32;
+    for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const uint8_t *x = a.x + t * a.sx;
+        const uint8_t *res = a.res ? a.res + t * a.sres : nullptr;
+        uint8_t *sum = a.sum ? a.sum + t * a.ssum : nullptr;
+        uint8_t *y = a.y + t * a.sy;
+        float *scale = E4M3 ? a.scale + t * ((H + AR_SCALE_BLOCK - 1) / AR_SCALE_BLOCK) : nullptr;
+
+        float v[UNITS][L::E];
+        float ss = 0.0f;
+        uint4 px[UNITS], pr[UNITS];
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
+            px[j] = pr[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (u < units) {
+                px[j] = L::load(x, u, H);
+                if (res)
+                    pr[j] = L::load(res, u, H);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            float w[L::E];
+            L::widen(px[j], v[j]);
+            L::widen(pr[j], w);
+#pragma unroll
+            for (int i = 0; i < L::E; ++i) {
+                v[j][i] = res ? v[j][i] + w[i] : v[j][i];
+                ss += v[j][i] * v[j][i];
+            }
+        }
+        for (uint64_t u = threadIdx.x + (uint64_t)UNITS * blockDim.x; u < units; u += blockDim.x) {
+            float b[L::E], w[L::E];
+            L::widen(L::load(x, u, H), b);
+            if (res)
+                L::widen(L::load(res, u, H), w);
+#pragma unroll
+            for (int i = 0; i < L::E; ++i) {
+                b[i] = res ? b[i] + w[i] : b[i];
+                ss += b[i] * b[i];
+            }
+        }
+        ss = block_sum(ss, part);
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)H) + a.eps));
+        if (a.rstd && threadIdx.x == 0)
+            a.rstd[t] = r;
+
+        auto finish = [&](uint64_t u, float *b) {
+            if (sum)
+                L::store(sum, u, H, b);
+            float g[L::E];
+            if (a.gamma)
+                L::widen(L::load(a.gamma, u, H), g);
+#pragma unroll
+            for (int i = 0; i < L::E; ++i)
+                b[i] = a.gamma ? b[i] * r * g[i] : b[i] * r;
+            if (E4M3)
+                store_e4m3<DT, WIDE>(y, scale, u, H, b);
+            else
+                L::store(y, u, H, b);
+        };
+        // the units past the registers first: sum may overwrite x or res
+        for (uint64_t u = threadIdx.x + (uint64_t)UNITS * blockDim.x; u < units; u += blockDim.x) {
+            float b[L::E], w[L::E];
+            L::widen(L::load(x, u, H), b);
+            if (res) {
+                L::widen(L::load(res, u, H), w);
+#pragma unroll
+                for (int i = 0; i < L::E; ++i)
+                    b[i] += w[i];
+            }
+            finish(u, b);
+        }
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
+            if (u < units)
+                finish(u, v[j]);
+        }
+        __syncthreads();                             // `part` is free for the next row
+    }
+}
+
+template <int DT, bool WIDE, bool E4M3>
+static cudaError_t norm_units(const NormArgs &a, cudaStream_t s) {
+    using L = Rows<DT, WIDE>;
+    const uint64_t units = (L::units(a.H) + 31) / 32 * 32;
+    const int grid = (int)(a.T < (1u << 30) ? a.T : (1u << 30));
+    auto threads = [&](uint64_t per) {
+        const uint64_t n = ((units + per - 1) / per + 31) / 32 * 32;
+        return (int)(n < 1024 ? n : 1024);
+    };
+    if (units <= 1024)
+        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 1>, grid, threads(1), 0, s, true, a);
+    return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 2>, grid, threads(2), 0, s, true, a);
+}
+
+template <int DT>
+static cudaError_t norm_dt(const NormArgs &a, bool w, bool e4m3, cudaStream_t s) {
+    if (e4m3)
+        return w ? norm_units<DT, true, true>(a, s) : norm_units<DT, false, true>(a, s);
+    return w ? norm_units<DT, true, false>(a, s) : norm_units<DT, false, false>(a, s);
+}
+
+// ---- gradient ----------------------------------------------------------------
+
+struct NormGradArgs {
+    const uint8_t *dy, *dsum, *s;
+    const void *gamma;
+    const float *rstd;
+    uint8_t *dx;
+    float *work;                      // gridDim.x rows of H partial sums, or NULL
+    uint64_t sdy, sdsum, ss, sdx;     // bytes between rows
+    uint64_t T, H;
+};
+
+// CTA b takes the rows b, b + gridDim.x, ...; each thread owns the columns of
+// its units and keeps their share of dgamma in registers over all of the
+// CTA's rows (units past the registers: in the CTA's row of `work`).
+template <int DT, bool WIDE, int UNITS>
+__global__ void __launch_bounds__(1024) k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
+    using L = Rows<DT, WIDE>;
+    __shared__ float part[2][32];
+    kernel_prologue();
+    const uint64_t H = a.H, units = (L::units(H) + 31) / 32 * 32;
+    float *work = a.work ? a.work + (uint64_t)blockIdx.x * H : nullptr;
+    float dg[UNITS][L::E];
+#pragma unroll
+    for (int j = 0; j < UNITS; ++j)
+#pragma unroll
+        for (int i = 0; i < L::E; ++i)
+            dg[j][i] = 0.0f;
+    int turn = 0;
+    for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+        const uint8_t *dy = a.dy + t * a.sdy, *s = a.s + t * a.ss;
+        const uint8_t *dsum = a.dsum ? a.dsum + t * a.sdsum : nullptr;
+        uint8_t *dx = a.dx + t * a.sdx;
+        const float r = a.rstd[t];
+        float n[L::E], d[L::E], g[L::E];
+        auto fetch = [&](uint64_t u) {               // n, d = gamma * dy, g = dy
+            L::widen(L::load(s, u, H), n);
+            L::widen(L::load(dy, u, H), g);
+            float w[L::E];
+            if (a.gamma)
+                L::widen(L::load(a.gamma, u, H), w);
+#pragma unroll
+            for (int i = 0; i < L::E; ++i) {
+                n[i] *= r;
+                d[i] = a.gamma ? w[i] * g[i] : g[i];
+            }
+        };
+        float dot = 0.0f;
+        for (uint64_t u = threadIdx.x; u < units; u += blockDim.x) {
+            fetch(u);
+#pragma unroll
+            for (int i = 0; i < L::E; ++i)
+                dot += d[i] * n[i];
+        }
+        const float mean = __fdiv_rn(block_sum(dot, part[turn]), (float)H);
+        auto finish = [&](uint64_t u) {
+            float w[L::E];
+            if (dsum)
+                L::widen(L::load(dsum, u, H), w);
+#pragma unroll
+            for (int i = 0; i < L::E; ++i) {
+                d[i] = r * (d[i] - n[i] * mean);
+                if (dsum)
+                    d[i] += w[i];
+            }
+            L::store(dx, u, H, d);
+        };
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
+            if (u < units) {
+                fetch(u);
+#pragma unroll
+                for (int i = 0; i < L::E; ++i)
+                    dg[j][i] += g[i] * n[i];
+                finish(u);
+            }
+        }
+        for (uint64_t u = threadIdx.x + (uint64_t)UNITS * blockDim.x; u < units; u += blockDim.x) {
+            fetch(u);
+            if (work) {
+#pragma unroll
+                for (int i = 0; i < L::E; ++i)
+                    if (L::at(u, i) < H) {
+                        float *w = work + L::at(u, i);
+                        *w = (t == blockIdx.x ? 0.0f : *w) + g[i] * n[i];
+                    }
+            }
+            finish(u);
+        }
+    }
+    if (work) {
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
+#pragma unroll
+            for (int i = 0; i < L::E; ++i)
+                if (L::at(u, i) < H)
+                    work[L::at(u, i)] = dg[j][i];
+        }
+    }
+}
+
+// dgamma[h] = sum of the G partial rows, a fixed tree: 32 columns a CTA, thread
+// row y adds the rows y, y + 32, ... and the 32 of a column are then joined.
+__global__ void __launch_bounds__(1024) k_join_rows(const float *work, float *out, uint64_t H,
+                                                    int G) {
+    __shared__ float part[32][33];
+    kernel_prologue();
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const uint64_t h = (uint64_t)blockIdx.x * 32 + x;
+    float v = 0.0f;
+    if (h < H)
+        for (int g = y; g < G; g += 32)
+            v += work[(uint64_t)g * H + h];
+    part[y][x] = v;
+    __syncthreads();
+    v = warp_sum(part[x][y]);
+    const uint64_t col = (uint64_t)blockIdx.x * 32 + y;
+    if (x == 0 && col < H)
+        out[col] = v;
+}
+
+template <int DT, bool WIDE>
+static cudaError_t norm_grad_units(const NormGradArgs &a, int grid, cudaStream_t s) {
+    using L = Rows<DT, WIDE>;
+    const uint64_t units = (L::units(a.H) + 31) / 32 * 32;
+    const int threads = (int)(units < 1024 ? units : 1024);
+    if (units <= 1024)
+        return launch_kernel(k_rmsnorm_grad<DT, WIDE, 1>, grid, threads, 0, s, true, a);
+    return launch_kernel(k_rmsnorm_grad<DT, WIDE, 2>, grid, threads, 0, s, true, a);
+}
+
+template <int DT> static cudaError_t norm_grad_dt(const NormGradArgs &a, bool w, int grid,
+                                                  cudaStream_t s) {
+    return w ? norm_grad_units<DT, true>(a, grid, s) : norm_grad_units<DT, false>(a, grid, s);
+}
+
+}  // namespace ar
+
+using namespace ar;
+
+extern "C" {
+
+int ar_rmsnorm(const void *x, size_t ldx, const void *res, size_t ldres, const void *gamma,
+               float eps, void *sum, size_t ldsum, void *y, size_t ldy, float *scale,
+               float *rstd, size_t T, size_t H, int dtype, int out_dtype, cudaStream_t stream) {
+    const bool e4m3 = out_dtype == AR_E4M3;
+    if (!float_dtype(dtype) || !(e4m3 || out_dtype == dtype) || H < 1 || !(eps >= 0.0f) ||
+        e4m3 != (scale != nullptr))
+        return AR_ERR_INVALID;
+    if (H >= (size_t)1 << 31)
+        return AR_ERR_UNSUPPORTED;
+    if (T == 0)
+        return AR_OK;
+    if (!x || !y)
+        return AR_ERR_INVALID;
+    const size_t esz = elem_size(dtype), nb = (H - 1) / AR_SCALE_BLOCK + 1;
+    const Matrix mx = matrix(x, ldx, T, H, esz), mr = matrix(res, ldres, T, H, esz);
+    const Matrix mg = matrix(gamma, 0, 1, H, esz);
+    const Matrix ms = matrix(sum, ldsum, T, H, esz), my = matrix(y, ldy, T, H, e4m3 ? 1 : esz);
+    const Matrix mc = matrix(scale, 0, T, nb, 4), mt = matrix(rstd, 0, T, 1, 4);
+    if (!mx.ok || !mr.ok || !mg.ok || !ms.ok || !my.ok || !mc.ok || !mt.ok)
+        return AR_ERR_INVALID;
+    if (clash(ms, mx) || clash(ms, mr) || meet(ms, mg) || meet(ms, my) || meet(my, mg) ||
+        (e4m3 ? meet(my, mx) || meet(my, mr) : clash(my, mx) || clash(my, mr)))
+        return AR_ERR_INVALID;
+    const Matrix *all[] = {&mx, &mr, &mg, &ms, &my};
+    for (const Matrix *m : all)
+        if (meet(mc, *m) || meet(mt, *m))
+            return AR_ERR_INVALID;
+    if (meet(mc, mt))
+        return AR_ERR_INVALID;
+    NormArgs a;
+    a.x = static_cast<const uint8_t *>(x);
+    a.res = static_cast<const uint8_t *>(res);
+    a.gamma = gamma;
+    a.sum = static_cast<uint8_t *>(sum);
+    a.y = static_cast<uint8_t *>(y);
+    a.scale = scale;
+    a.rstd = rstd;
+    a.sx = mx.stride;
+    a.sres = mr.stride;
+    a.ssum = ms.stride;
+    a.sy = my.stride;
+    a.T = T;
+    a.H = H;
+    a.eps = eps;
+    const bool w = wide(mx) && (!res || wide(mr)) && mg.p % 16 == 0 && (!sum || wide(ms)) &&
+                   wide(my, e4m3 ? 16 / esz : 16);
+    switch (dtype) {
+    case AR_BF16: return launched(norm_dt<AR_BF16>(a, w, e4m3, stream));
+    case AR_FP16: return launched(norm_dt<AR_FP16>(a, w, e4m3, stream));
+    default: return launched(norm_dt<AR_FP32>(a, w, e4m3, stream));
+    }
+}
+
+int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum, const void *s,
+                    size_t lds, const void *gamma, const float *rstd, void *dx, size_t lddx,
+                    float *dgamma, float *work, size_t work_bytes, size_t T, size_t H, int dtype,
+                    cudaStream_t stream) {
+    if (!float_dtype(dtype) || H < 1 || (uintptr_t)dgamma % 4 != 0)
+        return AR_ERR_INVALID;
+    if (H >= (size_t)1 << 31)
+        return AR_ERR_UNSUPPORTED;
+    if (T == 0) {
+        if (!dgamma)
+            return AR_OK;
+        return launched(launch_kernel(k_join_rows, dim3((unsigned)((H + 31) / 32)), 1024, 0,
+                                      stream, true, (const float *)nullptr, dgamma, (uint64_t)H,
+                                      0));
+    }
+    if (!dy || !s || !rstd || !dx || (dgamma != nullptr) != (work != nullptr))
+        return AR_ERR_INVALID;
+    const size_t esz = elem_size(dtype);
+    const size_t rows = T < AR_NORM_GRAD_ROWS ? T : AR_NORM_GRAD_ROWS;
+    const Matrix my = matrix(dy, lddy, T, H, esz), mu = matrix(dsum, lddsum, T, H, esz);
+    const Matrix ms = matrix(s, lds, T, H, esz), mx = matrix(dx, lddx, T, H, esz);
+    const Matrix mg = matrix(gamma, 0, 1, H, esz), mt = matrix(rstd, 0, T, 1, 4);
+    const Matrix md = matrix(dgamma, 0, 1, H, 4), mw = matrix(work, 0, rows, H, 4);
+    if (!my.ok || !mu.ok || !ms.ok || !mx.ok || !mg.ok || !mt.ok || !md.ok || !mw.ok ||
+        mw.p % 16 != 0 || (work && work_bytes < mw.bytes))
+        return AR_ERR_INVALID;
+    if (clash(mx, my) || clash(mx, mu) || clash(mx, ms) || meet(mx, mg) || meet(mx, mt) ||
+        meet(mx, md) || meet(mx, mw) || meet(md, mw))
+        return AR_ERR_INVALID;
+    const Matrix *in[] = {&my, &mu, &ms, &mg, &mt};
+    for (const Matrix *m : in)
+        if (meet(md, *m) || meet(mw, *m))
+            return AR_ERR_INVALID;
+    NormGradArgs a;
+    a.dy = static_cast<const uint8_t *>(dy);
+    a.dsum = static_cast<const uint8_t *>(dsum);
+    a.s = static_cast<const uint8_t *>(s);
+    a.gamma = gamma;
+    a.rstd = rstd;
+    a.dx = static_cast<uint8_t *>(dx);
+    a.work = work;
+    a.sdy = my.stride;
+    a.sdsum = mu.stride;
+    a.ss = ms.stride;
+    a.sdx = mx.stride;
+    a.T = T;
+    a.H = H;
+    const int grid = (int)(T < 304 ? T : 304);
+    const bool w = wide(my) && (!dsum || wide(mu)) && wide(ms) && wide(mx) && mg.p % 16 == 0;
+    cudaError_t e;
+    switch (dtype) {
+    case AR_BF16: e = norm_grad_dt<AR_BF16>(a, w, grid, stream); break;
+    case AR_FP16: e = norm_grad_dt<AR_FP16>(a, w, grid, stream); break;
+    default: e = norm_grad_dt<AR_FP32>(a, w, grid, stream); break;
+    }
+    if (e == cudaSuccess && dgamma)
+        e = launch_kernel(k_join_rows, dim3((unsigned)((H + 31) / 32)), 1024, 0, stream, true,
+                          (const float *)work, dgamma, (uint64_t)H, grid);
+    return launched(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,150 @@
+// Rows of a matrix, read and written by threads in units.
+//
+// A row of H elements is cut into units, one thread's share of it.  In the
+// wide form a unit is one 16-byte vector (the row's address is a multiple of
+// 16; the last unit may be short and is then accessed element by element).
+// In the general form a unit is four elements, lane l of a warp holding
+// elements l, l + 32, l + 64 and l + 96 of the warp's 128, so that each access
+// of the warp is one contiguous run whatever the alignment.  Either way the
+// units of 128 consecutive elements belong to consecutive lanes of one warp,
+// kBlockLanes of them, which lets a block that shares a scale be reduced by
+// shuffles alone.
+#pragma once
+
+#include "ar_device.cuh"
+
+namespace ar {
+
+template <int DT, bool WIDE> struct Rows {
+    static constexpr int kSize = Elem<DT>::kSize;
+    static constexpr int E = WIDE ? 16 / kSize : 4;               // elements per unit
+    static constexpr int kBlockLanes = AR_SCALE_BLOCK / E;        // units per scale block
+    static_assert(kBlockLanes <= 32, "a scale block is at most one warp");
+
+    // units that cover a row: whole scale blocks in the general form, whose
+    // units interleave within 128 elements
+    static __host__ __device__ __forceinline__ uint64_t units(uint64_t H) {
+        return WIDE ? (H + E - 1) / E : (H + 127) / 128 * 32;
+    }
+    // element i of unit u
+    static __device__ __forceinline__ uint64_t at(uint64_t u, int i) {
+        return WIDE ? u * E + i : u / 32 * 128 + u % 32 + 32 * i;
+    }
+    // The unit's bits: words of packed elements (wide) or one element a word.
+    // Elements past H read as zero.
+    static __device__ __forceinline__ uint4 load(const void *row, uint64_t u, uint64_t H) {
+        if (WIDE && (u + 1) * E <= H)
+            return ld_v4_stream(reinterpret_cast<const uint4 *>(row) + u);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (at(u, i) < H) {
+                const uint32_t b = ld_elem<DT>(row, at(u, i));
+                if (WIDE && kSize == 2)
+                    w[i / 2] |= b << (16 * (i & 1));
+                else
+                    w[i & 3] = b;
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ void widen(uint4 p, float v[E]) {
+        const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (WIDE && kSize == 2)
+                v[i] = widen1<DT>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+            else
+                v[i] = widen1<DT>(w[i & 3]);
+        }
+    }
+    static __device__ __forceinline__ void store(void *row, uint64_t u, uint64_t H,
+                                                 const float v[E]) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (WIDE && kSize == 2)
+                w[i / 2] |= narrow1<DT>(v[i]) << (16 * (i & 1));
+            else
+                w[i & 3] = narrow1<DT>(v[i]);
+        }
+        if (WIDE && (u + 1) * E <= H) {
+            st_v4(reinterpret_cast<uint4 *>(row) + u, make_uint4(w[0], w[1], w[2], w[3]));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (at(u, i) < H)
+                st_elem<DT>(row, at(u, i),
+                            WIDE && kSize == 2 ? (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu : w[i & 3]);
+    }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+}
+
+// Sum over the CTA, the same in every thread; `part` is shared memory of 32
+// floats, free again after the next __syncthreads.  blockDim.x is a multiple
+// of 32.
+__device__ __forceinline__ float block_sum(float v, float *part) {
+    v = warp_sum(v);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockDim.x == 32)
+        return v;
+    if (lane == 0)
+        part[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f);
+}
+
+// ---- host-side checks ------------------------------------------------------
+
+// A row-major matrix argument: its address, bytes from its first to past its
+// last element, and whether every row starts on a 16-byte boundary.
+struct Matrix {
+    uintptr_t p = 0;
+    size_t stride = 0;       // bytes between rows
+    size_t bytes = 0;
+    bool ok = true;
+};
+
+// ld = 0 stands for rows without gaps.  ok is false for a misaligned address,
+// a leading dimension below the row, or a size past 2^62 bytes.
+inline Matrix matrix(const void *p, size_t ld, size_t rows, size_t cols, size_t esz) {
+    Matrix m;
+    if (ld == 0)
+        ld = cols;
+    m.p = (uintptr_t)p;
+    const size_t limit = (size_t)1 << 62;
+    m.ok = m.p % esz == 0 && ld >= cols && ld <= limit / esz &&
+           (rows == 0 || ld * esz <= limit / rows);
+    if (m.ok) {
+        m.stride = ld * esz;
+        m.bytes = rows == 0 || cols == 0 ? 0 : (rows - 1) * m.stride + cols * esz;
+    }
+    return m;
+}
+inline bool meet(const Matrix &a, const Matrix &b) {
+    return a.p && b.p && a.p < b.p + b.bytes && b.p < a.p + a.bytes;
+}
+inline bool same(const Matrix &a, const Matrix &b) { return a.p == b.p && a.stride == b.stride; }
+// the output o meets the input i otherwise than exactly
+inline bool clash(const Matrix &o, const Matrix &i) { return meet(o, i) && !same(o, i); }
+inline bool wide(const Matrix &m, size_t align = 16) {
+    return m.p % align == 0 && m.stride % align == 0;
+}
+
+inline bool float_dtype(int d) { return d == AR_BF16 || d == AR_FP16 || d == AR_FP32; }
+
+// The launch's result as a status code.
+inline int launched(cudaError_t e) {
+    if (e == cudaSuccess)
+        return AR_OK;
+    (void)cudaGetLastError();
+    return AR_ERR_CUDA;
+}
+
+}  // namespace ar

@@ -572,6 +572,153 @@ int ar_plan_destroy(ar_plan_t p);
 int ar_allreduce_ll_static(int R, size_t N, int dtype, const void *const in[],
                            void *const out[], cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the all-reduce of one layer.
+ *
+ * What a layer does before and after its collectives: the norm that follows
+ * every tensor-parallel all-reduce, the order of the tokens by expert and
+ * back with its weights (ar_combine folds sources that are in order already),
+ * and the experts' products in 8 bits.  The pages describe the collectives
+ * only; these calls are this library's own design.
+ *
+ * They need no handle and keep nothing between calls: a call reads its
+ * arguments, enqueues its kernels on `stream` on the current device, and
+ * allocates, copies and waits for nothing, so every one can be captured in a
+ * CUDA graph.  Matrices are row-major; a leading dimension ld* counts elements
+ * between rows and 0 stands for rows without gaps.  16-byte aligned buffers
+ * whose row strides are multiples of 16 bytes take the vector paths; any other
+ * alignment that suits the element type is served too.  Zero rows (T, M or a
+ * group) are allowed: nothing is read or written for them.  All arithmetic is
+ * binary32 with one rounding to the output's type, to nearest even; no result
+ * depends on the order in which CTAs run.  NaN and infinities follow IEEE
+ * arithmetic.  AR_ERR_INVALID: a NULL that the call needs, a misaligned
+ * pointer, a bad type or range, a leading dimension below the row, an output
+ * that overlaps another buffer (what each call allows is said there);
+ * AR_ERR_UNSUPPORTED: rows of 2^31 elements or more, or sizes past a limit
+ * stated below; AR_ERR_CUDA: a failed launch. */
+
+/* 8-bit elements: E4M3 (4 exponent bits, 3 mantissa bits, largest value 448,
+ * no infinity), converted to nearest even.  Stands beside enum ar_dtype where
+ * a call says so. */
+enum ar_dtype8 {
+    AR_E4M3 = 8
+};
+
+/* Elements that share one scale along a row (and, in a weight matrix, rows). */
+#define AR_SCALE_BLOCK 128
+/* Most experts and most choices per token of the ar_moe_* calls. */
+#define AR_MOE_MAX_EXPERTS 1024
+#define AR_MOE_MAX_CHOICES 32
+/* Most rows of partial sums ar_rmsnorm_grad keeps in its workspace. */
+#define AR_NORM_GRAD_ROWS 512
+
+/* Root-mean-square norm of T rows of H elements, with the residual's addition.
+ * Per row, with v = x + res in binary32 (v = x if res is NULL):
+ *   sum  = round(v)
+ *   r    = 1 / sqrt(mean(v^2) + eps)
+ *   y    = round(v * r * gamma)
+ * The norm uses v, not its rounding.  With out_dtype AR_E4M3 each block of
+ * AR_SCALE_BLOCK elements of a row (the last may be shorter) has one scale:
+ *   scale = max(largest |v * r * gamma| of the block, 2^-96) / 448
+ *   y     = e4m3(v * r * gamma / scale)
+ * (a NaN element becomes the NaN code and does not enter the scale).
+ *   x, res, sum: dtype, T x H.   res may be NULL; sum may be NULL.
+ *   gamma:       dtype, H; NULL stands for ones.
+ *   y:           out_dtype (dtype itself or AR_E4M3), T x H.
+ *   scale:       T x ceil(H / AR_SCALE_BLOCK) binary32, for AR_E4M3 only
+ *                (NULL otherwise).
+ *   rstd:        T binary32, receives r; may be NULL.
+ * sum and y may each be x or res exactly (same address and stride), not both
+ * the same one; otherwise no output may overlap another buffer. */
+int ar_rmsnorm(const void *x, size_t ldx, const void *res, size_t ldres, const void *gamma,
+               float eps, void *sum, size_t ldsum, void *y, size_t ldy, float *scale,
+               float *rstd, size_t T, size_t H, int dtype, int out_dtype, cudaStream_t stream);
+
+/* Gradient of ar_rmsnorm with out_dtype = dtype.  With s the sum and r the
+ * rstd that the forward call gave, dy the gradient of y and dsum that of sum
+ * (NULL: none), n = s * r:
+ *   dx     = round(r * (gamma * dy - n * mean(gamma * dy * n)) + dsum)
+ *   dgamma = sum over the rows of dy * n                       (binary32)
+ * dx is the gradient of x and of res alike.
+ *   dy, dsum, s, dx: dtype, T x H.   gamma: dtype, H; NULL stands for ones.
+ *   rstd:   T binary32.
+ *   dgamma: H binary32; NULL: not wanted.  T = 0 writes zeros to it.
+ *   work:   device memory for partial sums, 16-byte aligned, of at least
+ *           min(T, AR_NORM_GRAD_ROWS) * H * 4 bytes; NULL if dgamma is.
+ * dx may be dy, dsum or s exactly (same address and stride); otherwise no
+ * output may overlap another buffer. */
+int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum, const void *s,
+                    size_t lds, const void *gamma, const float *rstd, void *dx, size_t lddx,
+                    float *dgamma, float *work, size_t work_bytes, size_t T, size_t H, int dtype,
+                    cudaStream_t stream);
+
+/* The order of the pairs (token t, choice k) by expert.  ids[t*K + k] names an
+ * expert; pairs whose id is outside [0, E) are not here (another rank's, or
+ * dropped) and get no row.  The others are sorted by expert, stable in t*K + k:
+ *   offsets: E + 1 words; expert e has the rows [offsets[e], offsets[e+1]).
+ *   row_of:  T * K words; the pair's row, or -1.
+ *   src:     T * K words; the pair (t*K + k) of each row, -1 from row
+ *            offsets[E] on; may be NULL.
+ *   ids:     T * K words of ids_bytes (4 or 8) bytes, signed.
+ * T * K < 2^31; E <= AR_MOE_MAX_EXPERTS; K <= AR_MOE_MAX_CHOICES. */
+int ar_moe_route(const void *ids, int ids_bytes, size_t T, int K, int E, int32_t *offsets,
+                 int32_t *row_of, int32_t *src, cudaStream_t stream);
+
+/* The tokens' rows, in that order: rows[row_of[t*K + k]] = x[t], bit for bit.
+ * Pairs whose row is outside [0, nrows) are skipped, and rows that no pair has
+ * are left as they are.
+ *   x, rows: dtype (AR_E4M3 too), T x H and nrows x H.
+ *   xscale, rscale: both NULL, or the rows' scales as ar_rmsnorm writes them
+ *            (ceil(H / AR_SCALE_BLOCK) a row), moved along.
+ * The gradient is ar_moe_return of the rows' gradients with w = NULL. */
+int ar_moe_dispatch(const void *x, size_t ldx, const float *xscale, const int32_t *row_of,
+                    void *rows, size_t ldrows, float *rscale, size_t nrows, size_t T, int K,
+                    size_t H, int dtype, cudaStream_t stream);
+
+/* The rows back at their tokens, weighted:
+ *   out[t] = round( fold over k = 0..K-1 of w[t*K + k] * rows[row_of[t*K + k]] )
+ * every product rounded to binary32 on its own and the products folded left
+ * to right, as in ar_combine; pairs without a row in [0, nrows) are left out
+ * of the fold, and a token without any gets zeros.
+ *   rows, out: dtype, nrows x H and T x H.   w: T x K binary32; NULL: ones. */
+int ar_moe_return(const void *rows, size_t ldrows, size_t nrows, const int32_t *row_of,
+                  const float *w, void *out, size_t ldout, size_t T, int K, size_t H, int dtype,
+                  cudaStream_t stream);
+
+/* Gradient of ar_moe_return: for every pair with a row in [0, nrows),
+ *   drows[row_of[t*K + k]] = round(w[t*K + k] * dout[t])
+ *   dw[t*K + k]            = sum over h of dout[t][h] * rows[row][h]
+ * and dw = 0 for the others.  Rows that no pair has are left as they are.
+ *   w may be NULL (ones).  drows or dw may be NULL (not wanted); rows is not
+ *   read without dw and may be NULL then.  drows may be rows exactly. */
+int ar_moe_return_grad(const void *dout, size_t lddout, const void *rows, size_t ldrows,
+                       size_t nrows, const int32_t *row_of, const float *w, void *drows,
+                       size_t lddrows, float *dw, size_t T, int K, size_t H, int dtype,
+                       cudaStream_t stream);
+
+/* Product of E4M3 rows with E4M3 weights that have a scale per block:
+ *   d[m][n] = round( sum over kb of sa[m][kb] * sb[e][n / 128][kb] *
+ *                    sum over k in block kb of a[m][k] * b[e][n][k] )
+ * with blocks of AR_SCALE_BLOCK elements along k (the last of each axis may
+ * be shorter).  The sum over a block and the sum over the blocks are binary32.
+ *   a:  M x K E4M3, row stride lda bytes.   sa: M x ceil(K/128) binary32.
+ *   b:  E matrices of N x K E4M3, row stride ldb bytes, N * ldb bytes apart.
+ *   sb: E x ceil(N/128) x ceil(K/128) binary32.
+ *   offsets: E + 1 words, not decreasing: rows [offsets[e], offsets[e+1]) of a
+ *       belong to matrix e; rows below offsets[0] or from offsets[E] on are
+ *       left as they are in d.  Words outside [0, M] count as the nearer end.
+ *       NULL (E = 1): all rows.
+ *   d:  M x N of out_dtype (enum ar_dtype).
+ *   status: a device word, or NULL.  Every wait inside the kernel is bounded;
+ *       one that ran out (none is known to) writes AR_ERR_TIMEOUT there.
+ * 16-byte aligned a and b with lda and ldb multiples of 16 take the tensor-core
+ * kernels, any other the general one.  M, N, K < 2^31 - 256;
+ * E <= AR_MOE_MAX_EXPERTS.  The input gradient is the same product with the
+ * weights transposed. */
+int ar_matmul8(const void *a, size_t lda, const float *sa, const void *b, size_t ldb,
+               const float *sb, const int32_t *offsets, int E, void *d, size_t ldd, size_t M,
+               size_t N, size_t K, int out_dtype, int *status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
