@@ -7,79 +7,9 @@
 // offsets that only the device knows.
 #include <cuda_fp8.h>
 
-#include "ar_rows.cuh"
+#include "ar_matmul8.cuh"
 
 namespace ar {
-
-struct MatmulArgs {
-    const uint8_t *a, *b;
-    const float *sa, *sb;
-    const int32_t *offsets;       // NULL: one group, all rows
-    uint8_t *d;
-    uint64_t sa_row, sb_group;    // scales between rows of a, between matrices of b
-    uint64_t lda, ldb, ldd;       // bytes between rows
-    uint32_t M, N, K;
-    int E;
-    int kb;                       // blocks along k
-    int out;                      // enum ar_dtype
-    int *status;
-};
-
-// Row tile `index` of all groups' tiles of TM rows: its group, first row and
-// rows.  Called by a whole warp; false if there are fewer tiles.
-__device__ __forceinline__ bool find_rows(const MatmulArgs &a, uint32_t tm, uint32_t index,
-                                          int &group, uint32_t &row, uint32_t &rows) {
-    if (!a.offsets) {
-        const uint64_t r = (uint64_t)index * tm;
-        if (r >= a.M)
-            return false;
-        group = 0;
-        row = (uint32_t)r;
-        rows = a.M - row < tm ? a.M - row : tm;
-        return true;
-    }
-    const int lane = threadIdx.x & 31;
-    uint32_t base = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-        const int e = e0 + lane;
-        uint32_t lo = 0, hi = 0;
-        if (e < a.E) {
-            const int32_t x = a.offsets[e], y = a.offsets[e + 1];
-            lo = x < 0 ? 0u : (uint32_t)x < a.M ? (uint32_t)x : a.M;
-            hi = y < 0 ? 0u : (uint32_t)y < a.M ? (uint32_t)y : a.M;
-            hi = hi < lo ? lo : hi;
-        }
-        const uint32_t tiles = (hi - lo + tm - 1) / tm;
-        uint32_t scan = tiles;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, scan, d);
-            scan += lane >= d ? v : 0u;
-        }
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, base + scan > index);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            const uint32_t first = __shfl_sync(0xFFFFFFFFu, base + scan - tiles, l);
-            const uint32_t start = __shfl_sync(0xFFFFFFFFu, lo, l);
-            const uint32_t end = __shfl_sync(0xFFFFFFFFu, hi, l);
-            group = e0 + l;
-            row = start + (index - first) * tm;
-            rows = end - row < tm ? end - row : tm;
-            return true;
-        }
-        base = __shfl_sync(0xFFFFFFFFu, base + scan, 31);
-    }
-    return false;
-}
-
-__device__ __forceinline__ void store_out(uint8_t *row, uint32_t n, float v, int out) {
-    if (out == AR_BF16)
-        reinterpret_cast<uint16_t *>(row)[n] = (uint16_t)narrow1<AR_BF16>(v);
-    else if (out == AR_FP16)
-        reinterpret_cast<uint16_t *>(row)[n] = (uint16_t)narrow1<AR_FP16>(v);
-    else
-        reinterpret_cast<float *>(row)[n] = v;
-}
 
 // ---- general form ------------------------------------------------------------
 // Any alignment.  64 x 64 of d per CTA, 4 x 4 a thread, the operands of 32
@@ -207,7 +137,13 @@ int ar_matmul8(const void *a, size_t lda, const float *sa, const void *b, size_t
     g.E = E;
     g.kb = (int)kb;
     g.out = out_dtype;
+    g.dwide = wide(md);
     g.status = status;
+    if (wide(ma) && wide(mb)) {
+        if (!matmul8_tc_ready())
+            return AR_ERR_CUDA;
+        return launched(launch_matmul8_tc(g, stream));
+    }
     bool too_large = false;
     const int rc = launched(launch_any(g, stream, &too_large));
     return too_large ? AR_ERR_UNSUPPORTED : rc;

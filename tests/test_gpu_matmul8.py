@@ -91,7 +91,8 @@ def _check(M, N, K, out, offsets=None, **kw):
     (1, 1, 1), (1, 128, 128), (3, 5, 7), (1, 1000, 200), (1, 8192, 1024), (2, 129, 257),
     (16, 256, 512), (17, 300, 144), (33, 640, 1000), (64, 2048, 256), (100, 384, 4096),
     (128, 256, 128), (129, 257, 129), (255, 513, 640), (256, 1024, 2048), (300, 100, 100),
-    (1000, 776, 520), (2048, 2048, 384)])
+    (1000, 776, 520), (2048, 2048, 384), (2500, 2600, 130), (4096, 1100, 1000), (129, 40000, 256),
+    (33000, 40, 64)])
 def test_one_matrix(M, N, K, out):
     _check(M, N, K, out, seed=M + N + K)
 
@@ -115,6 +116,15 @@ GROUPS = [
 def test_groups(offsets, N, K):
     """Empty groups, groups that end inside a tile, rows of no group on both ends."""
     _check(offsets[-1] + 9, N, K, "bf16", offsets, seed=N)
+
+
+@pytest.mark.parametrize("N,K", [(1500, 400), (513, 1024)])
+def test_groups_of_a_prefill(N, K):
+    """Enough tiles for every SM: uneven groups, some empty, columns ragged."""
+    rng = np.random.default_rng(N)
+    counts = np.where(rng.random(60) < 0.2, 0, rng.integers(1, 700, 60))
+    offsets = [0] + np.cumsum(counts).tolist()
+    _check(offsets[-1] + 200, N, K, "bf16", offsets, seed=N, ldd_pad=N % 2 * 3)
 
 
 def test_groups_without_alignment():
@@ -164,7 +174,7 @@ def test_zero_rows():
     assert bool((d == 3.0).all())
 
 
-@pytest.mark.parametrize("M", [24, 600])
+@pytest.mark.parametrize("M", [24, 600, 20000])
 def test_in_a_graph_with_other_offsets(M):
     """One capture serves any grouping: the offsets are read on the device."""
     need_gpu()
