@@ -25,6 +25,7 @@ struct RouteArgs {
 
 constexpr int kRouteCtas = 8;          // CTAs of the one cluster for larger inputs
 constexpr int kRouteWarps = 32;
+constexpr int kRouteHeld = 8;          // ids a lane keeps in registers
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -82,14 +83,25 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
     const uint32_t lo = lo64 < a.n ? (uint32_t)lo64 : a.n;
     const uint32_t hi = a.n - lo < len ? a.n : lo + len;
     uint32_t *mine = count + warp * E1;
-    for (uint32_t p0 = lo; p0 < hi; p0 += 32) {
-        const uint32_t p = p0 + lane;
-        const int e = p < hi ? expert_of(a, p) : -1;
+    // the run's first ids are read at once and kept for the second walk
+    int held[kRouteHeld];
+#pragma unroll
+    for (int i = 0; i < kRouteHeld; ++i) {
+        const uint32_t p = lo + 32 * i + lane;
+        held[i] = p < hi && p >= lo ? expert_of(a, p) : -1;
+    }
+    auto count_32 = [&](int e) {
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
         if (e >= 0 && lane == __ffs(same) - 1)
             mine[e] += __popc(same);
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kRouteHeld; ++i)
+        if (lo + 32 * i < hi)
+            count_32(held[i]);
+    for (uint32_t p0 = lo + 32 * kRouteHeld; p0 < hi; p0 += 32)
+        count_32(p0 + lane < hi ? expert_of(a, p0 + lane) : -1);
     __syncthreads();
     // over the CTA's warps: count[w][e] becomes the number before warp w
     for (int e = threadIdx.x; e < E1; e += blockDim.x) {
@@ -139,9 +151,7 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
         __syncthreads();
     }
     cluster_barrier();                                // every peer has read `total`
-    for (uint32_t p0 = lo; p0 < hi; p0 += 32) {
-        const uint32_t p = p0 + lane;
-        const int e = p < hi ? expert_of(a, p) : -1;
+    auto place_32 = [&](uint32_t p, int e) {
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
         const uint32_t base = e >= 0 ? first[e] + mine[e] : 0u;
         __syncwarp();
@@ -154,7 +164,13 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
                 mine[e] += __popc(same);
         }
         __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kRouteHeld; ++i)
+        if (lo + 32 * i < hi)
+            place_32(lo + 32 * i + lane, held[i]);
+    for (uint32_t p0 = lo + 32 * kRouteHeld; p0 < hi; p0 += 32)
+        place_32(p0 + lane, p0 + lane < hi ? expert_of(a, p0 + lane) : -1);
 }
 
 static cudaError_t launch_route(const RouteArgs &a, cudaStream_t s) {
@@ -218,22 +234,33 @@ __global__ void __launch_bounds__(256) k_moe_dispatch(const __grid_constant__ Mo
         for (int j = 0; j < PER; ++j)
             if (u0 + j * 256 < a.units)
                 v[j] = x[u0 + j * 256];
-        for (int k = 0; k < a.K; ++k) {
-            const int32_t r = row_of[k];
-            if (r < 0 || (uint64_t)r >= a.nrows)
-                continue;
-            uint8_t *row = a.rows + (uint64_t)r * a.srows;
-            UNIT *to = reinterpret_cast<UNIT *>(row);
+        for (int k0 = 0; k0 < a.K; k0 += 8) {
+            // the eight rows first: a store between two of these loads would
+            // hold the second back
+            int32_t r[8];
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (u0 + j * 256 < a.units)
-                    to[u0 + j * 256] = v[j];
-            if (part == 0) {
-                // the bytes past the last whole unit, and the scales
-                for (uint64_t i = a.units * sizeof(UNIT) + threadIdx.x; i < a.bytes; i += 256)
-                    row[i] = reinterpret_cast<const uint8_t *>(x)[i];
-                for (int i = threadIdx.x; i < a.nb; i += 256)
-                    a.rscale[(uint64_t)r * a.nb + i] = a.xscale[t * a.nb + i];
+            for (int k = 0; k < 8; ++k) {
+                r[k] = k0 + k < a.K ? row_of[k0 + k] : -1;
+                if ((uint64_t)(uint32_t)r[k] >= a.nrows)
+                    r[k] = -1;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (r[k] < 0)
+                    continue;
+                uint8_t *row = a.rows + (uint64_t)r[k] * a.srows;
+                UNIT *to = reinterpret_cast<UNIT *>(row);
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (u0 + j * 256 < a.units)
+                        to[u0 + j * 256] = v[j];
+                if (part == 0) {
+                    // the bytes past the last whole unit, and the scales
+                    for (uint64_t i = a.units * sizeof(UNIT) + threadIdx.x; i < a.bytes; i += 256)
+                        row[i] = reinterpret_cast<const uint8_t *>(x)[i];
+                    for (int i = threadIdx.x; i < a.nb; i += 256)
+                        a.rscale[(uint64_t)r[k] * a.nb + i] = a.xscale[t * a.nb + i];
+                }
             }
         }
     }
@@ -258,56 +285,76 @@ struct ReturnArgs {
     const float *w;
     uint8_t *out;
     uint64_t srows, sout;     // bytes between rows
-    uint64_t nrows, T, H;
+    uint64_t nrows, T;
+    uint32_t H;
     uint32_t parts;           // CTAs per token
     int K;
 };
 
-// CTA b computes part b % parts of token b / parts, one unit a thread, up to
-// eight rows' loads in flight.
+// The eight choices from k0 on of a token: their rows (-1: none) and weights.
+struct Choices {
+    int32_t r[8];
+    float w[8];
+    __device__ __forceinline__ void read(const int32_t *row_of, const float *w_of, uint64_t t,
+                                         int K, int k0, uint64_t nrows) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = k0 + j < K ? row_of[t * K + k0 + j] : -1;
+            w[j] = w_of && k0 + j < K ? w_of[t * K + k0 + j] : 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (r[j] < 0 || (uint64_t)r[j] >= nrows)
+                r[j] = -1;
+    }
+};
+
+// A job is 256 units of a token, one a thread; the CTAs stay and take job after
+// job.  Eight rows' loads are in flight at a time, and the next job's rows and
+// weights are read meanwhile, so that its loads need not wait for them.
 template <int DT, bool WIDE>
-__global__ void __launch_bounds__(256) k_moe_return(const __grid_constant__ ReturnArgs a) {
+__global__ void __launch_bounds__(256, 3) k_moe_return(const __grid_constant__ ReturnArgs a) {
     using L = Rows<DT, WIDE>;
     kernel_prologue();
-    const uint64_t units = L::units(a.H);
-    for (uint64_t job = blockIdx.x; job < a.T * a.parts; job += gridDim.x) {
+    const uint32_t units = L::units(a.H);
+    const uint64_t jobs = a.T * a.parts;
+    Choices next;
+    if (blockIdx.x < jobs)
+        next.read(a.row_of, a.w, blockIdx.x / a.parts, a.K, 0, a.nrows);
+    for (uint64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const uint64_t t = job / a.parts;
-        const uint64_t u = (job - t * a.parts) * 256 + threadIdx.x;
-        if (u >= units)
-            continue;
-        const int32_t *row_of = a.row_of + t * a.K;
+        const uint32_t u = (uint32_t)(job - t * a.parts) * 256 + threadIdx.x;
         float acc[L::E];
 #pragma unroll
         for (int i = 0; i < L::E; ++i)
             acc[i] = 0.0f;
         bool any = false;
         for (int k0 = 0; k0 < a.K; k0 += 8) {
+            Choices c = next;
+            if (k0 > 0)
+                c.read(a.row_of, a.w, t, a.K, k0, a.nrows);
             uint4 p[8];
-            float w[8];
-            bool here[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int32_t r = k0 + j < a.K ? row_of[k0 + j] : -1;
-                here[j] = r >= 0 && (uint64_t)r < a.nrows;
-                if (here[j]) {
-                    p[j] = L::load(a.rows + (uint64_t)r * a.srows, u, a.H);
-                    w[j] = a.w ? a.w[t * a.K + k0 + j] : 1.0f;
-                }
-            }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (here[j]) {
+                p[j] = L::load_if(c.r[j] >= 0 && u < units,
+                                  a.rows + (uint64_t)(c.r[j] < 0 ? 0 : c.r[j]) * a.srows, u, a.H);
+            if (k0 + 8 >= a.K && job + gridDim.x < jobs)
+                next.read(a.row_of, a.w, (job + gridDim.x) / a.parts, a.K, 0, a.nrows);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c.r[j] >= 0) {
                     float v[L::E];
                     L::widen(p[j], v);
 #pragma unroll
                     for (int i = 0; i < L::E; ++i) {
-                        const float x = __fmul_rn(w[j], v[i]);
+                        const float x = __fmul_rn(c.w[j], v[i]);
                         acc[i] = any ? __fadd_rn(acc[i], x) : x;
                     }
                     any = true;
                 }
         }
-        L::store(a.out + t * a.sout, u, a.H, acc);
+        if (u < units)
+            L::store(a.out + t * a.sout, u, a.H, acc);
     }
 }
 
@@ -320,7 +367,8 @@ struct ReturnGradArgs {
     uint8_t *drows;
     float *dw;
     uint64_t sdout, srows, sdrows;    // bytes between rows
-    uint64_t nrows, T, H;
+    uint64_t nrows, T;
+    uint32_t H;
     int K;
 };
 
@@ -328,11 +376,11 @@ struct ReturnGradArgs {
 // dout, writes the weighted unit to each choice's row of drows and adds its
 // product with the choice's row; the eight sums are then joined over the CTA.
 template <int DT, bool WIDE>
-__global__ void __launch_bounds__(1024) k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
+__global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
     using L = Rows<DT, WIDE>;
     __shared__ float part[8][32];
     kernel_prologue();
-    const uint64_t units = L::units(a.H);
+    const uint32_t units = L::units(a.H);
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const uint8_t *dout = a.dout + t * a.sdout;
@@ -347,13 +395,14 @@ __global__ void __launch_bounds__(1024) k_moe_return_grad(const __grid_constant_
                 w[j] = a.w && k0 + j < a.K ? a.w[t * a.K + k0 + j] : 1.0f;
                 dot[j] = 0.0f;
             }
-            for (uint64_t u = threadIdx.x; u < units; u += blockDim.x) {
+            for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
                 uint4 p[8];
                 if (a.dw) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (r[j] >= 0)
-                            p[j] = L::load(a.rows + (uint64_t)r[j] * a.srows, u, a.H);
+                        p[j] = L::load_if(r[j] >= 0,
+                                          a.rows + (uint64_t)(r[j] < 0 ? 0 : r[j]) * a.srows, u,
+                                          a.H);
                 }
                 float d[L::E];
                 L::widen(L::load(dout, u, a.H), d);
@@ -399,19 +448,17 @@ __global__ void __launch_bounds__(1024) k_moe_return_grad(const __grid_constant_
 
 template <int DT, bool WIDE>
 static cudaError_t return_grad_launch(const ReturnGradArgs &a, cudaStream_t s) {
-    const uint64_t units = (Rows<DT, WIDE>::units(a.H) + 31) / 32 * 32;
+    const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
     const int grid = (int)(a.T < (1u << 30) ? a.T : (1u << 30));
-    const int most = 512;
-    return launch_kernel(k_moe_return_grad<DT, WIDE>, grid, (int)(units < most ? units : most), 0, s,
+    return launch_kernel(k_moe_return_grad<DT, WIDE>, grid, (int)(units < 256 ? units : 256), 0, s,
                          true, a);
 }
 
 template <int DT, bool WIDE> static cudaError_t return_launch(ReturnArgs a, cudaStream_t s) {
-    const uint64_t parts = (Rows<DT, WIDE>::units(a.H) + 255) / 256;
-    a.parts = (uint32_t)parts;
-    const uint64_t g = a.T * parts;
-    return launch_kernel(k_moe_return<DT, WIDE>, (int)(g < (1u << 30) ? g : (1u << 30)), 256, 0, s,
-                         true, a);
+    a.parts = (Rows<DT, WIDE>::units(a.H) + 255) / 256;
+    const uint64_t jobs = a.T * a.parts, most = 152 * 3;
+    return launch_kernel(k_moe_return<DT, WIDE>, (int)(jobs < most ? jobs : most), 256, 0, s, true,
+                         a);
 }
 
 // Sizes every row mover shares: the status code, AR_OK if they hold.
@@ -524,7 +571,7 @@ int ar_moe_return(const void *rows, size_t ldrows, size_t nrows, const int32_t *
     a.sout = mo.stride;
     a.nrows = nrows;
     a.T = T;
-    a.H = H;
+    a.H = (uint32_t)H;
     a.K = K;
     const bool v = wide(mr) && wide(mo);
     switch (dtype) {
@@ -574,7 +621,7 @@ int ar_moe_return_grad(const void *dout, size_t lddout, const void *rows, size_t
     a.sdrows = md.stride;
     a.nrows = nrows;
     a.T = T;
-    a.H = H;
+    a.H = (uint32_t)H;
     a.K = K;
     const bool v = wide(mo) && (!rows || wide(mr)) && (!drows || wide(md));
     switch (dtype) {

@@ -6,7 +6,7 @@
 //
 // Both are bound by memory: a row is read once, kept in registers across the
 // row's reduction, and written once.  A CTA works on one row at a time; the
-// units beyond what the registers hold (rows past 2048 units, 16384 elements
+// units beyond what the registers hold (rows past 2048 units: 16384 elements
 // of a two-byte type) are read a second time.
 #include "ar_rows.cuh"
 
@@ -18,7 +18,8 @@ struct NormArgs {
     uint8_t *sum, *y;
     float *scale, *rstd;
     uint64_t sx, sres, ssum, sy;      // bytes between rows
-    uint64_t T, H;
+    uint64_t T;
+    uint32_t H;
     float eps;
 };
 
@@ -35,9 +36,11 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 constexpr float kLeastBlock = 0x1p-96f;
 constexpr float kTopE4M3 = 448.0f;
 
-// The unit's share of y in 8 bits, and its block's scale.
+constexpr uint64_t kNormManyRows = 304;
+
+// The unit's share of y in 8 bits, and its block's scale.  Called by whole warps.
 template <int DT, bool WIDE>
-__device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint64_t u, uint64_t H,
+__device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint32_t u, uint32_t H,
                                            const float *v) {
     using L = Rows<DT, WIDE>;
     float m = 0.0f;
@@ -47,8 +50,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint64_t
 #pragma unroll
     for (int d = L::kBlockLanes / 2; d > 0; d >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    const float scale = __fdiv_rn(fmaxf(m, kLeastBlock), kTopE4M3);
-    const float inv = __fdiv_rn(1.0f, scale);
+    const float scale = fmaxf(m, kLeastBlock) * (1.0f / kTopE4M3);
+    const float inv = __frcp_rn(scale);
     if (L::at(u, 0) >= H)
         return;
     if (u % L::kBlockLanes == 0)
@@ -58,11 +61,11 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint64_t
     for (int i = 0; i < L::E; i += 4)
         q[i / 4] = e4m3x2(v[i] * inv, v[i + 1] * inv) |
                    e4m3x2(v[i + 2] * inv, v[i + 3] * inv) << 16;
-    if (WIDE && (u + 1) * L::E <= H) {
+    if (L::whole(u, H)) {
         if (L::E == 8)
-            *reinterpret_cast<uint2 *>(row + u * 8) = make_uint2(q[0], q[L::E / 4 - 1]);
+            reinterpret_cast<uint2 *>(row)[u] = make_uint2(q[0], q[L::E / 4 - 1]);
         else
-            *reinterpret_cast<uint32_t *>(row + u * 4) = q[0];
+            reinterpret_cast<uint32_t *>(row)[u] = q[0];
         return;
     }
 #pragma unroll
@@ -74,12 +77,12 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint64_t
 // One CTA per row.  UNITS units of a thread stay in registers.  Every loop
 // over units has the same trip count in a whole warp (the bound is a multiple
 // of 32), which the shuffles of store_e4m3 need.
-template <int DT, bool WIDE, bool E4M3, int UNITS>
-__global__ void __launch_bounds__(1024) k_rmsnorm(const __grid_constant__ NormArgs a) {
+template <int DT, bool WIDE, bool E4M3, int UNITS, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant__ NormArgs a) {
     using L = Rows<DT, WIDE>;
     __shared__ float part[32];
     kernel_prologue();
-    const uint64_t H = a.H, units = (L::units(H) + 31) / 32 * 32;
+    const uint32_t H = a.H, units = L::warp_units(H);
     for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const uint8_t *x = a.x + t * a.sx;
         const uint8_t *res = a.res ? a.res + t * a.sres : nullptr;
@@ -87,75 +90,77 @@ __global__ void __launch_bounds__(1024) k_rmsnorm(const __grid_constant__ NormAr
         uint8_t *y = a.y + t * a.sy;
         float *scale = E4M3 ? a.scale + t * ((H + AR_SCALE_BLOCK - 1) / AR_SCALE_BLOCK) : nullptr;
 
+        auto total = [&](uint4 px, uint4 pr, float *b) {     // x + res
+            L::widen(px, b);
+            if (res) {
+                float w[L::E];
+                L::widen(pr, w);
+#pragma unroll
+                for (int i = 0; i < L::E; ++i)
+                    b[i] += w[i];
+            }
+        };
         float v[UNITS][L::E];
         float ss = 0.0f;
-        uint4 px[UNITS], pr[UNITS];
+        {
+            uint4 px[UNITS], pr[UNITS];
 #pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
-            px[j] = pr[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (u < units) {
-                px[j] = L::load(x, u, H);
-                if (res)
-                    pr[j] = L::load(res, u, H);
+            for (int j = 0; j < UNITS; ++j) {
+                const uint32_t u = threadIdx.x + j * blockDim.x;
+                px[j] = pr[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (u < units) {
+                    px[j] = L::load(x, u, H);
+                    if (res)
+                        pr[j] = L::load(res, u, H);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < UNITS; ++j) {
+                total(px[j], pr[j], v[j]);
+#pragma unroll
+                for (int i = 0; i < L::E; ++i)
+                    ss += v[j][i] * v[j][i];
             }
         }
+        for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+            float b[L::E];
+            total(L::load(x, u, H), res ? L::load(res, u, H) : make_uint4(0u, 0u, 0u, 0u), b);
 #pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            float w[L::E];
-            L::widen(px[j], v[j]);
-            L::widen(pr[j], w);
-#pragma unroll
-            for (int i = 0; i < L::E; ++i) {
-                v[j][i] = res ? v[j][i] + w[i] : v[j][i];
-                ss += v[j][i] * v[j][i];
-            }
-        }
-        for (uint64_t u = threadIdx.x + (uint64_t)UNITS * blockDim.x; u < units; u += blockDim.x) {
-            float b[L::E], w[L::E];
-            L::widen(L::load(x, u, H), b);
-            if (res)
-                L::widen(L::load(res, u, H), w);
-#pragma unroll
-            for (int i = 0; i < L::E; ++i) {
-                b[i] = res ? b[i] + w[i] : b[i];
+            for (int i = 0; i < L::E; ++i)
                 ss += b[i] * b[i];
-            }
         }
         ss = block_sum(ss, part);
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)H) + a.eps));
         if (a.rstd && threadIdx.x == 0)
             a.rstd[t] = r;
 
-        auto finish = [&](uint64_t u, float *b) {
+        auto finish = [&](uint32_t u, float *b) {
             if (sum)
                 L::store(sum, u, H, b);
-            float g[L::E];
-            if (a.gamma)
-                L::widen(L::load(a.gamma, u, H), g);
 #pragma unroll
             for (int i = 0; i < L::E; ++i)
-                b[i] = a.gamma ? b[i] * r * g[i] : b[i] * r;
+                b[i] *= r;
+            if (a.gamma) {
+                float g[L::E];
+                L::widen(L::template load<true>(a.gamma, u, H), g);
+#pragma unroll
+                for (int i = 0; i < L::E; ++i)
+                    b[i] *= g[i];
+            }
             if (E4M3)
                 store_e4m3<DT, WIDE>(y, scale, u, H, b);
             else
                 L::store(y, u, H, b);
         };
-        // the units past the registers first: sum may overwrite x or res
-        for (uint64_t u = threadIdx.x + (uint64_t)UNITS * blockDim.x; u < units; u += blockDim.x) {
-            float b[L::E], w[L::E];
-            L::widen(L::load(x, u, H), b);
-            if (res) {
-                L::widen(L::load(res, u, H), w);
-#pragma unroll
-                for (int i = 0; i < L::E; ++i)
-                    b[i] += w[i];
-            }
+        // the units past the registers: read again, before sum or y overwrites them
+        for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+            float b[L::E];
+            total(L::load(x, u, H), res ? L::load(res, u, H) : make_uint4(0u, 0u, 0u, 0u), b);
             finish(u, b);
         }
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
+            const uint32_t u = threadIdx.x + j * blockDim.x;
             if (u < units)
                 finish(u, v[j]);
         }
@@ -165,16 +170,23 @@ __global__ void __launch_bounds__(1024) k_rmsnorm(const __grid_constant__ NormAr
 
 template <int DT, bool WIDE, bool E4M3>
 static cudaError_t norm_units(const NormArgs &a, cudaStream_t s) {
-    using L = Rows<DT, WIDE>;
-    const uint64_t units = (L::units(a.H) + 31) / 32 * 32;
+    const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
     const int grid = (int)(a.T < (1u << 30) ? a.T : (1u << 30));
-    auto threads = [&](uint64_t per) {
-        const uint64_t n = ((units + per - 1) / per + 31) / 32 * 32;
-        return (int)(n < 1024 ? n : 1024);
+    auto threads = [&](uint32_t per, uint32_t most) {
+        const uint32_t n = ((units + per - 1) / per + 31) / 32 * 32;
+        return (int)(n < most ? n : most);
     };
-    if (units <= 1024)
-        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 1>, grid, threads(1), 0, s, true, a);
-    return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 2>, grid, threads(2), 0, s, true, a);
+    // Many rows: four units a thread, so that an SM holds several CTAs and one
+    // row's loads run while another's reduction waits.  Few rows: as many
+    // threads as the row has units, for latency.
+    if (a.T > kNormManyRows && units <= 1024)
+        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 4, 256, 4>, grid, threads(4, 256), 0, s,
+                             true, a);
+    if (a.T > kNormManyRows)
+        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 4, 512, 2>, grid, threads(4, 512), 0, s,
+                             true, a);
+    return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 2, 1024, 1>, grid,
+                         threads(units <= 1024 ? 1 : 2, 1024), 0, s, true, a);
 }
 
 template <int DT>
@@ -193,18 +205,84 @@ struct NormGradArgs {
     uint8_t *dx;
     float *work;                      // gridDim.x rows of H partial sums, or NULL
     uint64_t sdy, sdsum, ss, sdx;     // bytes between rows
-    uint64_t T, H;
+    uint64_t T;
+    uint32_t H;
 };
+
+// Copy of 16 bytes (or fewer: the rest reads as zero) to shared memory, done
+// in the background.
+__device__ __forceinline__ void copy_async(uint4 *to, const void *from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int LEFT> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+
+// One element block of the gradient.  With c = r^3 * sum(d * s) / H:
+//   d = gamma * dy,  dgamma += dy * (s * r),  dx = r * d - c * s + dsum
+// Pass 1: d from dy and gamma; the products' sum and dgamma's share.
+template <int DT, bool WIDE>
+__device__ __forceinline__ float grad_open(const NormGradArgs &a, uint32_t u, uint4 ps, uint4 pd,
+                                           float r, float *d, float *dg) {
+    using L = Rows<DT, WIDE>;
+    float s[L::E], dot = 0.0f;
+    L::widen(ps, s);
+    L::widen(pd, d);
+#pragma unroll
+    for (int i = 0; i < L::E; ++i)
+        dg[i] += d[i] * (s[i] * r);
+    if (a.gamma) {
+        float g[L::E];
+        L::widen(L::template load<true>(a.gamma, u, a.H), g);
+#pragma unroll
+        for (int i = 0; i < L::E; ++i)
+            d[i] *= g[i];
+    }
+#pragma unroll
+    for (int i = 0; i < L::E; ++i)
+        dot += d[i] * s[i];
+    return dot;
+}
+// Pass 2.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void grad_close(const NormGradArgs &a, uint32_t u, uint4 ps, float *d,
+                                           uint4 pu, float r, float c, uint8_t *dx) {
+    using L = Rows<DT, WIDE>;
+    float s[L::E];
+    L::widen(ps, s);
+#pragma unroll
+    for (int i = 0; i < L::E; ++i)
+        d[i] = r * d[i] - c * s[i];
+    if (a.dsum) {
+        float w[L::E];
+        L::widen(pu, w);
+#pragma unroll
+        for (int i = 0; i < L::E; ++i)
+            d[i] += w[i];
+    }
+    L::store(dx, u, a.H, d);
+}
 
 // CTA b takes the rows b, b + gridDim.x, ...; each thread owns the columns of
 // its units and keeps their share of dgamma in registers over all of the
-// CTA's rows (units past the registers: in the CTA's row of `work`).
-template <int DT, bool WIDE, int UNITS>
-__global__ void __launch_bounds__(1024) k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
+// CTA's rows.  RING: the next row's s, dy and dsum come to shared memory by
+// background copies while this row is at work; a thread copies and reads its
+// own units only, so the copies need no barrier.  Without it (rows that are
+// not 16-byte aligned, or longer than UNITS units a thread) rows are loaded in
+// their turn, and the units past the registers are read twice, their dgamma
+// kept in the CTA's row of `work`.
+template <int DT, bool WIDE, int UNITS, int THREADS, int CTAS, bool RING>
+__global__ void __launch_bounds__(THREADS, CTAS)
+k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
     using L = Rows<DT, WIDE>;
+    extern __shared__ uint4 ring[];               // [2][3][UNITS][THREADS]
     __shared__ float part[2][32];
     kernel_prologue();
-    const uint64_t H = a.H, units = (L::units(H) + 31) / 32 * 32;
+    const uint32_t H = a.H, units = L::warp_units(H);
     float *work = a.work ? a.work + (uint64_t)blockIdx.x * H : nullptr;
     float dg[UNITS][L::E];
 #pragma unroll
@@ -212,76 +290,100 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_grad(const __grid_constant__ N
 #pragma unroll
         for (int i = 0; i < L::E; ++i)
             dg[j][i] = 0.0f;
+    auto slot = [&](int turn, int array, int j) -> uint4 & {
+        return ring[((turn * 3 + array) * UNITS + j) * THREADS + threadIdx.x];
+    };
+    auto fetch = [&](uint64_t t, int turn) {      // the ring's copies of row t
+        if (t < a.T) {
+            const uint8_t *s = a.s + t * a.ss, *dy = a.dy + t * a.sdy;
+            const uint8_t *dsum = a.dsum ? a.dsum + t * a.sdsum : nullptr;
+#pragma unroll
+            for (int j = 0; j < UNITS; ++j) {
+                const uint32_t u = threadIdx.x + j * blockDim.x;
+                const uint32_t left = u * L::E < H ? (H - u * L::E) * L::kSize : 0u;
+                const uint32_t n = left < 16u ? left : 16u;
+                const uint64_t at = n ? (uint64_t)u * 16 : 0;
+                copy_async(&slot(turn, 0, j), s + at, n);
+                copy_async(&slot(turn, 1, j), dy + at, n);
+                if (dsum)
+                    copy_async(&slot(turn, 2, j), dsum + at, n);
+            }
+        }
+        copies_commit();
+    };
     int turn = 0;
+    if (RING)
+        fetch(blockIdx.x, 0);
     for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         const uint8_t *dy = a.dy + t * a.sdy, *s = a.s + t * a.ss;
         const uint8_t *dsum = a.dsum ? a.dsum + t * a.sdsum : nullptr;
         uint8_t *dx = a.dx + t * a.sdx;
         const float r = a.rstd[t];
-        float n[L::E], d[L::E], g[L::E];
-        auto fetch = [&](uint64_t u) {               // n, d = gamma * dy, g = dy
-            L::widen(L::load(s, u, H), n);
-            L::widen(L::load(dy, u, H), g);
-            float w[L::E];
-            if (a.gamma)
-                L::widen(L::load(a.gamma, u, H), w);
-#pragma unroll
-            for (int i = 0; i < L::E; ++i) {
-                n[i] *= r;
-                d[i] = a.gamma ? w[i] * g[i] : g[i];
-            }
-        };
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
         float dot = 0.0f;
-        for (uint64_t u = threadIdx.x; u < units; u += blockDim.x) {
-            fetch(u);
+        uint4 ps[UNITS], pd[UNITS], pu[UNITS];
+        float d[UNITS][L::E];
+        if (RING) {
+            fetch(t + gridDim.x, turn ^ 1);
+            copies_wait<1>();
 #pragma unroll
-            for (int i = 0; i < L::E; ++i)
-                dot += d[i] * n[i];
-        }
-        const float mean = __fdiv_rn(block_sum(dot, part[turn]), (float)H);
-        auto finish = [&](uint64_t u) {
-            float w[L::E];
-            if (dsum)
-                L::widen(L::load(dsum, u, H), w);
-#pragma unroll
-            for (int i = 0; i < L::E; ++i) {
-                d[i] = r * (d[i] - n[i] * mean);
-                if (dsum)
-                    d[i] += w[i];
+            for (int j = 0; j < UNITS; ++j) {
+                ps[j] = slot(turn, 0, j);
+                pd[j] = slot(turn, 1, j);
             }
-            L::store(dx, u, H, d);
-        };
+        } else {
+#pragma unroll
+            for (int j = 0; j < UNITS; ++j) {
+                const uint32_t u = threadIdx.x + j * blockDim.x;
+                ps[j] = pd[j] = pu[j] = none;
+                if (u < units) {
+                    ps[j] = L::load(s, u, H);
+                    pd[j] = L::load(dy, u, H);
+                    if (dsum)
+                        pu[j] = L::load(dsum, u, H);
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
-            if (u < units) {
-                fetch(u);
+            const uint32_t u = threadIdx.x + j * blockDim.x;
+            if (u < units)
+                dot += grad_open<DT, WIDE>(a, u, ps[j], pd[j], r, d[j], dg[j]);
+        }
+        if (!RING)
+            for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+                float e[L::E], w[L::E];
 #pragma unroll
                 for (int i = 0; i < L::E; ++i)
-                    dg[j][i] += g[i] * n[i];
-                finish(u);
-            }
-        }
-        for (uint64_t u = threadIdx.x + (uint64_t)UNITS * blockDim.x; u < units; u += blockDim.x) {
-            fetch(u);
-            if (work) {
+                    w[i] = work && L::at(u, i) < H && t != blockIdx.x ? work[L::at(u, i)] : 0.0f;
+                dot += grad_open<DT, WIDE>(a, u, L::load(s, u, H), L::load(dy, u, H), r, e, w);
 #pragma unroll
                 for (int i = 0; i < L::E; ++i)
-                    if (L::at(u, i) < H) {
-                        float *w = work + L::at(u, i);
-                        *w = (t == blockIdx.x ? 0.0f : *w) + g[i] * n[i];
-                    }
+                    if (work && L::at(u, i) < H)
+                        work[L::at(u, i)] = w[i];
             }
-            finish(u);
+        const float c = __fdiv_rn(block_sum(dot, part[turn]) * r * r * r, (float)H);
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const uint32_t u = threadIdx.x + j * blockDim.x;
+            if (u < units)
+                grad_close<DT, WIDE>(a, u, ps[j], d[j], RING ? slot(turn, 2, j) : pu[j], r, c, dx);
         }
+        if (!RING)
+            for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+                float e[L::E], w[L::E];
+                const uint4 s4 = L::load(s, u, H);
+                grad_open<DT, WIDE>(a, u, s4, L::load(dy, u, H), r, e, w);
+                grad_close<DT, WIDE>(a, u, s4, e, dsum ? L::load(dsum, u, H) : none, r, c, dx);
+            }
     }
     if (work) {
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const uint64_t u = threadIdx.x + (uint64_t)j * blockDim.x;
+            const uint32_t u = threadIdx.x + j * blockDim.x;
 #pragma unroll
             for (int i = 0; i < L::E; ++i)
-                if (L::at(u, i) < H)
+                if (L::at(u, i) < H && u < units)
                     work[L::at(u, i)] = dg[j][i];
         }
     }
@@ -309,12 +411,26 @@ __global__ void __launch_bounds__(1024) k_join_rows(const float *work, float *ou
 
 template <int DT, bool WIDE>
 static cudaError_t norm_grad_units(const NormGradArgs &a, int grid, cudaStream_t s) {
-    using L = Rows<DT, WIDE>;
-    const uint64_t units = (L::units(a.H) + 31) / 32 * 32;
-    const int threads = (int)(units < 1024 ? units : 1024);
+    const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
+    auto threads = [&](uint32_t per, uint32_t most) {
+        const uint32_t n = ((units + per - 1) / per + 31) / 32 * 32;
+        return (int)(n < most ? n : most);
+    };
+    // with the ring, 2 x 3 rows of 16 KB a CTA and two CTAs an SM
+    if (WIDE && units <= 1024) {
+        constexpr int kUnits = 2, kThreads = 512;
+        const auto kernel = k_rmsnorm_grad<DT, WIDE, kUnits, kThreads, 2, WIDE>;
+        const int smem = 2 * 3 * kUnits * kThreads * (int)sizeof(uint4);
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess)
+            return e;
+        return launch_kernel(kernel, grid, threads(kUnits, kThreads), smem, s, true, a);
+    }
     if (units <= 1024)
-        return launch_kernel(k_rmsnorm_grad<DT, WIDE, 1>, grid, threads, 0, s, true, a);
-    return launch_kernel(k_rmsnorm_grad<DT, WIDE, 2>, grid, threads, 0, s, true, a);
+        return launch_kernel(k_rmsnorm_grad<DT, WIDE, 4, 256, 2, false>, grid, threads(4, 256), 0, s,
+                             true, a);
+    return launch_kernel(k_rmsnorm_grad<DT, WIDE, 4, 512, 1, false>, grid, threads(4, 512), 0, s, true, a);
 }
 
 template <int DT> static cudaError_t norm_grad_dt(const NormGradArgs &a, bool w, int grid,
@@ -370,7 +486,7 @@ int ar_rmsnorm(const void *x, size_t ldx, const void *res, size_t ldres, const v
     a.ssum = ms.stride;
     a.sy = my.stride;
     a.T = T;
-    a.H = H;
+    a.H = (uint32_t)H;
     a.eps = eps;
     const bool w = wide(mx) && (!res || wide(mr)) && mg.p % 16 == 0 && (!sum || wide(ms)) &&
                    wide(my, e4m3 ? 16 / esz : 16);
@@ -427,8 +543,10 @@ int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum
     a.ss = ms.stride;
     a.sdx = mx.stride;
     a.T = T;
-    a.H = H;
-    const int grid = (int)(T < 304 ? T : 304);
+    a.H = (uint32_t)H;
+    // two CTAs per SM; more of them where rows are short
+    const size_t most = H <= 2048 ? AR_NORM_GRAD_ROWS : 304;
+    const int grid = (int)(T < most ? T : most);
     const bool w = wide(my) && (!dsum || wide(mu)) && wide(ms) && wide(mx) && mg.p % 16 == 0;
     cudaError_t e;
     switch (dtype) {

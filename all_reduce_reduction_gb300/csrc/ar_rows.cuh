@@ -15,67 +15,113 @@
 
 namespace ar {
 
+// Two elements of a two-byte type in one word, and back.
+template <int DT> __device__ __forceinline__ float2 widen2(uint32_t w) {
+    if (DT == AR_BF16)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <int DT> __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    if (DT == AR_BF16) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&p);
+    }
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
 template <int DT, bool WIDE> struct Rows {
     static constexpr int kSize = Elem<DT>::kSize;
     static constexpr int E = WIDE ? 16 / kSize : 4;               // elements per unit
     static constexpr int kBlockLanes = AR_SCALE_BLOCK / E;        // units per scale block
+    static constexpr bool kPairs = WIDE && kSize == 2;            // two elements a word
     static_assert(kBlockLanes <= 32, "a scale block is at most one warp");
 
-    // units that cover a row: whole scale blocks in the general form, whose
-    // units interleave within 128 elements
-    static __host__ __device__ __forceinline__ uint64_t units(uint64_t H) {
+    // units that cover a row of H < 2^31 elements: whole scale blocks in the
+    // general form, whose units interleave within 128 elements
+    static __host__ __device__ __forceinline__ uint32_t units(uint32_t H) {
         return WIDE ? (H + E - 1) / E : (H + 127) / 128 * 32;
     }
+    // the same, up to a whole number of warps
+    static __host__ __device__ __forceinline__ uint32_t warp_units(uint32_t H) {
+        return (units(H) + 31) / 32 * 32;
+    }
     // element i of unit u
-    static __device__ __forceinline__ uint64_t at(uint64_t u, int i) {
+    static __device__ __forceinline__ uint32_t at(uint32_t u, int i) {
         return WIDE ? u * E + i : u / 32 * 128 + u % 32 + 32 * i;
     }
+    static __device__ __forceinline__ bool whole(uint32_t u, uint32_t H) {
+        return WIDE && u * E + E <= H;
+    }
     // The unit's bits: words of packed elements (wide) or one element a word.
-    // Elements past H read as zero.
-    static __device__ __forceinline__ uint4 load(const void *row, uint64_t u, uint64_t H) {
-        if (WIDE && (u + 1) * E <= H)
-            return ld_v4_stream(reinterpret_cast<const uint4 *>(row) + u);
+    // Elements past H read as zero.  REUSED data may stay in L1.
+    template <bool REUSED = false>
+    static __device__ __forceinline__ uint4 load(const void *row, uint32_t u, uint32_t H) {
+        if (whole(u, H)) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(row) + u;
+            return REUSED ? ld_v4_l1(p) : ld_v4_stream(p);
+        }
         uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < E; ++i)
             if (at(u, i) < H) {
                 const uint32_t b = ld_elem<DT>(row, at(u, i));
-                if (WIDE && kSize == 2)
+                if (kPairs)
                     w[i / 2] |= b << (16 * (i & 1));
                 else
                     w[i & 3] = b;
             }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    // The same where `on` is true, zeros elsewhere.  The wide load is predicated,
+    // not branched around, so that a run of them is issued without a wait.
+    static __device__ __forceinline__ uint4 load_if(bool on, const void *row, uint32_t u,
+                                                    uint32_t H) {
+        if (!whole(u, H))
+            return on ? load(row, u, H) : make_uint4(0u, 0u, 0u, 0u);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+            : "l"(reinterpret_cast<const uint4 *>(row) + u), "r"((uint32_t)on));
+        return v;
+    }
     static __device__ __forceinline__ void widen(uint4 p, float v[E]) {
         const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+        if (kPairs) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (WIDE && kSize == 2)
-                v[i] = widen1<DT>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
-            else
+            for (int i = 0; i < E; i += 2) {
+                const float2 f = widen2<DT>(w[i / 2]);
+                v[i] = f.x;
+                v[i + (E > 1)] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
                 v[i] = widen1<DT>(w[i & 3]);
         }
     }
-    static __device__ __forceinline__ void store(void *row, uint64_t u, uint64_t H,
+    static __device__ __forceinline__ void store(void *row, uint32_t u, uint32_t H,
                                                  const float v[E]) {
         uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (kPairs) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (WIDE && kSize == 2)
-                w[i / 2] |= narrow1<DT>(v[i]) << (16 * (i & 1));
-            else
+            for (int i = 0; i < E; i += 2)
+                w[i / 2] = narrow2<DT>(v[i], v[i + (E > 1)]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
                 w[i & 3] = narrow1<DT>(v[i]);
         }
-        if (WIDE && (u + 1) * E <= H) {
+        if (whole(u, H)) {
             st_v4(reinterpret_cast<uint4 *>(row) + u, make_uint4(w[0], w[1], w[2], w[3]));
             return;
         }
 #pragma unroll
         for (int i = 0; i < E; ++i)
             if (at(u, i) < H)
-                st_elem<DT>(row, at(u, i),
-                            WIDE && kSize == 2 ? (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu : w[i & 3]);
+                st_elem<DT>(row, at(u, i), kPairs ? (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu : w[i & 3]);
     }
 };
 
