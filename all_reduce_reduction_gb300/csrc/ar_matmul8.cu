@@ -137,6 +137,7 @@ int ar_matmul8(const void *a, size_t lda, const float *sa, const void *b, size_t
     g.E = E;
     g.kb = (int)kb;
     g.out = out_dtype;
+    g.sa_wide = wide(ms);
     g.dwide = wide(md);
     g.status = status;
     if (wide(ma) && wide(mb)) {

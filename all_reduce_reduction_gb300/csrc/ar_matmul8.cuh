@@ -17,6 +17,7 @@ struct MatmulArgs {
     int E;
     int kb;                       // blocks along k
     int out;                      // enum ar_dtype
+    int sa_wide;                  // rows of sa start on 16-byte boundaries
     int dwide;                    // rows of d start on 16-byte boundaries
     int *status;
 };

@@ -6,11 +6,11 @@
 // binary32 sums in their registers, while the tensor core fills the next
 // accumulator.
 //
-// Two forms.  k_matmul8_rows puts 128 rows of a on the accumulator's lanes and
-// 256 rows of b on its columns: a thread's row scale is then one register.
-// k_matmul8_few is for few rows per group: 128 rows of b on the lanes, 16 to
-// 128 rows of a on the columns, several CTAs of a cluster along k; it streams
-// the weights once with all SMs even when there is one row.
+// Two forms.  k_matmul8_rows puts rows of a on the accumulator's lanes, 256 for a
+// pair of CTAs, and 256 rows of b on its columns: a thread's row scale is then
+// one register.  k_matmul8_few is for few rows per group: 128 rows of b on the
+// lanes, 16 to 64 rows of a on the columns, several CTAs of a cluster along k;
+// it streams the weights once with all SMs even when there is one row.
 //
 // Every wait is bounded: past kWaitNs it writes AR_ERR_TIMEOUT to the caller's
 // status word and the CTA's roles all leave.
@@ -49,16 +49,19 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 // Bounded wait for the phase of this parity; false if this wait ran out or
-// another role of the CTA gave up.
+// another role of the CTA gave up.  Called after a first try.
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort,
                                             int *status) {
-    const uint64_t deadline = globaltimer_ns() + kWaitNs;
-    for (;;) {
+    uint64_t deadline = 0;
+    for (uint32_t tries = 1;; ++tries) {
         if (mbar_test(bar, parity))
             return true;
         if (*abort)
             return false;
-        if (globaltimer_ns() > deadline) {
+        const uint64_t now = globaltimer_ns();
+        if (deadline == 0)
+            deadline = now + kWaitNs;
+        if (now > deadline) {
             if (status)
                 record_error(status, AR_ERR_TIMEOUT);
             *abort = 1;
@@ -69,6 +72,21 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volat
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *abort,
                                           int *status) {
     return mbar_test(bar, parity) || mbar_wait_slow(bar, parity, abort, status);
+}
+
+// The same by a whole warp, all lanes with one answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                          int *status) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))
+        return true;
+    return __all_sync(0xFFFFFFFFu, mbar_wait_slow(bar, parity, abort, status));
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok));
+    return ok != 0;
 }
 
 // After an abort only: bounded waits until what is in flight has ended, so that
@@ -101,15 +119,61 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
+// The same for a CTA of a pair, the bytes counted by a barrier of either CTA.
+__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];"
+        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+// This place of shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// Arrival at a barrier of either CTA.  It hands over tensor memory that has been
+// read, which tcgen05.fence orders; nothing in ordinary memory goes with it, so
+// it needs no wider release (at cluster scope that doubled the kernel's time).
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // ---- tcgen05 -------------------------------------------------------------------
 
-template <int COLS> __device__ __forceinline__ void tmem_alloc(uint32_t *slot) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 :: "r"(smem_addr(slot)), "n"(COLS) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+// PAIR: the two CTAs of a cluster work on one accumulator tile (cta_group::2);
+// one warp of each allocates and frees.
+template <int COLS, bool PAIR> __device__ __forceinline__ void tmem_alloc(uint32_t *slot) {
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_addr(slot)), "n"(COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :: "r"(smem_addr(slot)), "n"(COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
 }
-template <int COLS> __device__ __forceinline__ void tmem_free(uint32_t addr) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(addr), "n"(COLS));
+template <int COLS, bool PAIR> __device__ __forceinline__ void tmem_free(uint32_t addr) {
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;"
+                     :: "r"(addr), "n"(COLS));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
+                     :: "r"(addr), "n"(COLS));
 }
 __device__ __forceinline__ void fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -128,6 +192,21 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
         :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
 }
+// The pair's forms: both CTAs hold their half of each operand at the same place
+// of their shared memory, one thread of the first CTA issues, and a commit
+// arrives at the barrier of this place in both.
+__device__ __forceinline__ void mma_pair_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" :: "r"(bar), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void mma_pair_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
 // Operand tile of rows of 128 bytes, 128-byte swizzle, K-major: eight rows
 // (1024 bytes) between the groups of the stride offset.
 __device__ __forceinline__ uint64_t operand(uint32_t addr) {
@@ -138,55 +217,51 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
 __host__ __device__ constexpr uint32_t mma_shape(int m, int n) {
     return 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
 }
-// One block along k: 128 bytes, 32 per instruction.
-__device__ __forceinline__ void mma_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
-    const uint64_t da = operand(a), db = operand(b);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        mma_e4m3(d, da + 2 * k, db + 2 * k, idesc, k > 0);
-}
-
-// 16 columns of the warp's 32 lanes; the values are there after tmem_wait.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t v[16]) {
+// 16 columns of the warp's 32 lanes.  Load and wait are one statement: passing
+// the registers through a separate wait cost a move each, as many instructions
+// as the multiply-adds.
+__device__ __forceinline__ void tmem_load(uint32_t addr, float v[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-          "=r"(v[14]), "=r"(v[15])
-        : "r"(addr));
-}
-// The registers pass through the wait, so that nothing reads them before it.
-__device__ __forceinline__ void tmem_wait(uint32_t v[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
-                 :: "memory");
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15])
+        : "r"(addr) : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-__device__ __forceinline__ uint32_t pack_fp16(float a, float b) {
-    const __half2 p = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&p);
+// Two sums at once: x[i] += s[i] * v[i], each rounded once.
+__device__ __forceinline__ void add_scaled2(float *x, float s0, float s1, float v0, float v1) {
+    asm("{\n\t.reg .b64 s, t, u;\n\t"
+        "mov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmov.b64 u, {%0, %1};\n\t"
+        "fma.rn.f32x2 u, s, t, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(x[0]), "+f"(x[1]) : "f"(s0), "f"(s1), "f"(v0), "f"(v1));
 }
 
 // ---- many rows ----------------------------------------------------------------
 
-constexpr int kRowsM = 128, kRowsN = 256, kRowsStages = 4;
+constexpr int kRowsM = 256, kRowsN = 256, kRowsStages = 6;
+constexpr int kRowsHalf = 128;                    // rows of a, and of b, that a CTA of the pair holds
 constexpr int kRowsEpilogueWarps = 8;
-constexpr int kRowsThreads = 32 * (kRowsEpilogueWarps + 2);
-constexpr int kRowsABytes = kRowsM * 128, kRowsBBytes = kRowsN * 128;
-constexpr int kRowsStage = kRowsABytes + kRowsBBytes;
+constexpr int kRowsRun = 32;                      // columns an epilogue warp stores at a time
+constexpr int kRowsAccs = 4, kRowsAccCols = 128;  // accumulators, and columns of one
+constexpr int kRowsThreads = 32 * (kRowsEpilogueWarps + 3);
+constexpr int kRowsScales = 8;                    // blocks along k whose scales a slot holds
+constexpr int kRowsOperand = kRowsHalf * 128;
+constexpr int kRowsStage = 2 * kRowsOperand;
 // row tiles walked side by side before the next columns: the weights of a
 // column tile are read by that many CTAs at about the same time
-constexpr int kRowsBand = 16;
+constexpr int kRowsBand = 8;
 
 struct RowsShared {
-    uint64_t full[kRowsStages], empty[kRowsStages], acc_full[2], acc_empty[2], drain;
+    uint4 stage[kRowsEpilogueWarps][128];         // an epilogue warp's way to d
+    uint64_t full[kRowsStages], empty[kRowsStages], acc_full[kRowsAccs],
+        acc_empty[kRowsAccs], drain;
+    uint64_t scale_full[2], scale_empty[2];
+    // the row scales of kRowsScales blocks, and those of the tile's two weight blocks
+    float sa[2][kRowsScales][kRowsHalf];
+    alignas(8) float sb[2][kRowsScales][2];
     uint32_t tmem;
     int abort;
     uint32_t tiles;                               // row tiles of all groups
@@ -240,47 +315,69 @@ __device__ __forceinline__ RowsTile rows_tile(const MatmulArgs &a, const RowsSha
     return t;
 }
 
-// 128 sums of one row to d, columns n to n + 127 as far as N.
-__device__ __forceinline__ void store_row(const MatmulArgs &a, uint64_t m, uint32_t n,
-                                          const float acc[128]) {
-    uint8_t *row = a.d + m * a.ldd;
-    if (a.out == AR_FP32) {
-        float4 *to = reinterpret_cast<float4 *>(row + (uint64_t)n * 4);
+// A warp's 32 rows x 32 columns of sums to d: rows from m0 and columns from n0
+// on, as far as `rows` and N.  64 bytes of every row at a time go through the
+// warp's 2 KB of shared memory (16-byte words in an order that keeps both sides
+// free of bank conflicts), so that a store instruction writes whole sectors of
+// eight rows.
+template <int OUT>
+__device__ __forceinline__ void store_rows(const MatmulArgs &a, uint4 *stage, uint64_t m0,
+                                           uint32_t rows, uint32_t n0,
+                                           const float acc[kRowsRun]) {
+    constexpr int kSize = Elem<OUT>::kSize, kWord = 16 / kSize, kCols = 64 / kSize;
+    const uint32_t lane = threadIdx.x & 31;
+    auto word = [&](uint32_t row, uint32_t q) -> uint4 & {
+        return stage[row * 4 + (q ^ (row >> 1 & 3))];
+    };
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-            if (a.dwide && n + c + 4 <= a.N)
-                to[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-            else
+    for (int c = 0; c < kRowsRun; c += kCols) {
+        if (n0 + c >= a.N)
+            break;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n + c + j < a.N)
-                        store_out(row, n + c + j, acc[c + j], AR_FP32);
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = c + q * kWord + i * (kWord / 4);
+                w[i] = kSize == 4 ? __float_as_uint(acc[e])
+                                  : narrow2<OUT>(acc[e], acc[e + (kSize == 2)]);
+            }
+            word(lane, q) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-    } else {
-        uint4 *to = reinterpret_cast<uint4 *>(row + (uint64_t)n * 2);
-        const bool bf16 = a.out == AR_BF16;
+        __syncwarp();
+        if (a.dwide && n0 + c + kCols <= a.N) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-            if (a.dwide && n + c + 8 <= a.N) {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = bf16 ? pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1])
-                                : pack_fp16(acc[c + 2 * j], acc[c + 2 * j + 1]);
-                to[c / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (n + c + j < a.N)
-                        store_out(row, n + c + j, acc[c + j], a.out);
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t row = i * 8 + lane / 4, q = lane % 4;
+                if (row < rows)
+                    reinterpret_cast<uint4 *>(a.d + (m0 + row) * a.ldd +
+                                              (uint64_t)(n0 + c) * kSize)[q] = word(row, q);
+            }
+        } else {
+            for (uint32_t i = lane; i < rows * kCols; i += 32) {
+                const uint32_t row = i / kCols, col = i % kCols;
+                if (n0 + c + col < a.N)
+                    st_elem<OUT>(a.d + (m0 + row) * a.ldd, n0 + c + col,
+                                 ld_elem<OUT>(&word(row, col / kWord), col % kWord));
             }
         }
+        __syncwarp();
     }
 }
 
-// Persistent: one CTA per SM takes tiles blockIdx.x, + gridDim.x, ...
-// Warps 0-7: epilogue (lanes 32 * (warp % 4), columns 128 * (warp / 4));
-// warp 8: TMA; warp 9: MMA.
+// Persistent: a pair of CTAs takes a tile of 256 x 256, then the next of every
+// gridDim.x / 2.  CTA `rank` holds rows 128 * rank, ... of the tile's rows of a
+// and of its rows of b; the tensor cores of both SMs read both halves of b, and
+// the sums of a CTA's rows of a are in its own tensor memory.  One CTA's tile of
+// 128 x 256 needs 48 KB a block to be written to and read from shared memory,
+// more than its 128 bytes a clock allow beside the products; the pair's 32 KB
+// fit.
+// Warps 0-15: epilogue (lanes 32 * (warp % 4), columns 64 * (warp / 4));
+// warp 16: TMA; warp 17: MMA; warp 18: scales.  The scales of a tile's rows are
+// a column of sa, one sector a row: read by every epilogue warp for every block
+// they kept the L1 pipe, which also feeds the tensor core, half busy (8192^3:
+// 515 us).  Warp 18 reads each once, eight blocks at a time, and lays them out
+// by block in shared memory.
 __global__ void __launch_bounds__(kRowsThreads, 1)
 k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
@@ -288,25 +385,31 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
     uint8_t *stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     RowsShared &sh = *reinterpret_cast<RowsShared *>(stages + kRowsStages * kRowsStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     volatile int *abort = &sh.abort;
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
     const uint32_t acc_full = smem_addr(sh.acc_full), acc_empty = smem_addr(sh.acc_empty);
+    const uint32_t scale_full = smem_addr(sh.scale_full), scale_empty = smem_addr(sh.scale_empty);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRowsStages; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kRowsAccs; ++b) {
             mbar_init(acc_full + 8 * b, 1);
             mbar_init(acc_empty + 8 * b, kRowsEpilogueWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(scale_full + 8 * b, 1);
+            mbar_init(scale_empty + 8 * b, kRowsEpilogueWarps);
         }
         mbar_init(smem_addr(&sh.drain), 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9)
-        tmem_alloc<512>(&sh.tmem);
+    if (warp == kRowsEpilogueWarps + 1)
+        tmem_alloc<512, true>(&sh.tmem);
     kernel_prologue();
     if (warp == 0) {
         uint32_t base = 0;
@@ -329,100 +432,201 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
             sh.tiles = base;
     }
     fence_before();
-    __syncthreads();
+    cluster_barrier();                            // both CTAs' barriers are ready
     fence_after();
     const uint32_t tmem = sh.tmem;
     const uint32_t ntiles = (a.N + kRowsN - 1) / kRowsN;
     const uint64_t total = (uint64_t)sh.tiles * ntiles;
 
     uint32_t used = 0;                            // stages filled or drained by this role
-    if (warp == 8) {
+    if (warp == kRowsEpilogueWarps) {
         if (lane == 0) {
-            for (uint64_t i = blockIdx.x; i < total && !*abort; i += gridDim.x) {
+            for (uint64_t i = pair; i < total && !*abort; i += pairs) {
                 const RowsTile t = rows_tile(a, sh, ntiles, i);
                 for (int kb = 0; kb < a.kb; ++kb, ++used) {
                     const uint32_t s = used % kRowsStages, turn = used / kRowsStages;
                     if (turn > 0 && !mbar_wait(empty + 8 * s, (turn - 1) & 1, abort, a.status))
                         break;
                     const uint32_t at = smem_addr(stages) + s * kRowsStage;
-                    mbar_expect(full + 8 * s, kRowsStage);
-                    tma_2d(at, &map_a, kb * 128, (int)t.row, full + 8 * s);
-                    tma_3d(at + kRowsABytes, &map_b, kb * 128, (int)t.n0, t.group, full + 8 * s);
+                    const uint32_t bar = peer_addr(full + 8 * s, 0);
+                    // a tile of at most 128 rows leaves the second CTA's rows
+                    // of a alone: their sums are not stored
+                    const bool both = t.rows > kRowsHalf;
+                    if (rank == 0)
+                        mbar_expect(full + 8 * s, (both ? 4 : 3) * kRowsOperand);
+                    if (rank == 0 || both)
+                        tma_pair_2d(at, &map_a, kb * 128, (int)(t.row + rank * kRowsHalf), bar);
+                    tma_pair_3d(at + kRowsOperand, &map_b, kb * 128,
+                                (int)(t.n0 + rank * kRowsHalf), t.group, bar);
                 }
             }
+            // the last stages' arrivals come from the first CTA: this one stays
+            // until they are in
+            for (uint32_t k = used < kRowsStages ? 0 : used - kRowsStages; k < used && !*abort; ++k)
+                (void)mbar_wait(empty + 8 * (k % kRowsStages), (k / kRowsStages) & 1, abort,
+                                a.status);
         }
         __syncwarp();
-    } else if (warp == 9) {
-        if (lane == 0) {
-            uint32_t blocks = 0;                  // accumulators filled
-            for (uint64_t i = blockIdx.x; i < total && !*abort; i += gridDim.x) {
-                for (int kb = 0; kb < a.kb; ++kb, ++used, ++blocks) {
-                    const uint32_t s = used % kRowsStages, turn = used / kRowsStages;
-                    const uint32_t b = blocks & 1, round = blocks >> 1;
-                    if (round > 0 &&
-                        !mbar_wait(acc_empty + 8 * b, (round - 1) & 1, abort, a.status))
-                        break;
-                    if (!mbar_wait(full + 8 * s, turn & 1, abort, a.status))
+    } else if (warp == kRowsEpilogueWarps + 1 && rank == 0) {
+        // The whole warp walks the blocks and one lane issues: in a branch of
+        // one lane the descriptors would not stay in uniform registers, and
+        // the issue alone took longer than the products.
+        const uint64_t desc_a = operand(smem_addr(stages));
+        const uint64_t desc_b = operand(smem_addr(stages) + kRowsOperand);
+        const bool one = elect_one();
+        bool ok = true;
+        for (uint64_t i = pair; i < total && ok; i += pairs) {
+            for (int kb = 0; kb < a.kb; ++kb, ++used) {
+                const uint32_t s = used % kRowsStages;
+                if (!warp_wait(full + 8 * s, (used / kRowsStages) & 1, abort, a.status)) {
+                    ok = false;
+                    break;
+                }
+                // the block's two halves: rows 64 * half, ... of either CTA's b
+#pragma unroll
+                for (uint32_t half = 0; half < 2; ++half) {
+                    const uint32_t b = (2 * used + half) % kRowsAccs, turn = used / 2;
+                    ok = turn == 0 || warp_wait(acc_empty + 8 * b, (turn - 1) & 1, abort, a.status);
+                    if (!ok)
                         break;
                     fence_after();
-                    const uint32_t at = smem_addr(stages) + s * kRowsStage;
-                    mma_block(tmem + b * kRowsN, at, at + kRowsABytes,
-                              mma_shape(kRowsM, kRowsN));
-                    mma_commit(empty + 8 * s);
-                    mma_commit(acc_full + 8 * b);
+                    const uint64_t da = desc_a + s * (kRowsStage >> 4);
+                    const uint64_t db = desc_b + s * (kRowsStage >> 4) + half * (64 * 128 >> 4);
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_pair_e4m3(tmem + b * kRowsAccCols, da + 2 * k, db + 2 * k,
+                                          mma_shape(kRowsM, kRowsAccCols), k > 0);
+                        if (half == 1)
+                            mma_pair_commit(empty + 8 * s);
+                        mma_pair_commit(acc_full + 8 * b);
+                    }
+                    __syncwarp();
                 }
+                if (!ok)
+                    break;
+            }
+        }
+    } else if (warp == kRowsEpilogueWarps + 1) {
+        __syncwarp();                             // the first CTA issues for both
+    } else if (warp == kRowsEpilogueWarps + 2) {
+        uint32_t slots = 0;
+        bool ok = true;
+        for (uint64_t i = pair; i < total && ok; i += pairs) {
+            const RowsTile t = rows_tile(a, sh, ntiles, i);
+            for (int kb0 = 0; kb0 < a.kb; kb0 += kRowsScales, ++slots) {
+                // rows and columns past the tile's end take a valid scale and
+                // are not stored
+                float v[kRowsHalf / 32][kRowsScales], w = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kRowsHalf / 32; ++j) {
+                    const uint32_t r = rank * kRowsHalf + j * 32 + lane;
+                    const float *sa = a.sa + (uint64_t)(r < t.rows ? t.row + r : t.row) * a.sa_row +
+                                      kb0;
+                    if (a.sa_wide) {
+#pragma unroll
+                        for (int k = 0; k < kRowsScales; k += 4) {
+                            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (kb0 + k < a.kb)
+                                f = *reinterpret_cast<const float4 *>(sa + k);
+                            v[j][k] = f.x;
+                            v[j][k + 1] = f.y;
+                            v[j][k + 2] = f.z;
+                            v[j][k + 3] = f.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kRowsScales; ++k)
+                            v[j][k] = kb0 + k < a.kb ? sa[k] : 0.0f;
+                    }
+                }
+                const int k = lane & (kRowsScales - 1), side = lane / kRowsScales;
+                const uint32_t nb = t.n0 / 128 + side;
+                if (side < 2 && kb0 + k < a.kb)
+                    w = a.sb[t.group * a.sb_group + (uint64_t)(nb * 128 < a.N ? nb : 0) * a.kb +
+                             kb0 + k];
+                const uint32_t slot = slots & 1, round = slots >> 1;
+                ok = round == 0 || warp_wait(scale_empty + 8 * slot, (round - 1) & 1, abort,
+                                             a.status);
+                if (!ok)
+                    break;
+#pragma unroll
+                for (int j = 0; j < kRowsHalf / 32; ++j)
+#pragma unroll
+                    for (int b = 0; b < kRowsScales; ++b)
+                        sh.sa[slot][b][j * 32 + lane] = v[j][b];
+                if (side < 2)
+                    sh.sb[slot][k][side] = w;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(scale_full + 8 * slot);
             }
         }
         __syncwarp();
     } else {
-        const int quarter = warp & 3, side = warp >> 2;
-        const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16) + side * 128;
-        uint32_t blocks = 0;
+        // A warp takes one half of every block.  Columns 0-63 of a half are rows
+        // 64 * half, ... of the first CTA's b, columns 64-127 of the second's.
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t empty_bar = peer_addr(acc_empty, 0);
+        const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16);
+        const uint32_t in = quarter * 32 + lane;
+        uint32_t blocks = 0, slots = 0;
         bool ok = true;
-        for (uint64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        for (uint64_t i = pair; i < total && ok; i += pairs) {
             const RowsTile t = rows_tile(a, sh, ntiles, i);
-            const uint32_t r = quarter * 32 + lane;
-            const bool here = r < t.rows;
-            const uint32_t n = t.n0 + side * 128;
-            // rows and columns past the tile's end read a valid scale and are
-            // not stored
-            const float *sa = a.sa + (uint64_t)(here ? t.row + r : t.row) * a.sa_row;
-            const float *sb = a.sb + t.group * a.sb_group + (uint64_t)(n < a.N ? n / 128 : 0) * a.kb;
-            float acc[128];
+            float acc[4][kRowsRun];
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-                acc[c] = 0.0f;
-            float next = sa[0] * sb[0];
+            for (int c = 0; c < kRowsRun; ++c)
+                acc[0][c] = acc[1][c] = acc[2][c] = acc[3][c] = 0.0f;
             for (int kb = 0; kb < a.kb; ++kb, ++blocks) {
-                const float scale = next;
-                if (kb + 1 < a.kb)
-                    next = sa[kb + 1] * sb[kb + 1];
-                const uint32_t b = blocks & 1;
-                ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait(acc_full + 8 * b, (blocks >> 1) & 1, abort, a.status));
+                const uint32_t slot = slots & 1, k = kb & (kRowsScales - 1);
+                const uint32_t b = (2 * blocks + half) % kRowsAccs;
+                if (k == 0)
+                    ok = warp_wait(scale_full + 8 * slot, (slots >> 1) & 1, abort, a.status);
+                const float sa = sh.sa[slot][k][in];
+                const float2 sb = *reinterpret_cast<const float2 *>(sh.sb[slot][k]);
+                ok = ok && warp_wait(acc_full + 8 * b, (blocks / 2) & 1, abort, a.status);
                 if (!ok)
                     break;
                 fence_after();
-                uint32_t v[2][16];
-                tmem_load(lanes + b * kRowsN, v[0]);
+                const float scale[2] = {sa * sb.x, sa * sb.y};
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_wait(v[c & 1]);
-                    if (c < 7)
-                        tmem_load(lanes + b * kRowsN + (c + 1) * 16, v[(c + 1) & 1]);
-                    else {
+                for (int c = 0; c < kRowsAccCols; c += 16) {
+                    float v[16];
+                    tmem_load(lanes + b * kRowsAccCols + c, v);
+                    if (c + 16 == kRowsAccCols) {
                         fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(acc_empty + 8 * b);
+                            mbar_arrive_peer(empty_bar + 8 * b);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[c * 16 + j] += scale * __uint_as_float(v[c & 1][j]);
+                    for (int j = 0; j < 16; j += 2)
+                        add_scaled2(&acc[c / kRowsRun][c % kRowsRun + j], scale[c / 64],
+                                    scale[c / 64], v[j], v[j + 1]);
+                }
+                if (k == kRowsScales - 1 || kb + 1 == a.kb) {
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(scale_empty + 8 * slot);
+                    ++slots;
                 }
             }
-            if (ok && here)
-                store_row(a, t.row + r, n, acc);
+            const uint32_t first = rank * kRowsHalf + quarter * 32;
+            if (ok && first < t.rows) {
+                const uint32_t rows = t.rows - first < 32 ? t.rows - first : 32;
+                uint4 *stage = sh.stage[warp];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t n = t.n0 + (c / 2) * 128 + half * 64 + (c % 2) * kRowsRun;
+                    if (a.out == AR_BF16)
+                        store_rows<AR_BF16>(a, stage, t.row + first, rows, n, acc[c]);
+                    else if (a.out == AR_FP16)
+                        store_rows<AR_FP16>(a, stage, t.row + first, rows, n, acc[c]);
+                    else
+                        store_rows<AR_FP32>(a, stage, t.row + first, rows, n, acc[c]);
+                }
+            }
             __syncwarp();
         }
         __syncwarp();
@@ -431,56 +635,58 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
     __syncthreads();
     fence_after();
     if (*abort) {
-        if (threadIdx.x == 8 * 32)
+        if (threadIdx.x == kRowsEpilogueWarps * 32 && rank == 0)
             drain_loads(full, used, kRowsStages);
-        if (threadIdx.x == 9 * 32) {
-            mma_commit(smem_addr(&sh.drain));
+        if (warp == kRowsEpilogueWarps + 1 && rank == 0 && elect_one()) {
+            mma_pair_commit(smem_addr(&sh.drain));
             mbar_drain(smem_addr(&sh.drain), 0);
         }
         __syncthreads();
     }
-    if (warp == 9)
-        tmem_free<512>(tmem);
+    cluster_barrier();                            // nothing of the pair is in flight
+    if (warp == kRowsEpilogueWarps + 1)
+        tmem_free<512, true>(tmem);
 }
 
 // ---- few rows -------------------------------------------------------------------
 
 constexpr int kFewEpilogueWarps = 4;
-constexpr int kFewThreads = 32 * (kFewEpilogueWarps + 2);
+constexpr int kFewThreads = 32 * (kFewEpilogueWarps + 3);
+constexpr int kFewScales = 8;                     // blocks along k whose scales a slot holds
 constexpr int kFewWeights = 128 * 128;            // bytes of a stage's weights
 
 // NT: rows of a per tile.  Two CTAs per SM share its shared and tensor memory.
 template <int NT> struct Few {
     static constexpr int kStage = kFewWeights + NT * 128;
-    static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 3;
-    static constexpr int kAccs = NT <= 32 ? 4 : 2;
-    static constexpr int kCols = NT * kAccs < 32 ? 32 : NT * kAccs;
+    static constexpr int kStages = NT <= 32 ? 5 : 4;
+    static constexpr int kAccs = 4;
+    static constexpr int kCols = NT * kAccs;
     static_assert(kCols <= 256, "two CTAs' accumulators share 512 columns");
     static_assert(kStages * kStage >= NT * 512, "the joined sums reuse the stages");
 };
 template <int NT> struct FewShared {
     uint64_t full[Few<NT>::kStages], empty[Few<NT>::kStages];
     uint64_t acc_full[Few<NT>::kAccs], acc_empty[Few<NT>::kAccs], drain;
+    uint64_t scale_full[2], scale_empty[2];
+    alignas(16) float scale[2][kFewScales][NT];   // sa * sb by block and row
     uint32_t tmem;
     int abort;
-    alignas(16) float scale[kFewEpilogueWarps][2][NT];
 };
 template <int NT> constexpr size_t few_smem() {
     return 1024 + (size_t)Few<NT>::kStages * Few<NT>::kStage + sizeof(FewShared<NT>);
 }
 
 __device__ __forceinline__ float ld_peer_f32(uint32_t local, uint32_t rank) {
-    uint32_t remote;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(v) : "r"(peer_addr(local, rank)) : "memory");
     return v;
 }
 
 // blockIdx.x: CTA of the cluster (its share of the blocks along k);
 // blockIdx.y: tile of 128 weight rows; blockIdx.z: row tile, counted over the
 // groups.  Warps 0-3: epilogue, lane + 32 * warp is the weight row; warp 4:
-// TMA; warp 5: MMA.
+// TMA; warp 5: MMA; warp 6: scales.
 template <int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
 k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_a,
@@ -493,13 +699,9 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
     volatile int *abort = &sh.abort;
     const uint32_t full = smem_addr(sh.full), empty = smem_addr(sh.empty);
     const uint32_t acc_full = smem_addr(sh.acc_full), acc_empty = smem_addr(sh.acc_empty);
+    const uint32_t scale_full = smem_addr(sh.scale_full), scale_empty = smem_addr(sh.scale_empty);
 
-    kernel_prologue();
-    int group = 0;
-    uint32_t row = 0, rows = 0;
-    // the same answer in the whole cluster, before any barrier
-    if (!find_rows(a, NT, blockIdx.z, group, row, rows))
-        return;
+    // what needs no memory of earlier kernels comes before the wait for them
     if (threadIdx.x == 0) {
         for (int s = 0; s < F::kStages; ++s) {
             mbar_init(full + 8 * s, 1);
@@ -509,15 +711,29 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
             mbar_init(acc_full + 8 * b, 1);
             mbar_init(acc_empty + 8 * b, kFewEpilogueWarps);
         }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(scale_full + 8 * b, 1);
+            mbar_init(scale_empty + 8 * b, kFewEpilogueWarps);
+        }
         mbar_init(smem_addr(&sh.drain), 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 5)
-        tmem_alloc<F::kCols>(&sh.tmem);
+        tmem_alloc<F::kCols, false>(&sh.tmem);
+    kernel_prologue();
+    int group = 0;
+    uint32_t row = 0, rows = 0;
+    // the same answer in the whole cluster
+    const bool tile = find_rows(a, NT, blockIdx.z, group, row, rows);
     fence_before();
     __syncthreads();
     fence_after();
+    if (!tile) {
+        if (warp == 5)
+            tmem_free<F::kCols, false>(sh.tmem);
+        return;
+    }
     const uint32_t tmem = sh.tmem;
     const int parts = gridDim.x, part = blockIdx.x;
     const int kb0 = (int)((int64_t)a.kb * part / parts);
@@ -541,62 +757,74 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         }
         __syncwarp();
     } else if (warp == 5) {
-        if (lane == 0) {
-            for (int kb = kb0; kb < kb1; ++kb, ++used) {
-                const uint32_t s = used % F::kStages, turn = used / F::kStages;
-                const uint32_t b = used % F::kAccs, round = used / F::kAccs;
-                if (round > 0 && !mbar_wait(acc_empty + 8 * b, (round - 1) & 1, abort, a.status))
-                    break;
-                if (!mbar_wait(full + 8 * s, turn & 1, abort, a.status))
-                    break;
-                fence_after();
-                const uint32_t at = smem_addr(stages) + s * F::kStage;
-                mma_block(tmem + b * NT, at, at + kFewWeights, mma_shape(128, NT));
+        const uint64_t desc_b = operand(smem_addr(stages));
+        const uint64_t desc_a = operand(smem_addr(stages) + kFewWeights);
+        const bool one = elect_one();
+        for (int kb = kb0; kb < kb1; ++kb, ++used) {
+            const uint32_t s = used % F::kStages, b = used % F::kAccs, round = used / F::kAccs;
+            if (round > 0 && !warp_wait(acc_empty + 8 * b, (round - 1) & 1, abort, a.status))
+                break;
+            if (!warp_wait(full + 8 * s, (used / F::kStages) & 1, abort, a.status))
+                break;
+            fence_after();
+            if (one) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_e4m3(tmem + b * NT, desc_b + s * (F::kStage >> 4) + 2 * k,
+                             desc_a + s * (F::kStage >> 4) + 2 * k, mma_shape(128, NT), k > 0);
                 mma_commit(empty + 8 * s);
                 mma_commit(acc_full + 8 * b);
             }
+            __syncwarp();
+        }
+    } else if (warp == 6) {
+        constexpr int kPer = (NT + 31) / 32;
+        const float *sb = a.sb + group * a.sb_group + (uint64_t)(n0 / 128) * a.kb;
+        uint32_t slots = 0;
+        for (int kb = kb0; kb < kb1; kb += kFewScales, ++slots) {
+            // rows past the tile's end take a valid scale and are not stored
+            float v[kPer][kFewScales];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const uint32_t r = lane + 32 * j;
+                const float *sa = a.sa + (uint64_t)(r < rows ? row + r : row) * a.sa_row + kb;
+#pragma unroll
+                for (int k = 0; k < kFewScales; ++k)
+                    v[j][k] = kb + k < kb1 ? sa[k] * sb[kb + k] : 0.0f;
+            }
+            const uint32_t slot = slots & 1, round = slots >> 1;
+            if (round > 0 && !warp_wait(scale_empty + 8 * slot, (round - 1) & 1, abort, a.status))
+                break;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+#pragma unroll
+                for (int k = 0; k < kFewScales; ++k)
+                    if (lane + 32 * j < NT)
+                        sh.scale[slot][k][lane + 32 * j] = v[j][k];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(scale_full + 8 * slot);
         }
         __syncwarp();
     } else {
         const uint32_t lanes = tmem + ((uint32_t)warp * 32 << 16);
-        const float *sb = a.sb + group * a.sb_group + (uint64_t)(n0 / 128) * a.kb;
-        constexpr int kPer = (NT + 31) / 32;
-        // lane l brings the scales of rows l, l + 32, ... one block ahead
-        const float *sa[kPer];
-        float next[kPer];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const uint32_t r = lane + 32 * j;
-            sa[j] = a.sa + (uint64_t)(r < rows ? row + r : row) * a.sa_row;
-            next[j] = kb0 < kb1 ? sa[j][kb0] * sb[kb0] : 0.0f;
-        }
 #pragma unroll
         for (int c = 0; c < NT; ++c)
             acc[c] = 0.0f;
+        uint32_t slots = 0;
         for (int kb = kb0; kb < kb1; ++kb, ++used) {
-            float *scale = sh.scale[warp][used & 1];
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                if (lane + 32 * j < NT)
-                    scale[lane + 32 * j] = next[j];
-            __syncwarp();
-            if (kb + 1 < kb1)
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    next[j] = sa[j][kb + 1] * sb[kb + 1];
-            const uint32_t b = used % F::kAccs;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8 * b, (used / F::kAccs) & 1, abort,
-                                                   a.status)))
+            const uint32_t b = used % F::kAccs, slot = slots & 1, k = used % kFewScales;
+            if (k == 0 && !warp_wait(scale_full + 8 * slot, (slots >> 1) & 1, abort, a.status))
+                break;
+            if (!warp_wait(acc_full + 8 * b, (used / F::kAccs) & 1, abort, a.status))
                 break;
             fence_after();
-            uint32_t v[2][16];
-            tmem_load(lanes + b * NT, v[0]);
+            const float *scale = sh.scale[slot][k];
 #pragma unroll
-            for (int c = 0; c < NT / 16; ++c) {
-                tmem_wait(v[c & 1]);
-                if (c + 1 < NT / 16)
-                    tmem_load(lanes + b * NT + (c + 1) * 16, v[(c + 1) & 1]);
-                else {
+            for (int c = 0; c < NT; c += 16) {
+                float v[16];
+                tmem_load(lanes + b * NT + c, v);
+                if (c + 16 == NT) {
                     fence_before();
                     __syncwarp();
                     if (lane == 0)
@@ -604,12 +832,16 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 }
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(scale + c * 16 + j);
-                    acc[c * 16 + j] += f.x * __uint_as_float(v[c & 1][j]);
-                    acc[c * 16 + j + 1] += f.y * __uint_as_float(v[c & 1][j + 1]);
-                    acc[c * 16 + j + 2] += f.z * __uint_as_float(v[c & 1][j + 2]);
-                    acc[c * 16 + j + 3] += f.w * __uint_as_float(v[c & 1][j + 3]);
+                    const float4 f = *reinterpret_cast<const float4 *>(scale + c + j);
+                    add_scaled2(&acc[c + j], f.x, f.y, v[j], v[j + 1]);
+                    add_scaled2(&acc[c + j + 2], f.z, f.w, v[j + 2], v[j + 3]);
                 }
+            }
+            if (k == kFewScales - 1 || kb + 1 == kb1) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(scale_empty + 8 * slot);
+                ++slots;
             }
         }
         __syncwarp();
@@ -621,14 +853,14 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
     if (*abort) {
         if (threadIdx.x == 4 * 32)
             drain_loads(full, used, F::kStages);
-        if (threadIdx.x == 5 * 32) {
+        if (warp == 5 && elect_one()) {
             mma_commit(smem_addr(&sh.drain));
             mbar_drain(smem_addr(&sh.drain), 0);
         }
         __syncthreads();
     }
     if (warp == 5)
-        tmem_free<F::kCols>(tmem);
+        tmem_free<F::kCols, false>(tmem);
     if (parts == 1) {
         if (warp < kFewEpilogueWarps && n < a.N)
 #pragma unroll
@@ -644,8 +876,7 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
 #pragma unroll
         for (int c = 0; c < NT; ++c)
             sums[c * 128 + threadIdx.x] = acc[c];
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();
     if (warp < kFewEpilogueWarps)
         for (uint32_t c = part; c < rows; c += parts) {
             float v = 0.0f;
@@ -654,8 +885,7 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
             if (n < a.N)
                 store_out(a.d + (uint64_t)(row + c) * a.ldd, n, v, a.out);
         }
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_barrier();
 }
 
 // ---- host ---------------------------------------------------------------------
@@ -736,14 +966,28 @@ cudaError_t launch_few(const MatmulArgs &a, int parts, cudaStream_t s) {
 
 cudaError_t launch_rows(const MatmulArgs &a, int sms, cudaStream_t s) {
     CUtensorMap ma, mb;
-    if (!encode(&ma, a.a, a.K, a.M, a.lda, 0, kRowsM) ||
-        !encode(&mb, a.b, a.K, a.N, a.ldb, a.E, kRowsN))
+    if (!encode(&ma, a.a, a.K, a.M, a.lda, 0, kRowsHalf) ||
+        !encode(&mb, a.b, a.K, a.N, a.ldb, a.E, kRowsHalf))
         return cudaErrorInvalidValue;
     const cudaError_t e = cudaFuncSetAttribute(
         k_matmul8_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmem);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(k_matmul8_rows, sms, kRowsThreads, kRowsSmem, s, true, a, ma, mb);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = sms / 2 * 2;
+    cfg.blockDim = kRowsThreads;
+    cfg.dynamicSmemBytes = kRowsSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_matmul8_rows, a, ma, mb);
 }
 
 }  // namespace
@@ -755,24 +999,33 @@ cudaError_t launch_matmul8_tc(const MatmulArgs &a, cudaStream_t s) {
     if (sms < 1)
         return cudaErrorUnknown;
     const uint64_t groups = (uint64_t)a.E < a.M ? a.E : a.M;
+    // tiles of n rows: every group adds at most one that is not full
+    auto tiles = [&](uint64_t n) { return a.offsets ? a.M / n + groups : (a.M + n - 1) / n; };
+    auto waves = [](uint64_t n, uint64_t at_once) { return (n + at_once - 1) / at_once; };
+
     const uint64_t per = (a.M + groups - 1) / groups;              // rows per group, on average
-    const uint64_t tiles = (a.offsets ? a.M / kRowsM + groups : (a.M + kRowsM - 1) / kRowsM) *
-                           ((a.N + kRowsN - 1) / kRowsN);
-    const uint64_t columns = (a.N + 127) / 128;
-    // the grid's y and z dimensions of the form for few rows end at 65535
-    if (tiles >= (uint64_t)sms || columns > 65535 || a.M / 16 + groups > 65535)
-        return launch_rows(a, sms, s);
-    // as many CTAs along k as keep the SMs at two CTAs each
-    const int nt = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
-    const uint64_t ctas = (a.offsets ? a.M / nt + groups : (a.M + nt - 1) / nt) * columns;
+    const int nt = per <= 16 ? 16 : per <= 24 ? 32 : 64;
+    const uint64_t columns = (a.N + 127) / 128, ctas = tiles(nt) * columns;
+    // the few form fills the SMs, two CTAs each, by cutting k while it has too
+    // few tiles (one row of 8192 x 8192: 20.5, 15.7, 14.1 and 17.2 us in 1, 2, 4
+    // and 8 parts)
     int parts = 1;
     while (parts < 8 && ctas * parts * 2 <= 2 * (uint64_t)sms && parts * 2 <= a.kb)
         parts *= 2;
+    // Tenths of a us, as measured: a block along k takes the few form 0.5 us
+    // while two CTAs an SM are at work, the rows form 0.45 us a pair.  Either
+    // side (us) for K = N = 8192 at M = 64, 128, 256, 512: 19.6, 28.1, 34.9, 66.8
+    // and 31.9, 32.8, 33.0, 35.1; for 64 experts of 2048 x 8192 at M = 1024, 4096,
+    // 8192, 16384: 159, 192, 282, 478 and 218, 228, 265, 364.
+    const uint64_t few = waves(ctas * parts, 2 * (uint64_t)sms) * waves(a.kb, parts) * 50;
+    const uint64_t rows = waves(tiles(kRowsM) * ((a.N + kRowsN - 1) / kRowsN), sms / 2) * a.kb * 45;
+    // the grid's y and z dimensions end at 65535
+    if (few > rows || columns > 65535 || tiles(nt) > 65535)
+        return launch_rows(a, sms, s);
     switch (nt) {
     case 16: return launch_few<16>(a, parts, s);
     case 32: return launch_few<32>(a, parts, s);
-    case 64: return launch_few<64>(a, parts, s);
-    default: return launch_few<128>(a, parts, s);
+    default: return launch_few<64>(a, parts, s);
     }
 }
 
