@@ -180,17 +180,22 @@ def _ptr(x) -> int:
     return int(x.data_ptr())
 
 
-def _current_stream():
+_raw_stream = None            # torch's (raw stream of a device, current device)
+
+
+def _current_stream() -> int:
     """The caller's current CUDA stream as an integer.  torch's raw lookup
-    answers in a tenth of the time of building a Stream object (0.1 against
-    3 us), which is most of a small call's host cost; it is an internal name
-    of torch, so the public way stays where it is missing."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    device = getattr(torch._C, "_cuda_getDevice", None)
-    if raw is None or device is None or not torch.cuda.is_initialized():
-        return int(torch.cuda.current_stream().cuda_stream)
-    return raw(device())
+    answers in a tenth of the time of building a Stream object, which was most
+    of a small call's host cost (3 us); it is an internal name of torch, so the
+    public way stays where it is missing."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        names = ("_cuda_getCurrentRawStream", "_cuda_getDevice")
+        if not torch.cuda.is_initialized() or not all(hasattr(torch._C, n) for n in names):
+            return int(torch.cuda.current_stream().cuda_stream)
+        _raw_stream = tuple(getattr(torch._C, n) for n in names)
+    return _raw_stream[0](_raw_stream[1]())
 
 
 def _stream(s) -> int:

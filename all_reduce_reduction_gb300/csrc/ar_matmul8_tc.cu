@@ -940,8 +940,7 @@ cudaError_t launch_few(const MatmulArgs &a, int parts, cudaStream_t s) {
     if (!encode(&ma, a.a, a.K, a.M, a.lda, 0, NT) ||
         !encode(&mb, a.b, a.K, a.N, a.ldb, a.E, 128))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_matmul8_few<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem<NT>());
+    const cudaError_t e = opt_in_smem<k_matmul8_few<NT>>(few_smem<NT>());
     if (e != cudaSuccess)
         return e;
     // row tiles: every group adds at most one that is not full
@@ -969,8 +968,7 @@ cudaError_t launch_rows(const MatmulArgs &a, int sms, cudaStream_t s) {
     if (!encode(&ma, a.a, a.K, a.M, a.lda, 0, kRowsHalf) ||
         !encode(&mb, a.b, a.K, a.N, a.ldb, a.E, kRowsHalf))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_matmul8_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmem);
+    const cudaError_t e = opt_in_smem<k_matmul8_rows>(kRowsSmem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -90,18 +90,23 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
         const uint32_t p = lo + 32 * i + lane;
         held[i] = p < hi && p >= lo ? expert_of(a, p) : -1;
     }
+    // adds 32 pairs to the warp's counts; a pair's place within the warp's run
     auto count_32 = [&](int e) {
         const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        if (e >= 0 && lane == __ffs(same) - 1)
-            mine[e] += __popc(same);
+        const uint32_t before = e >= 0 ? mine[e] : 0u;
         __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1)
+            mine[e] = before + __popc(same);
+        __syncwarp();
+        return before + __popc(same & ((1u << lane) - 1u));
     };
+    uint32_t place[kRouteHeld];
 #pragma unroll
     for (int i = 0; i < kRouteHeld; ++i)
         if (lo + 32 * i < hi)
-            count_32(held[i]);
+            place[i] = count_32(held[i]);
     for (uint32_t p0 = lo + 32 * kRouteHeld; p0 < hi; p0 += 32)
-        count_32(p0 + lane < hi ? expert_of(a, p0 + lane) : -1);
+        (void)count_32(p0 + lane < hi ? expert_of(a, p0 + lane) : -1);
     __syncthreads();
     // over the CTA's warps: count[w][e] becomes the number before warp w
     for (int e = threadIdx.x; e < E1; e += blockDim.x) {
@@ -119,12 +124,17 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
     for (int e0 = 0; e0 < E1; e0 += blockDim.x) {
         const int e = e0 + threadIdx.x;
         uint32_t before = 0u, all = 0u;
-        if (e < E1)
-            for (uint32_t c = 0; c < ctas; ++c) {
-                const uint32_t v = ld_peer_u32(total + e, c);
-                before += c < rank ? v : 0u;
-                all += v;
+        if (e < E1) {
+            uint32_t v[kRouteCtas];               // at most kRouteCtas peers
+#pragma unroll
+            for (uint32_t c = 0; c < kRouteCtas; ++c)
+                v[c] = c < ctas ? ld_peer_u32(total + e, c) : 0u;
+#pragma unroll
+            for (uint32_t c = 0; c < kRouteCtas; ++c) {
+                before += c < rank ? v[c] : 0u;
+                all += v[c];
             }
+        }
         uint32_t scan = all;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -151,26 +161,29 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
         __syncthreads();
     }
     cluster_barrier();                                // every peer has read `total`
-    auto place_32 = [&](uint32_t p, int e) {
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-        const uint32_t base = e >= 0 ? first[e] + mine[e] : 0u;
-        __syncwarp();
-        if (e >= 0) {
-            const uint32_t row = base + __popc(same & ((1u << lane) - 1u));
-            a.row_of[p] = e < a.E ? (int32_t)row : -1;
-            if (a.src)
-                a.src[row] = e < a.E ? (int32_t)p : -1;
-            if (lane == __ffs(same) - 1)
-                mine[e] += __popc(same);
-        }
-        __syncwarp();
+    auto put = [&](uint32_t p, int e, uint32_t row) {
+        if (e < 0)
+            return;
+        a.row_of[p] = e < a.E ? (int32_t)row : -1;
+        if (a.src)
+            a.src[row] = e < a.E ? (int32_t)p : -1;
     };
 #pragma unroll
     for (int i = 0; i < kRouteHeld; ++i)
-        if (lo + 32 * i < hi)
-            place_32(lo + 32 * i + lane, held[i]);
-    for (uint32_t p0 = lo + 32 * kRouteHeld; p0 < hi; p0 += 32)
-        place_32(p0 + lane, p0 + lane < hi ? expert_of(a, p0 + lane) : -1);
+        if (lo + 32 * i < hi && held[i] >= 0)
+            put(lo + 32 * i + lane, held[i], first[held[i]] + mine[held[i]] + place[i]);
+    if (lo + 32 * kRouteHeld < hi) {
+        // the counts go on from the pairs that were held
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kRouteHeld; ++i)
+            (void)count_32(held[i]);
+        for (uint32_t p0 = lo + 32 * kRouteHeld; p0 < hi; p0 += 32) {
+            const int e = p0 + lane < hi ? expert_of(a, p0 + lane) : -1;
+            const uint32_t at = count_32(e);
+            put(p0 + lane, e, e >= 0 ? first[e] + at : 0u);
+        }
+    }
 }
 
 static cudaError_t launch_route(const RouteArgs &a, cudaStream_t s) {
@@ -180,9 +193,8 @@ static cudaError_t launch_route(const RouteArgs &a, cudaStream_t s) {
     const int ctas = groups > (uint32_t)kRouteWarps ? kRouteCtas : 1;
     const size_t smem = (size_t)(warps + 2) * (a.E + 1) * sizeof(uint32_t);
     // the opt-in holds for every size used: 34 rows of at most 1025 words
-    const cudaError_t e = cudaFuncSetAttribute(
-        k_moe_route, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        (int)((kRouteWarps + 2) * (AR_MOE_MAX_EXPERTS + 1) * sizeof(uint32_t)));
+    const cudaError_t e = opt_in_smem<k_moe_route>((kRouteWarps + 2) * (AR_MOE_MAX_EXPERTS + 1) *
+                                                   sizeof(uint32_t));
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

@@ -419,10 +419,9 @@ static cudaError_t norm_grad_units(const NormGradArgs &a, int grid, cudaStream_t
     // with the ring, 2 x 3 rows of 16 KB a CTA and two CTAs an SM
     if (WIDE && units <= 1024) {
         constexpr int kUnits = 2, kThreads = 512;
-        const auto kernel = k_rmsnorm_grad<DT, WIDE, kUnits, kThreads, 2, WIDE>;
-        const int smem = 2 * 3 * kUnits * kThreads * (int)sizeof(uint4);
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        constexpr auto kernel = k_rmsnorm_grad<DT, WIDE, kUnits, kThreads, 2, WIDE>;
+        const size_t smem = 2 * 3 * kUnits * kThreads * sizeof(uint4);
+        const cudaError_t e = opt_in_smem<kernel>(smem);
         if (e != cudaSuccess)
             return e;
         return launch_kernel(kernel, grid, threads(kUnits, kThreads), smem, s, true, a);

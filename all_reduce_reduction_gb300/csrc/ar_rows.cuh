@@ -11,6 +11,8 @@
 // shuffles alone.
 #pragma once
 
+#include <atomic>
+
 #include "ar_device.cuh"
 
 namespace ar {
@@ -184,6 +186,23 @@ inline bool wide(const Matrix &m, size_t align = 16) {
 }
 
 inline bool float_dtype(int d) { return d == AR_BF16 || d == AR_FP16 || d == AR_FP32; }
+
+// Opts a kernel in to `bytes` of dynamic shared memory, once per kernel and
+// device: asking the runtime every time costs a launch 0.5 us.
+template <auto KERNEL> inline cudaError_t opt_in_smem(size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // The launch's result as a status code.
 inline int launched(cudaError_t e) {
