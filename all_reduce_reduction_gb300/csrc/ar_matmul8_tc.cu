@@ -231,14 +231,6 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float v[16]) {
         : "r"(addr) : "memory");
 }
 
-// Two sums at once: x[i] += s[i] * v[i], each rounded once.
-__device__ __forceinline__ void add_scaled2(float *x, float s0, float s1, float v0, float v1) {
-    asm("{\n\t.reg .b64 s, t, u;\n\t"
-        "mov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmov.b64 u, {%0, %1};\n\t"
-        "fma.rn.f32x2 u, s, t, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
-        : "+f"(x[0]), "+f"(x[1]) : "f"(s0), "f"(s1), "f"(v0), "f"(v1));
-}
-
 // ---- many rows ----------------------------------------------------------------
 
 constexpr int kRowsM = 256, kRowsN = 256, kRowsStages = 6;
@@ -602,8 +594,8 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
                     }
 #pragma unroll
                     for (int j = 0; j < 16; j += 2)
-                        add_scaled2(&acc[c / kRowsRun][c % kRowsRun + j], scale[c / 64],
-                                    scale[c / 64], v[j], v[j + 1]);
+                        fma2(&acc[c / kRowsRun][c % kRowsRun + j], scale[c / 64], scale[c / 64],
+                             v[j], v[j + 1]);
                 }
                 if (k == kRowsScales - 1 || kb + 1 == a.kb) {
                     __syncwarp();
@@ -788,9 +780,26 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
             for (int j = 0; j < kPer; ++j) {
                 const uint32_t r = lane + 32 * j;
                 const float *sa = a.sa + (uint64_t)(r < rows ? row + r : row) * a.sa_row + kb;
+                if (a.sa_wide && kb % 4 == 0) {
+                    // rows of scales are whole 16-byte words up to the last
+#pragma unroll
+                    for (int k = 0; k < kFewScales; k += 4) {
+                        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (kb + k < kb1)
+                            f = *reinterpret_cast<const float4 *>(sa + k);
+                        v[j][k] = f.x;
+                        v[j][k + 1] = f.y;
+                        v[j][k + 2] = f.z;
+                        v[j][k + 3] = f.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kFewScales; ++k)
+                        v[j][k] = kb + k < kb1 ? sa[k] : 0.0f;
+                }
 #pragma unroll
                 for (int k = 0; k < kFewScales; ++k)
-                    v[j][k] = kb + k < kb1 ? sa[k] * sb[kb + k] : 0.0f;
+                    v[j][k] *= kb + k < kb1 ? sb[kb + k] : 0.0f;
             }
             const uint32_t slot = slots & 1, round = slots >> 1;
             if (round > 0 && !warp_wait(scale_empty + 8 * slot, (round - 1) & 1, abort, a.status))
@@ -833,8 +842,8 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(scale + c + j);
-                    add_scaled2(&acc[c + j], f.x, f.y, v[j], v[j + 1]);
-                    add_scaled2(&acc[c + j + 2], f.z, f.w, v[j + 2], v[j + 3]);
+                    fma2(&acc[c + j], f.x, f.y, v[j], v[j + 1]);
+                    fma2(&acc[c + j + 2], f.z, f.w, v[j + 2], v[j + 3]);
                 }
             }
             if (k == kFewScales - 1 || kb + 1 == kb1) {

@@ -358,9 +358,14 @@ __global__ void __launch_bounds__(256, 3) k_moe_return(const __grid_constant__ R
                     float v[L::E];
                     L::widen(p[j], v);
 #pragma unroll
-                    for (int i = 0; i < L::E; ++i) {
-                        const float x = __fmul_rn(c.w[j], v[i]);
-                        acc[i] = any ? __fadd_rn(acc[i], x) : x;
+                    for (int i = 0; i < L::E; i += 2) {
+                        mul2(v + i, c.w[j], c.w[j]);
+                        if (any)
+                            add2(acc + i, v[i], v[i + 1]);
+                        else {
+                            acc[i] = v[i];
+                            acc[i + 1] = v[i + 1];
+                        }
                     }
                     any = true;
                 }
@@ -398,14 +403,14 @@ __global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constan
         const uint8_t *dout = a.dout + t * a.sdout;
         for (int k0 = 0; k0 < a.K; k0 += 8) {
             int32_t r[8];
-            float w[8], dot[8];
+            float w[8], dot[8][2];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 r[j] = k0 + j < a.K ? a.row_of[t * a.K + k0 + j] : -1;
                 if (r[j] >= 0 && (uint64_t)r[j] >= a.nrows)
                     r[j] = -1;
                 w[j] = a.w && k0 + j < a.K ? a.w[t * a.K + k0 + j] : 1.0f;
-                dot[j] = 0.0f;
+                dot[j][0] = dot[j][1] = 0.0f;
             }
             for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
                 uint4 p[8];
@@ -426,14 +431,17 @@ __global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constan
                         float v[L::E];
                         L::widen(p[j], v);
 #pragma unroll
-                        for (int i = 0; i < L::E; ++i)
-                            dot[j] += d[i] * v[i];
+                        for (int i = 0; i < L::E; i += 2)
+                            fma2(dot[j], d[i], d[i + 1], v[i], v[i + 1]);
                     }
                     if (a.drows) {
                         float g[L::E];
 #pragma unroll
-                        for (int i = 0; i < L::E; ++i)
-                            g[i] = __fmul_rn(w[j], d[i]);
+                        for (int i = 0; i < L::E; i += 2) {
+                            g[i] = d[i];
+                            g[i + 1] = d[i + 1];
+                            mul2(g + i, w[j], w[j]);
+                        }
                         L::store(a.drows + (uint64_t)r[j] * a.sdrows, u, a.H, g);
                     }
                 }
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constan
             if (a.dw) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float v = warp_sum(dot[j]);
+                    const float v = warp_sum(dot[j][0] + dot[j][1]);
                     if (lane == 0)
                         part[j][warp] = v;
                 }

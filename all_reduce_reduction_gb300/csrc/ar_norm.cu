@@ -58,9 +58,12 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint32_t
         scales[u / L::kBlockLanes] = scale;
     uint32_t q[(L::E + 3) / 4];
 #pragma unroll
-    for (int i = 0; i < L::E; i += 4)
-        q[i / 4] = e4m3x2(v[i] * inv, v[i + 1] * inv) |
-                   e4m3x2(v[i + 2] * inv, v[i + 3] * inv) << 16;
+    for (int i = 0; i < L::E; i += 4) {
+        float t[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+        mul2(t, inv, inv);
+        mul2(t + 2, inv, inv);
+        q[i / 4] = e4m3x2(t[0], t[1]) | e4m3x2(t[2], t[3]) << 16;
+    }
     if (L::whole(u, H)) {
         if (L::E == 8)
             reinterpret_cast<uint2 *>(row)[u] = make_uint2(q[0], q[L::E / 4 - 1]);
@@ -96,12 +99,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
                 float w[L::E];
                 L::widen(pr, w);
 #pragma unroll
-                for (int i = 0; i < L::E; ++i)
-                    b[i] += w[i];
+                for (int i = 0; i < L::E; i += 2)
+                    add2(b + i, w[i], w[i + 1]);
             }
         };
         float v[UNITS][L::E];
-        float ss = 0.0f;
+        float squares[2] = {0.0f, 0.0f};
         {
             uint4 px[UNITS], pr[UNITS];
 #pragma unroll
@@ -118,18 +121,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
             for (int j = 0; j < UNITS; ++j) {
                 total(px[j], pr[j], v[j]);
 #pragma unroll
-                for (int i = 0; i < L::E; ++i)
-                    ss += v[j][i] * v[j][i];
+                for (int i = 0; i < L::E; i += 2)
+                    fma2(squares, v[j][i], v[j][i + 1], v[j][i], v[j][i + 1]);
             }
         }
         for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
             float b[L::E];
             total(L::load(x, u, H), res ? L::load(res, u, H) : make_uint4(0u, 0u, 0u, 0u), b);
 #pragma unroll
-            for (int i = 0; i < L::E; ++i)
-                ss += b[i] * b[i];
+            for (int i = 0; i < L::E; i += 2)
+                fma2(squares, b[i], b[i + 1], b[i], b[i + 1]);
         }
-        ss = block_sum(ss, part);
+        const float ss = block_sum(squares[0] + squares[1], part);
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)H) + a.eps));
         if (a.rstd && threadIdx.x == 0)
             a.rstd[t] = r;
@@ -138,14 +141,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
             if (sum)
                 L::store(sum, u, H, b);
 #pragma unroll
-            for (int i = 0; i < L::E; ++i)
-                b[i] *= r;
+            for (int i = 0; i < L::E; i += 2)
+                mul2(b + i, r, r);
             if (a.gamma) {
                 float g[L::E];
                 L::widen(L::template load<true>(a.gamma, u, H), g);
 #pragma unroll
-                for (int i = 0; i < L::E; ++i)
-                    b[i] *= g[i];
+                for (int i = 0; i < L::E; i += 2)
+                    mul2(b + i, g[i], g[i + 1]);
             }
             if (E4M3)
                 store_e4m3<DT, WIDE>(y, scale, u, H, b);
@@ -229,23 +232,27 @@ template <int DT, bool WIDE>
 __device__ __forceinline__ float grad_open(const NormGradArgs &a, uint32_t u, uint4 ps, uint4 pd,
                                            float r, float *d, float *dg) {
     using L = Rows<DT, WIDE>;
-    float s[L::E], dot = 0.0f;
+    float s[L::E], n[L::E], dot[2] = {0.0f, 0.0f};
     L::widen(ps, s);
     L::widen(pd, d);
 #pragma unroll
-    for (int i = 0; i < L::E; ++i)
-        dg[i] += d[i] * (s[i] * r);
+    for (int i = 0; i < L::E; i += 2) {
+        n[i] = s[i];
+        n[i + 1] = s[i + 1];
+        mul2(n + i, r, r);
+        fma2(dg + i, d[i], d[i + 1], n[i], n[i + 1]);
+    }
     if (a.gamma) {
         float g[L::E];
         L::widen(L::template load<true>(a.gamma, u, a.H), g);
 #pragma unroll
-        for (int i = 0; i < L::E; ++i)
-            d[i] *= g[i];
+        for (int i = 0; i < L::E; i += 2)
+            mul2(d + i, g[i], g[i + 1]);
     }
 #pragma unroll
-    for (int i = 0; i < L::E; ++i)
-        dot += d[i] * s[i];
-    return dot;
+    for (int i = 0; i < L::E; i += 2)
+        fma2(dot, d[i], d[i + 1], s[i], s[i + 1]);
+    return dot[0] + dot[1];
 }
 // Pass 2.
 template <int DT, bool WIDE>
@@ -255,14 +262,16 @@ __device__ __forceinline__ void grad_close(const NormGradArgs &a, uint32_t u, ui
     float s[L::E];
     L::widen(ps, s);
 #pragma unroll
-    for (int i = 0; i < L::E; ++i)
-        d[i] = r * d[i] - c * s[i];
+    for (int i = 0; i < L::E; i += 2) {
+        mul2(d + i, r, r);
+        fma2(d + i, -c, -c, s[i], s[i + 1]);
+    }
     if (a.dsum) {
         float w[L::E];
         L::widen(pu, w);
 #pragma unroll
-        for (int i = 0; i < L::E; ++i)
-            d[i] += w[i];
+        for (int i = 0; i < L::E; i += 2)
+            add2(d + i, w[i], w[i + 1]);
     }
     L::store(dx, u, a.H, d);
 }

@@ -127,6 +127,25 @@ template <int DT, bool WIDE> struct Rows {
     }
 };
 
+// Two binary32 operations in one instruction, each rounded to nearest even on
+// its own: x = x + y, x = x * y, x = a * b + x.
+__device__ __forceinline__ void add2(float *x, float y0, float y1) {
+    asm("{\n\t.reg .b64 t, u;\n\tmov.b64 t, {%2, %3};\n\tmov.b64 u, {%0, %1};\n\t"
+        "add.rn.f32x2 u, u, t;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(x[0]), "+f"(x[1]) : "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ void mul2(float *x, float y0, float y1) {
+    asm("{\n\t.reg .b64 t, u;\n\tmov.b64 t, {%2, %3};\n\tmov.b64 u, {%0, %1};\n\t"
+        "mul.rn.f32x2 u, u, t;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(x[0]), "+f"(x[1]) : "f"(y0), "f"(y1));
+}
+__device__ __forceinline__ void fma2(float *x, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 s, t, u;\n\t"
+        "mov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmov.b64 u, {%0, %1};\n\t"
+        "fma.rn.f32x2 u, s, t, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "+f"(x[0]), "+f"(x[1]) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
