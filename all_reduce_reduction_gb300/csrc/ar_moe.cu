@@ -225,27 +225,42 @@ struct MoveArgs {
     uint64_t sx, srows;       // bytes between rows
     uint64_t nrows, T;
     uint64_t bytes;           // of a row
-    uint64_t units;           // of a row, of sizeof(UNIT) bytes
-    uint32_t parts;           // CTAs per token
+    uint64_t per_token;       // threads per token
+    uint32_t units;           // 16-byte words of a row
     int K, nb;                // nb: scales per row
 };
 
-// CTA b moves part b % parts of token b / parts.  A thread loads PER units of
-// the token's row and stores them to each of its K rows.
-template <typename UNIT, int PER>
+// 16 bytes from an address that is a multiple of 4 only plus `shift` bits.
+__device__ __forceinline__ uint4 load_shifted(const uint32_t *p, uint32_t shift) {
+    const uint32_t a = p[0], b = p[1], c = p[2], d = p[3], e = p[4];
+    return make_uint4(__funnelshift_r(a, b, shift), __funnelshift_r(b, c, shift),
+                      __funnelshift_r(c, d, shift), __funnelshift_r(d, e, shift));
+}
+
+// The threads are counted over the tokens: a.units words, then the bytes past
+// them, then the scales of a token, one a thread, each stored to the token's K
+// rows.  ALIGNED: every row starts on a 16-byte boundary.  Otherwise a thread
+// has a 16-byte word of the destination, assembled from the five aligned words
+// of 4 bytes that hold its source; the words that are not whole, or whose
+// source words reach past the row, go byte by byte.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(256) k_moe_dispatch(const __grid_constant__ MoveArgs a) {
     kernel_prologue();
-    for (uint64_t job = blockIdx.x; job < a.T * a.parts; job += gridDim.x) {
-        const uint64_t t = job / a.parts;
-        const uint32_t part = (uint32_t)(job - t * a.parts);
-        const UNIT *x = reinterpret_cast<const UNIT *>(a.x + t * a.sx);
+    const uint64_t all = a.T * a.per_token;
+    for (uint64_t id = (uint64_t)blockIdx.x * 256 + threadIdx.x; id < all;
+         id += (uint64_t)gridDim.x * 256) {
+        const uint64_t t = id / a.per_token;
+        const uint32_t u = (uint32_t)(id - t * a.per_token);
+        const uint8_t *x = a.x + t * a.sx;
         const int32_t *row_of = a.row_of + t * a.K;
-        const uint64_t u0 = (uint64_t)part * (256 * PER) + threadIdx.x;
-        UNIT v[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (u0 + j * 256 < a.units)
-                v[j] = x[u0 + j * 256];
+        const uint32_t tail = ALIGNED ? (uint32_t)(a.bytes - (uint64_t)a.units * 16) : 0u;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (u >= a.units + tail)
+            v.x = __float_as_uint(a.xscale[t * a.nb + (u - a.units - tail)]);
+        else if (ALIGNED && u < a.units)
+            v = ld_v4_stream(reinterpret_cast<const uint4 *>(x) + u);
+        else if (ALIGNED)
+            v.x = x[(uint64_t)a.units * 16 + (u - a.units)];
         for (int k0 = 0; k0 < a.K; k0 += 8) {
             // the eight rows first: a store between two of these loads would
             // hold the second back
@@ -261,32 +276,38 @@ __global__ void __launch_bounds__(256) k_moe_dispatch(const __grid_constant__ Mo
                 if (r[k] < 0)
                     continue;
                 uint8_t *row = a.rows + (uint64_t)r[k] * a.srows;
-                UNIT *to = reinterpret_cast<UNIT *>(row);
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (u0 + j * 256 < a.units)
-                        to[u0 + j * 256] = v[j];
-                if (part == 0) {
-                    // the bytes past the last whole unit, and the scales
-                    for (uint64_t i = a.units * sizeof(UNIT) + threadIdx.x; i < a.bytes; i += 256)
-                        row[i] = reinterpret_cast<const uint8_t *>(x)[i];
-                    for (int i = threadIdx.x; i < a.nb; i += 256)
-                        a.rscale[(uint64_t)r[k] * a.nb + i] = a.xscale[t * a.nb + i];
+                if (u >= a.units + tail) {
+                    a.rscale[(uint64_t)r[k] * a.nb + (u - a.units - tail)] = __uint_as_float(v.x);
+                } else if (ALIGNED && u < a.units) {
+                    st_v4(reinterpret_cast<uint4 *>(row) + u, v);
+                } else if (ALIGNED) {
+                    row[(uint64_t)a.units * 16 + (u - a.units)] = (uint8_t)v.x;
+                } else {
+                    // bytes [lo, hi) of the row: this word of the destination
+                    const int64_t lo = (int64_t)u * 16 - (int64_t)((uintptr_t)row & 15u);
+                    const int64_t hi = lo + 16, end = (int64_t)a.bytes;
+                    const uint32_t low = (uint32_t)((uintptr_t)(x + lo) & 3u);
+                    if (lo - low >= 0 && lo - low + 20 <= end) {
+                        st_v4(row + lo, load_shifted(reinterpret_cast<const uint32_t *>(x + lo - low),
+                                                     8 * low));
+                    } else {
+                        for (int64_t i = lo < 0 ? 0 : lo; i < hi && i < end; ++i)
+                            row[i] = x[i];
+                    }
                 }
             }
         }
     }
 }
 
-template <typename UNIT> static cudaError_t dispatch_unit(MoveArgs a, cudaStream_t s) {
-    a.units = a.bytes / sizeof(UNIT);
-    auto grid = [&](int per) {
-        const uint64_t parts = (a.units + 256 * per - 1) / (256 * per);
-        a.parts = (uint32_t)(parts < 1 ? 1 : parts);
-        const uint64_t g = a.T * a.parts;
-        return (int)(g < (1u << 30) ? g : (1u << 30));
-    };
-    return launch_kernel(k_moe_dispatch<UNIT, 1>, grid(1), 256, 0, s, true, a);
+static cudaError_t launch_dispatch(MoveArgs a, bool aligned, cudaStream_t s) {
+    // not aligned: a row of n bytes touches at most n / 16 + 2 words
+    a.units = (uint32_t)(a.bytes / 16 + (aligned ? 0 : 2));
+    a.per_token = a.units + (aligned ? a.bytes % 16 : 0) + (uint64_t)a.nb;
+    const uint64_t ctas = (a.T * a.per_token + 255) / 256;
+    const int grid = (int)(ctas < (1u << 30) ? ctas : (1u << 30));
+    return aligned ? launch_kernel(k_moe_dispatch<true>, grid, 256, 0, s, true, a)
+                   : launch_kernel(k_moe_dispatch<false>, grid, 256, 0, s, true, a);
 }
 
 // ---- rows back at their tokens ---------------------------------------------------
@@ -299,7 +320,6 @@ struct ReturnArgs {
     uint64_t srows, sout;     // bytes between rows
     uint64_t nrows, T;
     uint32_t H;
-    uint32_t parts;           // CTAs per token
     int K;
 };
 
@@ -321,21 +341,33 @@ struct Choices {
     }
 };
 
-// A job is 256 units of a token, one a thread; the CTAs stay and take job after
-// job.  Eight rows' loads are in flight at a time, and the next job's rows and
-// weights are read meanwhile, so that its loads need not wait for them.
-template <int DT, bool WIDE>
+// A job is 256 units of a token, one a thread; FLAT (rows of fewer units): 256
+// units counted over the tokens.  The CTAs stay and take job after job.  Eight
+// rows' loads are in flight at a time, and the next job's rows and weights are
+// read meanwhile, so that its loads need not wait for them.
+template <int DT, bool WIDE, bool FLAT>
 __global__ void __launch_bounds__(256, 3) k_moe_return(const __grid_constant__ ReturnArgs a) {
     using L = Rows<DT, WIDE>;
     kernel_prologue();
-    const uint32_t units = L::units(a.H);
-    const uint64_t jobs = a.T * a.parts;
+    const uint32_t units = L::units(a.H), parts = (units + 255) / 256;
+    const uint64_t jobs = FLAT ? (a.T * units + 255) / 256 : a.T * parts;
+    // token and unit of this thread in a job; a token past the last: none
+    auto token = [&](uint64_t job) {
+        return FLAT ? (job * 256 + threadIdx.x) / units : job / parts;
+    };
+    auto unit = [&](uint64_t job, uint64_t t) {
+        return FLAT ? (uint32_t)(job * 256 + threadIdx.x - t * units)
+                    : (uint32_t)(job - t * parts) * 256 + threadIdx.x;
+    };
     Choices next;
-    if (blockIdx.x < jobs)
-        next.read(a.row_of, a.w, blockIdx.x / a.parts, a.K, 0, a.nrows);
+    if (blockIdx.x < jobs && token(blockIdx.x) < a.T)
+        next.read(a.row_of, a.w, token(blockIdx.x), a.K, 0, a.nrows);
     for (uint64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const uint64_t t = job / a.parts;
-        const uint32_t u = (uint32_t)(job - t * a.parts) * 256 + threadIdx.x;
+        const uint64_t t = token(job);
+        const uint32_t u = unit(job, t);
+        if (FLAT && t >= a.T)
+            break;                            // the last job's threads past the end
+        const bool on = FLAT || u < units;
         float acc[L::E];
 #pragma unroll
         for (int i = 0; i < L::E; ++i)
@@ -348,10 +380,10 @@ __global__ void __launch_bounds__(256, 3) k_moe_return(const __grid_constant__ R
             uint4 p[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                p[j] = L::load_if(c.r[j] >= 0 && u < units,
+                p[j] = L::load_if(on && c.r[j] >= 0,
                                   a.rows + (uint64_t)(c.r[j] < 0 ? 0 : c.r[j]) * a.srows, u, a.H);
-            if (k0 + 8 >= a.K && job + gridDim.x < jobs)
-                next.read(a.row_of, a.w, (job + gridDim.x) / a.parts, a.K, 0, a.nrows);
+            if (k0 + 8 >= a.K && job + gridDim.x < jobs && token(job + gridDim.x) < a.T)
+                next.read(a.row_of, a.w, token(job + gridDim.x), a.K, 0, a.nrows);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (c.r[j] >= 0) {
@@ -370,7 +402,7 @@ __global__ void __launch_bounds__(256, 3) k_moe_return(const __grid_constant__ R
                     any = true;
                 }
         }
-        if (u < units)
+        if (on)
             L::store(a.out + t * a.sout, u, a.H, acc);
     }
 }
@@ -474,11 +506,13 @@ static cudaError_t return_grad_launch(const ReturnGradArgs &a, cudaStream_t s) {
                          true, a);
 }
 
-template <int DT, bool WIDE> static cudaError_t return_launch(ReturnArgs a, cudaStream_t s) {
-    a.parts = (Rows<DT, WIDE>::units(a.H) + 255) / 256;
-    const uint64_t jobs = a.T * a.parts, most = 152 * 3;
-    return launch_kernel(k_moe_return<DT, WIDE>, (int)(jobs < most ? jobs : most), 256, 0, s, true,
-                         a);
+template <int DT, bool WIDE> static cudaError_t return_launch(const ReturnArgs &a, cudaStream_t s) {
+    const uint64_t units = Rows<DT, WIDE>::units(a.H), most = 152 * 3;
+    const bool flat = units < 256;
+    const uint64_t jobs = flat ? (a.T * units + 255) / 256 : a.T * ((units + 255) / 256);
+    const int grid = (int)(jobs < most ? jobs : most);
+    return flat ? launch_kernel(k_moe_return<DT, WIDE, true>, grid, 256, 0, s, true, a)
+                : launch_kernel(k_moe_return<DT, WIDE, false>, grid, 256, 0, s, true, a);
 }
 
 // Sizes every row mover shares: the status code, AR_OK if they hold.
@@ -555,14 +589,7 @@ int ar_moe_dispatch(const void *x, size_t ldx, const float *xscale, const int32_
     a.bytes = H * esz;
     a.K = K;
     a.nb = (int)nb;
-    const uintptr_t low = mx.p | mr.p | mx.stride | mr.stride;
-    if (low % 16 == 0)
-        return launched(dispatch_unit<uint4>(a, stream));
-    if (low % 4 == 0)
-        return launched(dispatch_unit<uint32_t>(a, stream));
-    if (low % 2 == 0)
-        return launched(dispatch_unit<uint16_t>(a, stream));
-    return launched(dispatch_unit<uint8_t>(a, stream));
+    return launched(launch_dispatch(a, wide(mx) && wide(mr), stream));
 }
 
 int ar_moe_return(const void *rows, size_t ldrows, size_t nrows, const int32_t *row_of,

@@ -77,16 +77,19 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint32_t
             row[L::at(u, i)] = (uint8_t)(q[i / 4] >> (8 * (i & 3)));
 }
 
-// One CTA per row.  UNITS units of a thread stay in registers.  Every loop
-// over units has the same trip count in a whole warp (the bound is a multiple
-// of 32), which the shuffles of store_e4m3 need.
-template <int DT, bool WIDE, bool E4M3, int UNITS, int THREADS, int CTAS>
+// One CTA, or one warp, per row.  UNITS units of a thread stay in registers.  Every loop over units has the same
+// trip count in a whole warp (the bound is a multiple of 32), which the
+// shuffles of store_e4m3 need.
+template <int DT, bool WIDE, bool E4M3, RowSplit SPLIT, int UNITS, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant__ NormArgs a) {
     using L = Rows<DT, WIDE>;
     __shared__ float part[32];
     kernel_prologue();
+    static_assert(SPLIT != kGroups, "a row has one warp or all of them");
+    const RowGroup<SPLIT> group(0);
     const uint32_t H = a.H, units = L::warp_units(H);
-    for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (uint64_t t = (uint64_t)blockIdx.x * group.groups() + group.g(); t < a.T;
+         t += (uint64_t)gridDim.x * group.groups()) {
         const uint8_t *x = a.x + t * a.sx;
         const uint8_t *res = a.res ? a.res + t * a.sres : nullptr;
         uint8_t *sum = a.sum ? a.sum + t * a.ssum : nullptr;
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
             uint4 px[UNITS], pr[UNITS];
 #pragma unroll
             for (int j = 0; j < UNITS; ++j) {
-                const uint32_t u = threadIdx.x + j * blockDim.x;
+                const uint32_t u = group.thread() + j * group.threads();
                 px[j] = pr[j] = make_uint4(0u, 0u, 0u, 0u);
                 if (u < units) {
                     px[j] = L::load(x, u, H);
@@ -125,16 +128,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
                     fma2(squares, v[j][i], v[j][i + 1], v[j][i], v[j][i + 1]);
             }
         }
-        for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+        for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
             float b[L::E];
             total(L::load(x, u, H), res ? L::load(res, u, H) : make_uint4(0u, 0u, 0u, 0u), b);
 #pragma unroll
             for (int i = 0; i < L::E; i += 2)
                 fma2(squares, b[i], b[i + 1], b[i], b[i + 1]);
         }
-        const float ss = block_sum(squares[0] + squares[1], part);
+        const float ss = group.sum(squares[0] + squares[1], part);
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)H) + a.eps));
-        if (a.rstd && threadIdx.x == 0)
+        if (a.rstd && group.thread() == 0)
             a.rstd[t] = r;
 
         auto finish = [&](uint32_t u, float *b) {
@@ -156,39 +159,48 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
                 L::store(y, u, H, b);
         };
         // the units past the registers: read again, before sum or y overwrites them
-        for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+        for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
             float b[L::E];
             total(L::load(x, u, H), res ? L::load(res, u, H) : make_uint4(0u, 0u, 0u, 0u), b);
             finish(u, b);
         }
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const uint32_t u = threadIdx.x + j * blockDim.x;
+            const uint32_t u = group.thread() + j * group.threads();
             if (u < units)
                 finish(u, v[j]);
         }
-        __syncthreads();                             // `part` is free for the next row
+        if (SPLIT == kOneRow)
+            __syncthreads();                         // `part` is free for the next row
     }
 }
 
 template <int DT, bool WIDE, bool E4M3>
 static cudaError_t norm_units(const NormArgs &a, cudaStream_t s) {
     const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
-    const int grid = (int)(a.T < (1u << 30) ? a.T : (1u << 30));
+    auto grid = [&](uint64_t rows) {
+        const uint64_t g = (a.T + rows - 1) / rows;
+        return (int)(g < (1u << 30) ? g : (1u << 30));
+    };
     auto threads = [&](uint32_t per, uint32_t most) {
         const uint32_t n = ((units + per - 1) / per + 31) / 32 * 32;
         return (int)(n < most ? n : most);
     };
     // Many rows: four units a thread, so that an SM holds several CTAs and one
-    // row's loads run while another's reduction waits.  Few rows: as many
-    // threads as the row has units, for latency.
+    // row's loads run while another's reduction waits (8192 x 8192 bf16 to 8
+    // bits: 75 us; with one unit a thread 107 to 154).  Short rows go eight to a
+    // CTA, one a warp (65536 x 512: 60 us; one a CTA 68; 32768 x 1024: 46 and
+    // 41).  Few rows: as many threads as the row has units, for latency.
+    if (a.T > kNormManyRows && units <= 64)
+        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kWarpRow, 4, 256, 4>, grid(8), 256, 0, s,
+                             true, a);
     if (a.T > kNormManyRows && units <= 1024)
-        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 4, 256, 4>, grid, threads(4, 256), 0, s,
-                             true, a);
+        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kOneRow, 4, 256, 4>, grid(1),
+                             threads(4, 256), 0, s, true, a);
     if (a.T > kNormManyRows)
-        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 4, 512, 2>, grid, threads(4, 512), 0, s,
-                             true, a);
-    return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, 2, 1024, 1>, grid,
+        return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kOneRow, 4, 512, 2>, grid(1),
+                             threads(4, 512), 0, s, true, a);
+    return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kOneRow, 2, 1024, 1>, grid(1),
                          threads(units <= 1024 ? 1 : 2, 1024), 0, s, true, a);
 }
 
@@ -210,6 +222,7 @@ struct NormGradArgs {
     uint64_t sdy, sdsum, ss, sdx;     // bytes between rows
     uint64_t T;
     uint32_t H;
+    int row_warps;                    // warps that share a row
 };
 
 // Copy of 16 bytes (or fewer: the rest reads as zero) to shared memory, done
@@ -276,22 +289,24 @@ __device__ __forceinline__ void grad_close(const NormGradArgs &a, uint32_t u, ui
     L::store(dx, u, a.H, d);
 }
 
-// CTA b takes the rows b, b + gridDim.x, ...; each thread owns the columns of
-// its units and keeps their share of dgamma in registers over all of the
-// CTA's rows.  RING: the next row's s, dy and dsum come to shared memory by
-// background copies while this row is at work; a thread copies and reads its
-// own units only, so the copies need no barrier.  Without it (rows that are
-// not 16-byte aligned, or longer than UNITS units a thread) rows are loaded in
-// their turn, and the units past the registers are read twice, their dgamma
-// kept in the CTA's row of `work`.
-template <int DT, bool WIDE, int UNITS, int THREADS, int CTAS, bool RING>
+// A CTA takes a row, or one per group of a.row_warps warps, at a time, then the
+// next of every gridDim.x such sets.  Each thread owns the columns of its units and keeps
+// their share of dgamma in registers over all of its rows; the groups' shares
+// are joined in order at the end.  RING: the next row's s, dy and dsum come to
+// shared memory by background copies while this row is at work; a thread copies
+// and reads its own units only, so the copies need no barrier.  Without it (rows
+// that are not 16-byte aligned, or longer than UNITS units a thread) rows are
+// loaded in their turn, and the units past the registers are read twice, their
+// dgamma kept in the CTA's row of `work` (one group then).
+template <int DT, bool WIDE, RowSplit SPLIT, int UNITS, int THREADS, int CTAS, bool RING>
 __global__ void __launch_bounds__(THREADS, CTAS)
 k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
     using L = Rows<DT, WIDE>;
-    extern __shared__ uint4 ring[];               // [2][3][UNITS][THREADS]
+    extern __shared__ uint4 ring[];               // [2][3][UNITS][THREADS], or the join's sums
     __shared__ float part[2][32];
     kernel_prologue();
-    const uint32_t H = a.H, units = L::warp_units(H);
+    const RowGroup<SPLIT> group(a.row_warps);
+    const uint32_t H = a.H;
     float *work = a.work ? a.work + (uint64_t)blockIdx.x * H : nullptr;
     float dg[UNITS][L::E];
 #pragma unroll
@@ -303,12 +318,12 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
         return ring[((turn * 3 + array) * UNITS + j) * THREADS + threadIdx.x];
     };
     auto fetch = [&](uint64_t t, int turn) {      // the ring's copies of row t
-        if (t < a.T) {
+        if (t < a.T && group.g() < group.groups()) {
             const uint8_t *s = a.s + t * a.ss, *dy = a.dy + t * a.sdy;
             const uint8_t *dsum = a.dsum ? a.dsum + t * a.sdsum : nullptr;
 #pragma unroll
             for (int j = 0; j < UNITS; ++j) {
-                const uint32_t u = threadIdx.x + j * blockDim.x;
+                const uint32_t u = group.thread() + j * group.threads();
                 const uint32_t left = u * L::E < H ? (H - u * L::E) * L::kSize : 0u;
                 const uint32_t n = left < 16u ? left : 16u;
                 const uint64_t at = n ? (uint64_t)u * 16 : 0;
@@ -321,9 +336,13 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
         copies_commit();
     };
     int turn = 0;
+    const uint64_t step = (uint64_t)gridDim.x * group.groups();
     if (RING)
-        fetch(blockIdx.x, 0);
-    for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+        fetch((uint64_t)blockIdx.x * group.groups() + group.g(), 0);
+    for (uint64_t t0 = (uint64_t)blockIdx.x * group.groups(); t0 < a.T; t0 += step, turn ^= 1) {
+        const bool on = group.g() < group.groups() && t0 + group.g() < a.T;
+        const uint64_t t = on ? t0 + group.g() : t0;
+        const uint32_t units = on ? L::warp_units(H) : 0u;
         const uint8_t *dy = a.dy + t * a.sdy, *s = a.s + t * a.ss;
         const uint8_t *dsum = a.dsum ? a.dsum + t * a.sdsum : nullptr;
         uint8_t *dx = a.dx + t * a.sdx;
@@ -333,7 +352,7 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
         uint4 ps[UNITS], pd[UNITS], pu[UNITS];
         float d[UNITS][L::E];
         if (RING) {
-            fetch(t + gridDim.x, turn ^ 1);
+            fetch(t0 + step + group.g(), turn ^ 1);
             copies_wait<1>();
 #pragma unroll
             for (int j = 0; j < UNITS; ++j) {
@@ -343,7 +362,7 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
         } else {
 #pragma unroll
             for (int j = 0; j < UNITS; ++j) {
-                const uint32_t u = threadIdx.x + j * blockDim.x;
+                const uint32_t u = group.thread() + j * group.threads();
                 ps[j] = pd[j] = pu[j] = none;
                 if (u < units) {
                     ps[j] = L::load(s, u, H);
@@ -355,12 +374,12 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const uint32_t u = threadIdx.x + j * blockDim.x;
+            const uint32_t u = group.thread() + j * group.threads();
             if (u < units)
                 dot += grad_open<DT, WIDE>(a, u, ps[j], pd[j], r, d[j], dg[j]);
         }
         if (!RING)
-            for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+            for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
                 float e[L::E], w[L::E];
 #pragma unroll
                 for (int i = 0; i < L::E; ++i)
@@ -371,30 +390,51 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
                     if (work && L::at(u, i) < H)
                         work[L::at(u, i)] = w[i];
             }
-        const float c = __fdiv_rn(block_sum(dot, part[turn]) * r * r * r, (float)H);
+        const float c = __fdiv_rn(group.sum(dot, part[turn]) * r * r * r, (float)H);
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const uint32_t u = threadIdx.x + j * blockDim.x;
+            const uint32_t u = group.thread() + j * group.threads();
             if (u < units)
                 grad_close<DT, WIDE>(a, u, ps[j], d[j], RING ? slot(turn, 2, j) : pu[j], r, c, dx);
         }
         if (!RING)
-            for (uint32_t u = threadIdx.x + UNITS * blockDim.x; u < units; u += blockDim.x) {
+            for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
                 float e[L::E], w[L::E];
                 const uint4 s4 = L::load(s, u, H);
                 grad_open<DT, WIDE>(a, u, s4, L::load(dy, u, H), r, e, w);
                 grad_close<DT, WIDE>(a, u, s4, e, dsum ? L::load(dsum, u, H) : none, r, c, dx);
             }
     }
-    if (work) {
+    if (!work)
+        return;
+    if (SPLIT == kOneRow) {
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-            const uint32_t u = threadIdx.x + j * blockDim.x;
+            const uint32_t u = group.thread() + j * group.threads();
 #pragma unroll
             for (int i = 0; i < L::E; ++i)
-                if (L::at(u, i) < H && u < units)
+                if (L::at(u, i) < H && u < L::warp_units(H))
                     work[L::at(u, i)] = dg[j][i];
         }
+        return;
+    }
+    float *sums = reinterpret_cast<float *>(ring);        // [groups][H]
+    __syncthreads();                                      // the ring is done with
+    if (group.g() < group.groups())
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+            const uint32_t u = group.thread() + j * group.threads();
+#pragma unroll
+            for (int i = 0; i < L::E; ++i)
+                if (L::at(u, i) < H && u < L::warp_units(H))
+                    sums[(uint32_t)group.g() * H + L::at(u, i)] = dg[j][i];
+        }
+    __syncthreads();
+    for (uint32_t h = threadIdx.x; h < H; h += blockDim.x) {
+        float v = sums[h];
+        for (int g = 1; g < group.groups(); ++g)
+            v += sums[(uint32_t)g * H + h];
+        work[h] = v;
     }
 }
 
@@ -418,32 +458,45 @@ __global__ void __launch_bounds__(1024) k_join_rows(const float *work, float *ou
         out[col] = v;
 }
 
-template <int DT, bool WIDE>
-static cudaError_t norm_grad_units(const NormGradArgs &a, int grid, cudaStream_t s) {
-    const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
-    auto threads = [&](uint32_t per, uint32_t most) {
-        const uint32_t n = ((units + per - 1) / per + 31) / 32 * 32;
-        return (int)(n < most ? n : most);
-    };
-    // with the ring, 2 x 3 rows of 16 KB a CTA and two CTAs an SM
-    if (WIDE && units <= 1024) {
-        constexpr int kUnits = 2, kThreads = 512;
-        constexpr auto kernel = k_rmsnorm_grad<DT, WIDE, kUnits, kThreads, 2, WIDE>;
-        const size_t smem = 2 * 3 * kUnits * kThreads * sizeof(uint4);
-        const cudaError_t e = opt_in_smem<kernel>(smem);
-        if (e != cudaSuccess)
-            return e;
-        return launch_kernel(kernel, grid, threads(kUnits, kThreads), smem, s, true, a);
-    }
-    if (units <= 1024)
-        return launch_kernel(k_rmsnorm_grad<DT, WIDE, 4, 256, 2, false>, grid, threads(4, 256), 0, s,
-                             true, a);
-    return launch_kernel(k_rmsnorm_grad<DT, WIDE, 4, 512, 1, false>, grid, threads(4, 512), 0, s, true, a);
+// Launches the gradient's form with these numbers; *partial: rows of `work` it fills.
+template <int DT, bool WIDE, RowSplit SPLIT, int UNITS, int THREADS, int CTAS, bool RING>
+static cudaError_t norm_grad_form(NormGradArgs a, cudaStream_t s, int *partial) {
+    using L = Rows<DT, WIDE>;
+    constexpr auto kernel = k_rmsnorm_grad<DT, WIDE, SPLIT, UNITS, THREADS, CTAS, RING>;
+    // the ring's six arrays; the join needs no more than THREADS * UNITS * E floats
+    constexpr size_t join = SPLIT == kGroups ? (size_t)UNITS * THREADS * L::E * sizeof(float) : 0;
+    constexpr size_t smem = RING ? (size_t)6 * UNITS * THREADS * sizeof(uint4) : join;
+    static_assert(smem >= join, "room for the join");
+    const cudaError_t e = opt_in_smem<kernel>(smem);
+    if (e != cudaSuccess)
+        return e;
+    a.row_warps = (int)((L::warp_units(a.H) / 32 + UNITS - 1) / UNITS);
+    const int groups = SPLIT == kGroups ? THREADS / 32 / a.row_warps : 1;
+    const uint64_t sets = (a.T + groups - 1) / groups;
+    *partial = (int)(sets < 152 * CTAS ? sets : 152 * CTAS);
+    return launch_kernel(kernel, *partial, THREADS, smem, s, true, a);
 }
 
-template <int DT> static cudaError_t norm_grad_dt(const NormGradArgs &a, bool w, int grid,
-                                                  cudaStream_t s) {
-    return w ? norm_grad_units<DT, true>(a, grid, s) : norm_grad_units<DT, false>(a, grid, s);
+template <int DT, bool WIDE>
+static cudaError_t norm_grad_units(const NormGradArgs &a, cudaStream_t s, int *partial) {
+    const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
+    // With the ring, two CTAs an SM (8192 x 8192 bf16: 101 us; one CTA 125,
+    // without the ring 124).  Rows that fill half a CTA or less go side by side
+    // (32768 x 1024: 57 us; one a CTA 195).
+    if (WIDE && units <= 512)
+        return norm_grad_form<DT, WIDE, kGroups, 2, 512, 2, WIDE>(a, s, partial);
+    if (WIDE && units <= 1024)
+        return norm_grad_form<DT, WIDE, kOneRow, 2, 512, 2, WIDE>(a, s, partial);
+    if (units <= 512)
+        return norm_grad_form<DT, WIDE, kGroups, 4, 256, 2, false>(a, s, partial);
+    if (units <= 1024)
+        return norm_grad_form<DT, WIDE, kOneRow, 4, 256, 2, false>(a, s, partial);
+    return norm_grad_form<DT, WIDE, kOneRow, 4, 512, 1, false>(a, s, partial);
+}
+
+template <int DT>
+static cudaError_t norm_grad_dt(const NormGradArgs &a, bool w, cudaStream_t s, int *partial) {
+    return w ? norm_grad_units<DT, true>(a, s, partial) : norm_grad_units<DT, false>(a, s, partial);
 }
 
 }  // namespace ar
@@ -552,19 +605,17 @@ int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum
     a.sdx = mx.stride;
     a.T = T;
     a.H = (uint32_t)H;
-    // two CTAs per SM; more of them where rows are short
-    const size_t most = H <= 2048 ? AR_NORM_GRAD_ROWS : 304;
-    const int grid = (int)(T < most ? T : most);
     const bool w = wide(my) && (!dsum || wide(mu)) && wide(ms) && wide(mx) && mg.p % 16 == 0;
     cudaError_t e;
+    int partial = 0;
     switch (dtype) {
-    case AR_BF16: e = norm_grad_dt<AR_BF16>(a, w, grid, stream); break;
-    case AR_FP16: e = norm_grad_dt<AR_FP16>(a, w, grid, stream); break;
-    default: e = norm_grad_dt<AR_FP32>(a, w, grid, stream); break;
+    case AR_BF16: e = norm_grad_dt<AR_BF16>(a, w, stream, &partial); break;
+    case AR_FP16: e = norm_grad_dt<AR_FP16>(a, w, stream, &partial); break;
+    default: e = norm_grad_dt<AR_FP32>(a, w, stream, &partial); break;
     }
     if (e == cudaSuccess && dgamma)
         e = launch_kernel(k_join_rows, dim3((unsigned)((H + 31) / 32)), 1024, 0, stream, true,
-                          (const float *)work, dgamma, (uint64_t)H, grid);
+                          (const float *)work, dgamma, (uint64_t)H, partial);
     return launched(e);
 }
 

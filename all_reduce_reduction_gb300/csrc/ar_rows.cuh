@@ -153,19 +153,50 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the CTA, the same in every thread; `part` is shared memory of 32
-// floats, free again after the next __syncthreads.  blockDim.x is a multiple
-// of 32.
-__device__ __forceinline__ float block_sum(float v, float *part) {
-    v = warp_sum(v);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (blockDim.x == 32)
-        return v;
-    if (lane == 0)
-        part[warp] = v;
-    __syncthreads();
-    return warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.0f);
-}
+// Rows of a CTA at a time.
+//   kOneRow:  the whole CTA works on a row.
+//   kWarpRow: every warp on its own.
+//   kGroups:  `warps` warps on each, groups of them side by side; the warps past
+//             the last whole group have g == groups() and no row.
+enum RowSplit { kOneRow, kWarpRow, kGroups };
+template <RowSplit SPLIT> struct RowGroup {
+    int warps_;
+    __device__ __forceinline__ explicit RowGroup(int warps) : warps_(warps) {}
+    __device__ __forceinline__ int warps() const {
+        return SPLIT == kOneRow ? (int)(blockDim.x >> 5) : SPLIT == kWarpRow ? 1 : warps_;
+    }
+    __device__ __forceinline__ int groups() const {
+        return SPLIT == kOneRow ? 1 : (int)(blockDim.x >> 5) / warps();
+    }
+    __device__ __forceinline__ int g() const {
+        if (SPLIT == kOneRow)
+            return 0;
+        const int g = (int)(threadIdx.x >> 5) / warps();
+        return g < groups() ? g : groups();
+    }
+    // this thread's place in its group, and the group's threads
+    __device__ __forceinline__ uint32_t thread() const {
+        return SPLIT == kOneRow    ? threadIdx.x
+               : SPLIT == kWarpRow ? threadIdx.x & 31
+                                   : threadIdx.x - (uint32_t)(g() * warps()) * 32;
+    }
+    __device__ __forceinline__ uint32_t threads() const {
+        return SPLIT == kOneRow ? blockDim.x : (uint32_t)warps() * 32;
+    }
+    // Sum over the group, the same in each of its threads.  Called by the
+    // whole CTA; `part` is shared memory of 32 floats, free again after the
+    // CTA's next barrier.
+    __device__ __forceinline__ float sum(float v, float *part) const {
+        v = warp_sum(v);
+        if (SPLIT == kWarpRow || warps() == 1)
+            return v;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0)
+            part[warp] = v;
+        __syncthreads();
+        return warp_sum(lane < warps() && g() < groups() ? part[g() * warps() + lane] : 0.0f);
+    }
+};
 
 // ---- host-side checks ------------------------------------------------------
 

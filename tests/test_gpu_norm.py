@@ -50,7 +50,8 @@ def _check_e4m3(codes, scale, y, what):
 @pytest.mark.parametrize("T,H,pad,shift", [
     (1, 1, 0, 0), (3, 7, 0, 0), (2, 127, 1, 0), (5, 128, 0, 0), (4, 129, 7, 8), (1, 8192, 0, 0),
     (7, 8192, 8, 0), (33, 4099, 5, 0), (3, 4099, 0, 1), (2, 4104, 0, 3), (3, 16384, 0, 0),
-    (2, 40000, 0, 0), (2, 33001, 0, 0)])
+    (2, 40000, 0, 0), (2, 33001, 0, 0), (700, 40, 0, 0), (403, 512, 8, 0), (350, 1001, 0, 0),
+    (306, 1500, 0, 0), (310, 8200, 0, 0), (305, 5001, 0, 1)])
 def test_norm(dtype, eight, T, H, pad, shift):
     need_gpu()
     x, res, g = _inputs(T, H, dtype, 10 * H + T)
@@ -158,7 +159,8 @@ def _grad64(dy, dsum, s, g, r):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("T,H,pad,shift", [
     (1, 1, 0, 0), (1, 8192, 0, 0), (3, 7, 2, 0), (305, 264, 0, 0), (700, 129, 0, 1),
-    (40, 4099, 5, 0), (5, 16384, 0, 0), (3, 20000, 0, 0), (3, 20001, 0, 0), (1300, 40, 0, 0)])
+    (40, 4099, 5, 0), (5, 16384, 0, 0), (3, 20000, 0, 0), (3, 20001, 0, 0), (1300, 40, 0, 0),
+    (2500, 512, 0, 0), (900, 1001, 0, 0), (650, 4096, 8, 0), (611, 2049, 0, 0), (330, 9000, 0, 0)])
 def test_norm_grad(dtype, T, H, pad, shift):
     need_gpu()
     s, dsum, g = _inputs(T, H, dtype, 20 * H + T)
