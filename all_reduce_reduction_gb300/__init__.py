@@ -177,7 +177,7 @@ def _ptr(x) -> int:
         return 0
     if isinstance(x, int):
         return x
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 _raw_stream = None            # torch's (raw stream of a device, current device)
@@ -426,9 +426,9 @@ def ar_plan_destroy(p: int) -> None:
     _check(load_library().ar_plan_destroy(p), "ar_plan_destroy")
 
 
-def _dtype8(dtype) -> int:
-    return DTYPES8[dtype] if isinstance(dtype, str) else dtype
-
+# The layer operators.  A decode step makes several of these calls per layer, and
+# the host's share of a small one is most of its time, so they go to the library
+# without the helpers in between.
 
 def ar_rmsnorm(x, res, gamma, eps: float, total, y, scale, rstd, T: int, H: int, dtype,
                out_dtype=None, ldx: int = 0, ldres: int = 0, ldsum: int = 0, ldy: int = 0,
@@ -437,11 +437,14 @@ def ar_rmsnorm(x, res, gamma, eps: float, total, y, scale, rstd, T: int, H: int,
     ``total = x + res``, ``y = norm(x + res) * gamma`` in ``out_dtype`` (default
     ``dtype``; ``"e4m3"`` with one ``scale`` per 128 elements).  ``res``,
     ``gamma``, ``total``, ``scale`` and ``rstd`` may be None."""
-    dt = _dtype8(dtype)
-    _check(load_library().ar_rmsnorm(_ptr(x), ldx, _ptr(res), ldres, _ptr(gamma), eps,
-                                     _ptr(total), ldsum, _ptr(y), ldy, _ptr(scale), _ptr(rstd),
-                                     T, H, dt, dt if out_dtype is None else _dtype8(out_dtype),
-                                     _stream(stream)), "ar_rmsnorm")
+    dt = DTYPES8.get(dtype, dtype)
+    lib = _lib or load_library()
+    rc = lib.ar_rmsnorm(_ptr(x), ldx, _ptr(res), ldres, _ptr(gamma), eps, _ptr(total), ldsum,
+                        _ptr(y), ldy, _ptr(scale), _ptr(rstd), T, H, dt,
+                        dt if out_dtype is None else DTYPES8.get(out_dtype, out_dtype),
+                        _stream(stream))
+    if rc:
+        raise ArError(rc, "ar_rmsnorm")
 
 
 def ar_rmsnorm_grad(dy, dtotal, total, gamma, rstd, dx, dgamma, work, work_bytes: int, T: int,
@@ -449,54 +452,68 @@ def ar_rmsnorm_grad(dy, dtotal, total, gamma, rstd, dx, dgamma, work, work_bytes
                     lddx: int = 0, stream=None) -> None:
     """Gradient of ar_rmsnorm: ``dx`` (of x and of the residual alike) and the
     binary32 ``dgamma``, joined in ``work`` (min(T, AR_NORM_GRAD_ROWS) * H floats)."""
-    _check(load_library().ar_rmsnorm_grad(_ptr(dy), lddy, _ptr(dtotal), lddtotal, _ptr(total),
-                                          ldtotal, _ptr(gamma), _ptr(rstd), _ptr(dx), lddx,
-                                          _ptr(dgamma), _ptr(work), work_bytes, T, H,
-                                          _dtype8(dtype), _stream(stream)), "ar_rmsnorm_grad")
+    lib = _lib or load_library()
+    rc = lib.ar_rmsnorm_grad(_ptr(dy), lddy, _ptr(dtotal), lddtotal, _ptr(total), ldtotal,
+                             _ptr(gamma), _ptr(rstd), _ptr(dx), lddx, _ptr(dgamma), _ptr(work),
+                             work_bytes, T, H, DTYPES8.get(dtype, dtype), _stream(stream))
+    if rc:
+        raise ArError(rc, "ar_rmsnorm_grad")
 
 
 def ar_moe_route(ids, T: int, K: int, E: int, offsets, row_of, src=None, ids_bytes: int = 4,
                  stream=None) -> None:
     """Stable order of the T * K (token, choice) pairs by expert; ids outside
     [0, E) get no row.  ``ids_bytes`` is 4 or 8."""
-    _check(load_library().ar_moe_route(_ptr(ids), ids_bytes, T, K, E, _ptr(offsets),
-                                       _ptr(row_of), _ptr(src), _stream(stream)), "ar_moe_route")
+    lib = _lib or load_library()
+    rc = lib.ar_moe_route(_ptr(ids), ids_bytes, T, K, E, _ptr(offsets), _ptr(row_of), _ptr(src),
+                          _stream(stream))
+    if rc:
+        raise ArError(rc, "ar_moe_route")
 
 
 def ar_moe_dispatch(x, xscale, row_of, rows, rscale, nrows: int, T: int, K: int, H: int, dtype,
                     ldx: int = 0, ldrows: int = 0, stream=None) -> None:
     """The tokens' rows (and their scales) in the experts' order."""
-    _check(load_library().ar_moe_dispatch(_ptr(x), ldx, _ptr(xscale), _ptr(row_of), _ptr(rows),
-                                          ldrows, _ptr(rscale), nrows, T, K, H, _dtype8(dtype),
-                                          _stream(stream)), "ar_moe_dispatch")
+    lib = _lib or load_library()
+    rc = lib.ar_moe_dispatch(_ptr(x), ldx, _ptr(xscale), _ptr(row_of), _ptr(rows), ldrows,
+                             _ptr(rscale), nrows, T, K, H, DTYPES8.get(dtype, dtype),
+                             _stream(stream))
+    if rc:
+        raise ArError(rc, "ar_moe_dispatch")
 
 
 def ar_moe_return(rows, nrows: int, row_of, w, out, T: int, K: int, H: int, dtype,
                   ldrows: int = 0, ldout: int = 0, stream=None) -> None:
     """The experts' rows back at their tokens, weighted (``w`` None: ones)."""
-    _check(load_library().ar_moe_return(_ptr(rows), ldrows, nrows, _ptr(row_of), _ptr(w),
-                                        _ptr(out), ldout, T, K, H, _dtype8(dtype),
-                                        _stream(stream)), "ar_moe_return")
+    lib = _lib or load_library()
+    rc = lib.ar_moe_return(_ptr(rows), ldrows, nrows, _ptr(row_of), _ptr(w), _ptr(out), ldout, T,
+                           K, H, DTYPES8.get(dtype, dtype), _stream(stream))
+    if rc:
+        raise ArError(rc, "ar_moe_return")
 
 
 def ar_moe_return_grad(dout, rows, nrows: int, row_of, w, drows, dw, T: int, K: int, H: int,
                        dtype, lddout: int = 0, ldrows: int = 0, lddrows: int = 0,
                        stream=None) -> None:
     """Gradient of ar_moe_return: of the rows and of the weights (either None)."""
-    _check(load_library().ar_moe_return_grad(_ptr(dout), lddout, _ptr(rows), ldrows, nrows,
-                                             _ptr(row_of), _ptr(w), _ptr(drows), lddrows,
-                                             _ptr(dw), T, K, H, _dtype8(dtype),
-                                             _stream(stream)), "ar_moe_return_grad")
+    lib = _lib or load_library()
+    rc = lib.ar_moe_return_grad(_ptr(dout), lddout, _ptr(rows), ldrows, nrows, _ptr(row_of),
+                                _ptr(w), _ptr(drows), lddrows, _ptr(dw), T, K, H,
+                                DTYPES8.get(dtype, dtype), _stream(stream))
+    if rc:
+        raise ArError(rc, "ar_moe_return_grad")
 
 
 def ar_matmul8(a, sa, b, sb, offsets, E: int, d, M: int, N: int, K: int, out_dtype,
                lda: int = 0, ldb: int = 0, ldd: int = 0, status=None, stream=None) -> None:
     """Product of E4M3 rows with E4M3 weights and their scales per block of
     128, for one matrix (``offsets`` None) or grouped by expert."""
-    _check(load_library().ar_matmul8(_ptr(a), lda, _ptr(sa), _ptr(b), ldb, _ptr(sb),
-                                     _ptr(offsets), E, _ptr(d), ldd, M, N, K,
-                                     _dtype8(out_dtype), _ptr(status), _stream(stream)),
-           "ar_matmul8")
+    lib = _lib or load_library()
+    rc = lib.ar_matmul8(_ptr(a), lda, _ptr(sa), _ptr(b), ldb, _ptr(sb), _ptr(offsets), E, _ptr(d),
+                        ldd, M, N, K, DTYPES8.get(out_dtype, out_dtype), _ptr(status),
+                        _stream(stream))
+    if rc:
+        raise ArError(rc, "ar_matmul8")
 
 
 class Handle:
