@@ -1,8 +1,10 @@
 """Build the CUDA library ``libar_gb300.so`` in-tree, for sm_103a only.
 
 Each ``csrc/*.cu`` file is compiled by its own nvcc process (in parallel),
-then the objects are linked into one shared library next to this file.  A
-rebuild happens only when a source or header is newer than the library.
+then the objects are linked into one shared library next to this file, and the
+extension module ``_native`` (``csrc/ar_python.c``) beside it against that
+library.  A rebuild happens only when a source or header is newer than what was
+built.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libar_gb300.so")
+NATIVE = os.path.join(HERE, "_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "ar_python.c")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -42,7 +47,7 @@ def sources() -> list[str]:
 
 def _newest_input() -> float:
     files = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-    files += glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+    files += glob.glob(os.path.join(INCLUDE, "*.h")) + [NATIVE_SOURCE, os.path.abspath(__file__)]
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -59,20 +64,31 @@ def _compile(src: str, extra: list[str]) -> str:
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile and link the library if needed; returns its path."""
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    newest = _newest_input()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest
+                         for f in (LIB, NATIVE)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     srcs = sources()
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
+    _link(LIB, [*objs, "-lcudart"])
+    _link(NATIVE, ["-O2", "-Xcompiler", "-fPIC,-Wall,-Wextra", "-I" + INCLUDE,
+                   "-I" + sysconfig.get_paths()["include"], NATIVE_SOURCE, "-L" + HERE,
+                   "-lar_gb300", "-Xlinker", "-rpath=$ORIGIN", "-cudart", "none"])
+    return LIB
+
+
+def _link(out: str, args: list[str]) -> None:
+    tmp = out + ".tmp.%d" % os.getpid()
+    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *args]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
-    os.replace(tmp, LIB)
-    return LIB
+    if res.stderr.strip():
+        sys.stderr.write(res.stderr)
+    os.replace(tmp, out)
 
 
 if __name__ == "__main__":
