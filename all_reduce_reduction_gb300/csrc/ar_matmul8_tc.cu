@@ -234,7 +234,7 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float v[16]) {
 // ---- many rows ----------------------------------------------------------------
 
 constexpr int kRowsM = 256, kRowsN = 256, kRowsStages = 6;
-constexpr int kRowsHalf = 128;                    // rows of a, and of b, that a CTA of the pair holds
+constexpr int kRowsHalf = 128;                    // rows of a, and of b, of one CTA of the pair
 constexpr int kRowsEpilogueWarps = 8;
 constexpr int kRowsRun = 32;                      // columns an epilogue warp stores at a time
 constexpr int kRowsAccs = 4, kRowsAccCols = 128;  // accumulators, and columns of one

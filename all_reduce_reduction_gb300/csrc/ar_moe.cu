@@ -288,8 +288,8 @@ __global__ void __launch_bounds__(256) k_moe_dispatch(const __grid_constant__ Mo
                     const int64_t hi = lo + 16, end = (int64_t)a.bytes;
                     const uint32_t low = (uint32_t)((uintptr_t)(x + lo) & 3u);
                     if (lo - low >= 0 && lo - low + 20 <= end) {
-                        st_v4(row + lo, load_shifted(reinterpret_cast<const uint32_t *>(x + lo - low),
-                                                     8 * low));
+                        const uint32_t *words = reinterpret_cast<const uint32_t *>(x + lo - low);
+                        st_v4(row + lo, load_shifted(words, 8 * low));
                     } else {
                         for (int64_t i = lo < 0 ? 0 : lo; i < hi && i < end; ++i)
                             row[i] = x[i];
@@ -421,17 +421,23 @@ struct ReturnGradArgs {
     int K;
 };
 
-// One CTA per token.  Eight choices at a time: every thread walks its units of
-// dout, writes the weighted unit to each choice's row of drows and adds its
-// product with the choice's row; the eight sums are then joined over the CTA.
+// A token's CTAs are one cluster, each with a run of the token's units.  Eight
+// choices at a time: every thread walks its units of dout, writes the weighted
+// unit to each choice's row of drows and adds its product with the choice's row;
+// the eight sums are then joined over the CTA and, in order, over the cluster.
 template <int DT, bool WIDE>
-__global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
+__global__ void __launch_bounds__(256, 2)
+k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
     using L = Rows<DT, WIDE>;
-    __shared__ float part[8][32];
+    __shared__ float part[8][32], sums[8];
     kernel_prologue();
-    const uint32_t units = L::units(a.H);
+    const uint32_t ctas = cluster_size(), rank = cluster_rank();
+    // whole warps of units per CTA
+    const uint32_t run = (L::warp_units(a.H) / 32 + ctas - 1) / ctas * 32;
+    const uint32_t first = rank * run;
+    const uint32_t units = first + run < L::units(a.H) ? first + run : L::units(a.H);
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (uint64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (uint64_t t = blockIdx.x / ctas; t < a.T; t += gridDim.x / ctas) {
         const uint8_t *dout = a.dout + t * a.sdout;
         for (int k0 = 0; k0 < a.K; k0 += 8) {
             int32_t r[8];
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constan
                 w[j] = a.w && k0 + j < a.K ? a.w[t * a.K + k0 + j] : 1.0f;
                 dot[j][0] = dot[j][1] = 0.0f;
             }
-            for (uint32_t u = threadIdx.x; u < units; u += blockDim.x) {
+            for (uint32_t u = first + threadIdx.x; u < units; u += blockDim.x) {
                 uint4 p[8];
                 if (a.dw) {
 #pragma unroll
@@ -489,10 +495,23 @@ __global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constan
                 // warp w joins choices w, w + warps, ...
                 for (int j = warp; j < 8; j += warps) {
                     const float v = warp_sum(lane < warps ? part[j][lane] : 0.0f);
-                    if (lane == 0 && k0 + j < a.K)
+                    if (lane == 0 && ctas > 1)
+                        sums[j] = v;
+                    else if (lane == 0 && k0 + j < a.K)
                         a.dw[t * a.K + k0 + j] = v;
                 }
-                __syncthreads();
+                if (ctas > 1) {
+                    cluster_barrier();
+                    if (rank == 0 && threadIdx.x < 8 && k0 + (int)threadIdx.x < a.K) {
+                        float v = 0.0f;
+                        for (uint32_t c = 0; c < ctas; ++c)
+                            v += __uint_as_float(ld_peer_u32(sums + threadIdx.x, c));
+                        a.dw[t * a.K + k0 + threadIdx.x] = v;
+                    }
+                    cluster_barrier();
+                } else {
+                    __syncthreads();
+                }
             }
         }
     }
@@ -501,9 +520,26 @@ __global__ void __launch_bounds__(256, 2) k_moe_return_grad(const __grid_constan
 template <int DT, bool WIDE>
 static cudaError_t return_grad_launch(const ReturnGradArgs &a, cudaStream_t s) {
     const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
-    const int grid = (int)(a.T < (1u << 30) ? a.T : (1u << 30));
-    return launch_kernel(k_moe_return_grad<DT, WIDE>, grid, (int)(units < 256 ? units : 256), 0, s,
-                         true, a);
+    const int threads = (int)(units < 256 ? units : 256);
+    // few tokens: as many CTAs a token as its units or half the SMs allow
+    int ctas = 1;
+    while (ctas < 8 && units >= 512u * ctas && a.T * ctas * 2 <= 152)
+        ctas *= 2;
+    const uint64_t grid = a.T * ctas, most = 1u << 30;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = (unsigned)(grid < most ? grid : most);
+    cfg.blockDim = threads;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_moe_return_grad<DT, WIDE>, a);
 }
 
 template <int DT, bool WIDE> static cudaError_t return_launch(const ReturnArgs &a, cudaStream_t s) {

@@ -36,7 +36,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 constexpr float kLeastBlock = 0x1p-96f;
 constexpr float kTopE4M3 = 448.0f;
 
-constexpr uint64_t kNormManyRows = 304;
+// More units than this are many: a thread for each no longer fits the SMs at once.
+constexpr uint64_t kNormManyUnits = 152 * 1024;
 
 // The unit's share of y in 8 bits, and its block's scale.  Called by whole warps.
 template <int DT, bool WIDE>
@@ -77,9 +78,9 @@ __device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint32_t
             row[L::at(u, i)] = (uint8_t)(q[i / 4] >> (8 * (i & 3)));
 }
 
-// One CTA, or one warp, per row.  UNITS units of a thread stay in registers.  Every loop over units has the same
-// trip count in a whole warp (the bound is a multiple of 32), which the
-// shuffles of store_e4m3 need.
+// One CTA, or one warp, per row.  UNITS units of a thread stay in registers.
+// Every loop over units has the same trip count in a whole warp (the bound is a
+// multiple of 32), which the shuffles of store_e4m3 need.
 template <int DT, bool WIDE, bool E4M3, RowSplit SPLIT, int UNITS, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant__ NormArgs a) {
     using L = Rows<DT, WIDE>;
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
                     add2(b + i, w[i], w[i + 1]);
             }
         };
+        const uint32_t past = group.thread() + UNITS * group.threads();
         float v[UNITS][L::E];
         float squares[2] = {0.0f, 0.0f};
         {
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
                     fma2(squares, v[j][i], v[j][i + 1], v[j][i], v[j][i + 1]);
             }
         }
-        for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
+        for (uint32_t u = past; u < units; u += group.threads()) {
             float b[L::E];
             total(L::load(x, u, H), res ? L::load(res, u, H) : make_uint4(0u, 0u, 0u, 0u), b);
 #pragma unroll
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) k_rmsnorm(const __grid_constant
                 L::store(y, u, H, b);
         };
         // the units past the registers: read again, before sum or y overwrites them
-        for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
+        for (uint32_t u = past; u < units; u += group.threads()) {
             float b[L::E];
             total(L::load(x, u, H), res ? L::load(res, u, H) : make_uint4(0u, 0u, 0u, 0u), b);
             finish(u, b);
@@ -186,18 +188,20 @@ static cudaError_t norm_units(const NormArgs &a, cudaStream_t s) {
         const uint32_t n = ((units + per - 1) / per + 31) / 32 * 32;
         return (int)(n < most ? n : most);
     };
-    // Many rows: four units a thread, so that an SM holds several CTAs and one
-    // row's loads run while another's reduction waits (8192 x 8192 bf16 to 8
-    // bits: 75 us; with one unit a thread 107 to 154).  Short rows go eight to a
-    // CTA, one a warp (65536 x 512: 60 us; one a CTA 68; 32768 x 1024: 46 and
-    // 41).  Few rows: as many threads as the row has units, for latency.
-    if (a.T > kNormManyRows && units <= 64)
+    // Many units: four a thread, so that an SM holds several CTAs and one row's
+    // loads run while another's reduction waits (8192 x 8192 bf16 to 8 bits: 75 us;
+    // with one unit a thread 107 to 154; 333 x 4099: 5.0 and 6.1).  Short rows go
+    // eight to a CTA, one a warp (65536 x 512: 60 us; one a CTA 68; 4000 x 100: 3.7
+    // and 5.2; 32768 x 1024: 46 and 41).  Few units: a thread for each, for latency (1000 x 1024: 3.8 us;
+    // four a thread 5.6).
+    const bool many = a.T > kNormManyUnits / units;
+    if (units <= 64 && a.T > 1024)
         return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kWarpRow, 4, 256, 4>, grid(8), 256, 0, s,
                              true, a);
-    if (a.T > kNormManyRows && units <= 1024)
+    if (many && units <= 1024)
         return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kOneRow, 4, 256, 4>, grid(1),
                              threads(4, 256), 0, s, true, a);
-    if (a.T > kNormManyRows)
+    if (many)
         return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kOneRow, 4, 512, 2>, grid(1),
                              threads(4, 512), 0, s, true, a);
     return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kOneRow, 2, 1024, 1>, grid(1),
@@ -348,6 +352,7 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
         uint8_t *dx = a.dx + t * a.sdx;
         const float r = a.rstd[t];
         const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t past = group.thread() + UNITS * group.threads();
         float dot = 0.0f;
         uint4 ps[UNITS], pd[UNITS], pu[UNITS];
         float d[UNITS][L::E];
@@ -379,7 +384,7 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
                 dot += grad_open<DT, WIDE>(a, u, ps[j], pd[j], r, d[j], dg[j]);
         }
         if (!RING)
-            for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
+            for (uint32_t u = past; u < units; u += group.threads()) {
                 float e[L::E], w[L::E];
 #pragma unroll
                 for (int i = 0; i < L::E; ++i)
@@ -398,7 +403,7 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
                 grad_close<DT, WIDE>(a, u, ps[j], d[j], RING ? slot(turn, 2, j) : pu[j], r, c, dx);
         }
         if (!RING)
-            for (uint32_t u = group.thread() + UNITS * group.threads(); u < units; u += group.threads()) {
+            for (uint32_t u = past; u < units; u += group.threads()) {
                 float e[L::E], w[L::E];
                 const uint4 s4 = L::load(s, u, H);
                 grad_open<DT, WIDE>(a, u, s4, L::load(dy, u, H), r, e, w);

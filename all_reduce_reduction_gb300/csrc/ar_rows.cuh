@@ -123,7 +123,8 @@ template <int DT, bool WIDE> struct Rows {
 #pragma unroll
         for (int i = 0; i < E; ++i)
             if (at(u, i) < H)
-                st_elem<DT>(row, at(u, i), kPairs ? (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu : w[i & 3]);
+                st_elem<DT>(row, at(u, i),
+                            kPairs ? (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu : w[i & 3]);
     }
 };
 

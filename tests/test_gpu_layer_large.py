@@ -89,7 +89,8 @@ def test_matmul8(N):
     at = torch.tensor([0, 1, mark - 1, mark, mark + 1, M - 2, M - 1], device="cuda")
     kb = torch.arange(K, device="cuda") // 128
     nb = torch.arange(N, device="cuda") // 128
-    a64 = a.view(torch.uint8)[at].view(torch.float8_e4m3fn).float().double() * sa[at].double()[:, kb]
+    codes = a.view(torch.uint8)[at].view(torch.float8_e4m3fn)
+    a64 = codes.float().double() * sa[at].double()[:, kb]
     b64 = b.float().double() * sb[0].double()[nb][:, kb]
     want, size = (a64 @ b64.t()).cpu().numpy(), (a64.abs() @ b64.abs().t()).cpu().numpy()
     assert_within(d[at].double().cpu().numpy(), want, (35 + K // 128) * U * size

@@ -158,8 +158,8 @@ def test_return(dtype, weighted, T, K, E, H, pad, shift):
     terms = y32.astype(np.float64)[np.maximum(row_of, 0)] * here
     terms = terms * (w.astype(np.float64)[:, :, None] if weighted else 1.0)
     exact = terms.sum(1)
-    assert_within(f64(out), exact, K * U * np.abs(terms).sum(1) * (1 + 1e-6) + half(f64(out), dtype),
-                  "return")
+    bound = K * U * np.abs(terms).sum(1) * (1 + 1e-6) + half(f64(out), dtype)
+    assert_within(f64(out), exact, bound, "return")
     assert untouched(buf, T, H, pad, shift)
 
 
