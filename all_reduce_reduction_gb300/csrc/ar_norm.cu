@@ -190,10 +190,10 @@ static cudaError_t norm_units(const NormArgs &a, cudaStream_t s) {
     };
     // Many units: four a thread, so that an SM holds several CTAs and one row's
     // loads run while another's reduction waits (8192 x 8192 bf16 to 8 bits: 75 us;
-    // with one unit a thread 107 to 154; 333 x 4099: 5.0 and 6.1).  Short rows go
-    // eight to a CTA, one a warp (65536 x 512: 60 us; one a CTA 68; 4000 x 100: 3.7
-    // and 5.2; 32768 x 1024: 46 and 41).  Few units: a thread for each, for latency (1000 x 1024: 3.8 us;
-    // four a thread 5.6).
+    // with one unit a thread 107 to 154; 333 x 4099: 5.0 and 6.1).  Few units: a
+    // thread for each, for latency (1000 x 1024: 3.9 us; four a thread 5.6).  Short
+    // rows go eight to a CTA, one a warp (65536 x 512: 60 us; one a CTA 68; 4000 x
+    // 100: 3.7 and 5.2; but 32768 x 1024: 46 and 41).
     const bool many = a.T > kNormManyUnits / units;
     if (units <= 64 && a.T > 1024)
         return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kWarpRow, 4, 256, 4>, grid(8), 256, 0, s,
