@@ -644,6 +644,7 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
 
 constexpr int kFewEpilogueWarps = 4;
 constexpr int kFewThreads = 32 * (kFewEpilogueWarps + 3);
+constexpr int kMaxParts = 8;                      // CTAs of a cluster
 constexpr int kFewScales = 8;                     // blocks along k whose scales a slot holds
 constexpr int kFewWeights = 128 * 128;            // bytes of a stage's weights
 
@@ -886,13 +887,31 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
         for (int c = 0; c < NT; ++c)
             sums[c * 128 + threadIdx.x] = acc[c];
     cluster_barrier();
+    // (the loads of kAt rows from every CTA are in flight together: one after
+    // the other they cost 0.5 us each, 14 us for 1000 x 1000 x 1000)
+    constexpr int kAt = 4;
     if (warp < kFewEpilogueWarps)
-        for (uint32_t c = part; c < rows; c += parts) {
-            float v = 0.0f;
-            for (int p = 0; p < parts; ++p)
-                v += ld_peer_f32(smem_addr(sums + c * 128 + threadIdx.x), p);
-            if (n < a.N)
-                store_out(a.d + (uint64_t)(row + c) * a.ldd, n, v, a.out);
+        for (uint32_t c0 = part; c0 < rows; c0 += parts * kAt) {
+            float v[kMaxParts][kAt];
+#pragma unroll
+            for (int p = 0; p < kMaxParts; ++p)
+#pragma unroll
+                for (int j = 0; j < kAt; ++j) {
+                    const uint32_t c = c0 + j * parts;
+                    v[p][j] = p < parts && c < rows
+                                  ? ld_peer_f32(smem_addr(sums + c * 128 + threadIdx.x), p)
+                                  : 0.0f;
+                }
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                const uint32_t c = c0 + j * parts;
+                float sum = v[0][j];
+#pragma unroll
+                for (int p = 1; p < kMaxParts; ++p)
+                    sum += v[p][j];
+                if (c < rows && n < a.N)
+                    store_out(a.d + (uint64_t)(row + c) * a.ldd, n, sum, a.out);
+            }
         }
     cluster_barrier();
 }
@@ -1017,7 +1036,7 @@ cudaError_t launch_matmul8_tc(const MatmulArgs &a, cudaStream_t s) {
     // few tiles (one row of 8192 x 8192: 20.5, 15.7, 14.1 and 17.2 us in 1, 2, 4
     // and 8 parts)
     int parts = 1;
-    while (parts < 8 && ctas * parts * 2 <= 2 * (uint64_t)sms && parts * 2 <= a.kb)
+    while (parts < kMaxParts && ctas * parts * 2 <= 2 * (uint64_t)sms && parts * 2 <= a.kb)
         parts *= 2;
     // Tenths of a us, as measured: a block along k takes the few form 0.5 us
     // while two CTAs an SM are at work, the rows form 0.45 us a pair.  Either

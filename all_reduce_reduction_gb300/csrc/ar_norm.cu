@@ -223,6 +223,7 @@ struct NormGradArgs {
     const float *rstd;
     uint8_t *dx;
     float *work;                      // gridDim.x rows of H partial sums, or NULL
+    float *dgamma;
     uint64_t sdy, sdsum, ss, sdx;     // bytes between rows
     uint64_t T;
     uint32_t H;
@@ -413,9 +414,17 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
     if (!work)
         return;
     if (SPLIT == kOneRow) {
+        const bool vectors = (uintptr_t)work % 16 == 0;
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
             const uint32_t u = group.thread() + j * group.threads();
+            if (L::whole(u, H) && vectors) {
+#pragma unroll
+                for (int i = 0; i < L::E; i += 4)
+                    *reinterpret_cast<float4 *>(work + L::at(u, i)) =
+                        make_float4(dg[j][i], dg[j][i + 1], dg[j][i + 2], dg[j][i + 3]);
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < L::E; ++i)
                 if (L::at(u, i) < H && u < L::warp_units(H))
@@ -444,28 +453,40 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
 }
 
 // dgamma[h] = sum of the G partial rows, a fixed tree: 32 columns a CTA, thread
-// row y adds the rows y, y + 32, ... and the 32 of a column are then joined.
-__global__ void __launch_bounds__(1024) k_join_rows(const float *work, float *out, uint64_t H,
-                                                    int G) {
-    __shared__ float part[32][33];
+// row y adds the rows y, y + TY, ... and the TY sums of a column are then joined.
+template <int TY>
+__global__ void __launch_bounds__(32 * TY)
+k_join_rows(const float *work, float *out, uint64_t H, int G) {
+    __shared__ float part[TY][33];
     kernel_prologue();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const uint64_t h = (uint64_t)blockIdx.x * 32 + x;
     float v = 0.0f;
     if (h < H)
-        for (int g = y; g < G; g += 32)
+#pragma unroll 4
+        for (int g = y; g < G; g += TY)
             v += work[(uint64_t)g * H + h];
     part[y][x] = v;
     __syncthreads();
-    v = warp_sum(part[x][y]);
-    const uint64_t col = (uint64_t)blockIdx.x * 32 + y;
-    if (x == 0 && col < H)
-        out[col] = v;
+    // warp y joins columns y, y + TY, ...
+    for (int c = y; c < 32; c += TY) {
+        v = warp_sum(x < TY ? part[x][c] : 0.0f);
+        const uint64_t col = (uint64_t)blockIdx.x * 32 + c;
+        if (x == 0 && col < H)
+            out[col] = v;
+    }
 }
 
-// Launches the gradient's form with these numbers; *partial: rows of `work` it fills.
+static cudaError_t join_rows(const float *work, float *out, uint64_t H, int G, cudaStream_t s) {
+    const dim3 grid((unsigned)((H + 31) / 32));
+    return G > 32 ? launch_kernel(k_join_rows<32>, grid, 1024, 0, s, true, work, out, H, G)
+                  : launch_kernel(k_join_rows<8>, grid, 256, 0, s, true, work, out, H, G);
+}
+
+// Launches the gradient's form with these numbers and at most `most` CTAs;
+// *partial: rows of `work` it fills.
 template <int DT, bool WIDE, RowSplit SPLIT, int UNITS, int THREADS, int CTAS, bool RING>
-static cudaError_t norm_grad_form(NormGradArgs a, cudaStream_t s, int *partial) {
+static cudaError_t norm_grad_form(NormGradArgs a, int most, cudaStream_t s, int *partial) {
     using L = Rows<DT, WIDE>;
     constexpr auto kernel = k_rmsnorm_grad<DT, WIDE, SPLIT, UNITS, THREADS, CTAS, RING>;
     // the ring's six arrays; the join needs no more than THREADS * UNITS * E floats
@@ -475,28 +496,42 @@ static cudaError_t norm_grad_form(NormGradArgs a, cudaStream_t s, int *partial) 
     const cudaError_t e = opt_in_smem<kernel>(smem);
     if (e != cudaSuccess)
         return e;
-    a.row_warps = (int)((L::warp_units(a.H) / 32 + UNITS - 1) / UNITS);
+    const uint32_t units = L::warp_units(a.H);
+    a.row_warps = (int)((units / 32 + UNITS - 1) / UNITS);
     const int groups = SPLIT == kGroups ? THREADS / 32 / a.row_warps : 1;
     const uint64_t sets = (a.T + groups - 1) / groups;
-    *partial = (int)(sets < 152 * CTAS ? sets : 152 * CTAS);
-    return launch_kernel(kernel, *partial, THREADS, smem, s, true, a);
+    *partial = (int)(sets < (uint64_t)most ? sets : most);
+    if (*partial == 1 && a.work)
+        a.work = a.dgamma;
+    const int few = units < THREADS ? (int)units : THREADS;
+    return launch_kernel(kernel, *partial, SPLIT == kGroups ? THREADS : few, smem, s, true, a);
 }
 
 template <int DT, bool WIDE>
 static cudaError_t norm_grad_units(const NormGradArgs &a, cudaStream_t s, int *partial) {
     const uint32_t units = Rows<DT, WIDE>::warp_units(a.H);
-    // With the ring, two CTAs an SM (8192 x 8192 bf16: 101 us; one CTA 125,
-    // without the ring 124).  Rows that fill half a CTA or less go side by side
+    // Few units: a CTA per row, no ring, for latency (one row of 8192 bf16: 3.8 us;
+    // with the ring 6.3; 300 x 4096: 7.1 and 10.9).
+    // Units of eight elements need twice the registers, so two of them a thread.
+    constexpr int kUnits = Rows<DT, WIDE>::E / 4, kThreads = 1024 / kUnits;
+    if (a.T <= kNormManyUnits / units && units <= 1024)
+        return norm_grad_form<DT, WIDE, kOneRow, kUnits, kThreads, 1, false>(a, AR_NORM_GRAD_ROWS,
+                                                                              s, partial);
+    if (a.T <= kNormManyUnits / units && units <= 2048)
+        return norm_grad_form<DT, WIDE, kOneRow, 2 * kUnits, kThreads, 1, false>(
+            a, AR_NORM_GRAD_ROWS, s, partial);
+    // With the ring, two CTAs an SM (8192 x 8192 bf16: 96 us; one CTA 120, without
+    // the ring 124).  Rows that fill half a CTA or less go side by side
     // (32768 x 1024: 57 us; one a CTA 195).
     if (WIDE && units <= 512)
-        return norm_grad_form<DT, WIDE, kGroups, 2, 512, 2, WIDE>(a, s, partial);
+        return norm_grad_form<DT, WIDE, kGroups, 2, 512, 2, WIDE>(a, 304, s, partial);
     if (WIDE && units <= 1024)
-        return norm_grad_form<DT, WIDE, kOneRow, 2, 512, 2, WIDE>(a, s, partial);
+        return norm_grad_form<DT, WIDE, kOneRow, 2, 512, 2, WIDE>(a, 304, s, partial);
     if (units <= 512)
-        return norm_grad_form<DT, WIDE, kGroups, 4, 256, 2, false>(a, s, partial);
+        return norm_grad_form<DT, WIDE, kGroups, 4, 256, 2, false>(a, 304, s, partial);
     if (units <= 1024)
-        return norm_grad_form<DT, WIDE, kOneRow, 4, 256, 2, false>(a, s, partial);
-    return norm_grad_form<DT, WIDE, kOneRow, 4, 512, 1, false>(a, s, partial);
+        return norm_grad_form<DT, WIDE, kOneRow, 4, 256, 2, false>(a, 304, s, partial);
+    return norm_grad_form<DT, WIDE, kOneRow, 4, 512, 1, false>(a, 152, s, partial);
 }
 
 template <int DT>
@@ -574,9 +609,7 @@ int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum
     if (T == 0) {
         if (!dgamma)
             return AR_OK;
-        return launched(launch_kernel(k_join_rows, dim3((unsigned)((H + 31) / 32)), 1024, 0,
-                                      stream, true, (const float *)nullptr, dgamma, (uint64_t)H,
-                                      0));
+        return launched(join_rows(nullptr, dgamma, H, 0, stream));
     }
     if (!dy || !s || !rstd || !dx || (dgamma != nullptr) != (work != nullptr))
         return AR_ERR_INVALID;
@@ -604,6 +637,7 @@ int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum
     a.rstd = rstd;
     a.dx = static_cast<uint8_t *>(dx);
     a.work = work;
+    a.dgamma = dgamma;
     a.sdy = my.stride;
     a.sdsum = mu.stride;
     a.ss = ms.stride;
@@ -618,9 +652,9 @@ int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum
     case AR_FP16: e = norm_grad_dt<AR_FP16>(a, w, stream, &partial); break;
     default: e = norm_grad_dt<AR_FP32>(a, w, stream, &partial); break;
     }
-    if (e == cudaSuccess && dgamma)
-        e = launch_kernel(k_join_rows, dim3((unsigned)((H + 31) / 32)), 1024, 0, stream, true,
-                          (const float *)work, dgamma, (uint64_t)H, partial);
+    // one partial row is the gradient itself
+    if (e == cudaSuccess && dgamma && partial > 1)
+        e = join_rows(work, dgamma, H, partial, stream);
     return launched(e);
 }
 
