@@ -1029,26 +1029,41 @@ cudaError_t launch_matmul8_tc(const MatmulArgs &a, cudaStream_t s) {
     auto tiles = [&](uint64_t n) { return a.offsets ? a.M / n + groups : (a.M + n - 1) / n; };
     auto waves = [](uint64_t n, uint64_t at_once) { return (n + at_once - 1) / at_once; };
 
-    const uint64_t per = (a.M + groups - 1) / groups;              // rows per group, on average
-    const int nt = per <= 16 ? 16 : per <= 24 ? 32 : 64;
-    const uint64_t columns = (a.N + 127) / 128, ctas = tiles(nt) * columns;
-    // the few form fills the SMs, two CTAs each, by cutting k while it has too
-    // few tiles (one row of 8192 x 8192: 20.5, 15.7, 14.1 and 17.2 us in 1, 2, 4
-    // and 8 parts)
-    int parts = 1;
-    while (parts < kMaxParts && ctas * parts * 2 <= 2 * (uint64_t)sms && parts * 2 <= a.kb)
-        parts *= 2;
-    // Tenths of a us, as measured: a block along k takes the few form 0.5 us
-    // while two CTAs an SM are at work, the rows form 0.45 us a pair.  Either
-    // side (us) for K = N = 8192 at M = 64, 128, 256, 512: 19.6, 28.1, 34.9, 66.8
-    // and 31.9, 32.8, 33.0, 35.1; for 64 experts of 2048 x 8192 at M = 1024, 4096,
-    // 8192, 16384: 159, 192, 282, 478 and 218, 228, 265, 364.
-    const uint64_t few = waves(ctas * parts, 2 * (uint64_t)sms) * waves(a.kb, parts) * 50;
-    const uint64_t rows = waves(tiles(kRowsM) * ((a.N + kRowsN - 1) / kRowsN), sms / 2) * a.kb * 45;
-    // the grid's y and z dimensions end at 65535
-    if (few > rows || columns > 65535 || tiles(nt) > 65535)
-        return launch_rows(a, sms, s);
+    const uint64_t columns = (a.N + 127) / 128;
+    // Estimates in hundredths of a us from measured launches.  The few form, two
+    // CTAs an SM: a wave of CTAs costs `wave` and `block` for each of its blocks
+    // along k; cutting k over the CTAs of a cluster shortens that and adds `join`,
+    // as long as the clusters fill at most 7/8 of a wave (a full one of fours ran in
+    // two: 300 x 500 x 700 8.3 us).  The rows form: 2.9 us and 0.45 a block for
+    // every wave of pairs.
+    // Either side as measured (us), few and rows: K = N = 8192 at M = 64, 128,
+    // 256, 512: 16.8, 22.9, 34.9, 66.8 and 31.9, 32.8, 33.1, 35.1; 64 experts of
+    // 2048 x 8192 at M = 1024, 4096, 8192, 16384: 159, 187, 282, 478 and 218, 228,
+    // 265, 364; 2000 x 3000 x 128: 13.3 and 11.2; 300 x 500 x 700: 4.1 and 13.7.
+    // Parts, one row of 8192 x 8192: 20.5, 15.7, 14.1 and 17.2 in 1, 2, 4 and 8.
+    struct { int nt, wave, block, join; } const kForms[] = {
+        {16, 200, 40, 150}, {32, 280, 42, 200}, {64, 380, 45, 250}};
+    uint64_t best = waves(tiles(kRowsM) * ((a.N + kRowsN - 1) / kRowsN), sms / 2) *
+                    (290 + 45 * (uint64_t)a.kb);
+    int nt = 0, parts = 1;
+    for (const auto &f : kForms) {
+        // the grid's y and z dimensions end at 65535
+        if (columns > 65535 || tiles(f.nt) > 65535)
+            continue;
+        const uint64_t ctas = tiles(f.nt) * columns, room = 2 * (uint64_t)sms;
+        for (int p = 1; p == 1 || (p <= kMaxParts && p <= a.kb && ctas * p * 8 <= room * 7);
+             p *= 2) {
+            const uint64_t cost = waves(ctas * p, room) * (f.wave + waves(a.kb, p) * f.block) +
+                                  (p > 1 ? f.join : 0);
+            if (cost < best) {
+                best = cost;
+                nt = f.nt;
+                parts = p;
+            }
+        }
+    }
     switch (nt) {
+    case 0: return launch_rows(a, sms, s);
     case 16: return launch_few<16>(a, parts, s);
     case 32: return launch_few<32>(a, parts, s);
     default: return launch_few<64>(a, parts, s);
