@@ -363,13 +363,20 @@ __device__ __forceinline__ void store_rows(const MatmulArgs &a, uint4 *stage, ui
 // the sums of a CTA's rows of a are in its own tensor memory.  One CTA's tile of
 // 128 x 256 needs 48 KB a block to be written to and read from shared memory,
 // more than its 128 bytes a clock allow beside the products; the pair's 32 KB
-// fit.
-// Warps 0-15: epilogue (lanes 32 * (warp % 4), columns 64 * (warp / 4));
-// warp 16: TMA; warp 17: MMA; warp 18: scales.  The scales of a tile's rows are
-// a column of sa, one sector a row: read by every epilogue warp for every block
-// they kept the L1 pipe, which also feeds the tensor core, half busy (8192^3:
-// 515 us).  Warp 18 reads each once, eight blocks at a time, and lays them out
-// by block in shared memory.
+// fit better.
+//
+// A block is multiplied in two halves of 128 columns with an accumulator each,
+// two blocks' worth in all, so that the products of a half run while the three
+// before it are read back.  Warps 0-7: epilogue (lanes 32 * (warp % 4), half
+// warp / 4); warp 8: TMA; warp 9: MMA, in the first CTA; warp 10: scales.  The
+// scales of a tile's rows are a column of sa, one sector a row: read by every
+// epilogue warp for every block they kept the L1 pipe, which also feeds the
+// tensor core, half busy.  Warp 10 reads each once, eight blocks at a time, and
+// lays them out by block in shared memory.
+//
+// Bound by the epilogue's chain per warp and block (wait, read back, multiply-
+// add, arrive: about 870 clocks) over the products' 640.  8192^3: 415 to 450 us
+// by box, 2.4 to 2.6 PFLOP/s; 16384 rows over 64 experts of 2048 x 8192: 340 us.
 __global__ void __launch_bounds__(kRowsThreads, 1)
 k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
@@ -679,7 +686,10 @@ __device__ __forceinline__ float ld_peer_f32(uint32_t local, uint32_t rank) {
 // blockIdx.x: CTA of the cluster (its share of the blocks along k);
 // blockIdx.y: tile of 128 weight rows; blockIdx.z: row tile, counted over the
 // groups.  Warps 0-3: epilogue, lane + 32 * warp is the weight row; warp 4:
-// TMA; warp 5: MMA; warp 6: scales.
+// TMA; warp 5: MMA; warp 6: scales, sa * sb for eight blocks at a time.  Bound by
+// the stream of the weights: 4096 rows over 64 experts of 2048 x 8192 190 us (5.9
+// TB/s); one row of 8192 x 8192 14.0 us, of which about 5 are launch, first loads
+// and join.
 template <int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
 k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_a,

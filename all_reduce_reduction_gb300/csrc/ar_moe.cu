@@ -187,9 +187,10 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
 }
 
 static cudaError_t launch_route(const RouteArgs &a, cudaStream_t s) {
-    // a warp's run is 32 pairs at least; one CTA up to 1024 pairs
+    // a warp's run is 32 pairs at least; one CTA up to 1024 pairs; eight warps at
+    // least, which also clear and scan the experts' counts
     const uint32_t groups = (a.n + 31) / 32;
-    const int warps = groups < 1 ? 1 : groups < (uint32_t)kRouteWarps ? (int)groups : kRouteWarps;
+    const int warps = groups < 8 ? 8 : groups < (uint32_t)kRouteWarps ? (int)groups : kRouteWarps;
     const int ctas = groups > (uint32_t)kRouteWarps ? kRouteCtas : 1;
     const size_t smem = (size_t)(warps + 2) * (a.E + 1) * sizeof(uint32_t);
     // the opt-in holds for every size used: 34 rows of at most 1025 words
