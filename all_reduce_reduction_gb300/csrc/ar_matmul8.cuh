@@ -22,6 +22,20 @@ struct MatmulArgs {
     int *status;
 };
 
+// The rows [lo, hi) of group e.
+__device__ __forceinline__ void group_range(const MatmulArgs &a, int e, uint32_t &lo,
+                                            uint32_t &hi) {
+    if (!a.offsets) {
+        lo = 0;
+        hi = a.M;
+        return;
+    }
+    const int32_t x = a.offsets[e], y = a.offsets[e + 1];
+    lo = x < 0 ? 0u : (uint32_t)x < a.M ? (uint32_t)x : a.M;
+    hi = y < 0 ? 0u : (uint32_t)y < a.M ? (uint32_t)y : a.M;
+    hi = hi < lo ? lo : hi;
+}
+
 // Row tile `index` of all groups' tiles of TM rows: its group, first row and
 // rows.  Called by a whole warp; false if there are fewer tiles.
 __device__ __forceinline__ bool find_rows(const MatmulArgs &a, uint32_t tm, uint32_t index,
@@ -40,12 +54,8 @@ __device__ __forceinline__ bool find_rows(const MatmulArgs &a, uint32_t tm, uint
     for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
         uint32_t lo = 0, hi = 0;
-        if (e < a.E) {
-            const int32_t x = a.offsets[e], y = a.offsets[e + 1];
-            lo = x < 0 ? 0u : (uint32_t)x < a.M ? (uint32_t)x : a.M;
-            hi = y < 0 ? 0u : (uint32_t)y < a.M ? (uint32_t)y : a.M;
-            hi = hi < lo ? lo : hi;
-        }
+        if (e < a.E)
+            group_range(a, e, lo, hi);
         const uint32_t tiles = (hi - lo + tm - 1) / tm;
         uint32_t scan = tiles;
 #pragma unroll

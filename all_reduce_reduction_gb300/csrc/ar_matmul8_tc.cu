@@ -266,19 +266,6 @@ struct RowsTile {
     uint32_t row, rows, n0;
 };
 
-__device__ __forceinline__ void group_range(const MatmulArgs &a, int e, uint32_t &lo,
-                                            uint32_t &hi) {
-    if (!a.offsets) {
-        lo = 0;
-        hi = a.M;
-        return;
-    }
-    const int32_t x = a.offsets[e], y = a.offsets[e + 1];
-    lo = x < 0 ? 0u : (uint32_t)x < a.M ? (uint32_t)x : a.M;
-    hi = y < 0 ? 0u : (uint32_t)y < a.M ? (uint32_t)y : a.M;
-    hi = hi < lo ? lo : hi;
-}
-
 // Tile `index`: bands of kRowsBand row tiles, in a band column tile by column
 // tile, so that CTAs at work at the same time share rows of a and of b in L2.
 __device__ __forceinline__ RowsTile rows_tile(const MatmulArgs &a, const RowsShared &sh,

@@ -51,7 +51,8 @@ def _check_e4m3(codes, scale, y, what):
     (1, 1, 0, 0), (3, 7, 0, 0), (2, 127, 1, 0), (5, 128, 0, 0), (4, 129, 7, 8), (1, 8192, 0, 0),
     (7, 8192, 8, 0), (33, 4099, 5, 0), (3, 4099, 0, 1), (2, 4104, 0, 3), (3, 16384, 0, 0),
     (2, 40000, 0, 0), (2, 33001, 0, 0), (700, 40, 0, 0), (403, 512, 8, 0), (350, 1001, 0, 0),
-    (306, 1500, 0, 0), (310, 8200, 0, 0), (305, 5001, 0, 1)])
+    (306, 1500, 0, 0), (310, 8200, 0, 0), (305, 5001, 0, 1), (1100, 40, 0, 0), (2000, 500, 12, 0),
+    (1030, 511, 0, 0), (200, 8192, 0, 0), (400, 4099, 0, 0)])
 def test_norm(dtype, eight, T, H, pad, shift):
     need_gpu()
     x, res, g = _inputs(T, H, dtype, 10 * H + T)
