@@ -41,6 +41,9 @@ constexpr float kTopE4M3 = 448.0f;
 constexpr uint64_t kNormManyUnits = 152 * 1024;
 
 // The unit's share of y in 8 bits, and its block's scale.  Called by whole warps.
+// Both quotients are products with a rounded reciprocal: correctly rounded
+// divisions cost an instruction sequence for every element (8192 x 8192 bf16: 94 us
+// against 75) and change only codes whose value lies on the middle between two.
 template <int DT, bool WIDE>
 __device__ __forceinline__ void store_e4m3(uint8_t *row, float *scales, uint32_t u, uint32_t H,
                                            const float *v) {

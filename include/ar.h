@@ -619,9 +619,12 @@ enum ar_dtype8 {
  *   y    = round(v * r * gamma)
  * The norm uses v, not its rounding.  With out_dtype AR_E4M3 each block of
  * AR_SCALE_BLOCK elements of a row (the last may be shorter) has one scale:
- *   scale = max(largest |v * r * gamma| of the block, 2^-96) / 448
- *   y     = e4m3(v * r * gamma / scale)
- * (a NaN element becomes the NaN code and does not enter the scale).
+ *   scale = max(largest |v * r * gamma| of the block, 2^-96) * round(1 / 448)
+ *   y     = e4m3(v * r * gamma * round(1 / scale))
+ * (a NaN element becomes the NaN code and does not enter the scale).  The two
+ * quotients are binary32 products with a rounded reciprocal: a scale is within
+ * two units in the last place of the largest magnitude over 448, and a value
+ * that close to the middle between two codes may become either.
  *   x, res, sum: dtype, T x H.   res may be NULL; sum may be NULL.
  *   gamma:       dtype, H; NULL stands for ones.
  *   y:           out_dtype (dtype itself or AR_E4M3), T x H.
