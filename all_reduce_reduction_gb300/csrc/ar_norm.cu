@@ -247,8 +247,10 @@ template <int LEFT> __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
 }
 
-// One element block of the gradient.  With c = r^3 * sum(d * s) / H:
-//   d = gamma * dy,  dgamma += dy * (s * r),  dx = r * d - c * s + dsum
+// One element block of the gradient.  With c = r^2 * sum(d * s) / H:
+//   d = gamma * dy,  dgamma += dy * (s * r),  dx = r * (d - c * s) + dsum
+// (c has the size of r and c * s that of d; r^3 would leave binary32 for rows
+// whose own gradient does not).
 // Pass 1: d from dy and gamma; the products' sum and dgamma's share.
 template <int DT, bool WIDE>
 __device__ __forceinline__ float grad_open(const NormGradArgs &a, uint32_t u, uint4 ps, uint4 pd,
@@ -285,8 +287,8 @@ __device__ __forceinline__ void grad_close(const NormGradArgs &a, uint32_t u, ui
     L::widen(ps, s);
 #pragma unroll
     for (int i = 0; i < L::E; i += 2) {
-        mul2(d + i, r, r);
         fma2(d + i, -c, -c, s[i], s[i + 1]);
+        mul2(d + i, r, r);
     }
     if (a.dsum) {
         float w[L::E];
@@ -400,7 +402,7 @@ k_rmsnorm_grad(const __grid_constant__ NormGradArgs a) {
                     if (work && L::at(u, i) < H)
                         work[L::at(u, i)] = w[i];
             }
-        const float c = __fdiv_rn(group.sum(dot, part[turn]) * r * r * r, (float)H);
+        const float c = __fdiv_rn(group.sum(dot, part[turn]) * r * r, (float)H);
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
             const uint32_t u = group.thread() + j * group.threads();

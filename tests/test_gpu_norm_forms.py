@@ -1,12 +1,15 @@
 """ar_rmsnorm and its gradient where the other norm tests do not reach: the E4M3
-arithmetic bit for bit."""
+arithmetic bit for bit, rows of very small and very large values.
+
+Bounds of the gradient.  dx: the 96 u of its terms' magnitudes that
+test_gpu_norm.py derives; they are relative, so they hold at every scale of s."""
 import numpy as np
 import pytest
 import torch
 
 import all_reduce_reduction_gb300 as ar
 from gpu_helpers import need_gpu
-from layer_helpers import LEAST, TORCH, randn
+from layer_helpers import LEAST, TORCH, U, assert_within, f64, half, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +37,29 @@ def test_scale_and_codes_are_products_with_rounded_reciprocals(dtype, T, H):
     inverse = np.repeat(np.float32(1.0) / want, 128, 1)[:, :H]
     codes = torch.from_numpy(y * inverse).to(torch.float8_e4m3fn)
     assert torch.equal(q.cpu().view(torch.uint8), codes.view(torch.uint8))
+
+
+def _grad64(dy, dsum, s, g, r):
+    """(dx, its bound before the output's rounding, dgamma, dgamma's magnitudes)."""
+    n, r = f64(s) * r.astype(np.float64)[:, None], r.astype(np.float64)[:, None]
+    gd = f64(dy) * f64(g)
+    extra = f64(dsum) if dsum is not None else np.zeros_like(n)
+    dx = r * (gd - n * (gd * n).mean(1, keepdims=True)) + extra
+    size = r * (np.abs(gd) + np.abs(n) * np.abs(gd * n).mean(1, keepdims=True)) + np.abs(extra)
+    return dx, 96 * U * size, (f64(dy) * n).sum(0), np.abs(f64(dy) * n).sum(0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [1e-20, 1e17])
+@pytest.mark.parametrize("T,H", [(5, 1000), (3, 20001), (2500, 512), (400, 8192)])
+def test_gradient_of_very_small_and_very_large_rows(dtype, scale, T, H):
+    """r^3 leaves binary32 where neither r nor dx does."""
+    need_gpu()
+    s = (randn(T, T, H) * scale).to(TORCH[dtype])
+    dy, g = randn(H, T, H).to(TORCH[dtype]), (1 + 0.2 * randn(7, H)).to(TORCH[dtype])
+    r = (1.0 / np.sqrt((f64(s) ** 2).mean(1))).astype(np.float32)
+    dx = torch.empty(T, H, dtype=TORCH[dtype], device="cuda")
+    ar.ar_rmsnorm_grad(dy.cuda(), None, s.cuda(), g.cuda(), torch.from_numpy(r).cuda(), dx, None,
+                       None, 0, T, H, dtype)
+    want, bound, _, _ = _grad64(dy, None, s, g, r)
+    assert_within(f64(dx), want, bound + half(want, dtype), "dx")
