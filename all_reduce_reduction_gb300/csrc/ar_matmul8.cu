@@ -18,7 +18,12 @@ namespace ar {
 constexpr int kAnyTile = 64, kAnyStep = 32;
 
 __global__ void __launch_bounds__(256) k_matmul8_any(const __grid_constant__ MatmulArgs a) {
-    __shared__ float as[kAnyStep][kAnyTile + 4], bs[kAnyStep][kAnyTile + 4];
+    __shared__ alignas(16) float as[kAnyStep][kAnyTile + 4];
+    __shared__ alignas(16) float bs[kAnyStep][kAnyTile + 4];
+    // the products' loop reads four at a time
+    static_assert(__alignof__(as) >= sizeof(float4) && __alignof__(bs) >= sizeof(float4),
+                  "operands in shared memory start on 16-byte boundaries");
+    static_assert((kAnyTile + 4) % 4 == 0, "and so does every step of them");
     kernel_prologue();
     int e;
     uint32_t row, rows;
