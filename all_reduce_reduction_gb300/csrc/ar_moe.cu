@@ -562,7 +562,7 @@ template <int DT, bool WIDE> static cudaError_t return_launch(const ReturnArgs &
 static int check_moe(size_t T, int K, size_t H) {
     if (K < 1 || K > AR_MOE_MAX_CHOICES || H < 1)
         return AR_ERR_INVALID;
-    if (H >= (size_t)1 << 31 || T >= ((size_t)1 << 31) / (size_t)K)
+    if (H >= (size_t)1 << 31 || T > (((size_t)1 << 31) - 1) / (size_t)K)
         return AR_ERR_UNSUPPORTED;
     return AR_OK;
 }

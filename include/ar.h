@@ -663,7 +663,8 @@ int ar_rmsnorm_grad(const void *dy, size_t lddy, const void *dsum, size_t lddsum
  *   src:     T * K words; the pair (t*K + k) of each row, -1 from row
  *            offsets[E] on; may be NULL.
  *   ids:     T * K words of ids_bytes (4 or 8) bytes, signed.
- * T * K < 2^31; E <= AR_MOE_MAX_EXPERTS; K <= AR_MOE_MAX_CHOICES. */
+ * T * K < 2^31 and K <= AR_MOE_MAX_CHOICES, here and in the calls below;
+ * E <= AR_MOE_MAX_EXPERTS. */
 int ar_moe_route(const void *ids, int ids_bytes, size_t T, int K, int E, int32_t *offsets,
                  int32_t *row_of, int32_t *src, cudaStream_t stream);
 

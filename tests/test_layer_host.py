@@ -1,0 +1,33 @@
+"""The host side of the layer operators, on the CPU: limits, and what the binding
+makes of its arguments.  No call here launches anything."""
+import pytest
+
+import all_reduce_reduction_gb300 as ar
+from all_reduce_reduction_gb300 import build as cuda_build
+
+A = [0x10000000 * (i + 1) for i in range(10)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    cuda_build.build()
+
+
+def _code(fn, *args, **kw):
+    try:
+        fn(*args, stream=0, **kw)
+    except ar.ArError as e:
+        return e.code
+    return ar.AR_OK
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 7, 8, 29, 32])
+def test_pairs_are_taken_up_to_the_stated_limit(K):
+    """T * K < 2^31; with the limit kept the calls go on to the missing pointer."""
+    most = (2 ** 31 - 1) // K
+    for T, code in ((most, ar.AR_ERR_INVALID), (most + 1, ar.AR_ERR_UNSUPPORTED)):
+        assert _code(ar.ar_moe_route, None, T, K, 64, A[0], A[1]) == code
+        assert _code(ar.ar_moe_dispatch, None, None, A[0], A[1], None, 8, T, K, 64, "bf16") == code
+        assert _code(ar.ar_moe_return, None, 8, A[0], None, A[1], T, K, 64, "bf16") == code
+        assert _code(ar.ar_moe_return_grad, None, A[0], 8, A[1], None, A[2], None, T, K, 64,
+                     "bf16") == code
