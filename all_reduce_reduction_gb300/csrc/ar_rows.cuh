@@ -201,11 +201,13 @@ template <RowSplit SPLIT> struct RowGroup {
 
 // ---- host-side checks ------------------------------------------------------
 
-// A row-major matrix argument: its address, bytes from its first to past its
-// last element, and whether every row starts on a 16-byte boundary.
+// A row-major matrix argument: its address, bytes between and in its rows, and
+// bytes from its first to past its last element.
 struct Matrix {
     uintptr_t p = 0;
+    size_t rows = 0;
     size_t stride = 0;       // bytes between rows
+    size_t width = 0;        // bytes of a row
     size_t bytes = 0;
     bool ok = true;
 };
@@ -217,19 +219,36 @@ inline Matrix matrix(const void *p, size_t ld, size_t rows, size_t cols, size_t 
     if (ld == 0)
         ld = cols;
     m.p = (uintptr_t)p;
+    m.rows = rows;
     const size_t limit = (size_t)1 << 62;
     m.ok = m.p % esz == 0 && ld >= cols && ld <= limit / esz &&
            (rows == 0 || ld * esz <= limit / rows);
     if (m.ok) {
         m.stride = ld * esz;
-        m.bytes = rows == 0 || cols == 0 ? 0 : (rows - 1) * m.stride + cols * esz;
+        m.width = cols * esz;
+        m.bytes = rows == 0 || cols == 0 ? 0 : (rows - 1) * m.stride + m.width;
     }
     return m;
 }
+// Whether the two share a byte.  Rows of one stride that lie in the gaps of the
+// other's (column slices of one wider buffer) do not; for rows of different
+// strides the answer is that of the whole ranges.
 inline bool meet(const Matrix &a, const Matrix &b) {
-    return a.p && b.p && a.p < b.p + b.bytes && b.p < a.p + a.bytes;
+    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0 || a.p >= b.p + b.bytes ||
+        b.p >= a.p + a.bytes)
+        return false;
+    const bool strided_a = a.rows > 1, strided_b = b.rows > 1;
+    if (strided_a == strided_b && (!strided_a || a.stride != b.stride))
+        return true;
+    const size_t stride = strided_a ? a.stride : b.stride;
+    // where rows of b start in those of a
+    const size_t at = b.p >= a.p ? (b.p - a.p) % stride : (stride - (a.p - b.p) % stride) % stride;
+    return at < a.width || at + b.width > stride;
 }
-inline bool same(const Matrix &a, const Matrix &b) { return a.p == b.p && a.stride == b.stride; }
+// The same rows, for matrices of as many rows of one length.
+inline bool same(const Matrix &a, const Matrix &b) {
+    return a.p == b.p && (a.stride == b.stride || a.rows <= 1);
+}
 // the output o meets the input i otherwise than exactly
 inline bool clash(const Matrix &o, const Matrix &i) { return meet(o, i) && !same(o, i); }
 inline bool wide(const Matrix &m, size_t align = 16) {

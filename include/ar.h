@@ -593,7 +593,8 @@ int ar_allreduce_ll_static(int R, size_t N, int dtype, const void *const in[],
  * depends on the order in which CTAs run.  NaN and infinities follow IEEE
  * arithmetic.  AR_ERR_INVALID: a NULL that the call needs, a misaligned
  * pointer, a bad type or range, a leading dimension below the row, an output
- * that overlaps another buffer (what each call allows is said there);
+ * that overlaps another buffer (what each call allows is said there; column
+ * slices of one wider buffer share no element and do not overlap);
  * AR_ERR_UNSUPPORTED: rows of 2^31 elements or more, or sizes past a limit
  * stated below; AR_ERR_CUDA: a failed launch. */
 
