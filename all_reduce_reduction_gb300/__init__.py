@@ -477,10 +477,13 @@ def ar_rmsnorm_grad(dy, dtotal, total, gamma, rstd, dx, dgamma, work, work_bytes
         raise ArError(rc, "ar_rmsnorm_grad")
 
 
-def ar_moe_route(ids, T: int, K: int, E: int, offsets, row_of, src=None, ids_bytes: int = 4,
+def ar_moe_route(ids, T: int, K: int, E: int, offsets, row_of, src=None, ids_bytes=None,
                  stream=None) -> None:
     """Stable order of the T * K (token, choice) pairs by expert; ids outside
-    [0, E) get no row.  ``ids_bytes`` is 4 or 8."""
+    [0, E) get no row.  ``ids_bytes`` (4 or 8) is a tensor's own element size
+    unless given, and 4 for an address."""
+    if ids_bytes is None:
+        ids_bytes = ids.element_size() if hasattr(ids, "element_size") else 4
     calls = _calls or _layer_calls()
     rc = calls.ar_moe_route(ids, ids_bytes, T, K, E, offsets, row_of, src, stream)
     if rc:

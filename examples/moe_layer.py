@@ -95,7 +95,7 @@ class Layer:
         ar.ar_rmsnorm(self.attention[0], self.residual, self.gamma, EPS, self.total, self.x,
                       self.xs, None, T, H, "bf16", "e4m3")
         self.ids, self.w = self.choose(dequantise(self.x, self.xs, 1))
-        ar.ar_moe_route(self.ids, T, K, self.E, self.offsets, self.row_of, ids_bytes=8)
+        ar.ar_moe_route(self.ids, T, K, self.E, self.offsets, self.row_of)
         ar.ar_moe_dispatch(self.x, self.xs, self.row_of, self.rows, self.rs, n, T, K, H, "e4m3")
         ar.ar_matmul8(self.rows, self.rs, *self.up, self.offsets, self.E, self.hidden, n,
                       2 * self.I, H, "bf16")
@@ -132,7 +132,7 @@ class Layer:
         normed, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
         ar.ar_rmsnorm(x, None, self.gamma, EPS, None, normed, None, rstd, T, H, "bf16")
         ids, w = self.choose(normed.float())
-        ar.ar_moe_route(ids, T, K, E, self.offsets, self.row_of, ids_bytes=8)
+        ar.ar_moe_route(ids, T, K, E, self.offsets, self.row_of)
         rows, y, out = torch.empty(n, H, dtype=x.dtype, device="cuda"), torch.empty(
             n, H, dtype=x.dtype, device="cuda"), torch.empty_like(x)
         ar.ar_moe_dispatch(normed, None, self.row_of, rows, None, n, T, K, H, "bf16")

@@ -31,3 +31,39 @@ def test_pairs_are_taken_up_to_the_stated_limit(K):
         assert _code(ar.ar_moe_return, None, 8, A[0], None, A[1], T, K, 64, "bf16") == code
         assert _code(ar.ar_moe_return_grad, None, A[0], 8, A[1], None, A[2], None, T, K, 64,
                      "bf16") == code
+
+
+class _Recorder:
+    """Stands in for the extension module; keeps what a call was given."""
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.args = args
+            return ar.AR_OK
+        return call
+
+
+class _Ids:
+    def __init__(self, size):
+        self.size = size
+
+    def data_ptr(self):
+        return A[0]
+
+    def element_size(self):
+        return self.size
+
+
+@pytest.mark.parametrize("ids,given,want", [
+    (_Ids(8), {}, 8), (_Ids(4), {}, 4), (_Ids(2), {}, 2), (_Ids(8), dict(ids_bytes=4), 4),
+    (A[0], {}, 4), (A[0], dict(ids_bytes=8), 8), (None, {}, 4)])
+def test_route_takes_the_width_of_its_ids(monkeypatch, ids, given, want):
+    """A tensor's own element size, 4 for an address, and always what the caller says."""
+    calls = _Recorder()
+    monkeypatch.setattr(ar, "_calls", calls)
+    ar.ar_moe_route(ids, 16, 8, 64, A[1], A[2], stream=0, **given)
+    assert calls.args[0] is ids and calls.args[1] == want
+
+
+def test_route_refuses_ids_of_another_width():
+    assert _code(ar.ar_moe_route, _Ids(2), 16, 8, 64, A[1], A[2]) == ar.AR_ERR_INVALID
