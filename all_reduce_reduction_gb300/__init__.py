@@ -2,19 +2,22 @@
 
 This module is a thin ctypes binding of the C ABI declared in
 ``include/ar.h`` (library ``libar_gb300.so``, built in-tree by
-``all_reduce_reduction_gb300.build``), but for the layer operators, which call it
-through a small extension module.  Every function has the name of the C
-entry point it calls and only marshals arguments: device buffers may be given
-as integers (device addresses) or as objects with ``data_ptr()`` (torch CUDA
-tensors); a stream as an integer ``cudaStream_t``, an object with
-``cuda_stream`` (``torch.cuda.Stream``), or ``None`` for torch's current
-stream.  All work runs in the library's CUDA kernels; there is no CPU path.
+``all_reduce_reduction_gb300.build``), but for the layer operators, which call
+it through a small extension module (through ctypes too where that was not
+built).  Every function has the name of the C entry point it calls and only
+marshals arguments: device buffers may be given as integers (device addresses)
+or as objects with ``data_ptr()`` (torch CUDA tensors); a stream as an integer
+``cudaStream_t``, an object with ``cuda_stream`` (``torch.cuda.Stream``), or
+``None`` for torch's current stream.  All work runs in the library's CUDA
+kernels; there is no CPU path.
 If the library is missing, the first call raises ``RuntimeError``.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import sysconfig
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -432,20 +435,49 @@ def ar_plan_destroy(p: int) -> None:
 # through an extension module that converts their arguments itself (one row of
 # ar_rmsnorm: 3.1 us of conversion with ctypes, 1 with it).
 
-_calls = None                  # the extension module _native
+_calls = None                  # the extension module _native, or what stands in for it
+# the running interpreter's own
+_NATIVE_PATH = os.path.join(HERE, "_native" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+class _CtypesCalls:
+    """The extension module's calls through ctypes, for an interpreter without it
+    (no Python.h when the library was built).  One row of ar_rmsnorm takes 8.1 us a
+    call so, 3.9 with the module."""
+
+    def __getattr__(self, name):
+        fn, kinds = getattr(load_library(), name), SIGNATURES[name][0]
+        whole = {_SZ: (0, 1 << 64), _I: (-1 << 31, 1 << 31)}
+
+        def call(*args):
+            if len(args) != len(kinds):
+                raise TypeError("%d arguments expected, %d given" % (len(kinds), len(args)))
+            given = []
+            for a, kind in zip(args[:-1], kinds):
+                if kind in whole and not whole[kind][0] <= a < whole[kind][1]:
+                    raise OverflowError("argument does not fit the C type")
+                given.append(_ptr(a) if kind is _VP else a)
+            try:
+                return fn(*given, _stream(args[-1]))
+            except ctypes.ArgumentError as e:
+                raise TypeError(str(e)) from None
+        setattr(self, name, call)
+        return call
 
 
 def _layer_calls():
-    """The extension module, loaded with the library.  Raises if it is absent."""
+    """The extension module, loaded with the library."""
     global _calls
     load_library()
     if _calls is None:
-        try:
-            from . import _native
-        except ImportError as e:
-            raise RuntimeError("the extension module _native is not built; run `python -c "
-                               "'import __graft_entry__ as g; g.build()'`") from e
-        _calls = _native
+        if os.path.exists(_NATIVE_PATH):
+            name = __name__ + "._native"
+            spec = importlib.util.spec_from_file_location(name, _NATIVE_PATH)
+            calls = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(calls)
+            _calls = calls
+        else:
+            _calls = _CtypesCalls()
     return _calls
 
 

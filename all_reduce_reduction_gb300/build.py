@@ -1,10 +1,11 @@
 """Build the CUDA library ``libar_gb300.so`` in-tree, for sm_103a only.
 
 Each ``csrc/*.cu`` file is compiled by its own nvcc process (in parallel),
-then the objects are linked into one shared library next to this file, and the
-extension module ``_native`` (``csrc/ar_python.c``) beside it against that
-library.  A rebuild happens only when a source or header is newer than what was
-built.
+then the objects are linked into one shared library next to this file.  The
+extension module ``_native`` (``csrc/ar_python.c``) is built beside it against
+that library for the running interpreter, whose tag is in its file name; without
+Python's headers it is left out.  A rebuild happens only when a source or header
+is newer than what was built.
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libar_gb300.so")
-NATIVE = os.path.join(HERE, "_native.so")
+NATIVE = os.path.join(HERE, "_native" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 NATIVE_SOURCE = os.path.join(CSRC, "ar_python.c")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,10 +46,12 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _newest_input() -> float:
-    files = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-    files += glob.glob(os.path.join(INCLUDE, "*.h")) + [NATIVE_SOURCE, os.path.abspath(__file__)]
-    return max(os.path.getmtime(f) for f in files)
+def _newest(files: list[str]) -> float:
+    return max(os.path.getmtime(f) for f in [*files, os.path.abspath(__file__)])
+
+
+def _fresh(built: str, newest: float) -> bool:
+    return os.path.exists(built) and os.path.getmtime(built) >= newest
 
 
 def _compile(src: str, extra: list[str]) -> str:
@@ -63,21 +66,30 @@ def _compile(src: str, extra: list[str]) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link the library if needed; returns its path."""
-    newest = _newest_input()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest
-                         for f in (LIB, NATIVE)):
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-    _link(LIB, [*objs, "-lcudart"])
-    _link(NATIVE, ["-O2", "-Xcompiler", "-fPIC,-Wall,-Wextra", "-I" + INCLUDE,
-                   "-I" + sysconfig.get_paths()["include"], NATIVE_SOURCE, "-L" + HERE,
-                   "-lar_gb300", "-Xlinker", "-rpath=$ORIGIN", "-cudart", "none"])
+    """Compile and link what is needed; returns the library's path."""
+    headers = glob.glob(os.path.join(INCLUDE, "*.h"))
+    private = [f for end in ("*.h", "*.cuh") for f in glob.glob(os.path.join(CSRC, end))]
+    if force or not _fresh(LIB, _newest(sources() + headers + private)):
+        os.makedirs(BUILD, exist_ok=True)
+        extra = ["-Xptxas", "-v"] if verbose_ptxas else []
+        srcs = sources()
+        with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+            objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        _link(LIB, [*objs, "-lcudart"])
+    if force or not _fresh(NATIVE, _newest([NATIVE_SOURCE, *headers])):
+        _build_native()
     return LIB
+
+
+def _build_native() -> None:
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        sys.stderr.write("no Python.h in %s: the layer operators are called through ctypes, a few "
+                         "us a call more\n" % include)
+        return
+    _link(NATIVE, ["-O2", "-Xcompiler", "-fPIC,-Wall,-Wextra", "-I" + INCLUDE, "-I" + include,
+                   NATIVE_SOURCE, "-L" + HERE, "-lar_gb300", "-Xlinker", "-rpath=$ORIGIN",
+                   "-cudart", "none"])
 
 
 def _link(out: str, args: list[str]) -> None:

@@ -1,5 +1,9 @@
 """The host side of the layer operators, on the CPU: limits, and what the binding
 makes of its arguments.  No call here launches anything."""
+import os
+import sys
+import sysconfig
+
 import pytest
 
 import all_reduce_reduction_gb300 as ar
@@ -67,3 +71,47 @@ def test_route_takes_the_width_of_its_ids(monkeypatch, ids, given, want):
 
 def test_route_refuses_ids_of_another_width():
     assert _code(ar.ar_moe_route, _Ids(2), 16, 8, 64, A[1], A[2]) == ar.AR_ERR_INVALID
+
+
+def test_the_module_names_its_interpreter():
+    """One built for another interpreter is neither fresh nor loaded."""
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert cuda_build.NATIVE.endswith("_native" + suffix) and suffix != ".so"
+    assert ar._layer_calls().__file__ == cuda_build.NATIVE
+
+
+@pytest.fixture
+def no_headers(monkeypatch, tmp_path):
+    """A machine without Python's headers, where no module was built."""
+    monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    monkeypatch.setattr(cuda_build, "NATIVE", str(tmp_path / "_native.so"))
+    monkeypatch.setattr(ar, "_calls", None)
+    monkeypatch.setattr(ar, "_NATIVE_PATH", str(tmp_path / "_native.so"), raising=False)
+    monkeypatch.delitem(sys.modules, ar.__name__ + "._native", raising=False)
+
+
+def test_the_library_builds_without_python_headers(no_headers, capfd):
+    before = os.path.getmtime(cuda_build.LIB)
+    assert cuda_build.build() == cuda_build.LIB
+    assert not os.path.exists(cuda_build.NATIVE) and "Python.h" in capfd.readouterr().err
+    assert os.path.getmtime(cuda_build.LIB) == before        # which was up to date
+
+
+def test_the_calls_without_the_module(no_headers):
+    """Through ctypes: the same answers and refusals."""
+    assert _code(ar.ar_rmsnorm, A[0], None, None, 1e-6, None, A[1], None, None, 0, 64,
+                 "bf16") == ar.AR_OK
+    assert _code(ar.ar_rmsnorm, None, None, None, 1e-6, None, A[1], None, None, 1, 64,
+                 "bf16") == ar.AR_ERR_INVALID
+    assert _code(ar.ar_moe_route, _Ids(2), 16, 8, 64, A[1], A[2]) == ar.AR_ERR_INVALID
+    assert _code(ar.ar_matmul8, A[0], A[1], A[2], A[3], None, 1, A[4], 0, 64, 64,
+                 "bf16") == ar.AR_OK
+    for bad in (dict(T=-1), dict(T=1.5), dict(H=2 ** 64), dict(dtype=2 ** 31), dict(x="text"),
+                dict(stream="x"), dict(eps="x")):
+        a = dict(x=A[0], res=None, gamma=None, eps=1e-6, total=None, y=A[1], scale=None, rstd=None,
+                 T=0, H=64, dtype="bf16", stream=0) | bad
+        with pytest.raises((TypeError, ValueError, OverflowError, AttributeError)):
+            ar.ar_rmsnorm(**a)
+    with pytest.raises(TypeError):
+        ar._layer_calls().ar_moe_route(0, 4)
+    assert "_native" not in [m.split(".")[-1] for m in sys.modules if m.startswith(ar.__name__)]
