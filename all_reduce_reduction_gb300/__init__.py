@@ -556,7 +556,9 @@ def ar_moe_return_grad(dout, rows, nrows: int, row_of, w, drows, dw, T: int, K: 
 def ar_matmul8(a, sa, b, sb, offsets, E: int, d, M: int, N: int, K: int, out_dtype,
                lda: int = 0, ldb: int = 0, ldd: int = 0, status=None, stream=None) -> None:
     """Product of E4M3 rows with E4M3 weights and their scales per block of
-    128, for one matrix (``offsets`` None) or grouped by expert."""
+    128, for one matrix (``offsets`` None) or grouped by expert.  ``status``: an
+    int32 word on the device, 0 before; a product whose wait ran out puts
+    AR_ERR_TIMEOUT there and leaves ``d`` unfinished, which nothing else tells."""
     calls = _calls or _layer_calls()
     rc = calls.ar_matmul8(a, lda, sa, b, ldb, sb, offsets, E, d, ldd, M, N, K,
                           DTYPES8.get(out_dtype, out_dtype), status, stream)

@@ -82,6 +82,7 @@ class Layer:
         self.rows, self.rs = torch.zeros(n, H, **e4m3), torch.zeros(n, blocks(H), device="cuda")
         self.hidden = torch.zeros(n, 2 * inner, **bf16)
         self.y = torch.zeros(n, H, **bf16)
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")   # of the products
         self.handle = ar.Handle(ranks, T * H, "bf16")
 
     def choose(self, normed: torch.Tensor):
@@ -98,13 +99,21 @@ class Layer:
         ar.ar_moe_route(self.ids, T, K, self.E, self.offsets, self.row_of)
         ar.ar_moe_dispatch(self.x, self.xs, self.row_of, self.rows, self.rs, n, T, K, H, "e4m3")
         ar.ar_matmul8(self.rows, self.rs, *self.up, self.offsets, self.E, self.hidden, n,
-                      2 * self.I, H, "bf16")
+                      2 * self.I, H, "bf16", status=self.status)
         gate, value = self.hidden.float().chunk(2, 1)
         act, act_scale = quantise(torch.nn.functional.silu(gate) * value, 1)
         ar.ar_matmul8(act, act_scale, *self.down, self.offsets, self.E, self.y, n, H, self.I,
-                      "bf16")
+                      "bf16", status=self.status)
         ar.ar_moe_return(self.y, n, self.row_of, self.w, self.out, T, K, H, "bf16")
         return self.out
+
+    def check(self) -> None:
+        """Raises if a product or the all-reduce gave up: the step's output is unfinished
+        then.  Waits for the device, so a program calls it where it reads its results."""
+        for what, status in (("ar_matmul8", int(self.status)),
+                             ("ar_allreduce_n", ar.ar_status(self.handle.h))):
+            if status != ar.AR_OK:
+                raise ar.ArError(status, what)
 
     def serve_plain(self) -> torch.Tensor:
         """The same layer in plain torch, binary32, from the codes and choices of serve()."""
@@ -181,6 +190,7 @@ def main() -> None:
     torch.cuda.set_device(0)
     layer = Layer(a.tokens, a.hidden, a.inner, a.experts, a.top, a.ranks)
     out = layer.serve()
+    layer.check()
     print("serving step against plain torch: %.2e off (the activations' E4M3 rounding between "
           "the products is in it)" % off(out, layer.serve_plain()))
     begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
@@ -191,6 +201,7 @@ def main() -> None:
         layer.serve()
     end.record()
     end.synchronize()
+    layer.check()
     print("serving step, %d tokens: %.1f us" % (a.tokens, begin.elapsed_time(end) / 20 * 1e3))
     for name, (got, want) in layer.train().items():
         print("training step, %s: %.2e off" % (name, off(got, want)))

@@ -716,7 +716,9 @@ int ar_moe_return_grad(const void *dout, size_t lddout, const void *rows, size_t
  *   d:  M x N of out_dtype (enum ar_dtype).
  *   status: a device word that holds 0, or NULL.  Every wait inside the kernel
  *       is bounded; one that ran out (none is known to) writes AR_ERR_TIMEOUT
- *       there.
+ *       there and leaves d unfinished.  Without the word nothing tells of it, so
+ *       a caller that uses d passes one and reads it with its results; one word
+ *       serves any number of calls.
  * 16-byte aligned a and b with lda and ldb multiples of 16 take the tensor-core
  * kernels, any other the general one.  M, N, K < 2^31 - 256;
  * E <= AR_MOE_MAX_EXPERTS.  The input gradient is the same product with the
