@@ -102,6 +102,14 @@ __device__ __forceinline__ void drain_loads(uint32_t full, uint32_t issued, uint
         mbar_drain(full + 8 * (k % stages), (k / stages) & 1);
 }
 
+// The same where the loads are counted by a barrier of the other CTA, which this one
+// cannot wait on: far longer than any load takes.
+__device__ __forceinline__ void linger() {
+    const uint64_t deadline = globaltimer_ns() + 1000000ull;
+    while (globaltimer_ns() < deadline) {
+    }
+}
+
 // Tile of a tensor map into shared memory; x is a byte offset along k, a
 // multiple of 128.
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
@@ -621,8 +629,12 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
     __syncthreads();
     fence_after();
     if (*abort) {
-        if (threadIdx.x == kRowsEpilogueWarps * 32 && rank == 0)
-            drain_loads(full, used, kRowsStages);
+        if (threadIdx.x == kRowsEpilogueWarps * 32) {
+            if (rank == 0)
+                drain_loads(full, used, kRowsStages);
+            else
+                linger();
+        }
         if (warp == kRowsEpilogueWarps + 1 && rank == 0 && elect_one()) {
             mma_pair_commit(smem_addr(&sh.drain));
             mbar_drain(smem_addr(&sh.drain), 0);
