@@ -1,6 +1,7 @@
 """The layer operators called as a program calls them: with tensors alone."""
 import os
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -50,3 +51,88 @@ def test_the_example_reads_what_its_products_report(monkeypatch):
         layer.check()
     assert e.value.code == ar.AR_ERR_TIMEOUT
     layer.close()
+
+
+def _every_call(T=64, K=2, E=4, H=256):
+    """(calls without a stream, the tensors that they write)."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+    n, kb = T * K, H // 128
+    x, res, gamma = normal(T, H), normal(T, H), normal(H)
+    ids = torch.topk(normal(T, E), K, dim=1).indices
+    w, weights = torch.rand(T, K, generator=g, device="cuda"), normal(E * H, H).mul_(50)
+    weights = weights.to(torch.float8_e4m3fn)
+    sb = torch.rand(E, kb, kb, generator=g, device="cuda")
+    out = {k: torch.zeros(*s, device="cuda") for k, s in dict(
+        total=(T, H), scale=(T, kb), rstd=(T,), dx=(T, H), dgamma=(H,), work=(T * H,),
+        rscale=(n, kb), y=(n, H), out=(T, H), drows=(n, H), dw=(T, K)).items()}
+    out |= {k: torch.zeros(*s, dtype=torch.int32, device="cuda") for k, s in dict(
+        offsets=(E + 1,), row_of=(T, K), src=(n,), status=(1,)).items()}
+    out |= {k: torch.zeros(s, H, device="cuda").to(torch.float8_e4m3fn) for k, s in
+            (("codes", T), ("rows", n))}
+    o = out
+
+    def calls():
+        ar.ar_rmsnorm(x, res, gamma, 1e-6, o["total"], o["codes"], o["scale"], o["rstd"], T, H,
+                      "fp32", "e4m3")
+        ar.ar_moe_route(ids, T, K, E, o["offsets"], o["row_of"], o["src"])
+        ar.ar_moe_dispatch(o["codes"], o["scale"], o["row_of"], o["rows"], o["rscale"], n, T, K, H,
+                           "e4m3")
+        ar.ar_matmul8(o["rows"], o["rscale"], weights, sb, o["offsets"], E, o["y"], n, H, H,
+                      "fp32", status=o["status"])
+        ar.ar_moe_return(o["y"], n, o["row_of"], w, o["out"], T, K, H, "fp32")
+        ar.ar_moe_return_grad(o["out"], o["y"], n, o["row_of"], w, o["drows"], o["dw"], T, K, H,
+                              "fp32")
+        ar.ar_rmsnorm_grad(o["out"], None, o["total"], gamma, o["rstd"], o["dx"], o["dgamma"],
+                           o["work"], 4 * T * H, T, H, "fp32")
+    return calls, out
+
+
+def _bits(out):
+    return {k: t.view(torch.uint8).clone() for k, t in out.items() if k != "work"}
+
+
+def test_calls_without_a_stream_take_the_current_one():
+    """Captured on a side stream (anything launched elsewhere would end the capture), and
+    from a thread with a stream of its own."""
+    need_gpu()
+    calls, out = _every_call()
+    calls()
+    torch.cuda.synchronize()
+    want = _bits(out)
+    assert int(out["status"]) == 0 and float(out["dw"].abs().sum()) > 0
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        assert ar._current_stream() == side.cuda_stream
+    with torch.cuda.graph(graph, stream=side):
+        calls()
+    for t in out.values():
+        t.view(torch.uint8).zero_()
+    torch.cuda.synchronize()
+    assert float(out["dw"].abs().sum()) == 0                 # captured, not run
+    graph.replay()
+    torch.cuda.synchronize()
+    got = _bits(out)
+    assert all(torch.equal(got[k], want[k]) for k in want)
+
+    seen = []
+
+    def other():
+        own = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=own, capture_error_mode="thread_local"):
+            calls()
+        seen.append((ar._current_stream() == torch.cuda.current_stream().cuda_stream, g))
+    thread = threading.Thread(target=other)
+    thread.start()
+    thread.join()
+    assert seen and seen[0][0]
+    for t in out.values():
+        t.view(torch.uint8).zero_()
+    seen[0][1].replay()
+    torch.cuda.synchronize()
+    got = _bits(out)
+    assert all(torch.equal(got[k], want[k]) for k in want)
