@@ -529,14 +529,17 @@ static cudaError_t norm_grad_units(const NormGradArgs &a, cudaStream_t s, int *p
     // With the ring, two CTAs an SM (8192 x 8192 bf16: 96 us; one CTA 120, without
     // the ring 124).  Rows that fill half a CTA or less go side by side
     // (32768 x 1024: 57 us; one a CTA 195).
-    if (WIDE && units <= 512)
-        return norm_grad_form<DT, WIDE, kGroups, 2, 512, 2, WIDE>(a, 304, s, partial);
-    if (WIDE && units <= 1024)
-        return norm_grad_form<DT, WIDE, kOneRow, 2, 512, 2, WIDE>(a, 304, s, partial);
-    if (units <= 512)
-        return norm_grad_form<DT, WIDE, kGroups, 4, 256, 2, false>(a, 304, s, partial);
-    if (units <= 1024)
-        return norm_grad_form<DT, WIDE, kOneRow, 4, 256, 2, false>(a, 304, s, partial);
+    if constexpr (WIDE) {
+        if (units <= 512)
+            return norm_grad_form<DT, WIDE, kGroups, 2, 512, 2, true>(a, 304, s, partial);
+        if (units <= 1024)
+            return norm_grad_form<DT, WIDE, kOneRow, 2, 512, 2, true>(a, 304, s, partial);
+    } else {
+        if (units <= 512)
+            return norm_grad_form<DT, WIDE, kGroups, 4, 256, 2, false>(a, 304, s, partial);
+        if (units <= 1024)
+            return norm_grad_form<DT, WIDE, kOneRow, 4, 256, 2, false>(a, 304, s, partial);
+    }
     return norm_grad_form<DT, WIDE, kOneRow, 4, 512, 1, false>(a, 152, s, partial);
 }
 
