@@ -26,9 +26,6 @@ namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
 }
@@ -143,21 +140,11 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap *map
         :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
-// This place of shared memory in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 // Arrival at a barrier of either CTA.  It hands over tensor memory that has been
 // read, which tcgen05.fence orders; nothing in ordinary memory goes with it, so
 // it needs no wider release (at cluster scope that doubled the kernel's time).
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---- tcgen05 -------------------------------------------------------------------
@@ -426,7 +413,7 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
             sh.tiles = base;
     }
     fence_before();
-    cluster_barrier();                            // both CTAs' barriers are ready
+    cluster_sync();                               // both CTAs' barriers are ready
     fence_after();
     const uint32_t tmem = sh.tmem;
     const uint32_t ntiles = (a.N + kRowsN - 1) / kRowsN;
@@ -442,7 +429,7 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
                     if (turn > 0 && !mbar_wait(empty + 8 * s, (turn - 1) & 1, abort, a.status))
                         break;
                     const uint32_t at = smem_addr(stages) + s * kRowsStage;
-                    const uint32_t bar = peer_addr(full + 8 * s, 0);
+                    const uint32_t bar = map_to_rank(full + 8 * s, 0);
                     // a tile of at most 128 rows leaves the second CTA's rows
                     // of a alone: their sums are not stored
                     const bool both = t.rows > kRowsHalf;
@@ -561,7 +548,7 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
         // A warp takes one half of every block.  Columns 0-63 of a half are rows
         // 64 * half, ... of the first CTA's b, columns 64-127 of the second's.
         const int quarter = warp & 3, half = warp >> 2;
-        const uint32_t empty_bar = peer_addr(acc_empty, 0);
+        const uint32_t empty_bar = map_to_rank(acc_empty, 0);
         const uint32_t lanes = tmem + ((uint32_t)quarter * 32 << 16);
         const uint32_t in = quarter * 32 + lane;
         uint32_t blocks = 0, slots = 0;
@@ -641,7 +628,7 @@ k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUt
         }
         __syncthreads();
     }
-    cluster_barrier();                            // nothing of the pair is in flight
+    cluster_sync();                               // nothing of the pair is in flight
     if (warp == kRowsEpilogueWarps + 1)
         tmem_free<512, true>(tmem);
 }
@@ -678,7 +665,7 @@ template <int NT> constexpr size_t few_smem() {
 __device__ __forceinline__ float ld_peer_f32(uint32_t local, uint32_t rank) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                 : "=f"(v) : "r"(peer_addr(local, rank)) : "memory");
+                 : "=f"(v) : "r"(map_to_rank(local, rank)) : "memory");
     return v;
 }
 
@@ -895,7 +882,7 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
 #pragma unroll
         for (int c = 0; c < NT; ++c)
             sums[c * 128 + threadIdx.x] = acc[c];
-    cluster_barrier();
+    cluster_sync();
     // (the loads of kAt rows from every CTA are in flight together: one after
     // the other they cost 0.5 us each, 14 us for 1000 x 1000 x 1000)
     constexpr int kAt = 4;
@@ -922,7 +909,7 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                     store_out(a.d + (uint64_t)(row + c) * a.ldd, n, sum, a.out);
             }
         }
-    cluster_barrier();
+    cluster_sync();
 }
 
 // ---- host ---------------------------------------------------------------------

@@ -37,15 +37,10 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t ld_peer_u32(const void *p, uint32_t rank) {
-    const uint32_t local = (uint32_t)__cvta_generic_to_shared(p);
-    uint32_t remote, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                 : "=r"(v) : "r"(map_to_rank(smem_addr(p), rank)) : "memory");
     return v;
 }
 
@@ -119,7 +114,7 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
         }
         total[e] = sum;
     }
-    cluster_barrier();
+    cluster_sync();
     // over the CTAs, then over the experts
     uint32_t carry = 0u;
     for (int e0 = 0; e0 < E1; e0 += blockDim.x) {
@@ -161,7 +156,7 @@ __global__ void __launch_bounds__(1024) k_moe_route(const __grid_constant__ Rout
         }
         __syncthreads();
     }
-    cluster_barrier();                                // every peer has read `total`
+    cluster_sync();                                   // every peer has read `total`
     auto put = [&](uint32_t p, int e, uint32_t row) {
         if (e < 0)
             return;
@@ -508,14 +503,14 @@ k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
                         a.dw[t * a.K + k0 + j] = v;
                 }
                 if (ctas > 1) {
-                    cluster_barrier();
+                    cluster_sync();
                     if (rank == 0 && threadIdx.x < 8 && k0 + (int)threadIdx.x < a.K) {
                         float v = 0.0f;
                         for (uint32_t c = 0; c < ctas; ++c)
                             v += __uint_as_float(ld_peer_u32(sums + threadIdx.x, c));
                         a.dw[t * a.K + k0 + threadIdx.x] = v;
                     }
-                    cluster_barrier();
+                    cluster_sync();
                 } else {
                     __syncthreads();
                 }
