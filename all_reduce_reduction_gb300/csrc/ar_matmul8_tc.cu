@@ -943,21 +943,6 @@ bool encode(CUtensorMap *map, const void *base, uint64_t k, uint64_t rows, uint6
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// SMs of the current device (asked once per device).
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0)
-        return 0;
-    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0)
-        return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    if (dev < 64)
-        known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 template <int NT>
 cudaError_t launch_few(const MatmulArgs &a, int parts, cudaStream_t s) {
     CUtensorMap ma, mb;

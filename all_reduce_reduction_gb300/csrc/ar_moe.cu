@@ -525,7 +525,7 @@ static cudaError_t return_grad_launch(const ReturnGradArgs &a, cudaStream_t s) {
     const int threads = (int)(units < 256 ? units : 256);
     // few tokens: as many CTAs a token as its units or half the SMs allow
     int ctas = 1;
-    while (ctas < 8 && units >= 512u * ctas && a.T * ctas * 2 <= 152)
+    while (ctas < 8 && units >= 512u * ctas && a.T * ctas * 2 <= (uint64_t)sm_count())
         ctas *= 2;
     const uint64_t grid = a.T * ctas, most = 1u << 30;
     cudaLaunchConfig_t cfg = {};
@@ -545,7 +545,9 @@ static cudaError_t return_grad_launch(const ReturnGradArgs &a, cudaStream_t s) {
 }
 
 template <int DT, bool WIDE> static cudaError_t return_launch(const ReturnArgs &a, cudaStream_t s) {
-    const uint64_t units = Rows<DT, WIDE>::units(a.H), most = 152 * 3;
+    const uint64_t units = Rows<DT, WIDE>::units(a.H), most = 3 * (uint64_t)sm_count();
+    if (most < 1)
+        return cudaErrorUnknown;
     const bool flat = units < 256;
     const uint64_t jobs = flat ? (a.T * units + 255) / 256 : a.T * ((units + 255) / 256);
     const int grid = (int)(jobs < most ? jobs : most);

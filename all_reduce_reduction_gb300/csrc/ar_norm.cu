@@ -37,8 +37,10 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 constexpr float kLeastBlock = 0x1p-96f;
 constexpr float kTopE4M3 = 448.0f;
 
-// More units than this are many: a thread for each no longer fits the SMs at once.
-constexpr uint64_t kNormManyUnits = 152 * 1024;
+// Whether a thread for each unit no longer fits the SMs at once.
+static bool many_units(uint64_t rows, uint32_t units) {
+    return rows > (uint64_t)sm_count() * 1024 / units;
+}
 
 // The unit's share of y in 8 bits, and its block's scale.  Called by whole warps.
 // Both quotients are products with a rounded reciprocal: correctly rounded
@@ -198,7 +200,7 @@ static cudaError_t norm_units(const NormArgs &a, cudaStream_t s) {
     // thread for each, for latency (1000 x 1024: 3.9 us; four a thread 5.6).  Short
     // rows go eight to a CTA, one a warp (65536 x 512: 60 us; one a CTA 68; 4000 x
     // 100: 3.7 and 5.2; but 32768 x 1024: 46 and 41).
-    const bool many = a.T > kNormManyUnits / units;
+    const bool many = many_units(a.T, units);
     if (units <= 64 && a.T > 1024)
         return launch_kernel(k_rmsnorm<DT, WIDE, E4M3, kWarpRow, 4, 256, 4>, grid(8), 256, 0, s,
                              true, a);
@@ -520,27 +522,32 @@ static cudaError_t norm_grad_units(const NormGradArgs &a, cudaStream_t s, int *p
     // with the ring 6.3; 300 x 4096: 7.1 and 10.9).
     // Units of eight elements need twice the registers, so two of them a thread.
     constexpr int kUnits = Rows<DT, WIDE>::E / 4, kThreads = 1024 / kUnits;
-    if (a.T <= kNormManyUnits / units && units <= 1024)
+    const bool few = !many_units(a.T, units);
+    if (few && units <= 1024)
         return norm_grad_form<DT, WIDE, kOneRow, kUnits, kThreads, 1, false>(a, AR_NORM_GRAD_ROWS,
                                                                               s, partial);
-    if (a.T <= kNormManyUnits / units && units <= 2048)
+    if (few && units <= 2048)
         return norm_grad_form<DT, WIDE, kOneRow, 2 * kUnits, kThreads, 1, false>(
             a, AR_NORM_GRAD_ROWS, s, partial);
+    // One or two CTAs an SM, each with a row of partial sums.
+    const int sms = sm_count(), most = 2 * sms < AR_NORM_GRAD_ROWS ? 2 * sms : AR_NORM_GRAD_ROWS;
+    if (sms < 1)
+        return cudaErrorUnknown;
     // With the ring, two CTAs an SM (8192 x 8192 bf16: 96 us; one CTA 120, without
     // the ring 124).  Rows that fill half a CTA or less go side by side
     // (32768 x 1024: 57 us; one a CTA 195).
     if constexpr (WIDE) {
         if (units <= 512)
-            return norm_grad_form<DT, WIDE, kGroups, 2, 512, 2, true>(a, 304, s, partial);
+            return norm_grad_form<DT, WIDE, kGroups, 2, 512, 2, true>(a, most, s, partial);
         if (units <= 1024)
-            return norm_grad_form<DT, WIDE, kOneRow, 2, 512, 2, true>(a, 304, s, partial);
+            return norm_grad_form<DT, WIDE, kOneRow, 2, 512, 2, true>(a, most, s, partial);
     } else {
         if (units <= 512)
-            return norm_grad_form<DT, WIDE, kGroups, 4, 256, 2, false>(a, 304, s, partial);
+            return norm_grad_form<DT, WIDE, kGroups, 4, 256, 2, false>(a, most, s, partial);
         if (units <= 1024)
-            return norm_grad_form<DT, WIDE, kOneRow, 4, 256, 2, false>(a, 304, s, partial);
+            return norm_grad_form<DT, WIDE, kOneRow, 4, 256, 2, false>(a, most, s, partial);
     }
-    return norm_grad_form<DT, WIDE, kOneRow, 4, 512, 1, false>(a, 152, s, partial);
+    return norm_grad_form<DT, WIDE, kOneRow, 4, 512, 1, false>(a, most / 2, s, partial);
 }
 
 template <int DT>

@@ -257,6 +257,21 @@ inline bool wide(const Matrix &m, size_t align = 16) {
 
 inline bool float_dtype(int d) { return d == AR_BF16 || d == AR_FP16 || d == AR_FP32; }
 
+// SMs of the current device (asked once per device); 0 if it does not answer.
+inline int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0)
+        return 0;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0)
+        return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    if (dev < 64)
+        known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Opts a kernel in to `bytes` of dynamic shared memory, once per kernel and
 // device: asking the runtime every time costs a launch 0.5 us.
 template <auto KERNEL> inline cudaError_t opt_in_smem(size_t bytes) {
