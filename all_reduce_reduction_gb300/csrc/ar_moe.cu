@@ -687,6 +687,8 @@ int ar_moe_return_grad(const void *dout, size_t lddout, const void *rows, size_t
         return AR_OK;
     if (!dout || !row_of || (dw && !rows && nrows > 0))
         return AR_ERR_INVALID;
+    if (!dw)
+        rows = nullptr;                       // not read
     const size_t esz = elem_size(dtype);
     const Matrix mo = matrix(dout, lddout, T, H, esz), mr = matrix(rows, ldrows, nrows, H, esz);
     const Matrix md = matrix(drows, lddrows, nrows, H, esz);

@@ -121,3 +121,19 @@ def test_one_row_in_place_has_no_stride(H):
     ar.ar_rmsnorm(x, res, None, 1e-6, s, y, None, None, 1, H, "bf16")
     ar.ar_rmsnorm(x, res, None, 1e-6, res, x, None, None, 1, H, "bf16", ldx=H + 8, ldsum=H + 16)
     assert torch.equal(s, res) and torch.equal(y, x)
+
+
+def test_rows_are_no_operand_without_dw():
+    """The return's gradient does not read rows then: drows may lie across them, and
+    their alignment is nothing to it."""
+    need_gpu()
+    T, K, H = 9, 2, 72
+    dout, w = _rand(1, T, H, "bf16"), torch.rand(T, K).cuda()
+    row_of = torch.randperm(T * K, generator=torch.Generator().manual_seed(1)).int().cuda()
+    want = torch.zeros(T * K, H, dtype=torch.bfloat16, device="cuda")
+    ar.ar_moe_return_grad(dout, None, T * K, row_of, w, want, None, T, K, H, "bf16")
+    drows = torch.zeros_like(want)
+    for rows in (drows.data_ptr() + 16, drows.data_ptr() + 1):
+        drows.zero_()
+        ar.ar_moe_return_grad(dout, rows, T * K, row_of, w, drows, None, T, K, H, "bf16")
+        assert torch.equal(drows, want)
