@@ -231,28 +231,6 @@ __device__ __forceinline__ void kernel_prologue() {
 }
 
 // ---------------------------------------------------------------------------
-// Shared memory and clusters.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-// Address of the same shared-memory location in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t local, uint32_t rank) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    return remote;
-}
-
-// Cluster-wide barrier (all threads of its CTAs); the warp is reconverged
-// first because the .aligned form needs every lane at the same instruction.
-__device__ __forceinline__ void cluster_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// ---------------------------------------------------------------------------
 // Errors and bounded waits.
 // ---------------------------------------------------------------------------
 

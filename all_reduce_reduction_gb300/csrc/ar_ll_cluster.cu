@@ -37,6 +37,17 @@
 
 namespace ar {
 
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// Address of the same shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t local, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    return remote;
+}
+
 __device__ __forceinline__ void st_cluster_pkt2(uint32_t addr, uint64_t a, uint64_t b) {
     asm volatile("st.relaxed.cluster.shared::cluster.v2.u64 [%0], {%1, %2};"
                  :: "r"(addr), "l"(a), "l"(b) : "memory");
@@ -53,6 +64,14 @@ __device__ __forceinline__ uint64_t ld_local_pkt(uint32_t addr) {
     asm volatile("ld.relaxed.cluster.shared::cta.u64 %0, [%1];" : "=l"(a) : "r"(addr) : "memory");
     return a;
 }
+// Cluster-wide barrier (all threads of all R CTAs); the warp is reconverged
+// first because the .aligned form needs every lane at the same instruction.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Poll until the packet pair at a local shared address carries `want`.
 __device__ __forceinline__ bool poll_local2(Poller &w, uint32_t addr, uint32_t want, uint64_t &a,
                                             uint64_t &b) {

@@ -19,6 +19,7 @@
 
 #include <atomic>
 
+#include "ar_cluster.cuh"
 #include "ar_matmul8.cuh"
 
 namespace ar {
@@ -662,13 +663,6 @@ template <int NT> constexpr size_t few_smem() {
     return 1024 + (size_t)Few<NT>::kStages * Few<NT>::kStage + sizeof(FewShared<NT>);
 }
 
-__device__ __forceinline__ float ld_peer_f32(uint32_t local, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                 : "=f"(v) : "r"(map_to_rank(local, rank)) : "memory");
-    return v;
-}
-
 // blockIdx.x: CTA of the cluster (its share of the blocks along k);
 // blockIdx.y: tile of 128 weight rows; blockIdx.z: row tile, counted over the
 // groups.  Warps 0-3: epilogue, lane + 32 * warp is the weight row; warp 4:
@@ -895,7 +889,7 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
                 for (int j = 0; j < kAt; ++j) {
                     const uint32_t c = c0 + j * parts;
                     v[p][j] = p < parts && c < rows
-                                  ? ld_peer_f32(smem_addr(sums + c * 128 + threadIdx.x), p)
+                                  ? ld_peer_f32(sums + c * 128 + threadIdx.x, p)
                                   : 0.0f;
                 }
 #pragma unroll

@@ -9,6 +9,7 @@
 // The row movers go by token, not by row: a token's row is read once and
 // written K times (dispatch, gradient), or K rows are read and one is written
 // (return), so each byte crosses memory once whatever the order.
+#include "ar_cluster.cuh"
 #include "ar_rows.cuh"
 
 namespace ar {
@@ -26,23 +27,6 @@ struct RouteArgs {
 constexpr int kRouteCtas = 8;          // CTAs of the one cluster for larger inputs
 constexpr int kRouteWarps = 32;
 constexpr int kRouteHeld = 8;          // ids a lane keeps in registers
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t ld_peer_u32(const void *p, uint32_t rank) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                 : "=r"(v) : "r"(map_to_rank(smem_addr(p), rank)) : "memory");
-    return v;
-}
 
 // The expert of pair p, or E for one that is not here.
 __device__ __forceinline__ int expert_of(const RouteArgs &a, uint32_t p) {
@@ -507,7 +491,7 @@ k_moe_return_grad(const __grid_constant__ ReturnGradArgs a) {
                     if (rank == 0 && threadIdx.x < 8 && k0 + (int)threadIdx.x < a.K) {
                         float v = 0.0f;
                         for (uint32_t c = 0; c < ctas; ++c)
-                            v += __uint_as_float(ld_peer_u32(sums + threadIdx.x, c));
+                            v += ld_peer_f32(sums + threadIdx.x, c);
                         a.dw[t * a.K + k0 + threadIdx.x] = v;
                     }
                     cluster_sync();
