@@ -14,7 +14,8 @@ namespace ar {
 // ---- general form ------------------------------------------------------------
 // Any alignment.  64 x 64 of d per CTA, 4 x 4 a thread, the operands of 32
 // steps along k in shared memory as binary32.  Bound by the shared-memory
-// reads of the multiply-adds.
+// reads of the multiply-adds: 4096 x 4096 x 4095 4949 us (27.8 TFLOP/s; 69 us with
+// padded rows, by the tensor cores); 1 x 8192 x 8191 1026 us (10.6).
 constexpr int kAnyTile = 64, kAnyStep = 32;
 
 __global__ void __launch_bounds__(256) k_matmul8_any(const __grid_constant__ MatmulArgs a) {

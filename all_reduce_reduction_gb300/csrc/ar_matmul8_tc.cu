@@ -358,8 +358,8 @@ __device__ __forceinline__ void store_rows(const MatmulArgs &a, uint4 *stage, ui
 // lays them out by block in shared memory.
 //
 // Bound by the epilogue's chain per warp and block (wait, read back, multiply-
-// add, arrive: about 870 clocks) over the products' 640.  8192^3: 415 to 450 us
-// by box, 2.4 to 2.6 PFLOP/s; 16384 rows over 64 experts of 2048 x 8192: 340 us.
+// add, arrive: about 870 clocks) over the products' 640.  8192^3: 415 to 457 us
+// by box, 2.4 to 2.6 PFLOP/s; 16384 rows over 64 experts of 2048 x 8192: 340 to 357.
 __global__ void __launch_bounds__(kRowsThreads, 1)
 k_matmul8_rows(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
@@ -667,8 +667,8 @@ template <int NT> constexpr size_t few_smem() {
 // blockIdx.y: tile of 128 weight rows; blockIdx.z: row tile, counted over the
 // groups.  Warps 0-3: epilogue, lane + 32 * warp is the weight row; warp 4:
 // TMA; warp 5: MMA; warp 6: scales, sa * sb for eight blocks at a time.  Bound by
-// the stream of the weights: 4096 rows over 64 experts of 2048 x 8192 190 us (5.9
-// TB/s); one row of 8192 x 8192 14.0 us, of which about 5 are launch, first loads
+// the stream of the weights: 4096 rows over 64 experts of 2048 x 8192 187 to 200 us
+// (5.6 to 6.0 TB/s); one row of 8192 x 8192 14.0 us, of which about 5 are launch, first loads
 // and join.
 template <int NT>
 __global__ void __launch_bounds__(kFewThreads, 2)
