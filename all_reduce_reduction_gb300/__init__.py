@@ -43,6 +43,11 @@ AR_SCALE_BLOCK = 128
 AR_MOE_MAX_EXPERTS = 1024
 AR_MOE_MAX_CHOICES = 32
 AR_NORM_GRAD_ROWS = 512
+AR_CACHE_MAX_DIM = 256
+AR_CACHE_MAX_HEADS = 1024
+AR_CACHE_WORK_ROWS = 16384
+AR_MOE_LAYER_TOKENS = 64
+AR_MOE_LAYER_PAIRS = 512
 
 DTYPES = {"bf16": AR_BF16, "fp16": AR_FP16, "fp32": AR_FP32}
 DTYPES8 = {**DTYPES, "e4m3": AR_E4M3}
@@ -152,6 +157,15 @@ SIGNATURES = {
                             _VP], _I),
     "ar_matmul8": ([_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _I, _VP, _SZ, _SZ, _SZ, _SZ, _I, _VP,
                     _VP], _I),
+    "ar_cache_write": ([_VP, _SZ, _VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _I, _VP, _SZ, _SZ, _VP,
+                        _VP, _SZ, _SZ, _I, _I, _I, _I, _VP], _I),
+    "ar_cache_read": ([_VP, _VP, _SZ, _VP, _VP, _SZ, _I, _VP, _SZ, _SZ, _VP, _VP, _VP, _SZ, _VP,
+                       _SZ, _SZ, _SZ, _I, _I, _I, _I, _VP], _I),
+    "ar_cache_attention": ([_VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _I, _VP, _SZ, _SZ, _VP,
+                            ctypes.c_float, _SZ, _VP, _SZ, _VP, _VP, _SZ, _SZ, _I, _I, _I, _I, _I,
+                            _VP], _I),
+    "ar_moe_layer": ([_VP, _SZ, _VP, _I, _VP, _VP, _SZ, _VP, _VP, _SZ, _VP, _VP, _SZ, _VP, _SZ,
+                      _SZ, _I, _I, _SZ, _SZ, _I, _VP], _I),
 }
 
 
@@ -564,6 +578,73 @@ def ar_matmul8(a, sa, b, sb, offsets, E: int, d, M: int, N: int, K: int, out_dty
                           DTYPES8.get(out_dtype, out_dtype), status, stream)
     if rc:
         raise ArError(rc, "ar_matmul8")
+
+
+def ar_cache_write(k, v, kcache, vcache, kscale, vscale, pages: int, page: int, table, width: int,
+                   lens, offsets, T: int, B: int, heads: int, D: int, dtype, cache_dtype=None,
+                   ldk: int = 0, ldv: int = 0, ldpage: int = 0, ldtable: int = 0,
+                   stream=None) -> None:
+    """New rows of keys and values into the pages of their sequences, in
+    ``cache_dtype`` (default ``dtype``; ``"e4m3"`` with a scale for each row and
+    head).  ``offsets`` None: one row a sequence."""
+    dt = DTYPES8.get(dtype, dtype)
+    calls = _calls or _layer_calls()
+    rc = calls.ar_cache_write(k, ldk, v, ldv, kcache, vcache, ldpage, kscale, vscale, pages, page,
+                              table, ldtable, width, lens, offsets, T, B, heads, D, dt,
+                              dt if cache_dtype is None else DTYPES8.get(cache_dtype, cache_dtype),
+                              stream)
+    if rc:
+        raise ArError(rc, "ar_cache_write")
+
+
+def ar_cache_read(kcache, vcache, kscale, vscale, pages: int, page: int, table, width: int, lens,
+                  offsets, k, v, T: int, B: int, heads: int, D: int, dtype, cache_dtype=None,
+                  ldpage: int = 0, ldtable: int = 0, ldk: int = 0, ldv: int = 0,
+                  stream=None) -> None:
+    """The rows that ar_cache_write would put there, back in ``dtype``."""
+    dt = DTYPES8.get(dtype, dtype)
+    calls = _calls or _layer_calls()
+    rc = calls.ar_cache_read(kcache, vcache, ldpage, kscale, vscale, pages, page, table, ldtable,
+                             width, lens, offsets, k, ldk, v, ldv, T, B, heads, D, dt,
+                             dt if cache_dtype is None else DTYPES8.get(cache_dtype, cache_dtype),
+                             stream)
+    if rc:
+        raise ArError(rc, "ar_cache_read")
+
+
+def ar_cache_attention(q, kcache, vcache, kscale, vscale, pages: int, page: int, table, width: int,
+                       lens, scale: float, out, lse, work, work_bytes: int, B: int, heads: int,
+                       kv_heads: int, D: int, dtype, cache_dtype=None, window: int = 0,
+                       ldq: int = 0, ldpage: int = 0, ldtable: int = 0, ldout: int = 0,
+                       stream=None) -> None:
+    """Attention of one new token a sequence over its cache (the last ``window``
+    positions of it, 0: all).  ``lse`` may be None; ``work``: AR_CACHE_WORK_ROWS *
+    (D + 2) floats."""
+    dt = DTYPES8.get(dtype, dtype)
+    calls = _calls or _layer_calls()
+    rc = calls.ar_cache_attention(q, ldq, kcache, vcache, ldpage, kscale, vscale, pages, page,
+                                  table, ldtable, width, lens, scale, window, out, ldout, lse,
+                                  work, work_bytes, B, heads, kv_heads, D, dt,
+                                  dt if cache_dtype is None
+                                  else DTYPES8.get(cache_dtype, cache_dtype), stream)
+    if rc:
+        raise ArError(rc, "ar_cache_attention")
+
+
+def ar_moe_layer(x, ids, w, up, up_scale, down, down_scale, out, work, work_bytes: int, T: int,
+                 K: int, E: int, H: int, F: int, dtype, ldx: int = 0, ldup: int = 0,
+                 lddown: int = 0, ldout: int = 0, ids_bytes=None, stream=None) -> None:
+    """A mixture-of-experts layer for a few tokens (T * K <= AR_MOE_LAYER_PAIRS): gated
+    first product, second product and the weighted sum over a token's choices.
+    ``ids_bytes`` as for ar_moe_route; ``work``: T * K * (F + 128) floats."""
+    if ids_bytes is None:
+        ids_bytes = ids.element_size() if hasattr(ids, "element_size") else 4
+    calls = _calls or _layer_calls()
+    rc = calls.ar_moe_layer(x, ldx, ids, ids_bytes, w, up, ldup, up_scale, down, lddown,
+                            down_scale, out, ldout, work, work_bytes, T, K, E, H, F,
+                            DTYPES8.get(dtype, dtype), stream)
+    if rc:
+        raise ArError(rc, "ar_moe_layer")
 
 
 class Handle:

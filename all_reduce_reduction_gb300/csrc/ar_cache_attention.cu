@@ -1,0 +1,520 @@
+// Attention of one new token a sequence over its paged cache, split over the
+// cache's length and joined.
+//
+//   s_j = scale <q, k_j>,  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+//
+// Bound by memory: every key and value of the cache is read once, for all query
+// heads that share it.  A unit is one sequence's key-value head with up to
+// kRows of its query heads; its positions are cut into tiles.  The tiles of all
+// units, in order, are dealt to the CTAs in runs of one length, so that a batch
+// of any lengths loads every SM alike.  A CTA walks its run with the running
+// maximum m and sum l of each row:
+//   m' = max(m, max s),  l' = l 2^(m - m') + sum 2^(s - m'),  o' likewise
+// (exponents of two: scale carries log2 e).  A unit that lies in one run is
+// finished there; the others leave (m, l, o) in the workspace and a second
+// launch joins them in order.
+#include "ar_cache.cuh"
+
+namespace ar {
+
+constexpr int kRows = 16;             // query heads of a unit
+constexpr int kMaxCtas = 480;         // what the workspace has room for
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    Pages g;
+    const uint8_t *q;
+    uint8_t *out;
+    float *lse;
+    float *work;
+    uint64_t sq, sout;                // bytes between rows
+    float scale2;                     // scale * log2 e
+    uint32_t B, heads, group;         // group: query heads that share a key-value head
+    uint32_t head_tiles;              // units of one key-value head
+    uint32_t window;                  // 0: none
+};
+
+// The workspace: where a CTA's first unit that others finish is, then (m, l) and o
+// of kRows rows for two parts of each CTA: part 0 continues a unit, part 1 begins one.
+struct WorkSpace {
+    int4 *meta;                       // sequence, unit, last CTA (-1: none)
+    float2 *ml;
+    float *o;
+    __device__ __forceinline__ explicit WorkSpace(float *work)
+        : meta(reinterpret_cast<int4 *>(work)),
+          ml(reinterpret_cast<float2 *>(work + 4 * kMaxCtas)),
+          o(work + 4 * kMaxCtas + 2 * 2 * kMaxCtas * kRows) {}
+};
+static_assert(4 * kMaxCtas + 2 * (2 * kMaxCtas * kRows) + 2 * kMaxCtas * kRows <=
+                      AR_CACHE_WORK_ROWS * 3 &&
+                  2 * kMaxCtas * kRows <= AR_CACHE_WORK_ROWS,
+              "the workspace has room for D = 1, and so for every D");
+
+// The range of positions [lo, n) of sequence b.
+struct Span {
+    uint32_t lo, n;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs &a, uint32_t b) {
+    const uint32_t n = a.g.length(b);
+    return {a.window && n > a.window ? n - a.window : 0u, n};
+}
+template <uint32_t TILE> __device__ __forceinline__ uint32_t tiles_of(Span s) {
+    return (s.n - s.lo + TILE - 1) / TILE;
+}
+
+// A place in the order of tiles: sequence, unit, tile; `left` tiles of the run.
+template <uint32_t TILE> struct Cursor {
+    uint32_t b, unit, t, tiles;
+    Span span;
+    uint64_t left;
+
+    __device__ __forceinline__ bool done() const { return left == 0; }
+    __device__ __forceinline__ void next(const AttnArgs &a) {
+        if (--left == 0 || ++t < tiles)
+            return;
+        t = 0;
+        if (++unit < a.g.heads * a.head_tiles)
+            return;
+        unit = 0;
+        do {
+            span = span_of(a, ++b);
+            tiles = tiles_of<TILE>(span);
+        } while (tiles == 0);             // `left` says that there is another
+    }
+};
+
+// This CTA's run.  `part` is shared memory of 33 words.  *per: tiles of a run.
+template <uint32_t TILE>
+__device__ __forceinline__ Cursor<TILE> find_run(const AttnArgs &a, uint64_t *part,
+                                                 uint64_t *per, uint64_t *start) {
+    // every thread counts a run of sequences; their sums are scanned
+    const uint32_t each = (a.B + blockDim.x - 1) / blockDim.x;
+    const uint32_t b0 = threadIdx.x * each;
+    const uint32_t b1 = b0 + each < a.B ? b0 + each : a.B;
+    const uint32_t units = a.g.heads * a.head_tiles;
+    uint64_t mine = 0;
+    for (uint32_t b = b0; b < b1; ++b)
+        mine += tiles_of<TILE>(span_of(a, b));
+    mine *= units;
+    uint64_t sum = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t other = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d)
+            sum += other;
+    }
+    __shared__ uint32_t at[4];
+    __shared__ uint64_t before;
+    if (lane == 31)
+        part[warp] = sum;
+    if (threadIdx.x == 0)
+        at[3] = 0;
+    __syncthreads();
+    uint64_t total = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+        if (w < warp)
+            sum += part[w];
+        total += part[w];
+    }
+    *per = (total + gridDim.x - 1) / gridDim.x;
+    if (*per < 1)
+        *per = 1;
+    *start = *per * blockIdx.x;
+    if (*start >= sum - mine && *start < sum) {
+        uint64_t base = sum - mine;
+        uint32_t b = b0;
+        for (;; ++b) {
+            const uint64_t n = (uint64_t)tiles_of<TILE>(span_of(a, b)) * units;
+            if (*start < base + n)
+                break;
+            base += n;
+        }
+        at[0] = b;
+        at[3] = 1;
+        before = base;
+    }
+    __syncthreads();
+    Cursor<TILE> c = {};
+    if (!at[3])
+        return c;                         // past the last tile
+    c.b = at[0];
+    c.span = span_of(a, c.b);
+    c.tiles = tiles_of<TILE>(c.span);
+    const uint64_t in = *start - before;
+    c.unit = (uint32_t)(in / c.tiles);
+    c.t = (uint32_t)(in % c.tiles);
+    c.left = total - *start < *per ? total - *start : *per;
+    return c;
+}
+
+template <int DT> __device__ __forceinline__ void store_row(uint8_t *row, uint32_t d, float v) {
+    st_elem<DT>(row, d, narrow1<DT>(v));
+}
+
+// Zeros (and -inf) for the sequences that have no position.
+template <int DT, uint32_t TILE> __device__ __forceinline__ void empty_rows(const AttnArgs &a) {
+    for (uint32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (tiles_of<TILE>(span_of(a, b)) != 0)
+            continue;
+        uint8_t *row = a.out + (uint64_t)b * a.sout;
+        for (uint32_t i = threadIdx.x; i < a.heads * a.g.D; i += blockDim.x)
+            store_row<DT>(row, i, 0.0f);
+        if (a.lse)
+            for (uint32_t h = threadIdx.x; h < a.heads; h += blockDim.x)
+                a.lse[(uint64_t)b * a.heads + h] = -INFINITY;
+    }
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+// o / l, and 0 for a row without a weight; NaN stays.
+__device__ __forceinline__ float output_of(float o, float l) {
+    return l == 0.0f ? 0.0f : __fdiv_rn(o, l);
+}
+// What the running maximum subtracts: a row of -inf alone keeps weights of 0.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Where a unit's rows go: first query head, rows.
+struct UnitRows {
+    uint32_t kv, head, rows;
+};
+__device__ __forceinline__ UnitRows unit_rows(const AttnArgs &a, uint32_t unit) {
+    UnitRows u;
+    u.kv = unit / a.head_tiles;
+    const uint32_t r0 = unit % a.head_tiles * kRows;
+    u.head = u.kv * a.group + r0;
+    u.rows = a.group - r0 < kRows ? a.group - r0 : kRows;
+    return u;
+}
+
+// How a segment [t0, t1) of a unit ends: finished, or a part for the join.
+// Returns the part's index, or -1.  Thread 0 notes the unit's last CTA.
+template <uint32_t TILE>
+__device__ __forceinline__ int segment_part(const AttnArgs &a, uint32_t b, uint32_t unit,
+                                            uint32_t t0, uint32_t t1, uint32_t tiles,
+                                            uint64_t per, uint64_t start_of_unit) {
+    if (t0 == 0 && t1 == tiles)
+        return -1;
+    if (t0 != 0)
+        return 2 * blockIdx.x;
+    if (threadIdx.x == 0) {
+        const uint64_t last = (start_of_unit + tiles - 1) / per;
+        WorkSpace(a.work).meta[blockIdx.x] = make_int4((int)b, (int)unit, (int)last, 0);
+    }
+    return 2 * blockIdx.x + 1;
+}
+
+// ---- any type and alignment -----------------------------------------------------
+
+// A tile of keys, then of values, in shared memory as binary32; a thread has one
+// key and four rows of the scores, then one or two columns of the outputs and half
+// of the rows.
+constexpr int kAnyThreads = 256;
+constexpr uint32_t kAnyTile = 64;
+
+static size_t any_smem(uint32_t D) {
+    return sizeof(float) * ((size_t)kRows * D + kAnyTile * (D | 1) + kRows * (kAnyTile + 1));
+}
+
+template <int DT, bool CACHE8>
+__global__ void __launch_bounds__(kAnyThreads)
+k_attention_any(const __grid_constant__ AttnArgs a) {
+    extern __shared__ float smem[];
+    __shared__ uint64_t scan[33];
+    __shared__ float m_[kRows], l_[kRows], alpha_[kRows];
+    __shared__ int2 place[kAnyTile];
+    kernel_prologue();
+    const uint32_t D = a.g.D, stride = D | 1, tid = threadIdx.x;
+    float *qs = smem, *kv = qs + kRows * D, *sc = kv + kAnyTile * stride;
+    if (tid == 0)
+        WorkSpace(a.work).meta[blockIdx.x] = make_int4(0, 0, -1, 0);
+    empty_rows<DT, kAnyTile>(a);
+    uint64_t per, start;
+    Cursor<kAnyTile> c = find_run<kAnyTile>(a, scan, &per, &start);
+    uint64_t index = start;               // of the cursor's tile
+    while (!c.done()) {
+        const UnitRows u = unit_rows(a, c.unit);
+        const uint32_t b = c.b, unit = c.unit, t0 = c.t, tiles = c.tiles;
+        __syncthreads();
+        const uint8_t *q = a.q + (uint64_t)b * a.sq + (uint64_t)u.head * D * Elem<DT>::kSize;
+        for (uint32_t i = tid; i < kRows * D; i += kAnyThreads)
+            qs[i] = i < u.rows * D ? widen1<DT>(ld_elem<DT>(q, i)) : 0.0f;
+        if (tid < kRows) {
+            m_[tid] = -INFINITY;
+            l_[tid] = 0.0f;
+        }
+        float acc[2][kRows / 2];          // columns tid % 128 (+ 128), rows of one half
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < kRows / 2; ++r)
+                acc[i][r] = 0.0f;
+        uint32_t t = t0;
+        for (;;) {
+            const uint32_t j0 = c.span.lo + t * kAnyTile;
+            __syncthreads();              // the last tile is done with
+            if (tid < kAnyTile) {
+                const uint32_t j = j0 + tid;
+                place[tid] = j < c.span.n ? make_int2(a.g.page_of(b, j), (int)(j % a.g.page))
+                                          : make_int2(-1, 0);
+            }
+            __syncthreads();
+            auto load = [&](const uint8_t *pool, const float *scales) {
+                for (uint32_t i = tid; i < kAnyTile * D; i += kAnyThreads) {
+                    const uint32_t r = i / D, d = i - r * D;
+                    const int2 p = place[r];
+                    float v = 0.0f;
+                    if (p.x >= 0) {
+                        const uint8_t *page = pool + (uint64_t)p.x * a.g.stride;
+                        const uint32_t e = a.g.in_page(u.kv, p.y) + d;
+                        if (CACHE8) {
+                            uint32_t h;
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)page[e]));
+                            v = __half2float(__ushort_as_half((unsigned short)h)) *
+                                scales[a.g.scale_at(p.x, u.kv, p.y)];
+                        } else {
+                            v = widen1<DT>(ld_elem<DT>(page, e));
+                        }
+                    }
+                    kv[r * stride + d] = v;
+                }
+            };
+            load(a.g.k, a.g.ks);
+            __syncthreads();
+            {
+                const uint32_t key = tid % kAnyTile, r0 = tid / kAnyTile * 4;
+                float s[4] = {};
+                if (r0 < u.rows)
+                    for (uint32_t d = 0; d < D; ++d) {
+                        const float k = kv[key * stride + d];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            s[r] += qs[(r0 + r) * D + d] * k;
+                    }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sc[(r0 + r) * (kAnyTile + 1) + key] =
+                        place[key].x >= 0 ? s[r] * a.scale2 : -INFINITY;
+            }
+            __syncthreads();
+            load(a.g.v, a.g.vs);
+            for (uint32_t r = tid / 32; r < u.rows; r += kAnyThreads / 32) {
+                float *row = sc + r * (kAnyTile + 1);
+                const uint32_t lane = tid & 31;
+                const float x = row[lane], y = row[lane + 32];
+                // a NaN score makes its row NaN: the maximum must not drop it
+                float top = fmaxf(x, y);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                const float was = m_[r], now = fmaxf(was, top), base = finite_max(now);
+                const float p0 = exp2f(x - base), p1 = exp2f(y - base);
+                const float sum = warp_sum(p0 + p1), al = exp2f(was - base);
+                row[lane] = p0;
+                row[lane + 32] = p1;
+                __syncwarp();
+                if (lane == 0) {
+                    m_[r] = now;
+                    l_[r] = l_[r] * al + sum;
+                    alpha_[r] = al;
+                }
+            }
+            __syncthreads();
+            {
+                const uint32_t d0 = tid % 128, r0 = tid / 128 * (kRows / 2);
+                const uint32_t keys = c.span.n - j0 < kAnyTile ? c.span.n - j0 : kAnyTile;
+                if (r0 < u.rows)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t d = d0 + 128 * i;
+                        if (d >= D)
+                            break;
+#pragma unroll
+                        for (int r = 0; r < kRows / 2; ++r)
+                            if (r0 + r < u.rows)
+                                acc[i][r] *= alpha_[r0 + r];
+                        for (uint32_t k = 0; k < keys; ++k) {
+                            const float v = kv[k * stride + d];
+#pragma unroll
+                            for (int r = 0; r < kRows / 2; ++r)
+                                acc[i][r] += sc[(r0 + r) * (kAnyTile + 1) + k] * v;
+                        }
+                    }
+            }
+            ++t;
+            ++index;
+            const bool more = c.left > 1 && t < tiles;
+            c.next(a);
+            if (!more)
+                break;
+        }
+        const int part = segment_part<kAnyTile>(a, b, unit, t0, t, tiles, per, index - t);
+        const uint32_t r0 = tid / 128 * (kRows / 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t d = tid % 128 + 128 * i;
+#pragma unroll
+            for (int r = 0; r < kRows / 2; ++r) {
+                if (d >= D || r0 + r >= u.rows)
+                    continue;
+                if (part < 0)
+                    store_row<DT>(a.out + (uint64_t)b * a.sout, (u.head + r0 + r) * D + d,
+                                  output_of(acc[i][r], l_[r0 + r]));
+                else
+                    WorkSpace(a.work).o[((uint64_t)part * kRows + r0 + r) * D + d] = acc[i][r];
+            }
+        }
+        if (tid < u.rows) {
+            if (part >= 0)
+                WorkSpace(a.work).ml[part * kRows + tid] = make_float2(m_[tid], l_[tid]);
+            else if (a.lse)
+                a.lse[(uint64_t)b * a.heads + u.head + tid] = lse_of(m_[tid], l_[tid]);
+        }
+    }
+}
+
+// ---- the join ---------------------------------------------------------------------
+
+// CTA (c, r): row r of the unit that begins in CTA c's run and ends in another's.
+// Parts are added in order; `THREADS / columns` groups of threads take a run of them
+// each, and their sums are added in order too.
+constexpr int kJoinThreads = 256;
+
+template <int DT> __global__ void __launch_bounds__(kJoinThreads)
+k_attention_join(const __grid_constant__ AttnArgs a) {
+    __shared__ float2 ml[kMaxCtas];
+    __shared__ float sums[kJoinThreads];
+    kernel_prologue();
+    const WorkSpace w(a.work);
+    const int c = blockIdx.x, r = blockIdx.y;
+    const int4 meta = w.meta[c];
+    if (meta.z < 0)
+        return;
+    const UnitRows u = unit_rows(a, (uint32_t)meta.y);
+    if (r >= (int)u.rows)
+        return;
+    const int parts = meta.z - c + 1;
+    auto slot = [&](int i) { return (i == 0 ? 2 * c + 1 : 2 * (c + i)) * kRows + r; };
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
+        ml[i] = w.ml[slot(i)];
+        top = fmaxf(top, ml[i].x);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if ((threadIdx.x & 31) == 0)
+        sums[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i)
+        top = fmaxf(top, sums[i]);
+    const float base = finite_max(top);
+    float l = 0.0f;
+    for (int i = 0; i < parts; ++i)
+        l += ml[i].y * exp2f(ml[i].x - base);
+    const uint32_t D = a.g.D, columns = (D + 31) / 32 * 32, groups = kJoinThreads / columns;
+    const uint32_t g = threadIdx.x / columns, d = threadIdx.x % columns;
+    const int each = (parts + (int)groups - 1) / (int)groups;
+    float o = 0.0f;
+    if (g < groups && d < D) {
+        const int end = ((int)g + 1) * each < parts ? ((int)g + 1) * each : parts;
+#pragma unroll 8
+        for (int i = (int)g * each; i < end; ++i)
+            o += w.o[(uint64_t)slot(i) * D + d] * exp2f(ml[i].x - base);
+    }
+    __syncthreads();
+    sums[threadIdx.x] = o;
+    __syncthreads();
+    if (g == 0 && d < D) {
+        for (uint32_t i = 1; i < groups; ++i)
+            o += sums[i * columns + d];
+        store_row<DT>(a.out + (uint64_t)meta.x * a.sout, (u.head + r) * D + d, output_of(o, l));
+    }
+    if (threadIdx.x == 0 && a.lse)
+        a.lse[(uint64_t)meta.x * a.heads + u.head + r] = lse_of(top, l);
+}
+
+template <int DT> static cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t s) {
+    const uint32_t rows = a.group < kRows ? a.group : kRows;
+    return launch_kernel(k_attention_join<DT>, dim3(grid, rows), kJoinThreads, 0, s, true, a);
+}
+
+template <int DT, bool CACHE8> static cudaError_t attention_any(const AttnArgs &a, cudaStream_t s) {
+    const size_t smem = any_smem(a.g.D);
+    cudaError_t e = opt_in_smem<k_attention_any<DT, CACHE8>>(any_smem(AR_CACHE_MAX_DIM));
+    if (e != cudaSuccess)
+        return e;
+    const int sms = sm_count();
+    if (sms < 1)
+        return cudaErrorUnknown;
+    const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    e = launch_kernel(k_attention_any<DT, CACHE8>, grid, kAnyThreads, smem, s, true, a);
+    return e != cudaSuccess ? e : launch_join<DT>(a, grid, s);
+}
+
+template <int DT> static cudaError_t attention_dt(const AttnArgs &a, bool e4m3, cudaStream_t s) {
+    return e4m3 ? attention_any<DT, true>(a, s) : attention_any<DT, false>(a, s);
+}
+
+}  // namespace ar
+
+using namespace ar;
+
+extern "C" {
+
+int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void *vcache,
+                       size_t ldpage, const float *kscale, const float *vscale, size_t pages,
+                       int page, const int32_t *table, size_t ldtable, size_t width,
+                       const int32_t *lens, float scale, size_t window, void *out, size_t ldout,
+                       float *lse, float *work, size_t work_bytes, size_t B, int heads,
+                       int kv_heads, int D, int dtype, int cache_dtype, cudaStream_t stream) {
+    AttnArgs a;
+    const PagesCheck c = check_pages(kcache, vcache, ldpage, kscale, vscale, pages, page, table,
+                                     ldtable, width, lens, B, kv_heads, D, dtype, cache_dtype,
+                                     &a.g);
+    if (c.rc != AR_OK)
+        return c.rc;
+    if (heads < 1 || heads % kv_heads != 0)
+        return AR_ERR_INVALID;
+    if (heads > AR_CACHE_MAX_HEADS)
+        return AR_ERR_UNSUPPORTED;
+    if (B == 0)
+        return AR_OK;
+    if (!q || !out || !work)
+        return AR_ERR_INVALID;
+    const size_t row = (size_t)heads * D, size = elem_size(dtype);
+    const Matrix mq = matrix(q, ldq, B, row, size), mo = matrix(out, ldout, B, row, size);
+    const Matrix ml = matrix(lse, 0, B, (size_t)heads, 4);
+    const Matrix mw = matrix(work, 0, AR_CACHE_WORK_ROWS, (size_t)D + 2, 4);
+    if (!mq.ok || !mo.ok || !ml.ok || !mw.ok || mw.p % 16 != 0 || work_bytes < mw.bytes)
+        return AR_ERR_INVALID;
+    const Matrix *outs[] = {&mo, &ml, &mw};
+    for (const Matrix *m : outs)
+        if (c.on(*m) || c.indexed(*m) || meet(*m, mq))
+            return AR_ERR_INVALID;
+    if (meet(mo, ml) || meet(mo, mw) || meet(ml, mw))
+        return AR_ERR_INVALID;
+    a.q = static_cast<const uint8_t *>(q);
+    a.out = static_cast<uint8_t *>(out);
+    a.lse = lse;
+    a.work = work;
+    a.sq = mq.stride;
+    a.sout = mo.stride;
+    a.scale2 = scale * kLog2E;
+    a.B = (uint32_t)B;
+    a.heads = (uint32_t)heads;
+    a.group = (uint32_t)(heads / kv_heads);
+    a.head_tiles = (a.group + kRows - 1) / kRows;
+    a.window = window < ((size_t)1 << 31) ? (uint32_t)window : 0u;
+    const bool e4m3 = cache_dtype == AR_E4M3;
+    switch (dtype) {
+    case AR_BF16: return launched(attention_dt<AR_BF16>(a, e4m3, stream));
+    case AR_FP16: return launched(attention_dt<AR_FP16>(a, e4m3, stream));
+    default: return launched(attention_dt<AR_FP32>(a, e4m3, stream));
+    }
+}
+
+}  // extern "C"

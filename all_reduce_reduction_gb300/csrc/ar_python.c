@@ -10,6 +10,13 @@
 
 #include "ar.h"
 
+/* Weak, so that the module also loads beside a library that has only the layer
+ * operators; such a call is then refused (CALL_NEW). */
+#pragma weak ar_cache_write
+#pragma weak ar_cache_read
+#pragma weak ar_cache_attention
+#pragma weak ar_moe_layer
+
 static PyObject *name_data_ptr, *name_cuda_stream;
 static PyObject *raw_stream, *current_device;      /* torch's, once it has CUDA up */
 
@@ -163,6 +170,13 @@ static cudaStream_t stream(Args *a) {
     Py_END_ALLOW_THREADS                                                                \
     return PyLong_FromLong(status)
 
+#define CALL_NEW(name, f)                                                               \
+    if (!name) {                                                                        \
+        PyErr_SetString(PyExc_NotImplementedError, #name " is not in the library");     \
+        return NULL;                                                                    \
+    }                                                                                   \
+    CALL(f)
+
 static PyObject *rmsnorm(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
     BEGIN(17)
     P(x); Z(ldx); P(res); Z(ldres); P(gamma);
@@ -221,6 +235,55 @@ static PyObject *matmul8(PyObject *self, PyObject *const *args, Py_ssize_t nargs
     CALL(ar_matmul8(x, lda, sa, b, ldb, sb, offsets, E, d, ldd, M, N, K, out_dtype, word, s));
 }
 
+static PyObject *cache_write(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+    BEGIN(23)
+    P(k); Z(ldk); P(v); Z(ldv); P(kcache); P(vcache); Z(ldpage); P(kscale); P(vscale); Z(pages);
+    I(page); P(table); Z(ldtable); Z(width); P(lens); P(offsets); Z(T); Z(B); I(heads); I(D);
+    I(dtype); I(cache_dtype);
+    const cudaStream_t s = stream(&a);
+    CALL_NEW(ar_cache_write,
+             ar_cache_write(k, ldk, v, ldv, kcache, vcache, ldpage, kscale, vscale, pages, page,
+                            table, ldtable, width, lens, offsets, T, B, heads, D, dtype,
+                            cache_dtype, s));
+}
+
+static PyObject *cache_read(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+    BEGIN(23)
+    P(kcache); P(vcache); Z(ldpage); P(kscale); P(vscale); Z(pages); I(page); P(table); Z(ldtable);
+    Z(width); P(lens); P(offsets); P(k); Z(ldk); P(v); Z(ldv); Z(T); Z(B); I(heads); I(D);
+    I(dtype); I(cache_dtype);
+    const cudaStream_t s = stream(&a);
+    CALL_NEW(ar_cache_read,
+             ar_cache_read(kcache, vcache, ldpage, kscale, vscale, pages, page, table, ldtable,
+                           width, lens, offsets, k, ldk, v, ldv, T, B, heads, D, dtype,
+                           cache_dtype, s));
+}
+
+static PyObject *cache_attention(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+    BEGIN(27)
+    P(q); Z(ldq); P(kcache); P(vcache); Z(ldpage); P(kscale); P(vscale); Z(pages); I(page);
+    P(table); Z(ldtable); Z(width); P(lens);
+    const float scale = real(&a);
+    Z(window); P(out); Z(ldout); P(lse); P(work); Z(work_bytes); Z(B); I(heads); I(kv_heads); I(D);
+    I(dtype); I(cache_dtype);
+    const cudaStream_t s = stream(&a);
+    CALL_NEW(ar_cache_attention,
+             ar_cache_attention(q, ldq, kcache, vcache, ldpage, kscale, vscale, pages, page, table,
+                                ldtable, width, lens, scale, window, out, ldout, lse, work,
+                                work_bytes, B, heads, kv_heads, D, dtype, cache_dtype, s));
+}
+
+static PyObject *moe_layer(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+    BEGIN(22)
+    P(x); Z(ldx); P(ids); I(ids_bytes); P(w); P(up); Z(ldup); P(up_scale); P(down); Z(lddown);
+    P(down_scale); P(out); Z(ldout); P(work); Z(work_bytes); Z(T); I(K); I(E); Z(H); Z(F);
+    I(dtype);
+    const cudaStream_t s = stream(&a);
+    CALL_NEW(ar_moe_layer,
+             ar_moe_layer(x, ldx, ids, ids_bytes, w, up, ldup, up_scale, down, lddown, down_scale,
+                          out, ldout, work, work_bytes, T, K, E, H, F, dtype, s));
+}
+
 #define FAST(name, f) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {
     FAST("ar_rmsnorm", rmsnorm),
@@ -230,6 +293,10 @@ static PyMethodDef methods[] = {
     FAST("ar_moe_return", moe_return),
     FAST("ar_moe_return_grad", moe_return_grad),
     FAST("ar_matmul8", matmul8),
+    FAST("ar_cache_write", cache_write),
+    FAST("ar_cache_read", cache_read),
+    FAST("ar_cache_attention", cache_attention),
+    FAST("ar_moe_layer", moe_layer),
     {NULL, NULL, 0, NULL},
 };
 

@@ -727,6 +727,115 @@ int ar_matmul8(const void *a, size_t lda, const float *sa, const void *b, size_t
                const float *sb, const int32_t *offsets, int E, void *d, size_t ldd, size_t M,
                size_t N, size_t K, int out_dtype, int *status, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A decode step: the paged cache, attention over it, and an experts' layer for
+ * a few tokens.  What holds for the layer operators above holds here too.
+ *
+ * The cache.  A pool of `pages` pages of `page` slots holds the keys and values
+ * of `heads` heads; a slot has D elements a head.  Element d of slot s of head h
+ * in page p is at p * ldpage + (h * page + s) * D + d of kcache and of vcache
+ * (elements; ldpage = 0 stands for pages without gaps, and pools whose pages
+ * alternate in one buffer are slices of it).  cache_dtype is dtype itself (bits
+ * unchanged) or AR_E4M3: then each row of D elements has one scale, at
+ * (p * heads + h) * page + s of kscale and of vscale (NULL otherwise), and a
+ * value is code * scale.
+ *
+ * The sequences.  Position j of sequence b lies in page table[b * ldtable + j /
+ * page], slot j % page (ldtable = 0: width).  lens[b] counts the sequence's
+ * tokens; words outside [0, width * page] count as the nearer end.  A position
+ * whose page is outside [0, pages) is not there: nothing is read or written for
+ * it.  lens, table and offsets are device memory, so that a captured graph
+ * serves sequences as they grow.
+ *
+ * B sequences, T rows; D <= AR_CACHE_MAX_DIM, heads <= AR_CACHE_MAX_HEADS;
+ * width * page, heads * page * D, B, T and pages < 2^31 (AR_ERR_UNSUPPORTED
+ * beyond). */
+#define AR_CACHE_MAX_DIM 256
+#define AR_CACHE_MAX_HEADS 1024
+/* Rows of partial results ar_cache_attention keeps in its workspace. */
+#define AR_CACHE_WORK_ROWS 16384
+/* Most tokens and most pairs (token, choice) of ar_moe_layer. */
+#define AR_MOE_LAYER_TOKENS 64
+#define AR_MOE_LAYER_PAIRS 512
+
+/* New keys and values into the cache.  Rows [offsets[b], offsets[b+1]) of k and
+ * v are the last tokens of sequence b, whose lens[b] counts them already:
+ *   row offsets[b] + i goes to position lens[b] - (offsets[b+1] - offsets[b]) + i
+ * offsets (B + 1 words, not decreasing) may be NULL: one row a sequence, T = B.
+ * Rows of no sequence and positions below 0 or that are not there are skipped.
+ * With cache_dtype AR_E4M3, per row and head:
+ *   scale = max(largest |x|, 2^-96) * round(1 / 448)
+ *   code  = e4m3(x * round(1 / scale))
+ * as in ar_rmsnorm (a NaN becomes the NaN code and does not enter the scale).
+ *   k, v: dtype, T rows of heads * D elements, row strides ldk and ldv.
+ * Two rows of one call for the same slot (sequences that share the page they
+ * write to) are the caller's to avoid: which elements are left there is open. */
+int ar_cache_write(const void *k, size_t ldk, const void *v, size_t ldv, void *kcache,
+                   void *vcache, size_t ldpage, float *kscale, float *vscale, size_t pages,
+                   int page, const int32_t *table, size_t ldtable, size_t width,
+                   const int32_t *lens, const int32_t *offsets, size_t T, size_t B, int heads,
+                   int D, int dtype, int cache_dtype, cudaStream_t stream);
+
+/* The same rows back: row offsets[b] + i of k and v receives the position that
+ * ar_cache_write gives it, as it is or round(code * scale).  Rows without a
+ * position that is there are left as they are. */
+int ar_cache_read(const void *kcache, const void *vcache, size_t ldpage, const float *kscale,
+                  const float *vscale, size_t pages, int page, const int32_t *table,
+                  size_t ldtable, size_t width, const int32_t *lens, const int32_t *offsets,
+                  void *k, size_t ldk, void *v, size_t ldv, size_t T, size_t B, int heads, int D,
+                  int dtype, int cache_dtype, cudaStream_t stream);
+
+/* Attention of one new token a sequence over its cache.  Per sequence b and head
+ * h, over the positions j in [max(0, lens[b] - window), lens[b]) that are there
+ * (window = 0: all), with the keys and values of head h / (heads / kv_heads):
+ *   s_j = scale * <q, k_j>,  m = max_j s_j
+ *   out = round( sum_j exp(s_j - m) * v_j / sum_j exp(s_j - m) )
+ *   lse = m + ln sum_j exp(s_j - m)
+ * Without any position (or with scores of -inf alone) out is 0 and lse -inf.
+ * The sums over j are taken in parts that depend on lens, window, B, the heads
+ * and the device, never on the order in which CTAs run.  exp is within a few
+ * units in the last place; where keys and values have two bytes or one, the
+ * weights exp(s_j - m) enter the second product with 16 bits or more.
+ *   q, out: dtype, B rows of heads * D elements, row strides ldq and ldout.
+ *   kv_heads divides heads.   lse: B x heads binary32; may be NULL.
+ *   kscale, vscale: not negative.
+ *   work:  device memory, 16-byte aligned, of at least
+ *          AR_CACHE_WORK_ROWS * (D + 2) * 4 bytes.  Calls that may run at the same
+ *          time (graphs too) need one each. */
+int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void *vcache,
+                       size_t ldpage, const float *kscale, const float *vscale, size_t pages,
+                       int page, const int32_t *table, size_t ldtable, size_t width,
+                       const int32_t *lens, float scale, size_t window, void *out, size_t ldout,
+                       float *lse, float *work, size_t work_bytes, size_t B, int heads,
+                       int kv_heads, int D, int dtype, int cache_dtype, cudaStream_t stream);
+
+/* A mixture-of-experts layer for a few tokens in two launches: what
+ * ar_moe_route, ar_moe_dispatch, ar_matmul8, the activation, ar_matmul8 and
+ * ar_moe_return do for many, without rounding anything to 8 bits on the way.
+ * For token t and its choice k of expert e = ids[t*K + k], with the weights
+ * W = code * scale of their blocks (as in ar_matmul8):
+ *   g = up[e][0 .. F) x[t],  u = up[e][F .. 2F) x[t]
+ *   h = g / (1 + exp(-g)) * u
+ *   out[t] = round( sum_k w[t*K + k] * down[e] h )
+ * Choices whose id is outside [0, E) (another rank's, or dropped) add nothing.
+ * The sums are binary32.
+ *   x, out: dtype, T x H.   ids: T x K words of ids_bytes (4 or 8) bytes, signed.
+ *   w:    T x K binary32; NULL stands for ones.
+ *   up:   E matrices of 2F x H E4M3, row stride ldup bytes, 2F * ldup apart;
+ *         up_scale: E x ceil(2F/128) x ceil(H/128) binary32.
+ *   down: E matrices of H x F E4M3, row stride lddown bytes, H * lddown apart;
+ *         down_scale: E x ceil(H/128) x ceil(F/128) binary32.
+ *   work: device memory, 16-byte aligned, of at least T * K * (F + 128) * 4 bytes.
+ *         Calls that may run at the same time (graphs too) need one each.
+ * T <= AR_MOE_LAYER_TOKENS, T * K <= AR_MOE_LAYER_PAIRS, K <= AR_MOE_MAX_CHOICES;
+ * E <= AR_MOE_MAX_EXPERTS, H and F < 2^24 (AR_ERR_UNSUPPORTED beyond).  Weights whose rows are multiples of
+ * 16 bytes at 16-byte boundaries take the vector path. */
+int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, const float *w,
+                 const void *up, size_t ldup, const float *up_scale, const void *down,
+                 size_t lddown, const float *down_scale, void *out, size_t ldout, float *work,
+                 size_t work_bytes, size_t T, int K, int E, size_t H, size_t F, int dtype,
+                 cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
