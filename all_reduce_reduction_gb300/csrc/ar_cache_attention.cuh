@@ -1,0 +1,203 @@
+// What the kernels of attention over the paged cache share: their arguments, the
+// deal of tiles to CTAs, the workspace, and how a unit ends.
+#pragma once
+
+#include "ar_cache.cuh"
+
+namespace ar {
+
+constexpr int kRows = 16;             // query heads of a unit
+constexpr int kMaxCtas = 480;         // what the workspace has room for
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    Pages g;
+    const uint8_t *q;
+    uint8_t *out;
+    float *lse;
+    float *work;
+    uint64_t sq, sout;                // bytes between rows
+    float scale2;                     // scale * log2 e
+    uint32_t B, heads, group;         // group: query heads that share a key-value head
+    uint32_t head_tiles;              // units of one key-value head
+    uint32_t window;                  // 0: none
+};
+
+// The workspace: where a CTA's first unit that others finish is, then (m, l) and o
+// of kRows rows for two parts of each CTA: part 0 continues a unit, part 1 begins one.
+struct WorkSpace {
+    int4 *meta;                       // sequence, unit, last CTA (-1: none)
+    float2 *ml;
+    float *o;
+    __device__ __forceinline__ explicit WorkSpace(float *work)
+        : meta(reinterpret_cast<int4 *>(work)),
+          ml(reinterpret_cast<float2 *>(work + 4 * kMaxCtas)),
+          o(work + 4 * kMaxCtas + 2 * 2 * kMaxCtas * kRows) {}
+};
+static_assert(4 * kMaxCtas + 2 * (2 * kMaxCtas * kRows) + 2 * kMaxCtas * kRows <=
+                      AR_CACHE_WORK_ROWS * 3 &&
+                  2 * kMaxCtas * kRows <= AR_CACHE_WORK_ROWS,
+              "the workspace has room for D = 1, and so for every D");
+
+// The range of positions [lo, n) of sequence b.
+struct Span {
+    uint32_t lo, n;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs &a, uint32_t b) {
+    const uint32_t n = a.g.length(b);
+    return {a.window && n > a.window ? n - a.window : 0u, n};
+}
+template <uint32_t TILE> __device__ __forceinline__ uint32_t tiles_of(Span s) {
+    return (s.n - s.lo + TILE - 1) / TILE;
+}
+
+// A place in the order of tiles: sequence, unit, tile; `left` tiles of the run.
+template <uint32_t TILE> struct Cursor {
+    uint32_t b, unit, t, tiles;
+    Span span;
+    uint64_t left;
+
+    __device__ __forceinline__ bool done() const { return left == 0; }
+    __device__ __forceinline__ void next(const AttnArgs &a) {
+        if (--left == 0 || ++t < tiles)
+            return;
+        t = 0;
+        if (++unit < a.g.heads * a.head_tiles)
+            return;
+        unit = 0;
+        do {
+            span = span_of(a, ++b);
+            tiles = tiles_of<TILE>(span);
+        } while (tiles == 0);             // `left` says that there is another
+    }
+};
+
+// This CTA's run.  `part` is shared memory of 33 words.  *per: tiles of a run.
+template <uint32_t TILE>
+__device__ __forceinline__ Cursor<TILE> find_run(const AttnArgs &a, uint64_t *part,
+                                                 uint64_t *per, uint64_t *start) {
+    // every thread counts a run of sequences; their sums are scanned
+    const uint32_t each = (a.B + blockDim.x - 1) / blockDim.x;
+    const uint32_t b0 = threadIdx.x * each;
+    const uint32_t b1 = b0 + each < a.B ? b0 + each : a.B;
+    const uint32_t units = a.g.heads * a.head_tiles;
+    uint64_t mine = 0;
+    for (uint32_t b = b0; b < b1; ++b)
+        mine += tiles_of<TILE>(span_of(a, b));
+    mine *= units;
+    uint64_t sum = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t other = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d)
+            sum += other;
+    }
+    __shared__ uint32_t at[4];
+    __shared__ uint64_t before;
+    if (lane == 31)
+        part[warp] = sum;
+    if (threadIdx.x == 0)
+        at[3] = 0;
+    __syncthreads();
+    uint64_t total = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+        if (w < warp)
+            sum += part[w];
+        total += part[w];
+    }
+    *per = (total + gridDim.x - 1) / gridDim.x;
+    if (*per < 1)
+        *per = 1;
+    *start = *per * blockIdx.x;
+    if (*start >= sum - mine && *start < sum) {
+        uint64_t base = sum - mine;
+        uint32_t b = b0;
+        for (;; ++b) {
+            const uint64_t n = (uint64_t)tiles_of<TILE>(span_of(a, b)) * units;
+            if (*start < base + n)
+                break;
+            base += n;
+        }
+        at[0] = b;
+        at[3] = 1;
+        before = base;
+    }
+    __syncthreads();
+    Cursor<TILE> c = {};
+    if (!at[3])
+        return c;                         // past the last tile
+    c.b = at[0];
+    c.span = span_of(a, c.b);
+    c.tiles = tiles_of<TILE>(c.span);
+    const uint64_t in = *start - before;
+    c.unit = (uint32_t)(in / c.tiles);
+    c.t = (uint32_t)(in % c.tiles);
+    c.left = total - *start < *per ? total - *start : *per;
+    return c;
+}
+
+template <int DT> __device__ __forceinline__ void store_row(uint8_t *row, uint32_t d, float v) {
+    st_elem<DT>(row, d, narrow1<DT>(v));
+}
+
+// Zeros (and -inf) for the sequences that have no position.
+template <int DT, uint32_t TILE> __device__ __forceinline__ void empty_rows(const AttnArgs &a) {
+    for (uint32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (tiles_of<TILE>(span_of(a, b)) != 0)
+            continue;
+        uint8_t *row = a.out + (uint64_t)b * a.sout;
+        for (uint32_t i = threadIdx.x; i < a.heads * a.g.D; i += blockDim.x)
+            store_row<DT>(row, i, 0.0f);
+        if (a.lse)
+            for (uint32_t h = threadIdx.x; h < a.heads; h += blockDim.x)
+                a.lse[(uint64_t)b * a.heads + h] = -INFINITY;
+    }
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+// o / l, and 0 for a row without a weight; NaN stays.
+__device__ __forceinline__ float output_of(float o, float l) {
+    return l == 0.0f ? 0.0f : __fdiv_rn(o, l);
+}
+// What the running maximum subtracts: a row of -inf alone keeps weights of 0.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Where a unit's rows go: first query head, rows.
+struct UnitRows {
+    uint32_t kv, head, rows;
+};
+__device__ __forceinline__ UnitRows unit_rows(const AttnArgs &a, uint32_t unit) {
+    UnitRows u;
+    u.kv = unit / a.head_tiles;
+    const uint32_t r0 = unit % a.head_tiles * kRows;
+    u.head = u.kv * a.group + r0;
+    u.rows = a.group - r0 < kRows ? a.group - r0 : kRows;
+    return u;
+}
+
+// How a segment [t0, t1) of a unit ends: finished, or a part for the join.
+// Returns the part's index, or -1.  Thread 0 notes the unit's last CTA.
+template <uint32_t TILE>
+__device__ __forceinline__ int segment_part(const AttnArgs &a, uint32_t b, uint32_t unit,
+                                            uint32_t t0, uint32_t t1, uint32_t tiles,
+                                            uint64_t per, uint64_t start_of_unit) {
+    if (t0 == 0 && t1 == tiles)
+        return -1;
+    if (t0 != 0)
+        return 2 * blockIdx.x;
+    if (threadIdx.x == 0) {
+        const uint64_t last = (start_of_unit + tiles - 1) / per;
+        WorkSpace(a.work).meta[blockIdx.x] = make_int4((int)b, (int)unit, (int)last, 0);
+    }
+    return 2 * blockIdx.x + 1;
+}
+
+// ar_cache_attention_mma.cu: the tensor-core form, for q of two bytes and a cache whose
+// rows are whole 16-byte vectors on 16-byte boundaries.  *grid: its CTAs.
+cudaError_t launch_attention_mma(const AttnArgs &a, int dtype, bool e4m3, int *grid,
+                                 cudaStream_t s);
+
+}  // namespace ar
