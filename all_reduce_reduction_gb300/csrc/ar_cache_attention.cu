@@ -64,7 +64,7 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
                 acc[i][r] = 0.0f;
         uint32_t t = t0;
         for (;;) {
-            const uint32_t j0 = c.span.lo + t * kAnyTile;
+            const uint32_t j0 = c.span.origin + t * kAnyTile;
             __syncthreads();              // the last tile is done with
             if (tid < kAnyTile) {
                 const uint32_t j = j0 + tid;
@@ -249,7 +249,7 @@ k_attention_join(const __grid_constant__ AttnArgs a) {
 }
 
 template <int DT> static cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t s) {
-    const uint32_t rows = a.group < kRows ? a.group : kRows;
+    const uint32_t rows = a.group < a.unit_rows ? a.group : a.unit_rows;
     return launch_kernel(k_attention_join<DT>, dim3(grid, rows), kJoinThreads, 0, s, true, a);
 }
 
@@ -267,7 +267,7 @@ template <int DT, bool CACHE8> static cudaError_t attention_any(const AttnArgs &
 }
 
 template <int DT>
-static cudaError_t attention_dt(const AttnArgs &a, bool e4m3, bool w, cudaStream_t s) {
+static cudaError_t attention_dt(AttnArgs &a, bool e4m3, bool w, cudaStream_t s) {
     if (DT != AR_FP32 && w) {
         int grid = 0;
         const cudaError_t e = launch_attention_mma(a, DT, e4m3, &grid, s);
@@ -324,7 +324,9 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
     a.B = (uint32_t)B;
     a.heads = (uint32_t)heads;
     a.group = (uint32_t)(heads / kv_heads);
+    a.unit_rows = kRows;
     a.head_tiles = (a.group + kRows - 1) / kRows;
+    a.runs = 0;
     a.window = window < ((size_t)1 << 31) ? (uint32_t)window : 0u;
     const bool e4m3 = cache_dtype == AR_E4M3;
     const bool w = pages > 0 && (size_t)D * (e4m3 ? 1 : size) % 16 == 0 && wide(c.k) && wide(c.v);

@@ -19,8 +19,10 @@ struct AttnArgs {
     uint64_t sq, sout;                // bytes between rows
     float scale2;                     // scale * log2 e
     uint32_t B, heads, group;         // group: query heads that share a key-value head
+    uint32_t unit_rows;               // query heads of a unit, at most kRows
     uint32_t head_tiles;              // units of one key-value head
     uint32_t window;                  // 0: none
+    int runs;                         // tiles begin at multiples of 16 positions
 };
 
 // The workspace: where a CTA's first unit that others finish is, then (m, l) and o
@@ -39,16 +41,16 @@ static_assert(4 * kMaxCtas + 2 * (2 * kMaxCtas * kRows) + 2 * kMaxCtas * kRows <
                   2 * kMaxCtas * kRows <= AR_CACHE_WORK_ROWS,
               "the workspace has room for D = 1, and so for every D");
 
-// The range of positions [lo, n) of sequence b.
+// The range of positions [lo, n) of a sequence; its first tile begins at `origin`.
 struct Span {
-    uint32_t lo, n;
+    uint32_t lo, n, origin;
 };
 __device__ __forceinline__ Span span_of(const AttnArgs &a, uint32_t b) {
-    const uint32_t n = a.g.length(b);
-    return {a.window && n > a.window ? n - a.window : 0u, n};
+    const uint32_t n = a.g.length(b), lo = a.window && n > a.window ? n - a.window : 0u;
+    return {lo, n, a.runs ? lo & ~15u : lo};
 }
 template <uint32_t TILE> __device__ __forceinline__ uint32_t tiles_of(Span s) {
-    return (s.n - s.lo + TILE - 1) / TILE;
+    return (s.n - s.origin + TILE - 1) / TILE;
 }
 
 // A place in the order of tiles: sequence, unit, tile; `left` tiles of the run.
@@ -172,9 +174,9 @@ struct UnitRows {
 __device__ __forceinline__ UnitRows unit_rows(const AttnArgs &a, uint32_t unit) {
     UnitRows u;
     u.kv = unit / a.head_tiles;
-    const uint32_t r0 = unit % a.head_tiles * kRows;
+    const uint32_t r0 = unit % a.head_tiles * a.unit_rows;
     u.head = u.kv * a.group + r0;
-    u.rows = a.group - r0 < kRows ? a.group - r0 : kRows;
+    u.rows = a.group - r0 < a.unit_rows ? a.group - r0 : a.unit_rows;
     return u;
 }
 
@@ -196,8 +198,8 @@ __device__ __forceinline__ int segment_part(const AttnArgs &a, uint32_t b, uint3
 }
 
 // ar_cache_attention_mma.cu: the tensor-core form, for q of two bytes and a cache whose
-// rows are whole 16-byte vectors on 16-byte boundaries.  *grid: its CTAs.
-cudaError_t launch_attention_mma(const AttnArgs &a, int dtype, bool e4m3, int *grid,
-                                 cudaStream_t s);
+// rows are whole 16-byte vectors on 16-byte boundaries.  Sets the units of `a`;
+// *grid: its CTAs.
+cudaError_t launch_attention_mma(AttnArgs &a, int dtype, bool e4m3, int *grid, cudaStream_t s);
 
 }  // namespace ar
