@@ -11,6 +11,24 @@ namespace ar {
 constexpr float kCacheLeast = 0x1p-96f;
 constexpr float kCacheTop = 448.0f;
 
+// n / d for n < 2^31 without a division: (n * mul) >> shift, exact for mul =
+// ceil(2^shift / d) with shift = 31 + ceil(log2 d).
+struct Divide {
+    uint32_t mul, shift;
+    __host__ __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+        return (uint32_t)(((uint64_t)n * mul) >> shift);
+    }
+};
+inline Divide divide_by(uint32_t d) {
+    uint32_t bits = 0;
+    while (bits < 31 && (1u << bits) < d)
+        ++bits;
+    Divide x;
+    x.shift = 31 + bits;
+    x.mul = (uint32_t)((((uint64_t)1 << x.shift) + d - 1) / d);
+    return x;
+}
+
 struct Pages {
     uint8_t *k, *v;
     float *ks, *vs;               // scales, or NULL
@@ -20,6 +38,7 @@ struct Pages {
     uint64_t ldtable;
     uint32_t count, page, width;  // pages in the pool, slots of one, pages of a sequence
     uint32_t heads, D;
+    Divide by_page;
 
     // tokens of sequence b
     __host__ __device__ __forceinline__ uint32_t length(uint32_t b) const {
@@ -29,8 +48,11 @@ struct Pages {
     }
     // the page of position j of sequence b, or -1
     __host__ __device__ __forceinline__ int32_t page_of(uint32_t b, uint32_t j) const {
-        const int32_t p = table[(uint64_t)b * ldtable + j / page];
+        const int32_t p = table[(uint64_t)b * ldtable + by_page(j)];
         return (uint32_t)p < count ? p : -1;
+    }
+    __host__ __device__ __forceinline__ uint32_t slot_of(uint32_t j) const {
+        return j - by_page(j) * page;
     }
     // elements before slot s of head h in its page; rows before it in the pool
     __host__ __device__ __forceinline__ uint32_t in_page(uint32_t h, uint32_t s) const {
@@ -69,7 +91,7 @@ struct Pages {
             return none;
         int2 at;
         at.x = page_of(b, (uint32_t)j);
-        at.y = (int)((uint32_t)j % page);
+        at.y = (int)slot_of((uint32_t)j);
         return at;
     }
 };
@@ -128,6 +150,7 @@ inline PagesCheck check_pages(const void *kcache, const void *vcache, size_t ldp
     g->ldtable = ldtable ? ldtable : width;
     g->count = (uint32_t)pages;
     g->page = (uint32_t)page;
+    g->by_page = divide_by((uint32_t)page);
     g->width = (uint32_t)width;
     g->heads = (uint32_t)heads;
     g->D = (uint32_t)D;

@@ -42,12 +42,11 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
     if (tid == 0)
         WorkSpace(a.work).meta[blockIdx.x] = make_int4(0, 0, -1, 0);
     empty_rows<DT, kAnyTile>(a);
-    uint64_t per, start;
-    Cursor<kAnyTile> c = find_run<kAnyTile>(a, scan, &per, &start);
-    uint64_t index = start;               // of the cursor's tile
-    while (!c.done()) {
+    uint64_t per;
+    Cursor<kAnyTile> c = find_run<kAnyTile>(a, scan, &per);
+    for (; !c.done(); c.next_unit(a)) {
         const UnitRows u = unit_rows(a, c.unit);
-        const uint32_t b = c.b, unit = c.unit, t0 = c.t, tiles = c.tiles;
+        const uint32_t b = c.b;
         __syncthreads();
         const uint8_t *q = a.q + (uint64_t)b * a.sq + (uint64_t)u.head * D * Elem<DT>::kSize;
         for (uint32_t i = tid; i < kRows * D; i += kAnyThreads)
@@ -62,13 +61,12 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
 #pragma unroll
             for (int r = 0; r < kRows / 2; ++r)
                 acc[i][r] = 0.0f;
-        uint32_t t = t0;
-        for (;;) {
+        for (uint32_t t = c.t; t < c.t1; ++t) {
             const uint32_t j0 = c.span.origin + t * kAnyTile;
             __syncthreads();              // the last tile is done with
             if (tid < kAnyTile) {
                 const uint32_t j = j0 + tid;
-                place[tid] = j < c.span.n ? make_int2(a.g.page_of(b, j), (int)(j % a.g.page))
+                place[tid] = j < c.span.n ? make_int2(a.g.page_of(b, j), (int)a.g.slot_of(j))
                                           : make_int2(-1, 0);
             }
             __syncthreads();
@@ -154,14 +152,8 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
                         }
                     }
             }
-            ++t;
-            ++index;
-            const bool more = c.left > 1 && t < tiles;
-            c.next(a);
-            if (!more)
-                break;
         }
-        const int part = segment_part<kAnyTile>(a, b, unit, t0, t, tiles, per, index - t);
+        const int part = segment_part(a, c, per);
         const uint32_t r0 = tid / 128 * (kRows / 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -174,12 +166,12 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
                     store_row<DT>(a.out + (uint64_t)b * a.sout, (u.head + r0 + r) * D + d,
                                   output_of(acc[i][r], l_[r0 + r]));
                 else
-                    WorkSpace(a.work).o[((uint64_t)part * kRows + r0 + r) * D + d] = acc[i][r];
+                    WorkSpace(a.work).o[((uint64_t)part * a.unit_rows + r0 + r) * D + d] = acc[i][r];
             }
         }
         if (tid < u.rows) {
             if (part >= 0)
-                WorkSpace(a.work).ml[part * kRows + tid] = make_float2(m_[tid], l_[tid]);
+                WorkSpace(a.work).ml[part * a.unit_rows + tid] = make_float2(m_[tid], l_[tid]);
             else if (a.lse)
                 a.lse[(uint64_t)b * a.heads + u.head + tid] = lse_of(m_[tid], l_[tid]);
         }
@@ -188,69 +180,106 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
 
 // ---- the join ---------------------------------------------------------------------
 
-// CTA (c, r): row r of the unit that begins in CTA c's run and ends in another's.
-// Parts are added in order; `THREADS / columns` groups of threads take a run of them
-// each, and their sums are added in order too.
-constexpr int kJoinThreads = 256;
+// CTA (c, y): half of the rows of the unit that begins in CTA c's run and ends in
+// another's.  One or two warps have a row; each adds its parts in order, VEC columns a
+// lane at a time, and the two are added at the end.  Bound by latency: most CTAs find
+// nothing to do, the others read a few rows each.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
-template <int DT> __global__ void __launch_bounds__(kJoinThreads)
+template <int DT, int VEC> __global__ void __launch_bounds__(kJoinThreads)
 k_attention_join(const __grid_constant__ AttnArgs a) {
-    __shared__ float2 ml[kMaxCtas];
-    __shared__ float sums[kJoinThreads];
+    constexpr int kSteps = AR_CACHE_MAX_DIM / (32 * VEC);
+    __shared__ float other[kJoinWarps / 2][AR_CACHE_MAX_DIM];
     kernel_prologue();
     const WorkSpace w(a.work);
-    const int c = blockIdx.x, r = blockIdx.y;
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 meta = w.meta[c];
     if (meta.z < 0)
         return;
     const UnitRows u = unit_rows(a, (uint32_t)meta.y);
-    if (r >= (int)u.rows)
-        return;
+    const int rows = (int)a.unit_rows / 2, share = kJoinWarps / rows;     // warps of a row
+    const int r = (int)blockIdx.y * rows + warp / share, mine = warp % share;
+    const bool on = r < (int)u.rows;
     const int parts = meta.z - c + 1;
-    auto slot = [&](int i) { return (i == 0 ? 2 * c + 1 : 2 * (c + i)) * kRows + r; };
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < parts; i += kJoinThreads) {
-        ml[i] = w.ml[slot(i)];
-        top = fmaxf(top, ml[i].x);
-    }
+    const uint32_t D = a.g.D;
+    auto slot = [&](int i) {
+        return (uint32_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.unit_rows + r;
+    };
+    float top = -INFINITY, l = 0.0f, o[kSteps][VEC];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if ((threadIdx.x & 31) == 0)
-        sums[threadIdx.x >> 5] = top;
-    __syncthreads();
+    for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i)
-        top = fmaxf(top, sums[i]);
-    const float base = finite_max(top);
-    float l = 0.0f;
-    for (int i = 0; i < parts; ++i)
-        l += ml[i].y * exp2f(ml[i].x - base);
-    const uint32_t D = a.g.D, columns = (D + 31) / 32 * 32, groups = kJoinThreads / columns;
-    const uint32_t g = threadIdx.x / columns, d = threadIdx.x % columns;
-    const int each = (parts + (int)groups - 1) / (int)groups;
-    float o = 0.0f;
-    if (g < groups && d < D) {
-        const int end = ((int)g + 1) * each < parts ? ((int)g + 1) * each : parts;
-#pragma unroll 8
-        for (int i = (int)g * each; i < end; ++i)
-            o += w.o[(uint64_t)slot(i) * D + d] * exp2f(ml[i].x - base);
+        for (int v = 0; v < VEC; ++v)
+            o[k][v] = 0.0f;
+    if (on) {
+        for (int i = lane; i < parts; i += 32)
+            top = fmaxf(top, w.ml[slot(i)].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const float base = finite_max(top);
+        for (int i = lane; i < parts; i += 32) {
+            const float2 ml = w.ml[slot(i)];
+            l += ml.y * exp2f(ml.x - base);
+        }
+        l = warp_sum(l);
+#pragma unroll 4
+        for (int i = mine; i < parts; i += share) {
+            const float f = exp2f(w.ml[slot(i)].x - base);
+            const float *row = w.o + (uint64_t)slot(i) * D;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const uint32_t d = (uint32_t)(k * 32 + lane) * VEC;
+                if (d >= D)
+                    continue;
+                if (VEC == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(row + d);
+                    o[k][0] += x.x * f;
+                    o[k][1 % VEC] += x.y * f;
+                    o[k][2 % VEC] += x.z * f;
+                    o[k][3 % VEC] += x.w * f;
+                } else {
+                    o[k][0] += row[d] * f;
+                }
+            }
+        }
     }
-    __syncthreads();
-    sums[threadIdx.x] = o;
-    __syncthreads();
-    if (g == 0 && d < D) {
-        for (uint32_t i = 1; i < groups; ++i)
-            o += sums[i * columns + d];
-        store_row<DT>(a.out + (uint64_t)meta.x * a.sout, (u.head + r) * D + d, output_of(o, l));
+    if (share == 2) {
+        if (mine == 1)
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    other[warp / 2][(k * 32 + lane) * VEC + v] = o[k][v];
+        __syncthreads();
+        if (mine == 0)
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    o[k][v] += other[warp / 2][(k * 32 + lane) * VEC + v];
     }
-    if (threadIdx.x == 0 && a.lse)
+    if (!on || mine != 0)
+        return;
+    uint8_t *out = a.out + (uint64_t)meta.x * a.sout;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const uint32_t d = (uint32_t)(k * 32 + lane) * VEC + v;
+            if (d < D)
+                store_row<DT>(out, (u.head + r) * D + d, output_of(o[k][v], l));
+        }
+    if (lane == 0 && a.lse)
         a.lse[(uint64_t)meta.x * a.heads + u.head + r] = lse_of(top, l);
 }
 
 template <int DT> static cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t s) {
-    const uint32_t rows = a.group < a.unit_rows ? a.group : a.unit_rows;
-    return launch_kernel(k_attention_join<DT>, dim3(grid, rows), kJoinThreads, 0, s, true, a);
+    // a unit of at most half the rows has them all in the first half
+    const dim3 ctas(grid, a.group > a.unit_rows / 2 ? 2 : 1);
+    return a.g.D % 4 == 0
+               ? launch_kernel(k_attention_join<DT, 4>, ctas, kJoinThreads, 0, s, true, a)
+               : launch_kernel(k_attention_join<DT, 1>, ctas, kJoinThreads, 0, s, true, a);
 }
 
 template <int DT, bool CACHE8> static cudaError_t attention_any(const AttnArgs &a, cudaStream_t s) {
@@ -261,7 +290,7 @@ template <int DT, bool CACHE8> static cudaError_t attention_any(const AttnArgs &
     const int sms = sm_count();
     if (sms < 1)
         return cudaErrorUnknown;
-    const int grid = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    const int grid = cta_limit(a.unit_rows, 2 * sms);
     e = launch_kernel(k_attention_any<DT, CACHE8>, grid, kAnyThreads, smem, s, true, a);
     return e != cudaSuccess ? e : launch_join<DT>(a, grid, s);
 }

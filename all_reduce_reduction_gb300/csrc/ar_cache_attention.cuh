@@ -6,8 +6,9 @@
 
 namespace ar {
 
-constexpr int kRows = 16;             // query heads of a unit
-constexpr int kMaxCtas = 480;         // what the workspace has room for
+constexpr int kRows = 16;             // most query heads of a unit
+constexpr int kPartRows = 14976;      // rows of partial results: two parts a CTA
+constexpr int kMaxCtas = kPartRows / 2 / 8;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
@@ -19,14 +20,21 @@ struct AttnArgs {
     uint64_t sq, sout;                // bytes between rows
     float scale2;                     // scale * log2 e
     uint32_t B, heads, group;         // group: query heads that share a key-value head
-    uint32_t unit_rows;               // query heads of a unit, at most kRows
+    uint32_t unit_rows;               // query heads of a unit: 8 or 16
     uint32_t head_tiles;              // units of one key-value head
     uint32_t window;                  // 0: none
     int runs;                         // tiles begin at multiples of 16 positions
 };
 
+// The CTAs that a launch of `most` may have: parts for all of them fit.
+inline int cta_limit(uint32_t unit_rows, int most) {
+    const int limit = kPartRows / 2 / (int)unit_rows;
+    return most < limit ? most : limit;
+}
+
 // The workspace: where a CTA's first unit that others finish is, then (m, l) and o
-// of kRows rows for two parts of each CTA: part 0 continues a unit, part 1 begins one.
+// of unit_rows rows for two parts of each CTA: part 0 continues a unit, part 1 begins
+// one.
 struct WorkSpace {
     int4 *meta;                       // sequence, unit, last CTA (-1: none)
     float2 *ml;
@@ -34,12 +42,12 @@ struct WorkSpace {
     __device__ __forceinline__ explicit WorkSpace(float *work)
         : meta(reinterpret_cast<int4 *>(work)),
           ml(reinterpret_cast<float2 *>(work + 4 * kMaxCtas)),
-          o(work + 4 * kMaxCtas + 2 * 2 * kMaxCtas * kRows) {}
+          o(work + 4 * kMaxCtas + 2 * kPartRows) {}
 };
-static_assert(4 * kMaxCtas + 2 * (2 * kMaxCtas * kRows) + 2 * kMaxCtas * kRows <=
-                      AR_CACHE_WORK_ROWS * 3 &&
-                  2 * kMaxCtas * kRows <= AR_CACHE_WORK_ROWS,
+static_assert(4 * kMaxCtas + 2 * kPartRows + kPartRows <= AR_CACHE_WORK_ROWS * 3 &&
+                  kPartRows <= AR_CACHE_WORK_ROWS,
               "the workspace has room for D = 1, and so for every D");
+static_assert((4 * kMaxCtas + 2 * kPartRows) % 4 == 0, "o starts on a 16-byte boundary");
 
 // The range of positions [lo, n) of a sequence; its first tile begins at `origin`.
 struct Span {
@@ -53,40 +61,67 @@ template <uint32_t TILE> __device__ __forceinline__ uint32_t tiles_of(Span s) {
     return (s.n - s.origin + TILE - 1) / TILE;
 }
 
-// A place in the order of tiles: sequence, unit, tile; `left` tiles of the run.
-template <uint32_t TILE> struct Cursor {
-    uint32_t b, unit, t, tiles;
-    Span span;
-    uint64_t left;
+// Beginning and ending a unit costs about as much as this many tiles (measured, see
+// k_attention_mma): the deal counts them, so that CTAs with many short units have
+// fewer tiles.  A unit of n tiles has kUnitCost + n places in the order; the first
+// kUnitCost of them stand for no tile.
+constexpr uint32_t kUnitCost = 2;
 
-    __device__ __forceinline__ bool done() const { return left == 0; }
+// A place in a CTA's run: tiles [t, t1) of a unit.
+template <uint32_t TILE> struct Cursor {
+    uint32_t b, unit, t, t1, tiles;
+    Span span;
+    uint64_t base;                    // place of the unit's first
+    uint64_t left;                    // places of the run past the unit's
+
+    __device__ __forceinline__ bool done() const { return t >= t1; }
+    __device__ __forceinline__ void begin(const AttnArgs &a, uint64_t in) {
+        // the run enters the unit at its place `in`
+        const uint64_t all = kUnitCost + tiles, end = all - in < left ? all : in + left;
+        left -= end - in;
+        t = in > kUnitCost ? (uint32_t)(in - kUnitCost) : 0u;
+        t1 = end > kUnitCost ? (uint32_t)(end - kUnitCost) : 0u;
+        if (t >= t1 && left > 0)      // places for no tile only
+            next_unit(a);
+    }
+    __device__ __forceinline__ void next_unit(const AttnArgs &a) {
+        t = t1 = 0;
+        if (left == 0)
+            return;
+        base += kUnitCost + tiles;
+        if (++unit == a.g.heads * a.head_tiles) {
+            unit = 0;
+            do {
+                span = span_of(a, ++b);
+                tiles = tiles_of<TILE>(span);
+            } while (tiles == 0);     // `left` says that there is another
+        }
+        const uint64_t all = kUnitCost + tiles, end = all < left ? all : left;
+        left -= end;
+        t1 = end > kUnitCost ? (uint32_t)(end - kUnitCost) : 0u;
+    }
     __device__ __forceinline__ void next(const AttnArgs &a) {
-        if (--left == 0 || ++t < tiles)
-            return;
-        t = 0;
-        if (++unit < a.g.heads * a.head_tiles)
-            return;
-        unit = 0;
-        do {
-            span = span_of(a, ++b);
-            tiles = tiles_of<TILE>(span);
-        } while (tiles == 0);             // `left` says that there is another
+        if (++t >= t1)
+            next_unit(a);
     }
 };
 
-// This CTA's run.  `part` is shared memory of 33 words.  *per: tiles of a run.
+// This CTA's run.  `part` is shared memory of 32 words.  *per: places of a run.
 template <uint32_t TILE>
 __device__ __forceinline__ Cursor<TILE> find_run(const AttnArgs &a, uint64_t *part,
-                                                 uint64_t *per, uint64_t *start) {
+                                                 uint64_t *per) {
     // every thread counts a run of sequences; their sums are scanned
     const uint32_t each = (a.B + blockDim.x - 1) / blockDim.x;
     const uint32_t b0 = threadIdx.x * each;
     const uint32_t b1 = b0 + each < a.B ? b0 + each : a.B;
     const uint32_t units = a.g.heads * a.head_tiles;
+    auto places = [&](uint32_t b) -> uint64_t {
+        const uint32_t n = tiles_of<TILE>(span_of(a, b));
+        return n ? (uint64_t)(n + kUnitCost) * units : 0;
+    };
     uint64_t mine = 0;
     for (uint32_t b = b0; b < b1; ++b)
-        mine += tiles_of<TILE>(span_of(a, b));
-    mine *= units;
+        mine += places(b);
     uint64_t sum = mine;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -95,12 +130,12 @@ __device__ __forceinline__ Cursor<TILE> find_run(const AttnArgs &a, uint64_t *pa
         if (lane >= d)
             sum += other;
     }
-    __shared__ uint32_t at[4];
+    __shared__ uint32_t at[2];
     __shared__ uint64_t before;
     if (lane == 31)
         part[warp] = sum;
     if (threadIdx.x == 0)
-        at[3] = 0;
+        at[1] = 0;
     __syncthreads();
     uint64_t total = 0;
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
@@ -109,33 +144,32 @@ __device__ __forceinline__ Cursor<TILE> find_run(const AttnArgs &a, uint64_t *pa
         total += part[w];
     }
     *per = (total + gridDim.x - 1) / gridDim.x;
-    if (*per < 1)
-        *per = 1;
-    *start = *per * blockIdx.x;
-    if (*start >= sum - mine && *start < sum) {
+    const uint64_t start = *per * blockIdx.x;
+    if (start >= sum - mine && start < sum) {
         uint64_t base = sum - mine;
         uint32_t b = b0;
         for (;; ++b) {
-            const uint64_t n = (uint64_t)tiles_of<TILE>(span_of(a, b)) * units;
-            if (*start < base + n)
+            const uint64_t n = places(b);
+            if (start < base + n)
                 break;
             base += n;
         }
         at[0] = b;
-        at[3] = 1;
+        at[1] = 1;
         before = base;
     }
     __syncthreads();
     Cursor<TILE> c = {};
-    if (!at[3])
-        return c;                         // past the last tile
+    if (!at[1])
+        return c;                         // past the last place
     c.b = at[0];
     c.span = span_of(a, c.b);
     c.tiles = tiles_of<TILE>(c.span);
-    const uint64_t in = *start - before;
-    c.unit = (uint32_t)(in / c.tiles);
-    c.t = (uint32_t)(in % c.tiles);
-    c.left = total - *start < *per ? total - *start : *per;
+    const uint64_t all = kUnitCost + c.tiles, in = start - before;
+    c.unit = (uint32_t)(in / all);
+    c.base = before + c.unit * all;
+    c.left = total - start < *per ? total - start : *per;
+    c.begin(a, in % all);
     return c;
 }
 
@@ -180,19 +214,18 @@ __device__ __forceinline__ UnitRows unit_rows(const AttnArgs &a, uint32_t unit) 
     return u;
 }
 
-// How a segment [t0, t1) of a unit ends: finished, or a part for the join.
-// Returns the part's index, or -1.  Thread 0 notes the unit's last CTA.
+// How the cursor's segment ends: its unit is finished (-1), or it is a part for the
+// join, and which.  Thread 0 notes the unit's last CTA.
 template <uint32_t TILE>
-__device__ __forceinline__ int segment_part(const AttnArgs &a, uint32_t b, uint32_t unit,
-                                            uint32_t t0, uint32_t t1, uint32_t tiles,
-                                            uint64_t per, uint64_t start_of_unit) {
-    if (t0 == 0 && t1 == tiles)
+__device__ __forceinline__ int segment_part(const AttnArgs &a, const Cursor<TILE> &c,
+                                            uint64_t per) {
+    if (c.t == 0 && c.t1 == c.tiles)
         return -1;
-    if (t0 != 0)
+    if (c.t != 0)
         return 2 * blockIdx.x;
     if (threadIdx.x == 0) {
-        const uint64_t last = (start_of_unit + tiles - 1) / per;
-        WorkSpace(a.work).meta[blockIdx.x] = make_int4((int)b, (int)unit, (int)last, 0);
+        const uint64_t last = (c.base + kUnitCost + c.tiles - 1) / per;
+        WorkSpace(a.work).meta[blockIdx.x] = make_int4((int)c.b, (int)c.unit, (int)last, 0);
     }
     return 2 * blockIdx.x + 1;
 }

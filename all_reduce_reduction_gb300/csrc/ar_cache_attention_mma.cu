@@ -34,7 +34,11 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t r[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// 16 bytes to shared memory in the background; `bytes` of them, the rest zeros.
+// 16 bytes to shared memory in the background.
+__device__ __forceinline__ void fetch16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
+}
+// `bytes` of them, the rest zeros.
 __device__ __forceinline__ void fetch16(uint32_t to, const void *from, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(to), "l"(from), "r"(bytes) : "memory");
@@ -79,10 +83,13 @@ template <int DT, bool CACHE8, int DC, int NT> struct MmaForm {
     static constexpr uint32_t kRing = kMmaWarps * kStages * kStage;
     static constexpr uint32_t kQ = kHeads * DC * 2;
     // columns of the output that the warps join at a time
-    static constexpr int kJoin = CACHE8 && DC == 256 ? 16 : 32;
+    static constexpr int kJoin = CACHE8 && DC >= 128 ? 16 : 32;
     static constexpr uint32_t kJoinRow = kJoin + 2;
     static constexpr uint32_t kSmem = kRing + kQ + 4 * kMmaWarps * kHeads * kJoinRow;
-    static constexpr int kCtas = DC == 256 ? (CACHE8 ? 2 : 1) : DC == 128 && !CACHE8 ? 2 : 3;
+    // CTAs of an SM: what registers and shared memory hold
+    static constexpr int kCtas = DC == 256   ? (CACHE8 ? 2 : 1)
+                                 : DC == 128 ? (!CACHE8 ? 2 : NT == 1 ? 4 : 3)
+                                             : (CACHE8 && NT == 1 ? 4 : 3);
 
     // chunk c of row r: the rows of a group of eight lie in different banks
     static __device__ __forceinline__ uint32_t chunk(uint32_t r, uint32_t c) {
@@ -106,7 +113,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaForm<DT, CACHE8, DC, NT>::kCta
 k_attention_mma(const __grid_constant__ AttnArgs a) {
     using M = MmaForm<DT, CACHE8, DC, NT>;
     constexpr uint32_t H = M::kHeads;
-    constexpr bool kKeepQ = DC * NT <= 256;  // q's operands stay in registers
+    constexpr bool kKeepQ = DC * NT <= (CACHE8 ? 128 : 256);  // q's operands stay in registers
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t scan[33];
     __shared__ float warp_m[kMmaWarps][H], warp_l[kMmaWarps][H], head_scale[H];
@@ -119,15 +126,42 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     if (tid == 0)
         WorkSpace(a.work).meta[blockIdx.x] = make_int4(0, 0, -1, 0);
     empty_rows<DT, kMmaTile>(a);
-    uint64_t per, start;
-    Cursor<kMmaTile> c = find_run<kMmaTile>(a, scan, &per, &start);
-    uint64_t index = start;
+    uint64_t per;
+    Cursor<kMmaTile> c = find_run<kMmaTile>(a, scan, &per);
+
+    // ---- q of a unit, two elements a word, a warp to a row: loaded a unit ahead
+    constexpr int kQRows = H / kMmaWarps, kQWords = DC / 64;
+    const bool q_words = ((uintptr_t)a.q | a.sq) % 4 == 0;
+    uint32_t qw[kQRows][kQWords];
+    auto load_q_rows = [&] {
+        if (c.done())
+            return;
+        const UnitRows u = unit_rows(a, c.unit);
+        const uint8_t *q = a.q + (uint64_t)c.b * a.sq + (uint64_t)u.head * D * 2;
+#pragma unroll
+        for (int k = 0; k < kQRows; ++k)
+#pragma unroll
+            for (int i = 0; i < kQWords; ++i) {
+                const uint32_t r = warp + k * kMmaWarps, d = 2 * lane + 64 * i;
+                qw[k][i] = 0u;
+                if (r < u.rows && d < D) {
+                    const uint8_t *x = q + (uint64_t)(r * D + d) * 2;
+                    if (q_words)
+                        qw[k][i] = *reinterpret_cast<const uint32_t *>(x);
+                    else
+                        qw[k][i] = ld_elem<DT>(x, 0) | ld_elem<DT>(x, 1) << 16;
+                }
+            }
+    };
+    load_q_rows();
 
     // ---- the copies, some tiles ahead.  Where 16 positions lie in one page (a.runs) the
     // warp looks up one page, otherwise a lane one for each of its rows.
     Cursor<kMmaTile> f = c;
     const uint32_t copy_row = lane / M::kChunks, copy_chunk = lane % M::kChunks;
     const uint32_t row_bytes = D * M::kCell;
+    const uint32_t copy_from = copy_row * row_bytes + copy_chunk * 16;
+    const bool column = copy_chunk * 16 < row_bytes;
     uint32_t slot = 0;
     int32_t page = -1;
     auto look_up = [&] {                                   // of the next tile to fetch
@@ -137,7 +171,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
         page = -1;
         if (j < f.span.n) {
             page = a.g.page_of(f.b, j);
-            slot = j % a.g.page;
+            slot = a.g.slot_of(j);
         }
     };
     auto fetch = [&](uint32_t stage) {
@@ -149,20 +183,30 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             const uint32_t from = f.span.lo > j0 ? f.span.lo - j0 : 0u;
             const uint32_t left = f.span.n > j0 ? f.span.n - j0 : 0u;
             uint32_t mask = ((left < 16 ? 1u << left : 0x10000u) - 1u) & (0xFFFFu << from);
-            uint64_t at = page >= 0 ? (uint64_t)page * a.g.stride +
-                                          (uint64_t)a.g.in_page(kv, slot) * M::kCell
-                                    : 0;
-            const bool column = copy_chunk * 16 < row_bytes;
+            const uint64_t at = page >= 0 ? (uint64_t)page * a.g.stride +
+                                                (uint64_t)a.g.in_page(kv, slot) * M::kCell
+                                          : 0;
             if (a.runs) {
                 mask = page >= 0 ? mask : 0u;
-                uint64_t src = at + copy_row * row_bytes + copy_chunk * 16;
+                const uint8_t *k = a.g.k + at + copy_from, *v = a.g.v + at + copy_from;
+                if (mask == 0xFFFFu && row_bytes == M::kRow) {
 #pragma unroll
-                for (uint32_t i = 0; i < 16 / M::kRowsPer; ++i) {
-                    const uint32_t r = i * M::kRowsPer + copy_row;
-                    const bool on = column && (mask >> r & 1u);
-                    const uint64_t x = on ? src + (uint64_t)(i * M::kRowsPer * row_bytes) : 0;
-                    fetch16(to + M::chunk(r, copy_chunk), a.g.k + x, on ? 16 : 0);
-                    fetch16(to + 16 * M::kRow + M::chunk(r, copy_chunk), a.g.v + x, on ? 16 : 0);
+                    for (uint32_t i = 0; i < 16 / M::kRowsPer; ++i) {
+                        const uint32_t r = i * M::kRowsPer + copy_row;
+                        const uint32_t x = i * M::kRowsPer * M::kRow;
+                        fetch16(to + M::chunk(r, copy_chunk), k + x);
+                        fetch16(to + 16 * M::kRow + M::chunk(r, copy_chunk), v + x);
+                    }
+                } else {
+#pragma unroll
+                    for (uint32_t i = 0; i < 16 / M::kRowsPer; ++i) {
+                        const uint32_t r = i * M::kRowsPer + copy_row;
+                        const bool on = column && (mask >> r & 1u);
+                        const uint32_t x = on ? i * M::kRowsPer * row_bytes : 0u;
+                        fetch16(to + M::chunk(r, copy_chunk), on ? k + x : a.g.k, on ? 16 : 0);
+                        fetch16(to + 16 * M::kRow + M::chunk(r, copy_chunk), on ? v + x : a.g.v,
+                                on ? 16 : 0);
+                    }
                 }
             } else {
                 mask &= __ballot_sync(0xFFFFFFFFu, page >= 0) & 0xFFFFu;
@@ -218,30 +262,32 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     };
 
     while (!c.done()) {
-        const UnitRows u = unit_rows(a, c.unit);
-        const uint32_t b = c.b, unit = c.unit, t0 = c.t, tiles = c.tiles;
-        // q, a warp to a row: binary16 after scaling by a power of two where the cache is E4M3
-        for (uint32_t r = warp; r < H; r += kMmaWarps) {
-            const uint8_t *q = a.q + (uint64_t)b * a.sq + (uint64_t)(u.head + r) * D * 2;
-            float v[DC / 32], top = 0.0f;
+        // q to shared memory: binary16 after scaling by a power of two where the cache is E4M3
 #pragma unroll
-            for (int i = 0; i < DC / 32; ++i) {
-                const uint32_t d = lane + 32 * i;
-                v[i] = r < u.rows && d < D ? widen1<DT>(ld_elem<DT>(q, d)) : 0.0f;
-                top = fmaxf(top, fabsf(v[i]));
-            }
+        for (int k = 0; k < kQRows; ++k) {
+            const uint32_t r = warp + k * kMmaWarps;
             float up = 1.0f, back = 1.0f;
             if (CACHE8) {
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kQWords; ++i) {
+                    const float2 x = widen2<DT>(qw[k][i]);
+                    top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+                }
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1)
                     top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
                 half_range(top, up, back);
             }
 #pragma unroll
-            for (int i = 0; i < DC / 32; ++i) {
-                const uint32_t e = M::q_column(lane + 32 * i);
-                *reinterpret_cast<uint16_t *>(qs + M::q_chunk(r, e / 8) + e % 8 * 2) =
-                    (uint16_t)narrow1<M::kType>(v[i] * up);
+            for (int i = 0; i < kQWords; ++i) {
+                const uint32_t e = M::q_column(2 * lane + 64 * i);
+                uint32_t w = qw[k][i];
+                if (CACHE8) {
+                    const float2 x = widen2<DT>(w);
+                    w = half2_of(x.x * up, x.y * up);
+                }
+                *reinterpret_cast<uint32_t *>(qs + M::q_chunk(r, e / 8) + e % 8 * 2) = w;
             }
             if (lane == 0)
                 head_scale[r] = a.scale2 * back;
@@ -253,14 +299,15 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             for (int k = 0; k < DC / 16; k += 2)
                 load_q(qf + (kKeepQ ? k : 0), k);
         // of a lane's columns: heads 8 * n + 2 * (lane % 4) + {0, 1}
-        float scale[NT][2], m[NT][2], l[NT][2], o[DC / 16][NT][4];
+        // m, and what a score is compared with and taken relative to
+        float scale[NT][2], m[NT][2], bound[NT][2], base[NT][2], l[NT][2], o[DC / 16][NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 scale[n][i] = head_scale[8 * n + lane % 4 * 2 + i];
-                m[n][i] = -INFINITY;
-                l[n][i] = 0.0f;
+                m[n][i] = bound[n][i] = -INFINITY;
+                base[n][i] = l[n][i] = 0.0f;
             }
 #pragma unroll
         for (int d = 0; d < DC / 16; ++d)
@@ -270,8 +317,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 for (int i = 0; i < 4; ++i)
                     o[d][n][i] = 0.0f;
 
-        uint32_t t = t0;
-        for (;;) {
+        for (uint32_t t = c.t; t < c.t1; ++t) {
             fetch_wait<M::kStages - 2>();
             __syncwarp();
             // every lane is done with the stage before this one
@@ -334,7 +380,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     if (mask != 0xFFFFu && !(mask >> (lane / 4 + i / 2 * 8) & 1u))
                         s[n][i] = -INFINITY;
                     s2[n][i] = CACHE8 ? s[n][i] + lead[i / 2] : s[n][i];
-                    above |= s2[n][i] > m[n][i & 1] + kSlack;
+                    above |= s2[n][i] > bound[n][i & 1];
                 }
             if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
@@ -348,6 +394,8 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                             now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, d));
                         al[i] = exp2_approx(m[n][i] - finite_max(now));
                         m[n][i] = now;
+                        bound[n][i] = now + kSlack;
+                        base[n][i] = finite_max(now) - (CACHE8 ? kWeightBits : 0.0f);
                         l[n][i] *= al[i];
                     }
 #pragma unroll
@@ -365,8 +413,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 float p[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float base = finite_max(m[n][i & 1]);
-                    p[i] = exp2_approx(CACHE8 ? s[n][i] - base + kWeightBits : s[n][i] - base);
+                    p[i] = exp2_approx(s[n][i] - base[n][i & 1]);
                     l[n][i & 1] += p[i];
                     if (CACHE8)
                         p[i] *= vs[i / 2];
@@ -408,13 +455,10 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     }
             }
             stage = (stage + 1) % M::kStages;
-            ++t;
-            ++index;
-            const bool more = c.left > 1 && t < tiles;
-            c.next(a);
-            if (!more)
-                break;
         }
+        const Cursor<kMmaTile> done = c;
+        c.next_unit(a);
+        load_q_rows();
 
         // the warps' parts, in their order; what they are relative to
 #pragma unroll
@@ -432,7 +476,8 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 }
             }
         __syncthreads();
-        const int part = segment_part<kMmaTile>(a, b, unit, t0, t, tiles, per, index - t);
+        const UnitRows u = unit_rows(a, done.unit);
+        const int part = segment_part(a, done, per);
         float own[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -484,17 +529,17 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 if (row >= u.rows || d >= D)
                     continue;
                 if (part < 0)
-                    store_row<DT>(a.out + (uint64_t)b * a.sout, (u.head + row) * D + d,
+                    store_row<DT>(a.out + (uint64_t)done.b * a.sout, (u.head + row) * D + d,
                                   output_of(v, row_l));
                 else
-                    WorkSpace(a.work).o[((uint64_t)part * kRows + row) * D + d] = v;
+                    WorkSpace(a.work).o[((uint64_t)part * H + row) * D + d] = v;
             }
         }
         if (tid % kLanes == 0 && row < u.rows) {
             if (part >= 0)
-                WorkSpace(a.work).ml[part * kRows + row] = make_float2(row_m, row_l);
+                WorkSpace(a.work).ml[part * H + row] = make_float2(row_m, row_l);
             else if (a.lse)
-                a.lse[(uint64_t)b * a.heads + u.head + row] = lse_of(row_m, row_l);
+                a.lse[(uint64_t)done.b * a.heads + u.head + row] = lse_of(row_m, row_l);
         }
     }
     fetch_wait<0>();
@@ -512,7 +557,7 @@ static cudaError_t mma_form(AttnArgs &a, int *grid, cudaStream_t s) {
     a.unit_rows = M::kHeads;
     a.head_tiles = (a.group + M::kHeads - 1) / M::kHeads;
     a.runs = a.g.page % 16 == 0;
-    *grid = M::kCtas * sms < kMaxCtas ? M::kCtas * sms : kMaxCtas;
+    *grid = cta_limit(a.unit_rows, M::kCtas * sms);
     return launch_kernel(k_attention_mma<DT, CACHE8, DC, NT>, *grid, kMmaThreads, M::kSmem, s, true,
                          a);
 }

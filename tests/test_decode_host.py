@@ -48,6 +48,7 @@ int main() {
         g.ldtable = width;
         g.count = count;
         g.page = page;
+        g.by_page = divide_by(page);
         g.width = width;
         g.heads = 2;
         g.D = 5;
@@ -80,6 +81,18 @@ int main() {
                 return printf("row %u at (%d, %d), not (%d, %d)\n", t, at.x, at.y, want, slot), 1;
         }
     }
+    // the division, at both ends of each quotient's range
+    for (uint32_t d = 1; d < 5000; ++d)
+        for (uint64_t n = 0; n < 1ull << 31; n = n * 2 + d) {
+            const uint64_t q = n / d * d;
+            for (uint64_t x : {n, q, q ? q - 1 : q, q + d - 1, (uint64_t)((1u << 31) - 1)})
+                if (x < 1ull << 31 && divide_by(d)((uint32_t)x) != x / d)
+                    return printf("%llu / %u\n", (unsigned long long)x, d), 1;
+        }
+    for (uint32_t d : {1u << 30, (1u << 30) + 1, (1u << 31) - 1, 1u << 31})
+        for (uint32_t x : {0u, 1u, (1u << 30) - 1, 1u << 30, (1u << 30) + 1, (1u << 31) - 1})
+            if (divide_by(d)(x) != x / d)
+                return printf("%u / %u\n", x, d), 1;
     // offsets past 32 bits
     Pages g = {};
     g.heads = 1024;
