@@ -22,6 +22,7 @@ namespace ar {
 // A tile of keys, then of values, in shared memory as binary32; a thread has one
 // key and four rows of the scores, then one or two columns of the outputs and half
 // of the rows.
+constexpr int kRows = 16;             // query heads of a unit
 constexpr int kAnyThreads = 256;
 constexpr uint32_t kAnyTile = 64;
 
@@ -180,93 +181,98 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
 
 // ---- the join ---------------------------------------------------------------------
 
-// CTA (c, y): half of the rows of the unit that begins in CTA c's run and ends in
-// another's.  One or two warps have a row; each adds its parts in order, VEC columns a
-// lane at a time, and the two are added at the end.  Bound by latency: most CTAs find
-// nothing to do, the others read a few rows each.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+// CTA (c, r): row r of the unit that begins in CTA c's run and ends in another's.  Its
+// warps take a share of the parts each, VEC columns a lane at a time, and their sums
+// are added in order.  Bound by latency: most CTAs find nothing to do, the others wait
+// three times for memory.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
 template <int DT, int VEC> __global__ void __launch_bounds__(kJoinThreads)
 k_attention_join(const __grid_constant__ AttnArgs a) {
     constexpr int kSteps = AR_CACHE_MAX_DIM / (32 * VEC);
-    __shared__ float other[kJoinWarps / 2][AR_CACHE_MAX_DIM];
+    __shared__ float weight[kMaxCtas], part[kJoinWarps], sums[kJoinWarps - 1][AR_CACHE_MAX_DIM];
     kernel_prologue();
     const WorkSpace w(a.work);
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int4 meta = w.meta[c];
     if (meta.z < 0)
         return;
     const UnitRows u = unit_rows(a, (uint32_t)meta.y);
-    const int rows = (int)a.unit_rows / 2, share = kJoinWarps / rows;     // warps of a row
-    const int r = (int)blockIdx.y * rows + warp / share, mine = warp % share;
-    const bool on = r < (int)u.rows;
+    if (r >= (int)u.rows)
+        return;
     const int parts = meta.z - c + 1;
     const uint32_t D = a.g.D;
     auto slot = [&](int i) {
         return (uint32_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.unit_rows + r;
     };
-    float top = -INFINITY, l = 0.0f, o[kSteps][VEC];
+    float top = -INFINITY;
+    for (int i = tid; i < parts; i += kJoinThreads)
+        top = fmaxf(top, weight[i] = w.ml[slot(i)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if (lane == 0)
+        part[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i)
+        top = fmaxf(top, part[i]);
+    float l = 0.0f;
+    for (int i = tid; i < parts; i += kJoinThreads) {
+        weight[i] = exp2f(weight[i] - finite_max(top));
+        l += w.ml[slot(i)].y * weight[i];
+    }
+    l = warp_sum(l);
+    __syncthreads();
+    if (lane == 0)
+        part[warp] = l;
+    float o[kSteps][VEC];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
             o[k][v] = 0.0f;
-    if (on) {
-        for (int i = lane; i < parts; i += 32)
-            top = fmaxf(top, w.ml[slot(i)].x);
+#pragma unroll 8
+    for (int i = warp; i < parts; i += kJoinWarps) {
+        const float *row = w.o + (uint64_t)slot(i) * D;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        const float base = finite_max(top);
-        for (int i = lane; i < parts; i += 32) {
-            const float2 ml = w.ml[slot(i)];
-            l += ml.y * exp2f(ml.x - base);
-        }
-        l = warp_sum(l);
-#pragma unroll 4
-        for (int i = mine; i < parts; i += share) {
-            const float f = exp2f(w.ml[slot(i)].x - base);
-            const float *row = w.o + (uint64_t)slot(i) * D;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const uint32_t d = (uint32_t)(k * 32 + lane) * VEC;
-                if (d >= D)
-                    continue;
-                if (VEC == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(row + d);
-                    o[k][0] += x.x * f;
-                    o[k][1 % VEC] += x.y * f;
-                    o[k][2 % VEC] += x.z * f;
-                    o[k][3 % VEC] += x.w * f;
-                } else {
-                    o[k][0] += row[d] * f;
-                }
+        for (int k = 0; k < kSteps; ++k) {
+            const uint32_t d = (uint32_t)(k * 32 + lane) * VEC;
+            if (d >= D)
+                continue;
+            if (VEC == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(row + d);
+                o[k][0] += x.x * weight[i];
+                o[k][1 % VEC] += x.y * weight[i];
+                o[k][2 % VEC] += x.z * weight[i];
+                o[k][3 % VEC] += x.w * weight[i];
+            } else {
+                o[k][0] += row[d] * weight[i];
             }
         }
     }
-    if (share == 2) {
-        if (mine == 1)
+    if (warp > 0)
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k)
+        for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    other[warp / 2][(k * 32 + lane) * VEC + v] = o[k][v];
-        __syncthreads();
-        if (mine == 0)
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    o[k][v] += other[warp / 2][(k * 32 + lane) * VEC + v];
-    }
-    if (!on || mine != 0)
+            for (int v = 0; v < VEC; ++v)
+                sums[warp - 1][(k * 32 + lane) * VEC + v] = o[k][v];
+    __syncthreads();
+    if (warp > 0)
         return;
+    l = part[0];
+#pragma unroll
+    for (int i = 1; i < kJoinWarps; ++i)
+        l += part[i];
     uint8_t *out = a.out + (uint64_t)meta.x * a.sout;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const uint32_t d = (uint32_t)(k * 32 + lane) * VEC + v;
+#pragma unroll
+            for (int i = 0; i < kJoinWarps - 1; ++i)
+                o[k][v] += sums[i][d];
             if (d < D)
                 store_row<DT>(out, (u.head + r) * D + d, output_of(o[k][v], l));
         }
@@ -275,8 +281,7 @@ k_attention_join(const __grid_constant__ AttnArgs a) {
 }
 
 template <int DT> static cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t s) {
-    // a unit of at most half the rows has them all in the first half
-    const dim3 ctas(grid, a.group > a.unit_rows / 2 ? 2 : 1);
+    const dim3 ctas(grid, a.group < a.unit_rows ? a.group : a.unit_rows);
     return a.g.D % 4 == 0
                ? launch_kernel(k_attention_join<DT, 4>, ctas, kJoinThreads, 0, s, true, a)
                : launch_kernel(k_attention_join<DT, 1>, ctas, kJoinThreads, 0, s, true, a);

@@ -6,7 +6,6 @@
 
 namespace ar {
 
-constexpr int kRows = 16;             // most query heads of a unit
 constexpr int kPartRows = 14976;      // rows of partial results: two parts a CTA
 constexpr int kMaxCtas = kPartRows / 2 / 8;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -20,7 +19,7 @@ struct AttnArgs {
     uint64_t sq, sout;                // bytes between rows
     float scale2;                     // scale * log2 e
     uint32_t B, heads, group;         // group: query heads that share a key-value head
-    uint32_t unit_rows;               // query heads of a unit: 8 or 16
+    uint32_t unit_rows;               // query heads of a unit: 8, 16 or 32
     uint32_t head_tiles;              // units of one key-value head
     uint32_t window;                  // 0: none
     int runs;                         // tiles begin at multiples of 16 positions

@@ -1,19 +1,20 @@
 // Attention over the paged cache on the tensor cores, for keys and values of two
 // bytes (in the type of q) or one (E4M3, in binary16).
 //
-// A warp's products have 16 positions by 8 or 16 query heads that share a key-value
-// head: s' = k q', then o' += v' p', so that keys and values are the operand of 16
-// rows and heads fill the columns.  A warp has its own positions of every tile, its
-// own ring of them in shared memory, filled by background copies a few tiles ahead
-// (across the ends of units), and its own running maximum and sums; nothing waits for
-// another warp until a unit ends.
+// A warp's products have 16 positions by 8 query heads that share a key-value head:
+// s' = k q', then o' += v' p', so that keys and values are the operand of 16 rows and
+// heads fill the columns.  Four groups of warps have 16 positions of every tile each,
+// in their own ring in shared memory, filled by background copies a few tiles ahead
+// (across the ends of units); the 1, 2 or 4 warps of a group take 8 heads each of the
+// same positions.  A warp has its own running maximum and sums; groups wait for one
+// another only where a unit ends.
 #include "ar_cache_attention.cuh"
 #include "ar_mma.cuh"
 
 namespace ar {
 
-constexpr int kMmaWarps = 4, kMmaThreads = 32 * kMmaWarps;
-constexpr uint32_t kMmaTile = 16 * kMmaWarps;
+constexpr int kTeams = 4;                     // of warps, 16 positions of a tile each
+constexpr uint32_t kMmaTile = 16 * kTeams;
 
 // The running maximum follows a row's scores only when one is this far above it
 // (as exponents of two): weights up to 2^4 cost nothing, new factors for all of o do.
@@ -69,27 +70,30 @@ template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return DT == AR_BF16 ? narrow2<AR_BF16>(a, b) : narrow2<AR_FP16>(a, b);
 }
 
-template <int DT, bool CACHE8, int DC, int NT> struct MmaForm {
+template <int DT, bool CACHE8, int DC, int HG> struct MmaForm {
     static constexpr int kType = CACHE8 ? (int)AR_FP16 : DT;      // of the products
     static constexpr uint32_t kCell = CACHE8 ? 1 : 2;
-    static constexpr uint32_t kHeads = 8 * NT;                     // columns
+    static constexpr uint32_t kHeads = 8 * HG;                     // of a unit
+    static constexpr int kThreads = 32 * kTeams * HG;
     static constexpr uint32_t kRow = DC * kCell;                   // bytes of a row in shared memory
     static constexpr uint32_t kChunks = kRow / 16;
     static constexpr uint32_t kRowsPer = 32 / kChunks;             // rows that a warp copies at once
     // a warp's stage: 16 keys, 16 values, their scales, which positions are there
     static constexpr uint32_t kScales = 32 * kRow, kMask = kScales + (CACHE8 ? 128 : 0);
     static constexpr uint32_t kStage = kMask + 16;
-    static constexpr int kStages = 3;
-    static constexpr uint32_t kRing = kMmaWarps * kStages * kStage;
+    static constexpr int kStages = HG == 4 && DC < 256 ? 5 : 3;
+    static constexpr uint32_t kRing = kTeams * kStages * kStage;
     static constexpr uint32_t kQ = kHeads * DC * 2;
     // columns of the output that the warps join at a time
-    static constexpr int kJoin = CACHE8 && DC >= 128 ? 16 : 32;
+    static constexpr int kJoin = DC == 256 || (CACHE8 && DC == 128) ? 16 : 32;
     static constexpr uint32_t kJoinRow = kJoin + 2;
-    static constexpr uint32_t kSmem = kRing + kQ + 4 * kMmaWarps * kHeads * kJoinRow;
-    // CTAs of an SM: what registers and shared memory hold
-    static constexpr int kCtas = DC == 256   ? (CACHE8 ? 2 : 1)
-                                 : DC == 128 ? (!CACHE8 ? 2 : NT == 1 ? 4 : 3)
-                                             : (CACHE8 && NT == 1 ? 4 : 3);
+    static constexpr uint32_t kSmem = kRing + kQ + 4 * kTeams * kHeads * kJoinRow;
+    // CTAs of an SM: what registers and shared memory hold (and, for 32 heads, parts in
+    // the workspace)
+    static constexpr int kCtas = HG == 4     ? 1
+                                 : DC == 256 ? (CACHE8 && HG == 1 ? 2 : 1)
+                                 : DC == 128 ? (!CACHE8 ? 2 : HG == 1 ? 4 : 2)
+                                             : (CACHE8 && HG == 1 ? 4 : HG == 1 ? 3 : 2);
 
     // chunk c of row r: the rows of a group of eight lie in different banks
     static __device__ __forceinline__ uint32_t chunk(uint32_t r, uint32_t c) {
@@ -108,19 +112,20 @@ template <int DT, bool CACHE8, int DC, int NT> struct MmaForm {
     }
 };
 
-template <int DT, bool CACHE8, int DC, int NT>
-__global__ void __launch_bounds__(kMmaThreads, MmaForm<DT, CACHE8, DC, NT>::kCtas)
+template <int DT, bool CACHE8, int DC, int HG>
+__global__ void __launch_bounds__(MmaForm<DT, CACHE8, DC, HG>::kThreads, MmaForm<DT, CACHE8, DC, HG>::kCtas)
 k_attention_mma(const __grid_constant__ AttnArgs a) {
-    using M = MmaForm<DT, CACHE8, DC, NT>;
+    using M = MmaForm<DT, CACHE8, DC, HG>;
     constexpr uint32_t H = M::kHeads;
-    constexpr bool kKeepQ = DC * NT <= (CACHE8 ? 128 : 256);  // q's operands stay in registers
+    constexpr bool kKeepQ = DC <= 128;   // q's operands stay in registers
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t scan[33];
-    __shared__ float warp_m[kMmaWarps][H], warp_l[kMmaWarps][H], head_scale[H];
+    __shared__ float group_m[kTeams][H], group_l[kTeams][H], head_scale[H];
     uint8_t *qs = smem + M::kRing;
     float *join = reinterpret_cast<float *>(qs + M::kQ);
     const uint32_t D = a.g.D, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    uint8_t *ring = smem + warp * (M::kStages * M::kStage);
+    const uint32_t group = warp / HG, part8 = warp % HG;   // positions; heads
+    uint8_t *ring = smem + group * (M::kStages * M::kStage);
     const uint32_t ring_addr = shared_addr(ring), q_addr = shared_addr(qs);
     kernel_prologue();
     if (tid == 0)
@@ -130,7 +135,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     Cursor<kMmaTile> c = find_run<kMmaTile>(a, scan, &per);
 
     // ---- q of a unit, two elements a word, a warp to a row: loaded a unit ahead
-    constexpr int kQRows = H / kMmaWarps, kQWords = DC / 64;
+    constexpr int kWarps = kTeams * HG, kQRows = H / kWarps, kQWords = DC / 64;
     const bool q_words = ((uintptr_t)a.q | a.sq) % 4 == 0;
     uint32_t qw[kQRows][kQWords];
     auto load_q_rows = [&] {
@@ -142,7 +147,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
         for (int k = 0; k < kQRows; ++k)
 #pragma unroll
             for (int i = 0; i < kQWords; ++i) {
-                const uint32_t r = warp + k * kMmaWarps, d = 2 * lane + 64 * i;
+                const uint32_t r = warp + k * kWarps, d = 2 * lane + 64 * i;
                 qw[k][i] = 0u;
                 if (r < u.rows && d < D) {
                     const uint8_t *x = q + (uint64_t)(r * D + d) * 2;
@@ -158,7 +163,10 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     // ---- the copies, some tiles ahead.  Where 16 positions lie in one page (a.runs) the
     // warp looks up one page, otherwise a lane one for each of its rows.
     Cursor<kMmaTile> f = c;
-    const uint32_t copy_row = lane / M::kChunks, copy_chunk = lane % M::kChunks;
+    // The group's warps copy kCopies sets of kRowsPer rows each.
+    constexpr uint32_t kSets = 16 / M::kRowsPer, kCopies = (kSets + HG - 1) / HG;
+    const uint32_t copy_row = part8 * kCopies * M::kRowsPer + lane / M::kChunks;
+    const uint32_t copy_chunk = lane % M::kChunks;
     const uint32_t row_bytes = D * M::kCell;
     const uint32_t copy_from = copy_row * row_bytes + copy_chunk * 16;
     const bool column = copy_chunk * 16 < row_bytes;
@@ -167,7 +175,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     auto look_up = [&] {                                   // of the next tile to fetch
         if (f.done())
             return;
-        const uint32_t j = f.span.origin + f.t * kMmaTile + warp * 16 + (a.runs ? 0 : lane & 15);
+        const uint32_t j = f.span.origin + f.t * kMmaTile + group * 16 + (a.runs ? 0 : lane & 15);
         page = -1;
         if (j < f.span.n) {
             page = a.g.page_of(f.b, j);
@@ -178,7 +186,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
         if (!f.done()) {
             const uint32_t kv = f.unit / a.head_tiles;
             const uint32_t to = ring_addr + stage * M::kStage;
-            const uint32_t j0 = f.span.origin + f.t * kMmaTile + warp * 16;
+            const uint32_t j0 = f.span.origin + f.t * kMmaTile + group * 16;
             // positions [lo, n) of the 16
             const uint32_t from = f.span.lo > j0 ? f.span.lo - j0 : 0u;
             const uint32_t left = f.span.n > j0 ? f.span.n - j0 : 0u;
@@ -191,7 +199,9 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 const uint8_t *k = a.g.k + at + copy_from, *v = a.g.v + at + copy_from;
                 if (mask == 0xFFFFu && row_bytes == M::kRow) {
 #pragma unroll
-                    for (uint32_t i = 0; i < 16 / M::kRowsPer; ++i) {
+                    for (uint32_t i = 0; i < kCopies; ++i) {
+                        if (kCopies * HG > kSets && part8 * kCopies + i >= kSets)
+                            break;
                         const uint32_t r = i * M::kRowsPer + copy_row;
                         const uint32_t x = i * M::kRowsPer * M::kRow;
                         fetch16(to + M::chunk(r, copy_chunk), k + x);
@@ -199,7 +209,9 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     }
                 } else {
 #pragma unroll
-                    for (uint32_t i = 0; i < 16 / M::kRowsPer; ++i) {
+                    for (uint32_t i = 0; i < kCopies; ++i) {
+                        if (kCopies * HG > kSets && part8 * kCopies + i >= kSets)
+                            break;
                         const uint32_t r = i * M::kRowsPer + copy_row;
                         const bool on = column && (mask >> r & 1u);
                         const uint32_t x = on ? i * M::kRowsPer * row_bytes : 0u;
@@ -211,7 +223,9 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             } else {
                 mask &= __ballot_sync(0xFFFFFFFFu, page >= 0) & 0xFFFFu;
 #pragma unroll
-                for (uint32_t i = 0; i < 16 / M::kRowsPer; ++i) {
+                for (uint32_t i = 0; i < kCopies; ++i) {
+                    if (kCopies * HG > kSets && part8 * kCopies + i >= kSets)
+                        break;
                     const uint32_t r = i * M::kRowsPer + copy_row;
                     const uint64_t row = __shfl_sync(0xFFFFFFFFu, at, r);
                     const bool on = column && (mask >> r & 1u);
@@ -220,14 +234,14 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     fetch16(to + 16 * M::kRow + M::chunk(r, copy_chunk), a.g.v + x, on ? 16 : 0);
                 }
             }
-            if (CACHE8) {
+            if (CACHE8 && part8 == 0) {
                 const float *scales = lane < 16 ? a.g.ks : a.g.vs;
                 const bool on = mask >> (lane & 15) & 1u;
                 const uint64_t x =
                     on ? a.g.scale_at(page, kv, slot) + (a.runs ? lane & 15 : 0u) : 0;
                 fetch4(to + M::kScales + lane * 4, scales + x, on ? 4 : 0);
             }
-            if (lane == 0)
+            if (lane == 0 && part8 == 0)
                 *reinterpret_cast<uint32_t *>(ring + stage * M::kStage + M::kMask) = mask;
             f.next(a);
             look_up();
@@ -244,28 +258,28 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     const uint32_t k_row = lane % 16, k_chunk = lane / 16;
     const uint32_t v_row = CACHE8 ? lane % 16 : lane % 8 + lane / 16 * 8;
     const uint32_t v_chunk = CACHE8 ? lane / 16 : lane / 8 & 1;
-    const uint32_t q_row = NT == 2 ? lane % 8 + lane / 16 * 8 : lane % 8;
-    const uint32_t q_part = NT == 2 ? lane / 8 & 1 : lane / 8;
-    // q's operands of steps k, k + 1 of 16 columns: two words for each 8 heads and step
-    auto load_q = [&](uint32_t (*q)[2 * NT], int k) {
-        if (NT == 2) {
-            ldmatrix4(q[0], q_addr + M::q_chunk(q_row, 2 * k + q_part));
-            ldmatrix4(q[1], q_addr + M::q_chunk(q_row, 2 * k + 2 + q_part));
-        } else {
-            uint32_t w[4];
-            ldmatrix4(w, q_addr + M::q_chunk(q_row, 2 * k + q_part));
-            q[0][0] = w[0];
-            q[0][1] = w[1];
-            q[1][0] = w[2];
-            q[1][1] = w[3];
-        }
+    const uint32_t q_row = part8 * 8 + lane % 8, q_part = lane / 8;
+    // q's operands of steps k, k + 1 of 16 columns: two words for each
+    auto load_q = [&](uint32_t (*q)[2], int k) {
+        uint32_t w[4];
+        ldmatrix4(w, q_addr + M::q_chunk(q_row, 2 * k + q_part));
+        q[0][0] = w[0];
+        q[0][1] = w[1];
+        q[1][0] = w[2];
+        q[1][1] = w[3];
+    };
+    auto group_sync = [&] {
+        if (HG == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" :: "r"(1 + group), "n"(32 * HG) : "memory");
     };
 
     while (!c.done()) {
         // q to shared memory: binary16 after scaling by a power of two where the cache is E4M3
 #pragma unroll
         for (int k = 0; k < kQRows; ++k) {
-            const uint32_t r = warp + k * kMmaWarps;
+            const uint32_t r = warp + k * kWarps;
             float up = 1.0f, back = 1.0f;
             if (CACHE8) {
                 float top = 0.0f;
@@ -293,45 +307,37 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 head_scale[r] = a.scale2 * back;
         }
         __syncthreads();
-        uint32_t qf[kKeepQ ? DC / 16 : 2][2 * NT];
+        uint32_t qf[kKeepQ ? DC / 16 : 2][2];
         if (kKeepQ)
 #pragma unroll
             for (int k = 0; k < DC / 16; k += 2)
                 load_q(qf + (kKeepQ ? k : 0), k);
-        // of a lane's columns: heads 8 * n + 2 * (lane % 4) + {0, 1}
+        // of a lane's columns: heads first + {0, 1}
+        const uint32_t first = part8 * 8 + lane % 4 * 2;
         // m, and what a score is compared with and taken relative to
-        float scale[NT][2], m[NT][2], bound[NT][2], base[NT][2], l[NT][2], o[DC / 16][NT][4];
+        float scale[2], m[2], bound[2], base[2], l[2], o[DC / 16][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                scale[n][i] = head_scale[8 * n + lane % 4 * 2 + i];
-                m[n][i] = bound[n][i] = -INFINITY;
-                base[n][i] = l[n][i] = 0.0f;
-            }
+        for (int i = 0; i < 2; ++i) {
+            scale[i] = head_scale[first + i];
+            m[i] = bound[i] = -INFINITY;
+            base[i] = l[i] = 0.0f;
+        }
 #pragma unroll
         for (int d = 0; d < DC / 16; ++d)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[d][n][i] = 0.0f;
+            for (int i = 0; i < 4; ++i)
+                o[d][i] = 0.0f;
 
         for (uint32_t t = c.t; t < c.t1; ++t) {
             fetch_wait<M::kStages - 2>();
-            __syncwarp();
-            // every lane is done with the stage before this one
+            group_sync();
+            // the group has this stage's copies, and is done with the stage before it
             fetch((stage + M::kStages - 1) % M::kStages);
             const uint32_t at = ring_addr + stage * M::kStage;
             const uint8_t *here = ring + stage * M::kStage;
             const uint32_t mask = *reinterpret_cast<const uint32_t *>(here + M::kMask);
             // scores: positions lane / 4 (0, 1) and that + 8 (2, 3), in two sums
-            float s[NT][4], s2[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[n][i] = s2[n][i] = 0.0f;
+            float s[4] = {}, s2[4] = {};
 #pragma unroll
             for (int k = 0; k < DC / 16; k += 2) {
                 if (k * 16 >= (int)D)
@@ -351,12 +357,9 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 }
                 if (!kKeepQ)
                     load_q(qf, k);
-                const uint32_t(*q)[2 * NT] = qf + (kKeepQ ? k : 0);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma16<M::kType>(s[n], ka[0], q[0][2 * n], q[0][2 * n + 1]);
-                    mma16<M::kType>(s2[n], ka[1], q[1][2 * n], q[1][2 * n + 1]);
-                }
+                const uint32_t(*q)[2] = qf + (kKeepQ ? k : 0);
+                mma16<M::kType>(s, ka[0], q[0][0], q[0][1]);
+                mma16<M::kType>(s2, ka[1], q[1][0], q[1][1]);
             }
             // scales of the two positions; what they add to the maximum's exponent
             float ks[2], vs[2], lead[2];
@@ -372,59 +375,50 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             }
             bool above = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[n][i] = (s[n][i] + s2[n][i]) *
-                              (CACHE8 ? scale[n][i & 1] * ks[i / 2] : scale[n][i & 1]);
-                    if (mask != 0xFFFFu && !(mask >> (lane / 4 + i / 2 * 8) & 1u))
-                        s[n][i] = -INFINITY;
-                    s2[n][i] = CACHE8 ? s[n][i] + lead[i / 2] : s[n][i];
-                    above |= s2[n][i] > bound[n][i & 1];
-                }
+            for (int i = 0; i < 4; ++i) {
+                s[i] = (s[i] + s2[i]) * (CACHE8 ? scale[i & 1] * ks[i / 2] : scale[i & 1]);
+                if (mask != 0xFFFFu && !(mask >> (lane / 4 + i / 2 * 8) & 1u))
+                    s[i] = -INFINITY;
+                s2[i] = CACHE8 ? s[i] + lead[i / 2] : s[i];
+                above |= s2[i] > bound[i & 1];
+            }
             if (__any_sync(0xFFFFFFFFu, above)) {
+                float al[2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float al[2];
+                for (int i = 0; i < 2; ++i) {
+                    float now = fmaxf(m[i], fmaxf(s2[i], s2[2 + i]));
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float now = fmaxf(m[n][i], fmaxf(s2[n][i], s2[n][2 + i]));
+                    for (int d = 4; d < 32; d <<= 1)
+                        now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, d));
+                    al[i] = exp2_approx(m[i] - finite_max(now));
+                    m[i] = now;
+                    bound[i] = now + kSlack;
+                    base[i] = finite_max(now) - (CACHE8 ? kWeightBits : 0.0f);
+                    l[i] *= al[i];
+                }
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1)
-                            now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, d));
-                        al[i] = exp2_approx(m[n][i] - finite_max(now));
-                        m[n][i] = now;
-                        bound[n][i] = now + kSlack;
-                        base[n][i] = finite_max(now) - (CACHE8 ? kWeightBits : 0.0f);
-                        l[n][i] *= al[i];
-                    }
-#pragma unroll
-                    for (int d = 0; d < DC / 16; ++d) {
-                        mul2(o[d][n], al[0], al[1]);
-                        mul2(o[d][n] + 2, al[0], al[1]);
-                    }
+                for (int d = 0; d < DC / 16; ++d) {
+                    mul2(o[d], al[0], al[1]);
+                    mul2(o[d] + 2, al[0], al[1]);
                 }
             }
             // weights, in two parts: one would keep 8 (bf16) or 11 bits of them.  Transposed,
             // they are the second operand.
-            uint32_t hi[NT][2], lo[NT][2];
+            float p[4];
+            uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float p[4];
+            for (int i = 0; i < 4; ++i) {
+                p[i] = exp2_approx(s[i] - base[i & 1]);
+                l[i & 1] += p[i];
+                if (CACHE8)
+                    p[i] *= vs[i / 2];
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[i] = exp2_approx(s[n][i] - base[n][i & 1]);
-                    l[n][i & 1] += p[i];
-                    if (CACHE8)
-                        p[i] *= vs[i / 2];
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t w = pack2<M::kType>(p[2 * j], p[2 * j + 1]);
-                    const float2 x = widen2<M::kType>(w);
-                    hi[n][j] = transpose8(w);
-                    lo[n][j] = transpose8(pack2<M::kType>(p[2 * j] - x.x, p[2 * j + 1] - x.y));
-                }
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t w = pack2<M::kType>(p[2 * j], p[2 * j + 1]);
+                const float2 x = widen2<M::kType>(w);
+                hi[j] = transpose8(w);
+                lo[j] = transpose8(pack2<M::kType>(p[2 * j] - x.x, p[2 * j + 1] - x.y));
             }
             const uint32_t v_at = at + 16 * M::kRow;
 #pragma unroll
@@ -447,12 +441,10 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     ldmatrix4_trans(va[1], v_at + M::chunk(v_row, 2 * d + 2 + v_chunk));
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma16<M::kType>(o[d + i][n], va[i], hi[n][0], hi[n][1]);
-                        mma16<M::kType>(o[d + i][n], va[i], lo[n][0], lo[n][1]);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    mma16<M::kType>(o[d + i], va[i], hi[0], hi[1]);
+                    mma16<M::kType>(o[d + i], va[i], lo[0], lo[1]);
+                }
             }
             stage = (stage + 1) % M::kStages;
         }
@@ -460,63 +452,57 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
         c.next_unit(a);
         load_q_rows();
 
-        // the warps' parts, in their order; what they are relative to
+        // the groups' parts, in their order; what they are relative to
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1)
-                    l[n][i] += __shfl_xor_sync(0xFFFFFFFFu, l[n][i], d);
-                if (CACHE8)
-                    m[n][i] = m[n][i] == -INFINITY ? m[n][i] : m[n][i] - kWeightBits;
-                if (lane < 4) {
-                    warp_m[warp][8 * n + lane * 2 + i] = m[n][i];
-                    warp_l[warp][8 * n + lane * 2 + i] = l[n][i];
-                }
+            for (int d = 4; d < 32; d <<= 1)
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], d);
+            if (CACHE8)
+                m[i] = m[i] == -INFINITY ? m[i] : m[i] - kWeightBits;
+            if (lane < 4) {
+                group_m[group][first + i] = m[i];
+                group_l[group][first + i] = l[i];
             }
+        }
         __syncthreads();
         const UnitRows u = unit_rows(a, done.unit);
         const int part = segment_part(a, done, per);
-        float own[NT][2];
+        float own[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < 2; ++i) {
+            float all = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float all = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kMmaWarps; ++w)
-                    all = fmaxf(all, warp_m[w][8 * n + lane % 4 * 2 + i]);
-                own[n][i] = exp2_approx(m[n][i] - finite_max(all));
-            }
+            for (int w = 0; w < kTeams; ++w)
+                all = fmaxf(all, group_m[w][first + i]);
+            own[i] = exp2_approx(m[i] - finite_max(all));
+        }
         // the head that this thread finishes, with kLanes - 1 others
-        constexpr uint32_t kLanes = kMmaThreads / H;
+        constexpr uint32_t kLanes = M::kThreads / H;
         const uint32_t row = tid / kLanes;
         float row_m = -INFINITY, row_l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w)
-            row_m = fmaxf(row_m, warp_m[w][row]);
+        for (int w = 0; w < kTeams; ++w)
+            row_m = fmaxf(row_m, group_m[w][row]);
 #pragma unroll
-        for (int w = 0; w < kMmaWarps; ++w)
-            row_l += warp_l[w][row] * exp2_approx(warp_m[w][row] - finite_max(row_m));
+        for (int w = 0; w < kTeams; ++w)
+            row_l += group_l[w][row] * exp2_approx(group_m[w][row] - finite_max(row_m));
 #pragma unroll
         for (int d0 = 0; d0 < DC; d0 += M::kJoin) {
             if (d0 >= (int)D)
                 break;
             if (d0 > 0)
                 __syncthreads();
-            float *mine = join + warp * H * M::kJoinRow;
+            float *mine = join + group * H * M::kJoinRow;
 #pragma unroll
             for (int d = 0; d < M::kJoin / 16; ++d)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t column = 16 * d + (CACHE8 ? lane / 4 * 2 + i / 2
-                                                                 : lane / 4 + i / 2 * 8);
-                        mine[(8 * n + lane % 4 * 2 + (i & 1)) * M::kJoinRow + column] =
-                            o[d0 / 16 + d][n][i] * own[n][i & 1];
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t column = 16 * d + (CACHE8 ? lane / 4 * 2 + i / 2
+                                                             : lane / 4 + i / 2 * 8);
+                    mine[(first + (i & 1)) * M::kJoinRow + column] =
+                        o[d0 / 16 + d][i] * own[i & 1];
+                }
             __syncthreads();
 #pragma unroll
             for (uint32_t i = 0; i < M::kJoin / kLanes; ++i) {
@@ -524,7 +510,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 const uint32_t at = row * M::kJoinRow + column;
                 float v = join[at];
 #pragma unroll
-                for (int w = 1; w < kMmaWarps; ++w)
+                for (int w = 1; w < kTeams; ++w)
                     v += join[w * H * M::kJoinRow + at];
                 if (row >= u.rows || d >= D)
                     continue;
@@ -545,10 +531,10 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     fetch_wait<0>();
 }
 
-template <int DT, bool CACHE8, int DC, int NT>
+template <int DT, bool CACHE8, int DC, int HG>
 static cudaError_t mma_form(AttnArgs &a, int *grid, cudaStream_t s) {
-    using M = MmaForm<DT, CACHE8, DC, NT>;
-    const cudaError_t e = opt_in_smem<k_attention_mma<DT, CACHE8, DC, NT>>(M::kSmem);
+    using M = MmaForm<DT, CACHE8, DC, HG>;
+    const cudaError_t e = opt_in_smem<k_attention_mma<DT, CACHE8, DC, HG>>(M::kSmem);
     if (e != cudaSuccess)
         return e;
     const int sms = sm_count();
@@ -558,14 +544,15 @@ static cudaError_t mma_form(AttnArgs &a, int *grid, cudaStream_t s) {
     a.head_tiles = (a.group + M::kHeads - 1) / M::kHeads;
     a.runs = a.g.page % 16 == 0;
     *grid = cta_limit(a.unit_rows, M::kCtas * sms);
-    return launch_kernel(k_attention_mma<DT, CACHE8, DC, NT>, *grid, kMmaThreads, M::kSmem, s, true,
+    return launch_kernel(k_attention_mma<DT, CACHE8, DC, HG>, *grid, M::kThreads, M::kSmem, s, true,
                          a);
 }
 
 template <int DT, bool CACHE8, int DC>
 static cudaError_t mma_heads(AttnArgs &a, int *grid, cudaStream_t s) {
-    return a.group <= 8 ? mma_form<DT, CACHE8, DC, 1>(a, grid, s)
-                        : mma_form<DT, CACHE8, DC, 2>(a, grid, s);
+    return a.group <= 8    ? mma_form<DT, CACHE8, DC, 1>(a, grid, s)
+           : a.group <= 16 ? mma_form<DT, CACHE8, DC, 2>(a, grid, s)
+                           : mma_form<DT, CACHE8, DC, 4>(a, grid, s);
 }
 
 template <int DT, bool CACHE8>
