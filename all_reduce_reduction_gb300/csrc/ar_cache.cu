@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 k_cache_move(const __grid_constant__ MoveArgs a) {
     using L = Line<DT, WIDE, N>;
     __shared__ int2 places[kMoveRows];
-    kernel_prologue();
+    wait_for_input();
     const uint32_t group = blockIdx.x / a.jobs_per_row, part = blockIdx.x % a.jobs_per_row;
     const uint32_t row0 = group * a.rows;
     const uint32_t rows = a.T - row0 < a.rows ? a.T - row0 : a.rows;

@@ -96,6 +96,14 @@ struct Pages {
     }
 };
 
+// The wait of kernel_prologue() without its call for the next kernel, which then comes
+// when the CTAs of this one have ended.  For kernels that a kernel follows whose CTAs
+// fill an SM to the last register: placed between warps that are still there, fewer of
+// them fit, and the others wait for a second turn.
+__device__ __forceinline__ void wait_for_input() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---- host side -----------------------------------------------------------------
 
 // The buffers of a cache argument.

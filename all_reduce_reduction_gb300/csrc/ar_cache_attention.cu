@@ -191,7 +191,7 @@ template <int DT, int VEC> __global__ void __launch_bounds__(kJoinThreads)
 k_attention_join(const __grid_constant__ AttnArgs a) {
     constexpr int kSteps = AR_CACHE_MAX_DIM / (32 * VEC);
     __shared__ float weight[kMaxCtas], part[kJoinWarps], sums[kJoinWarps - 1][AR_CACHE_MAX_DIM];
-    kernel_prologue();
+    wait_for_input();
     const WorkSpace w(a.work);
     const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int4 meta = w.meta[c];
@@ -280,11 +280,13 @@ k_attention_join(const __grid_constant__ AttnArgs a) {
         a.lse[(uint64_t)meta.x * a.heads + u.head + r] = lse_of(top, l);
 }
 
-template <int DT> static cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t s) {
+template <int DT, int VEC>
+static cudaError_t join_form(const AttnArgs &a, int grid, cudaStream_t s) {
     const dim3 ctas(grid, a.group < a.unit_rows ? a.group : a.unit_rows);
-    return a.g.D % 4 == 0
-               ? launch_kernel(k_attention_join<DT, 4>, ctas, kJoinThreads, 0, s, true, a)
-               : launch_kernel(k_attention_join<DT, 1>, ctas, kJoinThreads, 0, s, true, a);
+    return launch_kernel(k_attention_join<DT, VEC>, ctas, kJoinThreads, 0, s, true, a);
+}
+template <int DT> static cudaError_t launch_join(const AttnArgs &a, int grid, cudaStream_t s) {
+    return a.g.D % 4 == 0 ? join_form<DT, 4>(a, grid, s) : join_form<DT, 1>(a, grid, s);
 }
 
 template <int DT, bool CACHE8> static cudaError_t attention_any(const AttnArgs &a, cudaStream_t s) {
