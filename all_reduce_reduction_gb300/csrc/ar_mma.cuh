@@ -39,6 +39,12 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// What is left of a and b once half2_of(a, b) is taken away; an infinity leaves nothing.
+__device__ __forceinline__ uint32_t rest_of(uint32_t taken, float a, float b) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&taken));
+    return half2_of(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
+}
+
 // The power of two that brings magnitudes up to `top` below 2^15, and its inverse
 // (both exact; infinities and NaN stay what they are).
 __device__ __forceinline__ void half_range(float top, float &scale, float &inverse) {

@@ -5,26 +5,29 @@
 //
 // Bound by memory: the weights of every expert that a token chose are read once.
 // They are the 16-row operand of warp-wide products (E4M3 is exact in binary16), the
-// tokens its 8 columns: x and h are scaled by a power of two for each 128 of a row
-// so that binary16 holds them, in two parts where one would round.  A block of 128
-// along k gets its scales in binary32 when it is summed.
+// pairs (token, choice) of the expert the 8 or 16 columns: x and h are scaled by a
+// power of two for each 128 of a row so that binary16 holds them, in two parts where
+// one would round x.  A block of 128 along k gets its scales in binary32 when it is
+// summed.
 //
 // Weights go from global memory straight to the lanes that multiply with them: a
 // lane takes 16 bytes of a row, and the order of k inside a block is that of the
-// lanes, for the tokens too.
+// lanes (see place_of), for the columns too.
 //
-// First launch: a CTA takes 16 rows of both halves of one expert, its warps share
-// the blocks along k.  Second launch: a CTA takes rows of the output, its warps share
-// the blocks along k of all experts; each keeps its own sums of all tokens, which
+// First launch (up): a CTA takes 16 rows of both halves of one expert at a time, its
+// warps share the blocks along k.  The columns lie in shared memory, converted when
+// the expert changes.  Second launch (down): a CTA takes rows of the output, its warps
+// share the blocks along k of all experts; each keeps its own sums of all tokens, which
 // are added in order.
 #include "ar_mma.cuh"
 #include "ar_rows.cuh"
 
 namespace ar {
 
-constexpr int kMoeThreads = 256, kMoeWarps = kMoeThreads / 32;
 constexpr int kMoePairs = AR_MOE_LAYER_PAIRS;
-constexpr int kColumns = 32;          // most pairs of an expert in one pass over its weights
+// Dynamic shared memory of an SM that one or two CTAs share.
+constexpr size_t kMoeSmem = 224 * 1024;
+constexpr int kColumns = 16;          // most pairs of an expert in one pass over its weights
 
 struct MoeArgs {
     const uint8_t *x;
@@ -33,14 +36,17 @@ struct MoeArgs {
     const uint8_t *up, *down;
     const float *up_scale, *down_scale;
     uint8_t *out;
-    float *h;                         // T * K rows of ldh
-    uint64_t sx, sout;                // bytes between rows
-    uint64_t ldup, lddown, ldh;
+    uint8_t *h;                       // T * K rows of sh bytes, see HiddenRow
+    uint64_t sx, sout, sh;            // bytes between rows
+    uint64_t ldup, lddown;
     uint32_t T, K, H, F, E;
     uint32_t hb, fb, ub;              // blocks of 128 along H, F and 2F
+    uint32_t columns;                 // pairs that the first launch's shared memory holds
     int wide_up, wide_down, wide_x;
     int ids8;
 };
+
+// ---- who goes where ---------------------------------------------------------------
 
 // The pairs that are here, and the experts they go to in the order of their first pair.
 struct Chosen {
@@ -51,34 +57,48 @@ struct Chosen {
     int warp_count[kMoePairs / 32];
 };
 
+__device__ __forceinline__ int expert_of(const MoeArgs &a, uint32_t p) {
+    const int64_t id = a.ids8 ? static_cast<const int64_t *>(a.ids)[p]
+                              : (int64_t) static_cast<const int32_t *>(a.ids)[p];
+    return id >= 0 && id < (int64_t)a.E ? (int)id : -1;
+}
+
 __device__ __forceinline__ void choose(const MoeArgs &a, Chosen &c) {
-    const uint32_t pairs = a.T * a.K;
-    for (uint32_t e = threadIdx.x; e < a.E; e += kMoeThreads)
+    const uint32_t pairs = a.T * a.K, lane = threadIdx.x & 31;
+    if (pairs <= 32) {                // one warp sees them all
+        if (threadIdx.x < 32) {
+            const int e = lane < pairs ? expert_of(a, lane) : -1;
+            const uint32_t like = __match_any_sync(0xFFFFFFFFu, e);
+            const bool lead = e >= 0 && (like & ((1u << lane) - 1u)) == 0;
+            const uint32_t leads = __ballot_sync(0xFFFFFFFFu, lead);
+            c.expert[lane] = (int16_t)e;
+            if (lead)
+                c.active[__popc(leads & ((1u << lane) - 1u))] = (int16_t)e;
+            if (lane == 0)
+                c.count = __popc(leads);
+        }
+        __syncthreads();
+        return;
+    }
+    for (uint32_t e = threadIdx.x; e < a.E; e += blockDim.x)
         c.first[e] = kMoePairs;
     __syncthreads();
-    for (uint32_t p = threadIdx.x; p < pairs; p += kMoeThreads) {
-        const int64_t id = a.ids8 ? static_cast<const int64_t *>(a.ids)[p]
-                                  : (int64_t) static_cast<const int32_t *>(a.ids)[p];
-        const bool here = id >= 0 && id < (int64_t)a.E;
-        c.expert[p] = here ? (int16_t)id : (int16_t)-1;
-        if (here)
-            atomicMin(&c.first[id], (int)p);
+    for (uint32_t p = threadIdx.x; p < pairs; p += blockDim.x) {
+        const int e = expert_of(a, p);
+        c.expert[p] = (int16_t)e;
+        if (e >= 0)
+            atomicMin(&c.first[e], (int)p);
     }
     __syncthreads();
     // the first pair of an expert stands for it
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < kMoePairs / kMoeThreads; ++i) {
-        const uint32_t p = threadIdx.x + i * kMoeThreads;
+    for (uint32_t p = threadIdx.x; p < kMoePairs; p += blockDim.x) {
         const bool lead = p < pairs && c.expert[p] >= 0 && c.first[c.expert[p]] == (int)p;
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, lead);
         if (lane == 0)
             c.warp_count[p / 32] = __popc(m);
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMoePairs / kMoeThreads; ++i) {
-        const uint32_t p = threadIdx.x + i * kMoeThreads;
+    for (uint32_t p = threadIdx.x; p < kMoePairs; p += blockDim.x) {
         const bool lead = p < pairs && c.expert[p] >= 0 && c.first[c.expert[p]] == (int)p;
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, lead);
         int before = 0;
@@ -93,9 +113,9 @@ __device__ __forceinline__ void choose(const MoeArgs &a, Chosen &c) {
 }
 
 // The pairs of expert e in order, by one warp: `list` receives those from `skip` on,
-// at most kColumns; returns how many there are in all.
+// at most `most`; returns how many there are in all.
 __device__ __forceinline__ int list_pairs(const MoeArgs &a, const Chosen &c, int e, int skip,
-                                          int16_t *list) {
+                                          int most, int16_t *list) {
     const uint32_t pairs = a.T * a.K, lane = threadIdx.x & 31;
     int n = 0;
     for (uint32_t p0 = 0; p0 < pairs; p0 += 32) {
@@ -103,7 +123,7 @@ __device__ __forceinline__ int list_pairs(const MoeArgs &a, const Chosen &c, int
         const bool mine = p < pairs && c.expert[p] == e;
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
         const int at = n + __popc(m & ((1u << lane) - 1u)) - skip;
-        if (mine && at >= 0 && at < kColumns)
+        if (mine && at >= 0 && at < most)
             list[at] = (int16_t)p;
         n += __popc(m);
     }
@@ -111,11 +131,19 @@ __device__ __forceinline__ int list_pairs(const MoeArgs &a, const Chosen &c, int
     return n;
 }
 
+// ---- a block of 128 along k ----------------------------------------------------------
+
+// Lane l holds row or column l / 4 of an operand and, with c = l % 4, the elements
+// 16 c .. 16 c + 15 of each half of 64: four steps of a product's 16 (4 elements a lane).
+// In memory, converted columns have the 8-element pieces of the four lanes side by side.
+__device__ __forceinline__ uint32_t place_of(uint32_t k) {
+    return (k & ~63u) + (k / 8 & 1) * 32 + (k / 16 & 3) * 8 + k % 8;
+}
+
 // 16 codes of a weight row from k on; zeros past K.
-__device__ __forceinline__ uint4 load_codes(const uint8_t *row, uint32_t k, uint32_t K, bool wide,
-                                            bool on) {
+__device__ __forceinline__ uint4 load_codes(const uint8_t *row, uint32_t k, uint32_t K, bool wide) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (on && k < K) {
+    if (k < K) {
         if (wide && k + 16 <= K)
             return ld_v4_stream(row + k);
         for (uint32_t i = 0; i < 16 && k + i < K; ++i)
@@ -124,7 +152,96 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *row, uint32_t k, uint
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 16 elements of a row of x (type DT) from k on as binary32; zeros past K.
+// The lane's codes of MT tiles of 16 rows: [tile][half][row l / 4 or that + 8].
+template <int MT> struct Codes {
+    uint4 q[MT][2][2];
+    // rows: the lane's row pointers, [tile][2]; block kb of K
+    __device__ __forceinline__ void load(const uint8_t *const (*rows)[2], uint32_t kb, uint32_t K,
+                                         bool wide) {
+        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 16;
+        if (wide && kb * 128 + 128 <= K) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    q[m][0][i] = ld_v4_stream(rows[m][i] + k);
+                    q[m][1][i] = ld_v4_stream(rows[m][i] + k + 64);
+                }
+        } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    q[m][0][i] = load_codes(rows[m][i], k, K, wide);
+                    q[m][1][i] = load_codes(rows[m][i], k + 64, K, wide);
+                }
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// part += codes * columns.  column(nt, half, piece): eight of the lane's elements of
+// column l / 4 of tile nt, two steps' worth.
+template <int MT, int NT, typename Column>
+__device__ __forceinline__ void block_product(float (*part)[NT][4], const Codes<MT> &w,
+                                              Column column) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece) {
+            uint4 b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                b[n] = column(n, half, piece);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    uint32_t r[4];
+                    from_e4m3x4(word_of(w.q[m][half][0], 2 * piece + k), r[0], r[2]);
+                    from_e4m3x4(word_of(w.q[m][half][1], 2 * piece + k), r[1], r[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma16<AR_FP16>(part[m][n], r, word_of(b[n], 2 * k),
+                                       word_of(b[n], 2 * k + 1));
+                }
+        }
+}
+
+// 32 binary32 values of a column (of two halves, 16 each) to binary16: scaled by a power
+// of two for the block, in one part or two.  Returns the inverse of the scale.
+template <bool LO>
+__device__ __forceinline__ float convert_column(const float *v, uint4 (*hi)[2], uint4 (*lo)[2]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        top = fmaxf(top, fabsf(v[i]));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    float s, inverse;
+    half_range(top, s, inverse);
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float *x = v + 16 * half + 8 * j + 2 * i;
+                a[i] = half2_of(x[0] * s, x[1] * s);
+                b[i] = LO ? rest_of(a[i], x[0] * s, x[1] * s) : 0u;
+            }
+            hi[half][j] = make_uint4(a[0], a[1], a[2], a[3]);
+            if (LO)
+                lo[half][j] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+    return inverse;
+}
+
+// 16 elements of a row of type DT from k on as binary32; zeros past K.
 template <int DT>
 __device__ __forceinline__ void load_column(const uint8_t *row, uint32_t k, uint32_t K, bool wide,
                                             bool on, float *v) {
@@ -140,204 +257,401 @@ __device__ __forceinline__ void load_column(const uint8_t *row, uint32_t k, uint
         v[i] = on && k + i < K ? widen1<DT>(ld_elem<DT>(row, k + i)) : 0.0f;
 }
 
-// One block of 128 along k: MT tiles of 16 weight rows by NT tiles of 8 columns.
-//   weights(mt, half, i): the lane's 16 codes of row lane / 4 (i = 0) or that + 8
-//   column(nt, half, v):  the lane's 16 values of column lane / 4
-// sum[mt][nt] += scale(mt, i) * product.
-template <int MT, int NT, bool LO, typename Weights, typename Column, typename Scale>
-__device__ __forceinline__ void block_product(float (*sum)[NT][4], Weights weights, Column column,
-                                              Scale scale) {
-    const int lane = threadIdx.x & 31;
-    uint4 q[MT][2][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                q[mt][half][i] = weights(mt, half, i);
-    float ws[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            ws[mt][i] = scale(mt, i);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        float v[32];
-        column(nt, 0, v);
-        column(nt, 1, v + 16);
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            top = fmaxf(top, fabsf(v[i]));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        float s, inverse;
-        half_range(top, s, inverse);
-        float part[MT][4] = {};
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float *x = v + 16 * half + 4 * k;
-                const float y[4] = {x[0] * s, x[1] * s, x[2] * s, x[3] * s};
-                const uint32_t b0 = half2_of(y[0], y[1]), b1 = half2_of(y[2], y[3]);
-                uint32_t c0 = 0, c1 = 0;
-                if (LO) {
-                    const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&b0));
-                    const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&b1));
-                    // an infinity has no second part
-                    c0 = half2_of(isinf(f0.x) ? 0.0f : y[0] - f0.x, isinf(f0.y) ? 0.0f : y[1] - f0.y);
-                    c1 = half2_of(isinf(f1.x) ? 0.0f : y[2] - f1.x, isinf(f1.y) ? 0.0f : y[3] - f1.y);
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const uint4 g = q[mt][half][0], u = q[mt][half][1];
-                    uint32_t m[4];
-                    from_e4m3x4(k == 0 ? g.x : k == 1 ? g.y : k == 2 ? g.z : g.w, m[0], m[2]);
-                    from_e4m3x4(k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w, m[1], m[3]);
-                    mma16<AR_FP16>(part[mt], m, b0, b1);
-                    if (LO)
-                        mma16<AR_FP16>(part[mt], m, c0, c1);
-                }
-            }
-        // the columns that this lane has sums of
-        const float i0 = __shfl_sync(0xFFFFFFFFu, inverse, lane % 4 * 8);
-        const float i1 = __shfl_sync(0xFFFFFFFFu, inverse, lane % 4 * 8 + 4);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            sum[mt][nt][0] += part[mt][0] * i0 * ws[mt][0];
-            sum[mt][nt][1] += part[mt][1] * i1 * ws[mt][0];
-            sum[mt][nt][2] += part[mt][2] * i0 * ws[mt][1];
-            sum[mt][nt][3] += part[mt][3] * i1 * ws[mt][1];
-        }
+// ---- h between the launches ----------------------------------------------------------
+
+// Where the output has two bytes, h is held in binary16: 16 neighbours share a power of
+// two (its biased exponent in a byte), 11 bits of the largest, an eighth of the output's
+// own rounding in bf16 and of its size in fp16.  Otherwise it is binary32.
+template <int DT> struct HiddenRow {
+    static constexpr bool kHalf = DT != AR_FP32;
+    static __host__ __device__ __forceinline__ uint64_t bytes(uint32_t F, uint32_t fb) {
+        // rows are read by 16-byte vectors
+        return kHalf ? ((uint64_t)fb * (128 * 2 + 8) + 15) / 16 * 16 : (uint64_t)(F + 3) / 4 * 16;
     }
-}
+};
 
 // ---- first launch -------------------------------------------------------------
 
 constexpr int kUpTiles = 2, kUpRows = 8 * kUpTiles;       // rows of each half
 
-struct UpShared {
+template <int WARPS> struct UpShared {
     Chosen c;
-    int16_t list[kMoeWarps][kColumns];
-    float part[kMoeWarps][2][kUpRows][kColumns + 1];
+    int16_t list[WARPS][kColumns];
+    float part[WARPS][2][kUpRows][kColumns + 1];
+};
+// A column in shared memory: blocks of 256 bytes, in one part or two, and an inverse
+// scale each.  Columns start 64 bytes apart in the banks.
+template <int DT> struct UpColumn {
+    static constexpr int kParts = DT == AR_FP32 ? 2 : 1;
+    static __host__ __device__ __forceinline__ uint32_t bytes(uint32_t hb) {
+        return (kParts * hb * 256 + hb * 4 + 127) / 128 * 128 + 64;
+    }
 };
 
-// Rows f0.. of both halves of expert e times the listed pairs.
-template <int DT, int NT>
-__device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, int e, uint32_t f0, int n) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The listed pairs' tokens to shared memory, a warp to a block.
+template <int DT, int WARPS>
+__device__ __forceinline__ void stage_columns(const MoeArgs &a, const int16_t *list, int n,
+                                              uint8_t *xs) {
+    using C = UpColumn<DT>;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bytes = C::bytes(a.hb);
+#pragma unroll 4
+    for (uint32_t item = warp; item < n * a.hb; item += WARPS) {
+        const uint32_t c = item / a.hb, kb = item - c * a.hb, k = kb * 128 + lane * 4;
+        const uint8_t *row = a.x + (uint64_t)(list[c] / a.K) * a.sx;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (a.wide_x && k + 4 <= a.H) {
+            if (Elem<DT>::kSize == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(row + (uint64_t)k * 4);
+                v[0] = f.x;
+                v[1] = f.y;
+                v[2] = f.z;
+                v[3] = f.w;
+            } else {
+                const uint2 u = *reinterpret_cast<const uint2 *>(row + (uint64_t)k * 2);
+                const float2 f = widen2<DT == AR_FP32 ? AR_BF16 : DT>(u.x);
+                const float2 g = widen2<DT == AR_FP32 ? AR_BF16 : DT>(u.y);
+                v[0] = f.x;
+                v[1] = f.y;
+                v[2] = g.x;
+                v[3] = g.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k + i < a.H)
+                    v[i] = widen1<DT>(ld_elem<DT>(row, k + i));
+        }
+        float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        float s, inverse;
+        half_range(top, s, inverse);
+        uint8_t *column = xs + c * bytes;
+        uint8_t *at = column + kb * 256 + place_of(lane * 4) * 2;
+        const uint2 hi = make_uint2(half2_of(v[0] * s, v[1] * s), half2_of(v[2] * s, v[3] * s));
+        *reinterpret_cast<uint2 *>(at) = hi;
+        if (C::kParts == 2)
+            *reinterpret_cast<uint2 *>(at + a.hb * 256) =
+                make_uint2(rest_of(hi.x, v[0] * s, v[1] * s), rest_of(hi.y, v[2] * s, v[3] * s));
+        if (lane == 0)
+            reinterpret_cast<float *>(column + C::kParts * a.hb * 256)[kb] = inverse;
+    }
+}
+
+// Rows f0.. of both halves of expert e times n listed pairs.  STAGED: they lie in shared
+// memory at xs; otherwise they are read and converted on the way.
+template <int DT, int WARPS, bool STAGED, int NT>
+__device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, const uint8_t *xs,
+                                        int e, uint32_t f0, int n) {
+    using C = UpColumn<DT>;
+    constexpr bool kLo = C::kParts == 2;
+    constexpr bool kAhead = STAGED && NT == 1;    // registers for the next block's weights
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int16_t *list = s.list[warp];
     const uint8_t *w = a.up + (uint64_t)e * 2 * a.F * a.ldup;
     const float *ws = a.up_scale + (uint64_t)e * a.ub * a.hb;
+    // rows past the last stand in for it: their sums go nowhere
+    const uint8_t *rows[kUpTiles][2];
+    uint32_t scales[kUpTiles][2];
+#pragma unroll
+    for (int m = 0; m < kUpTiles; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t f = f0 + m * 8 + lane / 4;
+            const uint32_t r = (f < a.F ? f : a.F - 1) + i * a.F;
+            rows[m][i] = w + (uint64_t)r * a.ldup;
+            scales[m][i] = r / 128 * a.hb;
+        }
+    const uint32_t bytes = C::bytes(a.hb), first = lane % 4 * 2;
+    const uint8_t *mine = xs + lane / 4 * bytes + lane % 4 * 16;
+    const float *inverses = reinterpret_cast<const float *>(xs + first * bytes +
+                                                            C::kParts * a.hb * 256);
     float sum[kUpTiles][NT][4] = {};
-    for (uint32_t kb = warp; kb < a.hb; kb += kMoeWarps) {
-        auto weights = [&](int mt, int half, int i) {
-            const uint32_t f = f0 + mt * 8 + lane / 4;
-            return load_codes(w + (uint64_t)(f + i * a.F) * a.ldup,
-                              kb * 128 + half * 64 + lane % 4 * 16, a.H, a.wide_up, f < a.F);
-        };
-        auto column = [&](int nt, int half, float *v) {
-            const int c = nt * 8 + lane / 4;
-            const uint32_t t = c < n ? list[c] / a.K : 0u;
-            load_column<DT>(a.x + t * a.sx, kb * 128 + half * 64 + lane % 4 * 16, a.H, a.wide_x,
-                            c < n, v);
-        };
-        auto scale = [&](int mt, int i) {
-            const uint32_t f = f0 + mt * 8 + lane / 4;
-            return f < a.F ? ws[(uint64_t)((f + i * a.F) / 128) * a.hb + kb] : 0.0f;
-        };
-        block_product<kUpTiles, NT, DT == AR_FP32>(sum, weights, column, scale);
+    Codes<kUpTiles> next;
+    if (kAhead && warp < a.hb)
+        next.load(rows, warp, a.H, a.wide_up);
+    for (uint32_t kb = warp; kb < a.hb; kb += WARPS) {
+        Codes<kUpTiles> now;
+        if (kAhead) {
+            now = next;
+            if (kb + WARPS < a.hb)
+                next.load(rows, kb + WARPS, a.H, a.wide_up);
+        } else {
+            now.load(rows, kb, a.H, a.wide_up);
+        }
+        float part[kUpTiles][NT][4] = {}, inverse[NT][2];   // of this lane's columns
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int lo = 0; lo < C::kParts; ++lo)
+                block_product<kUpTiles, NT>(part, now, [&](int nt, int half, int piece) {
+                    return nt * 8 + (int)lane / 4 < n
+                               ? *reinterpret_cast<const uint4 *>(
+                                     mine + nt * 8 * bytes + (lo * a.hb + kb) * 256 + half * 128 +
+                                     piece * 64)
+                               : make_uint4(0u, 0u, 0u, 0u);
+                });
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    inverse[nt][i] = nt * 8 + (int)first + i < n
+                                         ? inverses[(nt * 8 + i) * (bytes / 4) + kb]
+                                         : 0.0f;
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int c = nt * 8 + (int)lane / 4;
+                const uint8_t *row = a.x + (uint64_t)(c < n ? list[c] / a.K : 0u) * a.sx;
+                const uint32_t k = kb * 128 + lane % 4 * 16;
+                float v[32];
+                load_column<DT>(row, k, a.H, a.wide_x, c < n, v);
+                load_column<DT>(row, k + 64, a.H, a.wide_x, c < n, v + 16);
+                uint4 hi[2][2], lo[2][2];
+                const float inv = convert_column<kLo>(v, hi, lo);
+                inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
+                inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
+                float one[kUpTiles][1][4] = {};
+                block_product<kUpTiles, 1>(
+                    one, now, [&](int, int half, int piece) { return hi[half][piece]; });
+                if (kLo)
+                    block_product<kUpTiles, 1>(
+                        one, now, [&](int, int half, int piece) { return lo[half][piece]; });
+#pragma unroll
+                for (int m = 0; m < kUpTiles; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        part[m][nt][i] = one[m][0][i];
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < kUpTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float sc = ws[scales[m][i] + kb];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        sum[m][nt][2 * i + j] += part[m][nt][2 * i + j] * (inverse[nt][j] * sc);
+            }
     }
 #pragma unroll
-    for (int mt = 0; mt < kUpTiles; ++mt)
+    for (int m = 0; m < kUpTiles; ++m)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s.part[warp][i / 2][mt * 8 + lane / 4][nt * 8 + lane % 4 * 2 + i % 2] =
-                    sum[mt][nt][i];
+                s.part[warp][i / 2][m * 8 + lane / 4][nt * 8 + lane % 4 * 2 + i % 2] =
+                    sum[m][nt][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < kUpRows * n; i += kMoeThreads) {
-        const int r = i % kUpRows, c = i / kUpRows;
-        float g = 0.0f, u = 0.0f;
+    // 16 lanes have the rows of one pair
+    for (int c0 = warp * 2; c0 < n; c0 += 2 * WARPS) {
+        const int c = c0 + lane / kUpRows, r = lane % kUpRows;
+        float h = 0.0f;
+        if (c < n && f0 + r < a.F) {
+            float g = 0.0f, u = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kMoeWarps; ++k) {
-            g += s.part[k][0][r][c];
-            u += s.part[k][1][r][c];
+            for (int k = 0; k < WARPS; ++k) {
+                g += s.part[k][0][r][c];
+                u += s.part[k][1][r][c];
+            }
+            h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
         }
-        if (f0 + r < a.F)
-            a.h[(uint64_t)list[c] * a.ldh + f0 + r] = __fdiv_rn(g, 1.0f + expf(-g)) * u;
+        uint8_t *row = a.h + (uint64_t)(c < n ? list[c] : 0) * a.sh;
+        if (!HiddenRow<DT>::kHalf) {
+            if (c < n && f0 + r < a.F)
+                reinterpret_cast<float *>(row)[f0 + r] = h;
+            continue;
+        }
+        float top = fabsf(h);
+#pragma unroll
+        for (int d = kUpRows / 2; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        float scale, inverse;
+        half_range(top, scale, inverse);
+        if (c >= n)
+            continue;
+        const uint32_t f = f0 + r, tile = f0 / 16;
+        reinterpret_cast<uint16_t *>(row)[f / 128 * 128 + place_of(f % 128)] =
+            (uint16_t)narrow1<AR_FP16>(h * scale);
+        // and the exponents of what is left of the row's last block
+        uint8_t *exponents = row + (uint64_t)a.fb * 256;
+        if (r == 0)
+            exponents[tile] = (uint8_t)(__float_as_uint(scale) >> 23);
+        else if (tile + 1 == (a.F + 15) / 16 && tile + r < a.fb * 8)
+            exponents[tile + r] = 255;
     }
     __syncthreads();
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant__ MoeArgs a) {
+template <int DT, int WARPS, bool STAGED>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
+k_moe_up(const __grid_constant__ MoeArgs a) {
     extern __shared__ uint4 smem[];
-    UpShared &s = *reinterpret_cast<UpShared *>(smem);
-    kernel_prologue();
+    UpShared<WARPS> &s = *reinterpret_cast<UpShared<WARPS> *>(smem);
+    uint8_t *xs = reinterpret_cast<uint8_t *>(&s) + (sizeof(s) + 127) / 128 * 128;
+    // the second launch reads the choices before its own wait, so it may come only once
+    // what was before this one is done
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     choose(a, s.c);
     const uint32_t tiles = (a.F + kUpRows - 1) / kUpRows;
+    // this CTA's run of (expert, rows)
     const uint64_t units = (uint64_t)s.c.count * tiles;
-    for (uint64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int e = s.c.active[unit / tiles];
-        const uint32_t f0 = (uint32_t)(unit % tiles) * kUpRows;
-        for (int skip = 0;; skip += kColumns) {
-            const int all = list_pairs(a, s.c, e, skip, s.list[threadIdx.x >> 5]);
-            const int n = all - skip < kColumns ? all - skip : kColumns;
-            if (n <= 8)
-                up_unit<DT, 1>(a, s, e, f0, n);
-            else if (n <= 16)
-                up_unit<DT, 2>(a, s, e, f0, n);
-            else
-                up_unit<DT, 4>(a, s, e, f0, n);
-            if (all - skip <= kColumns)
+    uint64_t unit = units * blockIdx.x / gridDim.x;
+    const uint64_t end = units * (blockIdx.x + 1) / gridDim.x;
+    const int most = STAGED ? (int)a.columns : kColumns;
+    while (unit < end) {
+        const uint32_t i = (uint32_t)(unit / tiles), tile = (uint32_t)(unit - (uint64_t)i * tiles);
+        const uint32_t last = end - unit < tiles - tile ? tile + (uint32_t)(end - unit) : tiles;
+        const int e = s.c.active[i];
+        for (int skip = 0;; skip += most) {
+            int16_t *list = s.list[threadIdx.x >> 5];
+            const int all = list_pairs(a, s.c, e, skip, most, list);
+            const int n = all - skip < most ? all - skip : most;
+            if (STAGED) {
+                stage_columns<DT, WARPS>(a, list, n, xs);
+                __syncthreads();
+            }
+            for (uint32_t t = tile; t < last; ++t) {
+                if (n <= 8)
+                    up_unit<DT, WARPS, STAGED, 1>(a, s, xs, e, t * kUpRows, n);
+                else
+                    up_unit<DT, WARPS, STAGED, 2>(a, s, xs, e, t * kUpRows, n);
+            }
+            if (all - skip <= most)
                 break;
         }
+        unit += last - tile;
     }
 }
 
 // ---- second launch --------------------------------------------------------------
 
+constexpr int kDownWarps = 8, kDownThreads = 32 * kDownWarps;
 constexpr int kDownTiles = 1, kDownRows = 16 * kDownTiles;
 
 struct DownShared {
     Chosen c;
-    int16_t list[kMoeWarps][kColumns];
+    int16_t list[kDownWarps][kColumns];
 };
 static size_t down_smem(uint32_t T) {
-    return sizeof(DownShared) + sizeof(float) * kMoeWarps * kDownRows * T;
+    return sizeof(DownShared) + sizeof(float) * kDownWarps * kDownRows * T;
+}
+
+// The lane's elements of h, block kb of a row, all at one scale; returns its inverse.
+template <int DT, bool LO>
+__device__ __forceinline__ float load_hidden(const MoeArgs &a, const uint8_t *row, uint32_t kb,
+                                             bool on, uint4 (*hi)[2], uint4 (*lo)[2]) {
+    const uint32_t lane = threadIdx.x & 31, k = kb * 128 + lane % 4 * 16;
+    if (!HiddenRow<DT>::kHalf) {
+        float v[32];
+        load_column<AR_FP32>(row, k, a.F, true, on, v);
+        load_column<AR_FP32>(row, k + 64, a.F, true, on, v + 16);
+        return convert_column<LO>(v, hi, lo);
+    }
+    uint2 exponents = make_uint2(~0u, ~0u);
+    const uint8_t *at = row + kb * 256 + lane % 4 * 16;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            hi[half][j] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && k + 64 * half < a.F)
+                hi[half][j] = ld_v4_l1(at + half * 128 + j * 64);
+        }
+    if (on)
+        exponents = *reinterpret_cast<const uint2 *>(row + a.fb * 256ull + kb * 8);
+    // the largest magnitude has the least exponent of scale; the others come down to it
+    uint32_t least = __vminu4(exponents.x, exponents.y);
+    least = __vminu4(least, least >> 16);
+    least = min(least & 255u, least >> 8 & 255u);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t mine = (half ? exponents.y : exponents.x) >> (8 * (lane % 4)) & 255u;
+        const uint32_t down = mine - least;                  // at most 241
+        const float f = __uint_as_float(down < 126u ? (127u - down) << 23 : 0u);
+        const __half2 by = __float2half2_rn(f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t *w = &hi[half][j].x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(w + i), by);
+                w[i] = *reinterpret_cast<const uint32_t *>(&x);
+            }
+        }
+    }
+    return least >= 254u ? 0x1p-127f : __uint_as_float((254u - least) << 23);
 }
 
 // Blocks [kb0, kb1) along k of expert e times the listed pairs, added to this warp's
 // sums of their tokens.
-template <int NT>
+template <int DT, int NT>
 __device__ __forceinline__ void down_part(const MoeArgs &a, const int16_t *list, float *sums, int e,
                                           uint32_t r0, uint32_t kb0, uint32_t kb1, int n) {
+    constexpr bool kLo = !HiddenRow<DT>::kHalf;
     const int lane = threadIdx.x & 31;
     const uint8_t *w = a.down + (uint64_t)e * a.H * a.lddown;
     const float *ws = a.down_scale + (uint64_t)e * a.hb * a.fb;
+    const uint8_t *rows[kDownTiles][2];
+    const float *scales[kDownTiles][2];
+#pragma unroll
+    for (int m = 0; m < kDownTiles; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t r = r0 + m * 16 + i * 8 + lane / 4;
+            r = r < a.H ? r : a.H - 1;    // past the last: their sums go nowhere
+            rows[m][i] = w + (uint64_t)r * a.lddown;
+            scales[m][i] = ws + (uint64_t)(r / 128) * a.fb;
+        }
+    const uint8_t *columns[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int c = nt * 8 + lane / 4;
+        columns[nt] = a.h + (uint64_t)(c < n ? list[c] : 0) * a.sh;
+    }
     float sum[kDownTiles][NT][4] = {};
+    Codes<kDownTiles> next;
+    next.load(rows, kb0, a.F, a.wide_down);
     for (uint32_t kb = kb0; kb < kb1; ++kb) {
-        auto weights = [&](int mt, int half, int i) {
-            const uint32_t r = r0 + mt * 16 + i * 8 + lane / 4;
-            return load_codes(w + (uint64_t)r * a.lddown, kb * 128 + half * 64 + lane % 4 * 16, a.F,
-                              a.wide_down, r < a.H);
-        };
-        auto column = [&](int nt, int half, float *v) {
-            const int c = nt * 8 + lane / 4;
-            const uint32_t p = c < n ? list[c] : 0u;
-            load_column<AR_FP32>(reinterpret_cast<const uint8_t *>(a.h + p * a.ldh),
-                                 kb * 128 + half * 64 + lane % 4 * 16, a.F, true, c < n, v);
-        };
-        auto scale = [&](int mt, int i) {
-            const uint32_t r = r0 + mt * 16 + i * 8 + lane / 4;
-            return r < a.H ? ws[(uint64_t)(r / 128) * a.fb + kb] : 0.0f;
-        };
-        block_product<kDownTiles, NT, true>(sum, weights, column, scale);
+        const Codes<kDownTiles> now = next;
+        if (kb + 1 < kb1)
+            next.load(rows, kb + 1, a.F, a.wide_down);
+        float sc[kDownTiles][2];
+#pragma unroll
+        for (int m = 0; m < kDownTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                sc[m][i] = scales[m][i][kb];
+        float part[kDownTiles][NT][4] = {}, inverse[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            uint4 hi[2][2], lo[2][2];
+            const float inv = load_hidden<DT, kLo>(a, columns[nt], kb, nt * 8 + lane / 4 < n, hi,
+                                                   lo);
+            inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
+            inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
+            float one[kDownTiles][1][4] = {};
+            block_product<kDownTiles, 1>(
+                one, now, [&](int, int half, int piece) { return hi[half][piece]; });
+            if (kLo)
+                block_product<kDownTiles, 1>(
+                    one, now, [&](int, int half, int piece) { return lo[half][piece]; });
+#pragma unroll
+            for (int m = 0; m < kDownTiles; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    part[m][nt][i] = one[m][0][i];
+        }
+#pragma unroll
+        for (int m = 0; m < kDownTiles; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum[m][nt][i] += part[m][nt][i] * (inverse[nt][i & 1] * sc[m][i / 2]);
     }
     // columns of different pairs may be one token's (its choices of one expert): one
     // column at a time
@@ -347,82 +661,103 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const int16_t *list,
         if (lane % 4 == c % 8 / 2) {
             float *token = sums + (uint32_t)p / a.K * kDownRows;
 #pragma unroll
-            for (int mt = 0; mt < kDownTiles; ++mt)
+            for (int m = 0; m < kDownTiles; ++m)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     if (nt == c / 8)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            token[mt * 16 + i * 8 + lane / 4] +=
-                                g * (c & 1 ? sum[mt][nt][2 * i + 1] : sum[mt][nt][2 * i]);
+                            token[m * 16 + i * 8 + lane / 4] +=
+                                g * (c & 1 ? sum[m][nt][2 * i + 1] : sum[m][nt][2 * i]);
         }
         __syncwarp();
     }
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(const __grid_constant__ MoeArgs a) {
     extern __shared__ uint4 smem[];
     DownShared &s = *reinterpret_cast<DownShared *>(smem);
     float *sums = reinterpret_cast<float *>(&s + 1);      // [warp][token][row]
-    kernel_prologue();
+    // before the wait: the choices, which were there before the first launch
     choose(a, s.c);
     const int warp = threadIdx.x >> 5;
     const uint32_t r0 = blockIdx.x * kDownRows, each = a.T * kDownRows;
     float *mine = sums + (uint32_t)warp * each;
-    for (uint32_t i = threadIdx.x; i < each * kMoeWarps; i += kMoeThreads)
+    for (uint32_t i = threadIdx.x; i < each * kDownWarps; i += kDownThreads)
         sums[i] = 0.0f;
     __syncthreads();
+    kernel_prologue();
     // this warp's run of (expert, block)
     const uint32_t steps = (uint32_t)s.c.count * a.fb;
-    uint32_t at = (uint32_t)((uint64_t)steps * warp / kMoeWarps);
-    const uint32_t end = (uint32_t)((uint64_t)steps * (warp + 1) / kMoeWarps);
+    uint32_t at = (uint32_t)((uint64_t)steps * warp / kDownWarps);
+    const uint32_t end = (uint32_t)((uint64_t)steps * (warp + 1) / kDownWarps);
     while (at < end) {
         const uint32_t i = at / a.fb, kb0 = at - i * a.fb;
         const uint32_t kb1 = end - at < a.fb - kb0 ? kb0 + (end - at) : a.fb;
         const int e = s.c.active[i];
         for (int skip = 0;; skip += kColumns) {
-            const int all = list_pairs(a, s.c, e, skip, s.list[warp]);
+            const int all = list_pairs(a, s.c, e, skip, kColumns, s.list[warp]);
             const int n = all - skip < kColumns ? all - skip : kColumns;
             if (n <= 8)
-                down_part<1>(a, s.list[warp], mine, e, r0, kb0, kb1, n);
-            else if (n <= 16)
-                down_part<2>(a, s.list[warp], mine, e, r0, kb0, kb1, n);
+                down_part<DT, 1>(a, s.list[warp], mine, e, r0, kb0, kb1, n);
             else
-                down_part<4>(a, s.list[warp], mine, e, r0, kb0, kb1, n);
+                down_part<DT, 2>(a, s.list[warp], mine, e, r0, kb0, kb1, n);
             if (all - skip <= kColumns)
                 break;
         }
         at += kb1 - kb0;
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < each; i += kMoeThreads) {
+    for (uint32_t i = threadIdx.x; i < each; i += kDownThreads) {
         const uint32_t t = i / kDownRows, r = i % kDownRows;
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kMoeWarps; ++k)
+        for (int k = 0; k < kDownWarps; ++k)
             v += sums[k * each + i];
         if (r0 + r < a.H)
             st_elem<DT>(a.out + t * a.sout, r0 + r, narrow1<DT>(v));
     }
 }
 
-template <int DT> static cudaError_t moe_dt(const MoeArgs &a, cudaStream_t s) {
+template <int DT, int WARPS, bool STAGED>
+static cudaError_t launch_up(MoeArgs a, size_t room, int sms, cudaStream_t s) {
+    constexpr size_t base = (sizeof(UpShared<WARPS>) + 127) / 128 * 128;
+    constexpr auto kernel = k_moe_up<DT, WARPS, STAGED>;
+    const cudaError_t e = opt_in_smem<kernel>(kMoeSmem / (16 / WARPS));
+    if (e != cudaSuccess)
+        return e;
+    const size_t column = UpColumn<DT>::bytes(a.hb);
+    if (STAGED) {
+        const size_t held = room / column, pairs = (size_t)a.T * a.K;
+        a.columns = (uint32_t)(held < kColumns ? held : kColumns);
+        a.columns = a.columns < pairs ? a.columns : (uint32_t)pairs;
+    }
+    const uint64_t units = (uint64_t)((a.F + kUpRows - 1) / kUpRows) * a.T * a.K;
+    const uint64_t most = (uint64_t)(16 / WARPS) * sms;
+    return launch_kernel(kernel, (unsigned)(units < most ? units : most), 32 * WARPS,
+                         base + a.columns * column, s, true, a);
+}
+
+template <int DT> static cudaError_t moe_dt(MoeArgs a, cudaStream_t s) {
     const int sms = sm_count();
     if (sms < 1)
         return cudaErrorUnknown;
-    cudaError_t e = opt_in_smem<k_moe_up<DT>>(sizeof(UpShared));
-    if (e == cudaSuccess)
-        e = opt_in_smem<k_moe_down<DT>>(down_smem(AR_MOE_LAYER_TOKENS));
+    cudaError_t e = opt_in_smem<k_moe_down<DT>>(down_smem(AR_MOE_LAYER_TOKENS));
     if (e != cudaSuccess)
         return e;
-    const uint64_t units = (uint64_t)((a.F + kUpRows - 1) / kUpRows) * a.T * a.K;
-    const uint64_t most = 2 * (uint64_t)sms;
-    e = launch_kernel(k_moe_up<DT>, (unsigned)(units < most ? units : most), kMoeThreads,
-                      sizeof(UpShared), s, true, a);
+    a.sh = HiddenRow<DT>::bytes(a.F, a.fb);
+    // Two CTAs an SM of eight warps while each holds the columns of every token, so that one
+    // has its weights in flight while the other sums up; else one of sixteen.
+    constexpr size_t kTwo = kMoeSmem / 2 - (sizeof(UpShared<8>) + 127) / 128 * 128;
+    constexpr size_t kOne = kMoeSmem - (sizeof(UpShared<16>) + 127) / 128 * 128;
+    const size_t tokens = a.T < kColumns ? a.T : kColumns, column = UpColumn<DT>::bytes(a.hb);
+    e = tokens * column <= kTwo ? launch_up<DT, 8, true>(a, kTwo, sms, s)
+        : column <= kOne        ? launch_up<DT, 16, true>(a, kOne, sms, s)
+                                : launch_up<DT, 8, false>(a, 0, sms, s);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(k_moe_down<DT>, (a.H + kDownRows - 1) / kDownRows, kMoeThreads,
+    return launch_kernel(k_moe_down<DT>, (a.H + kDownRows - 1) / kDownRows, kDownThreads,
                          down_smem(a.T), s, true, a);
 }
 
@@ -475,12 +810,11 @@ int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, cons
     a.up_scale = up_scale;
     a.down_scale = down_scale;
     a.out = static_cast<uint8_t *>(out);
-    a.h = work;
+    a.h = reinterpret_cast<uint8_t *>(work);
     a.sx = mx.stride;
     a.sout = mo.stride;
     a.ldup = mu.stride;
     a.lddown = md.stride;
-    a.ldh = (F + 3) / 4 * 4;
     a.T = (uint32_t)T;
     a.K = (uint32_t)K;
     a.H = (uint32_t)H;
@@ -489,6 +823,7 @@ int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, cons
     a.hb = (uint32_t)hb;
     a.fb = (uint32_t)fb;
     a.ub = (uint32_t)ub;
+    a.columns = 0;
     a.wide_up = wide(mu);
     a.wide_down = wide(md);
     a.wide_x = wide(mx);

@@ -6,9 +6,12 @@ x or h has two parts: 64 u.  Scales, joining the blocks and the warps' sums: 6 u
 one more per addition.  With a = (80 + 2 blocks) u:
   |dg| <= a sum |up||x|,  likewise u
   |dh| <= 1.1 |u| |dg| + |silu(g)| |du| + 16 u |h|     (the slope of silu is below 1.1)
-  |dy| <= sum |down| (|dh| + 2^-21 |h|) + a' sum |down||h|
-x in binary32 has two parts of 11 bits, 2^-21 of x, and so has h.  Then the weighted sum
-over the choices, and one rounding to the output."""
+  |dy| <= sum |down| (|dh| + r |h|) + a' sum |down||h|
+x in binary32 has two parts of 11 bits, 2^-21 of x, and so has h then (r = 2^-21); for
+outputs of two bytes h has one, off by half a unit of binary16: r = 2^-11.  What lies more
+than 2^-29 below a block's largest element is a subnormal there, off by 2^-25 where the
+largest is at least 2^14: 2^-39 of it.  Then the weighted sum over the choices, and one
+rounding to the output."""
 import pytest
 import torch
 
@@ -68,13 +71,16 @@ class Layer:
             w2 = self.down[e].float().double() * self.ds[e].double()[i[H]][:, i[F]]
             v = x[t].double()
             both, mag = v @ w1.t(), v.abs() @ w1.abs().t()
+            mag = a1 * mag + 2.0 ** -39 * v.abs().amax(1, keepdim=True) * w1.abs().sum(1)
             g, u = both.split(F, 1)
-            dg, du = (a1 * m for m in mag.split(F, 1))
+            dg, du = mag.split(F, 1)
             act = g * torch.sigmoid(g)
             h = act * u
             dh = 1.1 * (u.abs() + du) * dg + act.abs() * du + 16 * U * h.abs()
             y = h @ w2.t()
-            dy = (dh + 2.0 ** -21 * h.abs()) @ w2.abs().t() + a2 * (h.abs() @ w2.abs().t())
+            off = 2.0 ** (-21 if dtype == "fp32" else -11)
+            dy = (dh + off * h.abs()) @ w2.abs().t() + a2 * (h.abs() @ w2.abs().t())
+            dy += 2.0 ** -39 * h.abs().amax(1, keepdim=True) * w2.abs().sum(1)
             gate = torch.ones(len(t), 1, dtype=torch.float64, device="cuda") if w is None else \
                 w[t, k, None].double()
             out.index_add_(0, t, gate * y)
