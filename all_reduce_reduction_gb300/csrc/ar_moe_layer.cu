@@ -134,10 +134,28 @@ __device__ __forceinline__ int list_pairs(const MoeArgs &a, const Chosen &c, int
 // ---- a block of 128 along k ----------------------------------------------------------
 
 // Lane l holds row or column l / 4 of an operand and, with c = l % 4, the elements
-// 16 c .. 16 c + 15 of each half of 64: four steps of a product's 16 (4 elements a lane).
+// 32 c .. 32 c + 31 of the block: eight steps of a product's 16 (4 elements a lane).  So
+// a load of 32 bytes a lane takes whole lines of eight rows: with 16 bytes a lane, half
+// lines, an SM's loads in flight ran out first (3.2 TB/s).
 // In memory, converted columns have the 8-element pieces of the four lanes side by side.
 __device__ __forceinline__ uint32_t place_of(uint32_t k) {
-    return (k & ~63u) + (k / 8 & 1) * 32 + (k / 16 & 3) * 8 + k % 8;
+    return (k & ~127u) + (k / 8 & 3) * 32 + (k / 32 & 3) * 8 + k % 8;
+}
+
+struct alignas(16) Words8 {
+    uint4 lo, hi;
+    __device__ __forceinline__ uint32_t operator[](int i) const {
+        const uint4 &v = i < 4 ? lo : hi;
+        return i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
+    }
+};
+__device__ __forceinline__ Words8 ld_v8_stream(const void *p) {
+    Words8 v;
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x),
+                   "=r"(v.hi.y), "=r"(v.hi.z), "=r"(v.hi.w)
+                 : "l"(p));
+    return v;
 }
 
 // 16 codes of a weight row from k on; zeros past K.
@@ -152,28 +170,27 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *row, uint32_t k, uint
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The lane's codes of MT tiles of 16 rows: [tile][half][row l / 4 or that + 8].
+// The lane's codes of MT tiles of 16 rows: [tile][row l / 4 or that + 8].
 template <int MT> struct Codes {
-    uint4 q[MT][2][2];
-    // rows: the lane's row pointers, [tile][2]; block kb of K
+    Words8 q[MT][2];
+    // rows: the lane's row pointers, [tile][2]; block kb of K.  wide: rows on 16-byte (1) or
+    // 32-byte boundaries (2).
     __device__ __forceinline__ void load(const uint8_t *const (*rows)[2], uint32_t kb, uint32_t K,
-                                         bool wide) {
-        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 16;
-        if (wide && kb * 128 + 128 <= K) {
+                                         int wide) {
+        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 32;
+        if (wide == 2 && kb * 128 + 128 <= K) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    q[m][0][i] = ld_v4_stream(rows[m][i] + k);
-                    q[m][1][i] = ld_v4_stream(rows[m][i] + k + 64);
-                }
+                for (int i = 0; i < 2; ++i)
+                    q[m][i] = ld_v8_stream(rows[m][i] + k);
         } else {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    q[m][0][i] = load_codes(rows[m][i], k, K, wide);
-                    q[m][1][i] = load_codes(rows[m][i], k + 64, K, wide);
+                    q[m][i].lo = load_codes(rows[m][i], k, K, wide);
+                    q[m][i].hi = load_codes(rows[m][i], k + 16, K, wide);
                 }
         }
     }
@@ -183,38 +200,35 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// part += codes * columns.  column(nt, half, piece): eight of the lane's elements of
-// column l / 4 of tile nt, two steps' worth.
+// part += codes * columns.  column(nt, piece): eight of the lane's elements of column
+// l / 4 of tile nt, two steps' worth.
 template <int MT, int NT, typename Column>
 __device__ __forceinline__ void block_product(float (*part)[NT][4], const Codes<MT> &w,
                                               Column column) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int piece = 0; piece < 4; ++piece) {
+        uint4 b[NT];
 #pragma unroll
-        for (int piece = 0; piece < 2; ++piece) {
-            uint4 b[NT];
+        for (int n = 0; n < NT; ++n)
+            b[n] = column(n, piece);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                b[n] = column(n, half, piece);
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int m = 0; m < MT; ++m) {
+                uint32_t r[4];
+                from_e4m3x4(w.q[m][0][2 * piece + k], r[0], r[2]);
+                from_e4m3x4(w.q[m][1][2 * piece + k], r[1], r[3]);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t r[4];
-                    from_e4m3x4(word_of(w.q[m][half][0], 2 * piece + k), r[0], r[2]);
-                    from_e4m3x4(word_of(w.q[m][half][1], 2 * piece + k), r[1], r[3]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma16<AR_FP16>(part[m][n], r, word_of(b[n], 2 * k),
-                                       word_of(b[n], 2 * k + 1));
-                }
-        }
+                for (int n = 0; n < NT; ++n)
+                    mma16<AR_FP16>(part[m][n], r, word_of(b[n], 2 * k), word_of(b[n], 2 * k + 1));
+            }
+    }
 }
 
-// 32 binary32 values of a column (of two halves, 16 each) to binary16: scaled by a power
-// of two for the block, in one part or two.  Returns the inverse of the scale.
+// The lane's 32 binary32 values of a column to binary16: scaled by a power of two for the
+// block, in one part or two.  Returns the inverse of the scale.
 template <bool LO>
-__device__ __forceinline__ float convert_column(const float *v, uint4 (*hi)[2], uint4 (*lo)[2]) {
+__device__ __forceinline__ float convert_column(const float *v, uint4 *hi, uint4 *lo) {
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
@@ -224,20 +238,18 @@ __device__ __forceinline__ float convert_column(const float *v, uint4 (*hi)[2], 
     float s, inverse;
     half_range(top, s, inverse);
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int j = 0; j < 4; ++j) {
+        uint32_t a[4], b[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float *x = v + 16 * half + 8 * j + 2 * i;
-                a[i] = half2_of(x[0] * s, x[1] * s);
-                b[i] = LO ? rest_of(a[i], x[0] * s, x[1] * s) : 0u;
-            }
-            hi[half][j] = make_uint4(a[0], a[1], a[2], a[3]);
-            if (LO)
-                lo[half][j] = make_uint4(b[0], b[1], b[2], b[3]);
+        for (int i = 0; i < 4; ++i) {
+            const float *x = v + 8 * j + 2 * i;
+            a[i] = half2_of(x[0] * s, x[1] * s);
+            b[i] = LO ? rest_of(a[i], x[0] * s, x[1] * s) : 0u;
         }
+        hi[j] = make_uint4(a[0], a[1], a[2], a[3]);
+        if (LO)
+            lo[j] = make_uint4(b[0], b[1], b[2], b[3]);
+    }
     return inverse;
 }
 
@@ -384,11 +396,10 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, co
         if constexpr (STAGED) {
 #pragma unroll
             for (int lo = 0; lo < C::kParts; ++lo)
-                block_product<kUpTiles, NT>(part, now, [&](int nt, int half, int piece) {
+                block_product<kUpTiles, NT>(part, now, [&](int nt, int piece) {
                     return nt * 8 + (int)lane / 4 < n
                                ? *reinterpret_cast<const uint4 *>(
-                                     mine + nt * 8 * bytes + (lo * a.hb + kb) * 256 + half * 128 +
-                                     piece * 64)
+                                     mine + nt * 8 * bytes + (lo * a.hb + kb) * 256 + piece * 64)
                                : make_uint4(0u, 0u, 0u, 0u);
                 });
 #pragma unroll
@@ -403,20 +414,20 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, co
             for (int nt = 0; nt < NT; ++nt) {
                 const int c = nt * 8 + (int)lane / 4;
                 const uint8_t *row = a.x + (uint64_t)(c < n ? list[c] / a.K : 0u) * a.sx;
-                const uint32_t k = kb * 128 + lane % 4 * 16;
+                const uint32_t k = kb * 128 + lane % 4 * 32;
                 float v[32];
                 load_column<DT>(row, k, a.H, a.wide_x, c < n, v);
-                load_column<DT>(row, k + 64, a.H, a.wide_x, c < n, v + 16);
-                uint4 hi[2][2], lo[2][2];
+                load_column<DT>(row, k + 16, a.H, a.wide_x, c < n, v + 16);
+                uint4 hi[4], lo[4];
                 const float inv = convert_column<kLo>(v, hi, lo);
                 inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
                 inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
                 float one[kUpTiles][1][4] = {};
                 block_product<kUpTiles, 1>(
-                    one, now, [&](int, int half, int piece) { return hi[half][piece]; });
+                    one, now, [&](int, int piece) { return hi[piece]; });
                 if (kLo)
                     block_product<kUpTiles, 1>(
-                        one, now, [&](int, int half, int piece) { return lo[half][piece]; });
+                        one, now, [&](int, int piece) { return lo[piece]; });
 #pragma unroll
                 for (int m = 0; m < kUpTiles; ++m)
 #pragma unroll
@@ -543,24 +554,22 @@ static size_t down_smem(uint32_t T) {
 // The lane's elements of h, block kb of a row, all at one scale; returns its inverse.
 template <int DT, bool LO>
 __device__ __forceinline__ float load_hidden(const MoeArgs &a, const uint8_t *row, uint32_t kb,
-                                             bool on, uint4 (*hi)[2], uint4 (*lo)[2]) {
-    const uint32_t lane = threadIdx.x & 31, k = kb * 128 + lane % 4 * 16;
+                                             bool on, uint4 *hi, uint4 *lo) {
+    const uint32_t lane = threadIdx.x & 31, k = kb * 128 + lane % 4 * 32;
     if (!HiddenRow<DT>::kHalf) {
         float v[32];
         load_column<AR_FP32>(row, k, a.F, true, on, v);
-        load_column<AR_FP32>(row, k + 64, a.F, true, on, v + 16);
+        load_column<AR_FP32>(row, k + 16, a.F, true, on, v + 16);
         return convert_column<LO>(v, hi, lo);
     }
     uint2 exponents = make_uint2(~0u, ~0u);
     const uint8_t *at = row + kb * 256 + lane % 4 * 16;
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            hi[half][j] = make_uint4(0u, 0u, 0u, 0u);
-            if (on && k + 64 * half < a.F)
-                hi[half][j] = ld_v4_l1(at + half * 128 + j * 64);
-        }
+    for (int j = 0; j < 4; ++j) {
+        hi[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (on && k + 16 * (j / 2) < a.F)
+            hi[j] = ld_v4_l1(at + j * 64);
+    }
     if (on)
         exponents = *reinterpret_cast<const uint2 *>(row + a.fb * 256ull + kb * 8);
     // the largest magnitude has the least exponent of scale; the others come down to it
@@ -569,13 +578,15 @@ __device__ __forceinline__ float load_hidden(const MoeArgs &a, const uint8_t *ro
     least = min(least & 255u, least >> 8 & 255u);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const uint32_t mine = (half ? exponents.y : exponents.x) >> (8 * (lane % 4)) & 255u;
+        // tiles 2 c and 2 c + 1
+        const uint32_t mine = (lane & 2 ? exponents.y : exponents.x) >>
+                                  (16 * (lane & 1) + 8 * half) & 255u;
         const uint32_t down = mine - least;                  // at most 241
         const float f = __uint_as_float(down < 126u ? (127u - down) << 23 : 0u);
         const __half2 by = __float2half2_rn(f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            uint32_t *w = &hi[half][j].x;
+            uint32_t *w = &hi[2 * half + j].x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(w + i), by);
@@ -628,17 +639,17 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const int16_t *list,
         float part[kDownTiles][NT][4] = {}, inverse[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            uint4 hi[2][2], lo[2][2];
+            uint4 hi[4], lo[4];
             const float inv = load_hidden<DT, kLo>(a, columns[nt], kb, nt * 8 + lane / 4 < n, hi,
                                                    lo);
             inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
             inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
             float one[kDownTiles][1][4] = {};
             block_product<kDownTiles, 1>(
-                one, now, [&](int, int half, int piece) { return hi[half][piece]; });
+                one, now, [&](int, int piece) { return hi[piece]; });
             if (kLo)
                 block_product<kDownTiles, 1>(
-                    one, now, [&](int, int half, int piece) { return lo[half][piece]; });
+                    one, now, [&](int, int piece) { return lo[piece]; });
 #pragma unroll
             for (int m = 0; m < kDownTiles; ++m)
 #pragma unroll
@@ -824,8 +835,8 @@ int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, cons
     a.fb = (uint32_t)fb;
     a.ub = (uint32_t)ub;
     a.columns = 0;
-    a.wide_up = wide(mu);
-    a.wide_down = wide(md);
+    a.wide_up = wide(mu) + wide(mu, 32);
+    a.wide_down = wide(md) + wide(md, 32);
     a.wide_x = wide(mx);
     a.ids8 = ids_bytes == 8;
     switch (dtype) {
