@@ -14,38 +14,15 @@
 //
 // Every wait is bounded: past kWaitNs it writes AR_ERR_TIMEOUT to the caller's
 // status word and the CTA's roles all leave.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <atomic>
-
 #include "ar_cluster.cuh"
 #include "ar_matmul8.cuh"
+#include "ar_tensor_map.cuh"
 
 namespace ar {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;"
-                 :: "r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
 // Bounded wait for the phase of this parity; false if this wait ran out or
 // another role of the CTA gave up.  Called after a first try.
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort,
@@ -106,23 +83,6 @@ __device__ __forceinline__ void linger() {
     const uint64_t deadline = globaltimer_ns() + 1000000ull;
     while (globaltimer_ns() < deadline) {
     }
-}
-
-// Tile of a tensor map into shared memory; x is a byte offset along k, a
-// multiple of 128.
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                       uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];"
-        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
-                                       uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];"
-        :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
 // The same for a CTA of a pair, the bytes counted by a barrier of either CTA.
@@ -907,35 +867,6 @@ k_matmul8_few(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUte
 }
 
 // ---- host ---------------------------------------------------------------------
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static std::atomic<void *> found{nullptr};
-    void *p = found.load(std::memory_order_acquire);
-    if (!p) {
-        cudaDriverEntryPointQueryResult how;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &how) != cudaSuccess ||
-            how != cudaDriverEntryPointSuccess) {
-            (void)cudaGetLastError();
-            return nullptr;
-        }
-        found.store(p, std::memory_order_release);
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-}
-
-// Tiles of 128 bytes x `rows`; bytes past k and rows past the end read as zero.
-bool encode(CUtensorMap *map, const void *base, uint64_t k, uint64_t rows, uint64_t stride,
-            uint64_t groups, uint32_t box_rows) {
-    const cuuint64_t dims[3] = {k, rows, groups};
-    const cuuint64_t strides[2] = {stride, stride * rows};
-    const cuuint32_t box[3] = {128, box_rows, 1}, ones[3] = {1, 1, 1};
-    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups ? 3 : 2,
-                     const_cast<void *>(base), dims, strides, box, ones,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int NT>
 cudaError_t launch_few(const MatmulArgs &a, int parts, cudaStream_t s) {

@@ -10,24 +10,35 @@
 // one would round x.  A block of 128 along k gets its scales in binary32 when it is
 // summed.
 //
-// Weights go from global memory straight to the lanes that multiply with them: a
-// lane takes 16 bytes of a row, and the order of k inside a block is that of the
-// lanes (see place_of), for the columns too.
+// Weights come by TMA, a warp's own tiles of 16 rows by 128 bytes, through a ring of two
+// stages per warp: a stage is free as soon as its codes are in the lanes' registers, and
+// the ring runs on across the ends of units.  (By loads to registers, 16 rows at a time,
+// an SM's requests in flight ran out: 2.5 TB/s with 16 bytes a lane, 3.5 with 32.)  Rows
+// that are not on 16-byte boundaries are read by bytes.  A lane takes 32 bytes of a row,
+// and the order of k inside a block is that of the lanes (see place_of), for the columns
+// too.
 //
 // First launch (up): a CTA takes 16 rows of both halves of one expert at a time, its
-// warps share the blocks along k.  The columns lie in shared memory, converted when
-// the expert changes.  Second launch (down): a CTA takes rows of the output, its warps
-// share the blocks along k of all experts; each keeps its own sums of all tokens, which
-// are added in order.
+// warps share the blocks along k.  The columns lie in shared memory, converted when the
+// expert changes, or, where they are too many for it, are converted on the way.  Second
+// launch (down): a CTA takes rows of the output, its warps share the blocks along k of
+// all experts; each keeps its own sums of all tokens, which are added in order.
+//
+// Every wait is bounded; after one that ran out the output is NaN.
 #include "ar_mma.cuh"
 #include "ar_rows.cuh"
+#include "ar_tensor_map.cuh"
 
 namespace ar {
 
 constexpr int kMoePairs = AR_MOE_LAYER_PAIRS;
-// Dynamic shared memory of an SM that one or two CTAs share.
-constexpr size_t kMoeSmem = 224 * 1024;
+// Dynamic shared memory of a CTA that has an SM to itself.
+constexpr size_t kMoeSmem = 226 * 1024;
 constexpr int kColumns = 16;          // most pairs of an expert in one pass over its weights
+
+__device__ __forceinline__ uint32_t smem_at(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
 
 struct MoeArgs {
     const uint8_t *x;
@@ -42,8 +53,10 @@ struct MoeArgs {
     uint32_t T, K, H, F, E;
     uint32_t hb, fb, ub;              // blocks of 128 along H, F and 2F
     uint32_t columns;                 // pairs that the first launch's shared memory holds
-    int wide_up, wide_down, wide_x;
+    int wide_x;
     int ids8;
+    uint8_t *failed;                  // of each CTA of the first launch: a wait ran out
+    uint32_t ups;                     // those CTAs
 };
 
 // ---- who goes where ---------------------------------------------------------------
@@ -52,6 +65,7 @@ struct MoeArgs {
 struct Chosen {
     int16_t expert[kMoePairs];        // of a pair, or -1
     int16_t active[kMoePairs];
+    int16_t pairs[kMoePairs];         // of an active expert
     int first[AR_MOE_MAX_EXPERTS];
     int count;                        // of active
     int warp_count[kMoePairs / 32];
@@ -63,6 +77,25 @@ __device__ __forceinline__ int expert_of(const MoeArgs &a, uint32_t p) {
     return id >= 0 && id < (int64_t)a.E ? (int)id : -1;
 }
 
+// The pairs of expert e in order, by one warp: `list` receives those from `skip` on,
+// at most `most`; returns how many there are in all.
+__device__ __forceinline__ int list_pairs(const MoeArgs &a, const Chosen &c, int e, int skip,
+                                          int most, int16_t *list) {
+    const uint32_t pairs = a.T * a.K, lane = threadIdx.x & 31;
+    int n = 0;
+    for (uint32_t p0 = 0; p0 < pairs; p0 += 32) {
+        const uint32_t p = p0 + lane;
+        const bool mine = p < pairs && c.expert[p] == e;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
+        const int at = n + __popc(m & ((1u << lane) - 1u)) - skip;
+        if (mine && at >= 0 && at < most)
+            list[at] = (int16_t)p;
+        n += __popc(m);
+    }
+    __syncwarp();
+    return n;
+}
+
 __device__ __forceinline__ void choose(const MoeArgs &a, Chosen &c) {
     const uint32_t pairs = a.T * a.K, lane = threadIdx.x & 31;
     if (pairs <= 32) {                // one warp sees them all
@@ -72,8 +105,11 @@ __device__ __forceinline__ void choose(const MoeArgs &a, Chosen &c) {
             const bool lead = e >= 0 && (like & ((1u << lane) - 1u)) == 0;
             const uint32_t leads = __ballot_sync(0xFFFFFFFFu, lead);
             c.expert[lane] = (int16_t)e;
-            if (lead)
-                c.active[__popc(leads & ((1u << lane) - 1u))] = (int16_t)e;
+            if (lead) {
+                const int at = __popc(leads & ((1u << lane) - 1u));
+                c.active[at] = (int16_t)e;
+                c.pairs[at] = (int16_t)__popc(like);
+            }
             if (lane == 0)
                 c.count = __popc(leads);
         }
@@ -110,88 +146,101 @@ __device__ __forceinline__ void choose(const MoeArgs &a, Chosen &c) {
             c.count = before + __popc(m);
     }
     __syncthreads();
-}
-
-// The pairs of expert e in order, by one warp: `list` receives those from `skip` on,
-// at most `most`; returns how many there are in all.
-__device__ __forceinline__ int list_pairs(const MoeArgs &a, const Chosen &c, int e, int skip,
-                                          int most, int16_t *list) {
-    const uint32_t pairs = a.T * a.K, lane = threadIdx.x & 31;
-    int n = 0;
-    for (uint32_t p0 = 0; p0 < pairs; p0 += 32) {
-        const uint32_t p = p0 + lane;
-        const bool mine = p < pairs && c.expert[p] == e;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, mine);
-        const int at = n + __popc(m & ((1u << lane) - 1u)) - skip;
-        if (mine && at >= 0 && at < most)
-            list[at] = (int16_t)p;
-        n += __popc(m);
+    for (int i = threadIdx.x >> 5; i < c.count; i += blockDim.x >> 5) {
+        const int n = list_pairs(a, c, c.active[i], 0, 0, nullptr);
+        if (lane == 0)
+            c.pairs[i] = (int16_t)n;
     }
-    __syncwarp();
-    return n;
+    __syncthreads();
 }
 
 // ---- a block of 128 along k ----------------------------------------------------------
 
 // Lane l holds row or column l / 4 of an operand and, with c = l % 4, the elements
-// 32 c .. 32 c + 31 of the block: eight steps of a product's 16 (4 elements a lane).  So
-// a load of 32 bytes a lane takes whole lines of eight rows: with 16 bytes a lane, half
-// lines, an SM's loads in flight ran out first (3.2 TB/s).
+// 32 c .. 32 c + 31 of the block: eight steps of a product's 16 (4 elements a lane).
 // In memory, converted columns have the 8-element pieces of the four lanes side by side.
 __device__ __forceinline__ uint32_t place_of(uint32_t k) {
     return (k & ~127u) + (k / 8 & 3) * 32 + (k / 32 & 3) * 8 + k % 8;
 }
 
-struct alignas(16) Words8 {
+struct Words8 {
     uint4 lo, hi;
     __device__ __forceinline__ uint32_t operator[](int i) const {
         const uint4 &v = i < 4 ? lo : hi;
         return i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w;
     }
 };
-__device__ __forceinline__ Words8 ld_v8_stream(const void *p) {
-    Words8 v;
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x),
-                   "=r"(v.hi.y), "=r"(v.hi.z), "=r"(v.hi.w)
-                 : "l"(p));
-    return v;
-}
 
-// 16 codes of a weight row from k on; zeros past K.
-__device__ __forceinline__ uint4 load_codes(const uint8_t *row, uint32_t k, uint32_t K, bool wide) {
+// 16 codes of a weight row from k on, byte by byte; zeros past K.
+__device__ __forceinline__ uint4 load_codes(const uint8_t *row, uint32_t k, uint32_t K) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (k < K) {
-        if (wide && k + 16 <= K)
-            return ld_v4_stream(row + k);
-        for (uint32_t i = 0; i < 16 && k + i < K; ++i)
-            w[i / 4] |= (uint32_t)row[k + i] << (8 * (i & 3));
-    }
+    for (uint32_t i = 0; i < 16 && k + i < K; ++i)
+        w[i / 4] |= (uint32_t)row[k + i] << (8 * (i & 3));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The lane's codes of MT tiles of 16 rows: [tile][row l / 4 or that + 8].
 template <int MT> struct Codes {
     Words8 q[MT][2];
-    // rows: the lane's row pointers, [tile][2]; block kb of K.  wide: rows on 16-byte (1) or
-    // 32-byte boundaries (2).
-    __device__ __forceinline__ void load(const uint8_t *const (*rows)[2], uint32_t kb, uint32_t K,
-                                         int wide) {
-        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 32;
-        if (wide == 2 && kb * 128 + 128 <= K) {
+};
+
+// A warp's ring of two stages of `BOXES` tiles of 16 rows by 128 bytes, in 1024-byte
+// units whose 16-byte pieces are exchanged by row (the map's 128-byte swizzle).
+constexpr uint64_t kMoeWaitNs = 2000000000ull;
+constexpr uint32_t kBox = 16 * 128;
+template <int BOXES> struct Ring {
+    static constexpr uint32_t kStage = BOXES * kBox;
+    uint32_t at, bars;                // this warp's stages and barriers
+    const uint8_t *memory;
+    volatile int *failed;             // of the CTA
+    uint32_t issued, used;
+
+    __device__ __forceinline__ void begin(uint8_t *stages, uint64_t *barriers, int *flag) {
+        at = (uint32_t)__cvta_generic_to_shared(stages);
+        bars = (uint32_t)__cvta_generic_to_shared(barriers);
+        memory = stages;
+        failed = flag;
+        issued = used = 0;
+    }
+    // Boxes at (k, rows[b]) of matrix e to the next stage; by one lane.
+    __device__ __forceinline__ void issue(const CUtensorMap *map, uint32_t k,
+                                          const uint32_t *rows, int e) {
+        const uint32_t s = issued & 1, bar = bars + 8 * s;
+        mbar_expect(bar, kStage);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    q[m][i] = ld_v8_stream(rows[m][i] + k);
-        } else {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    q[m][i].lo = load_codes(rows[m][i], k, K, wide);
-                    q[m][i].hi = load_codes(rows[m][i], k + 16, K, wide);
-                }
+        for (int b = 0; b < BOXES; ++b)
+            tma_3d(at + s * kStage + b * kBox, map, (int)k, (int)rows[b], e, bar);
+    }
+    // Until the oldest stage is there; after a failure at once.
+    __device__ __forceinline__ void wait() {
+        const uint32_t bar = bars + 8 * (used & 1), parity = used >> 1 & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))
+            wait_slow(bar, parity);
+    }
+    __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity) {
+        const uint64_t deadline = globaltimer_ns() + kMoeWaitNs;
+        while (!*failed && !mbar_test(bar, parity))
+            if (globaltimer_ns() > deadline)
+                *failed = 1;
+        __syncwarp();
+    }
+    // This lane's codes of row r of box b.
+    __device__ __forceinline__ Words8 codes(int b, uint32_t r) const {
+        const uint8_t *row = memory + (used & 1) * kStage + b * kBox + r * 128;
+        const uint32_t c = (threadIdx.x & 3) * 2;
+        Words8 w;
+        w.lo = *reinterpret_cast<const uint4 *>(row + ((c ^ (r & 7)) << 4));
+        w.hi = *reinterpret_cast<const uint4 *>(row + (((c + 1) ^ (r & 7)) << 4));
+        return w;
+    }
+    // After a failure: until what is in flight has landed, so that nothing comes to the
+    // CTA's memory once it has left.
+    __device__ __forceinline__ void drain() {
+        for (; used < issued; ++used) {
+            const uint64_t deadline = globaltimer_ns() + kMoeWaitNs;
+            while (!mbar_test(bars + 8 * (used & 1), used >> 1 & 1) &&
+                   globaltimer_ns() < deadline) {
+            }
         }
     }
 };
@@ -285,11 +334,15 @@ template <int DT> struct HiddenRow {
 // ---- first launch -------------------------------------------------------------
 
 constexpr int kUpTiles = 2, kUpRows = 8 * kUpTiles;       // rows of each half
+constexpr int kUpWarps = 16, kUpThreads = 32 * kUpWarps;
+static_assert(kUpRows == 16, "a box of each half; and what shares an exponent of h");
 
-template <int WARPS> struct UpShared {
+struct UpShared {
     Chosen c;
-    int16_t list[WARPS][kColumns];
-    float part[WARPS][2][kUpRows][kColumns + 1];
+    int16_t list[kUpWarps][kColumns];
+    float part[kUpWarps][2][kUpRows][kColumns + 1];
+    uint64_t bars[kUpWarps][2];
+    int failed;
 };
 // A column in shared memory: blocks of 256 bytes, in one part or two, and an inverse
 // scale each.  Columns start 64 bytes apart in the banks.
@@ -301,13 +354,13 @@ template <int DT> struct UpColumn {
 };
 
 // The listed pairs' tokens to shared memory, a warp to a block.
-template <int DT, int WARPS>
+template <int DT>
 __device__ __forceinline__ void stage_columns(const MoeArgs &a, const int16_t *list, int n,
                                               uint8_t *xs) {
     using C = UpColumn<DT>;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bytes = C::bytes(a.hb);
 #pragma unroll 4
-    for (uint32_t item = warp; item < n * a.hb; item += WARPS) {
+    for (uint32_t item = warp; item < n * a.hb; item += kUpWarps) {
         const uint32_t c = item / a.hb, kb = item - c * a.hb, k = kb * 128 + lane * 4;
         const uint8_t *row = a.x + (uint64_t)(list[c] / a.K) * a.sx;
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -351,14 +404,72 @@ __device__ __forceinline__ void stage_columns(const MoeArgs &a, const int16_t *l
     }
 }
 
-// Rows f0.. of both halves of expert e times n listed pairs.  STAGED: they lie in shared
-// memory at xs; otherwise they are read and converted on the way.
-template <int DT, int WARPS, bool STAGED, int NT>
-__device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, const uint8_t *xs,
-                                        int e, uint32_t f0, int n) {
+// The weights that a warp of the first launch fetches, in the order in which it uses them:
+// for each expert of the CTA's run, for each pass over its pairs, for each tile of rows,
+// its blocks along k.
+struct UpCursor {
+    uint32_t i, tile, first, last, kb, pass;
+    uint64_t left;                    // tiles of the run past this expert's
+    bool done;
+
+    __device__ __forceinline__ void begin(const MoeArgs &a, uint32_t tiles, uint64_t unit,
+                                          uint64_t end) {
+        const uint32_t warp = threadIdx.x >> 5;
+        done = unit >= end || warp >= a.hb;
+        i = (uint32_t)(unit / tiles);
+        first = tile = (uint32_t)(unit - (uint64_t)i * tiles);
+        last = end - unit < tiles - tile ? tile + (uint32_t)(end - unit) : tiles;
+        left = end - unit - (last - tile);
+        kb = warp;
+        pass = 0;
+    }
+    __device__ __forceinline__ void next(const MoeArgs &a, const Chosen &c, uint32_t tiles) {
+        kb += kUpWarps;
+        if (kb < a.hb)
+            return;
+        kb = threadIdx.x >> 5;
+        if (++tile < last)
+            return;
+        tile = first;
+        if (++pass * kColumns < (uint32_t)c.pairs[i])
+            return;
+        pass = 0;
+        ++i;
+        first = tile = 0;
+        last = left < tiles ? (uint32_t)left : tiles;
+        left -= last;
+        done = last == 0;
+    }
+};
+
+// What a warp of the first launch works with.
+struct UpWarp {
+    Ring<2> ring;
+    UpCursor cursor;
+    const CUtensorMap *map;
+    uint32_t tiles;
+
+    // the next step's weights on their way, if there is one
+    __device__ __forceinline__ void fetch(const MoeArgs &a, const Chosen &c) {
+        if (cursor.done)
+            return;
+        if ((threadIdx.x & 31) == 0 && !*ring.failed) {
+            const uint32_t rows[2] = {cursor.tile * kUpRows, a.F + cursor.tile * kUpRows};
+            ring.issue(map, cursor.kb * 128, rows, c.active[cursor.i]);
+        }
+        ++ring.issued;
+        cursor.next(a, c, tiles);
+    }
+};
+
+// Rows f0.. of both halves of expert e times n listed pairs.  BULK: the weights come
+// through the ring.  STAGED: the columns lie in shared memory at xs; otherwise they are
+// read and converted on the way.
+template <int DT, bool BULK, bool STAGED, int NT>
+__device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &me,
+                                        const uint8_t *xs, int e, uint32_t f0, int n) {
     using C = UpColumn<DT>;
     constexpr bool kLo = C::kParts == 2;
-    constexpr bool kAhead = STAGED && NT == 1;    // registers for the next block's weights
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int16_t *list = s.list[warp];
     const uint8_t *w = a.up + (uint64_t)e * 2 * a.F * a.ldup;
@@ -379,18 +490,45 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, co
     const uint8_t *mine = xs + lane / 4 * bytes + lane % 4 * 16;
     const float *inverses = reinterpret_cast<const float *>(xs + first * bytes +
                                                             C::kParts * a.hb * 256);
-    float sum[kUpTiles][NT][4] = {};
-    Codes<kUpTiles> next;
-    if (kAhead && warp < a.hb)
-        next.load(rows, warp, a.H, a.wide_up);
-    for (uint32_t kb = warp; kb < a.hb; kb += WARPS) {
+    float sum[kUpTiles][NT][4] = {}, next_scale[kUpTiles][2];
+    auto load_scales = [&](uint32_t kb) {
+#pragma unroll
+        for (int m = 0; m < kUpTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                next_scale[m][i] = ws[scales[m][i] + kb];
+    };
+    if (warp < a.hb)
+        load_scales(warp);
+    for (uint32_t kb = warp; kb < a.hb; kb += kUpWarps) {
+        float sc[kUpTiles][2];
+#pragma unroll
+        for (int m = 0; m < kUpTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                sc[m][i] = next_scale[m][i];
+        if (kb + kUpWarps < a.hb)
+            load_scales(kb + kUpWarps);
         Codes<kUpTiles> now;
-        if (kAhead) {
-            now = next;
-            if (kb + WARPS < a.hb)
-                next.load(rows, kb + WARPS, a.H, a.wide_up);
+        if (BULK) {
+            me.ring.wait();
+#pragma unroll
+            for (int m = 0; m < kUpTiles; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    now.q[m][i] = me.ring.codes(i, m * 8 + lane / 4);
+            __syncwarp();
+            ++me.ring.used;
+            me.fetch(a, s.c);
         } else {
-            now.load(rows, kb, a.H, a.wide_up);
+            const uint32_t k = kb * 128 + lane % 4 * 32;
+#pragma unroll
+            for (int m = 0; m < kUpTiles; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    now.q[m][i].lo = load_codes(rows[m][i], k, a.H);
+                    now.q[m][i].hi = load_codes(rows[m][i], k + 16, a.H);
+                }
         }
         float part[kUpTiles][NT][4] = {}, inverse[NT][2];   // of this lane's columns
         if constexpr (STAGED) {
@@ -423,11 +561,10 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, co
                 inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
                 inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
                 float one[kUpTiles][1][4] = {};
-                block_product<kUpTiles, 1>(
-                    one, now, [&](int, int piece) { return hi[piece]; });
+                block_product<kUpTiles, 1>(one, now, [&](int, int piece) { return hi[piece]; });
                 if (kLo)
-                    block_product<kUpTiles, 1>(
-                        one, now, [&](int, int piece) { return lo[piece]; });
+                    block_product<kUpTiles, 1>(one, now,
+                                               [&](int, int piece) { return lo[piece]; });
 #pragma unroll
                 for (int m = 0; m < kUpTiles; ++m)
 #pragma unroll
@@ -438,14 +575,10 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, co
 #pragma unroll
         for (int m = 0; m < kUpTiles; ++m)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float sc = ws[scales[m][i] + kb];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        sum[m][nt][2 * i + j] += part[m][nt][2 * i + j] * (inverse[nt][j] * sc);
-            }
+                for (int i = 0; i < 4; ++i)
+                    sum[m][nt][i] += part[m][nt][i] * (inverse[nt][i & 1] * sc[m][i / 2]);
     }
 #pragma unroll
     for (int m = 0; m < kUpTiles; ++m)
@@ -457,13 +590,13 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, co
                     sum[m][nt][i];
     __syncthreads();
     // 16 lanes have the rows of one pair
-    for (int c0 = warp * 2; c0 < n; c0 += 2 * WARPS) {
+    for (int c0 = (int)warp * 2; c0 < n; c0 += 2 * kUpWarps) {
         const int c = c0 + lane / kUpRows, r = lane % kUpRows;
         float h = 0.0f;
         if (c < n && f0 + r < a.F) {
             float g = 0.0f, u = 0.0f;
 #pragma unroll
-            for (int k = 0; k < WARPS; ++k) {
+            for (int k = 0; k < kUpWarps; ++k) {
                 g += s.part[k][0][r][c];
                 u += s.part[k][1][r][c];
             }
@@ -496,14 +629,25 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared<WARPS> &s, co
     __syncthreads();
 }
 
-template <int DT, int WARPS, bool STAGED>
-__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS)
-k_moe_up(const __grid_constant__ MoeArgs a) {
-    extern __shared__ uint4 smem[];
-    UpShared<WARPS> &s = *reinterpret_cast<UpShared<WARPS> *>(smem);
+template <int DT, bool BULK>
+__global__ void __launch_bounds__(kUpThreads, 1)
+k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap map) {
+    extern __shared__ uint8_t raw[];
+    // the rings first: their swizzle wants 1024-byte boundaries
+    uint8_t *rings = raw + ((1024u - (smem_at(raw) & 1023u)) & 1023u);
+    UpShared &s = *reinterpret_cast<UpShared *>(
+        rings + (BULK ? (uint32_t)kUpWarps * 2 * Ring<2>::kStage : 0u));
     uint8_t *xs = reinterpret_cast<uint8_t *>(&s) + (sizeof(s) + 127) / 128 * 128;
-    // the second launch reads the choices before its own wait, so it may come only once
-    // what was before this one is done
+    const uint32_t warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        s.failed = 0;
+        for (int w = 0; w < kUpWarps; ++w)
+            for (int i = 0; i < 2; ++i)
+                mbar_init((uint32_t)__cvta_generic_to_shared(&s.bars[w][i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // the second launch reads the choices and weights before its own wait, so it may come
+    // only once what was before this one is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     choose(a, s.c);
@@ -512,264 +656,394 @@ k_moe_up(const __grid_constant__ MoeArgs a) {
     const uint64_t units = (uint64_t)s.c.count * tiles;
     uint64_t unit = units * blockIdx.x / gridDim.x;
     const uint64_t end = units * (blockIdx.x + 1) / gridDim.x;
-    const int most = STAGED ? (int)a.columns : kColumns;
+    UpWarp me;
+    me.map = &map;
+    me.tiles = tiles;
+    me.ring.begin(rings + warp * 2 * Ring<2>::kStage, s.bars[warp], &s.failed);
+    me.cursor.begin(a, tiles, unit, end);
+    if (BULK) {
+        me.fetch(a, s.c);
+        me.fetch(a, s.c);
+    }
     while (unit < end) {
         const uint32_t i = (uint32_t)(unit / tiles), tile = (uint32_t)(unit - (uint64_t)i * tiles);
         const uint32_t last = end - unit < tiles - tile ? tile + (uint32_t)(end - unit) : tiles;
-        const int e = s.c.active[i];
-        for (int skip = 0;; skip += most) {
-            int16_t *list = s.list[threadIdx.x >> 5];
-            const int all = list_pairs(a, s.c, e, skip, most, list);
-            const int n = all - skip < most ? all - skip : most;
-            if (STAGED) {
-                stage_columns<DT, WARPS>(a, list, n, xs);
+        const int e = s.c.active[i], all = s.c.pairs[i];
+        for (int skip = 0; skip < all; skip += kColumns) {
+            int16_t *list = s.list[warp];
+            list_pairs(a, s.c, e, skip, kColumns, list);
+            const int n = all - skip < kColumns ? all - skip : kColumns;
+            const bool staged = n <= (int)a.columns;
+            if (staged) {
+                stage_columns<DT>(a, list, n, xs);
                 __syncthreads();
             }
             for (uint32_t t = tile; t < last; ++t) {
-                if (n <= 8)
-                    up_unit<DT, WARPS, STAGED, 1>(a, s, xs, e, t * kUpRows, n);
+                if (staged && n <= 8)
+                    up_unit<DT, BULK, true, 1>(a, s, me, xs, e, t * kUpRows, n);
+                else if (staged)
+                    up_unit<DT, BULK, true, 2>(a, s, me, xs, e, t * kUpRows, n);
+                else if (n <= 8)
+                    up_unit<DT, BULK, false, 1>(a, s, me, xs, e, t * kUpRows, n);
                 else
-                    up_unit<DT, WARPS, STAGED, 2>(a, s, xs, e, t * kUpRows, n);
+                    up_unit<DT, BULK, false, 2>(a, s, me, xs, e, t * kUpRows, n);
             }
-            if (all - skip <= most)
-                break;
         }
         unit += last - tile;
     }
+    __syncthreads();
+    if (BULK && s.failed)
+        me.ring.drain();
+    if (threadIdx.x == 0)
+        a.failed[blockIdx.x] = s.failed != 0;
 }
 
 // ---- second launch --------------------------------------------------------------
 
 constexpr int kDownWarps = 8, kDownThreads = 32 * kDownWarps;
-constexpr int kDownTiles = 1, kDownRows = 16 * kDownTiles;
+constexpr int kDownRows = 16;
 
 struct DownShared {
     Chosen c;
     int16_t list[kDownWarps][kColumns];
+    uint64_t bars[kDownWarps][2];
+    int failed;
+    alignas(16) float sums[1];        // [warp][token][row]
 };
-static size_t down_smem(uint32_t T) {
-    return sizeof(DownShared) + sizeof(float) * kDownWarps * kDownRows * T;
+static size_t down_smem(uint32_t T, bool bulk) {
+    return (bulk ? 1024 + kDownWarps * 2 * Ring<1>::kStage : 0) + sizeof(DownShared) +
+           sizeof(float) * kDownWarps * kDownRows * T;
 }
 
-// The lane's elements of h, block kb of a row, all at one scale; returns its inverse.
-template <int DT, bool LO>
-__device__ __forceinline__ float load_hidden(const MoeArgs &a, const uint8_t *row, uint32_t kb,
-                                             bool on, uint4 *hi, uint4 *lo) {
-    const uint32_t lane = threadIdx.x & 31, k = kb * 128 + lane % 4 * 32;
-    if (!HiddenRow<DT>::kHalf) {
-        float v[32];
+// The steps of a warp of the second launch: its blocks of (expert, k), a run of them, and
+// for each expert's share of it the passes over the expert's pairs.
+struct DownCursor {
+    uint32_t i, kb0, kb1, kb, pass, left;     // left: blocks past this expert's
+    bool done;
+
+    __device__ __forceinline__ void begin(const MoeArgs &a, uint32_t at, uint32_t end) {
+        i = at / a.fb;
+        kb = kb0 = at - i * a.fb;
+        kb1 = end - at < a.fb - kb0 ? kb0 + (end - at) : a.fb;
+        left = end - at - (kb1 - kb0);
+        pass = 0;
+        done = at >= end;
+    }
+    // true if the expert or the pass changes
+    __device__ __forceinline__ bool next(const MoeArgs &a, const Chosen &c) {
+        if (++kb < kb1)
+            return false;
+        kb = kb0;
+        if (++pass * kColumns < (uint32_t)c.pairs[i])
+            return true;
+        pass = 0;
+        ++i;
+        kb = kb0 = 0;
+        kb1 = left < a.fb ? left : a.fb;
+        left -= kb1;
+        done = kb1 == 0;
+        return true;
+    }
+};
+
+struct DownWarp {
+    Ring<1> ring;
+    DownCursor cursor;
+    const CUtensorMap *map;
+    uint32_t r0;
+
+    __device__ __forceinline__ void fetch(const MoeArgs &a, const Chosen &c) {
+        if (cursor.done)
+            return;
+        if ((threadIdx.x & 31) == 0 && !*ring.failed)
+            ring.issue(map, cursor.kb * 128, &r0, c.active[cursor.i]);
+        ++ring.issued;
+        cursor.next(a, c);
+    }
+};
+
+// The lane's elements of a row of h, block kb: as they lie in memory.
+template <int DT> struct Hidden;
+template <> struct Hidden<AR_FP32> {
+    float v[32];
+    __device__ __forceinline__ void load(const MoeArgs &a, const uint8_t *row, uint32_t kb,
+                                         bool on) {
+        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 32;
         load_column<AR_FP32>(row, k, a.F, true, on, v);
         load_column<AR_FP32>(row, k + 16, a.F, true, on, v + 16);
-        return convert_column<LO>(v, hi, lo);
     }
-    uint2 exponents = make_uint2(~0u, ~0u);
-    const uint8_t *at = row + kb * 256 + lane % 4 * 16;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        hi[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (on && k + 16 * (j / 2) < a.F)
-            hi[j] = ld_v4_l1(at + j * 64);
+    // in two parts; returns the inverse of their scale
+    __device__ __forceinline__ float convert(uint4 *hi, uint4 *lo) const {
+        return convert_column<true>(v, hi, lo);
     }
-    if (on)
-        exponents = *reinterpret_cast<const uint2 *>(row + a.fb * 256ull + kb * 8);
-    // the largest magnitude has the least exponent of scale; the others come down to it
-    uint32_t least = __vminu4(exponents.x, exponents.y);
-    least = __vminu4(least, least >> 16);
-    least = min(least & 255u, least >> 8 & 255u);
+};
+template <int DT> struct Hidden {
+    uint4 v[4];
+    uint2 exponents;
+    __device__ __forceinline__ void load(const MoeArgs &a, const uint8_t *row, uint32_t kb,
+                                         bool on) {
+        const uint32_t c = threadIdx.x & 3, k = kb * 128 + c * 32;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        // tiles 2 c and 2 c + 1
-        const uint32_t mine = (lane & 2 ? exponents.y : exponents.x) >>
-                                  (16 * (lane & 1) + 8 * half) & 255u;
-        const uint32_t down = mine - least;                  // at most 241
-        const float f = __uint_as_float(down < 126u ? (127u - down) << 23 : 0u);
-        const __half2 by = __float2half2_rn(f);
+        for (int j = 0; j < 4; ++j) {
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && k + 16 * (j / 2) < a.F)
+                v[j] = ld_v4_l1(row + kb * 256 + j * 64 + c * 16);
+        }
+        exponents = make_uint2(~0u, ~0u);
+        if (on)
+            exponents = *reinterpret_cast<const uint2 *>(row + a.fb * 256ull + kb * 8);
+    }
+    // The largest magnitude has the least exponent of scale; the others come down to it.
+    __device__ __forceinline__ float convert(uint4 *hi, uint4 *) const {
+        const uint32_t lane = threadIdx.x & 31;
+        uint32_t least = __vminu4(exponents.x, exponents.y);
+        least = __vminu4(least, least >> 16);
+        least = min(least & 255u, least >> 8 & 255u);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t *w = &hi[2 * half + j].x;
+        for (int half = 0; half < 2; ++half) {
+            // tiles 2 c and 2 c + 1
+            const uint32_t mine = (lane & 2 ? exponents.y : exponents.x) >>
+                                      (16 * (lane & 1) + 8 * half) & 255u;
+            const uint32_t down = mine - least;              // at most 241
+            const float f = __uint_as_float(down < 126u ? (127u - down) << 23 : 0u);
+            const __half2 by = __float2half2_rn(f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(w + i), by);
-                w[i] = *reinterpret_cast<const uint32_t *>(&x);
+            for (int j = 0; j < 2; ++j) {
+                const uint4 &x = v[2 * half + j];
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(w + i), by);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&y);
+                }
+                hi[2 * half + j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
+        return least >= 254u ? 0x1p-127f : __uint_as_float((254u - least) << 23);
     }
-    return least >= 254u ? 0x1p-127f : __uint_as_float((254u - least) << 23);
-}
+};
 
 // Blocks [kb0, kb1) along k of expert e times the listed pairs, added to this warp's
 // sums of their tokens.
-template <int DT, int NT>
-__device__ __forceinline__ void down_part(const MoeArgs &a, const int16_t *list, float *sums, int e,
-                                          uint32_t r0, uint32_t kb0, uint32_t kb1, int n) {
+template <int DT, bool BULK, int NT>
+__device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, DownWarp &me,
+                                          const int16_t *list, float *sums, int e, uint32_t kb0,
+                                          uint32_t kb1, int n) {
     constexpr bool kLo = !HiddenRow<DT>::kHalf;
     const int lane = threadIdx.x & 31;
     const uint8_t *w = a.down + (uint64_t)e * a.H * a.lddown;
     const float *ws = a.down_scale + (uint64_t)e * a.hb * a.fb;
-    const uint8_t *rows[kDownTiles][2];
-    const float *scales[kDownTiles][2];
+    const uint8_t *rows[2];
+    const float *scales[2];
 #pragma unroll
-    for (int m = 0; m < kDownTiles; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t r = r0 + m * 16 + i * 8 + lane / 4;
-            r = r < a.H ? r : a.H - 1;    // past the last: their sums go nowhere
-            rows[m][i] = w + (uint64_t)r * a.lddown;
-            scales[m][i] = ws + (uint64_t)(r / 128) * a.fb;
-        }
+    for (int i = 0; i < 2; ++i) {
+        uint32_t r = me.r0 + i * 8 + lane / 4;
+        r = r < a.H ? r : a.H - 1;        // past the last: their sums go nowhere
+        rows[i] = w + (uint64_t)r * a.lddown;
+        scales[i] = ws + (uint64_t)(r / 128) * a.fb;
+    }
     const uint8_t *columns[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int c = nt * 8 + lane / 4;
-        columns[nt] = a.h + (uint64_t)(c < n ? list[c] : 0) * a.sh;
+        const int x = nt * 8 + lane / 4;
+        columns[nt] = a.h + (uint64_t)(x < n ? list[x] : 0) * a.sh;
     }
-    float sum[kDownTiles][NT][4] = {};
-    Codes<kDownTiles> next;
-    next.load(rows, kb0, a.F, a.wide_down);
-    for (uint32_t kb = kb0; kb < kb1; ++kb) {
-        const Codes<kDownTiles> now = next;
-        if (kb + 1 < kb1)
-            next.load(rows, kb + 1, a.F, a.wide_down);
-        float sc[kDownTiles][2];
+    float sum[1][NT][4] = {};
+    // what the next block needs besides its weights is loaded a block ahead, while
+    // registers hold it
+    constexpr bool kAhead = NT == 1 && !kLo;
+    Hidden<DT> next_h[NT];
+    float next_scale[2];
+    auto load = [&](uint32_t kb) {
 #pragma unroll
-        for (int m = 0; m < kDownTiles; ++m)
+        for (int nt = 0; nt < NT; ++nt)
+            next_h[nt].load(a, columns[nt], kb, nt * 8 + lane / 4 < n);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            next_scale[i] = scales[i][kb];
+    };
+    if (kAhead)
+        load(kb0);
+    for (uint32_t kb = kb0; kb < kb1; ++kb) {
+        if (!kAhead)
+            load(kb);
+        Hidden<DT> now_h[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            now_h[nt] = next_h[nt];
+        const float sc[2] = {next_scale[0], next_scale[1]};
+        if (kAhead && kb + 1 < kb1)
+            load(kb + 1);
+        Codes<1> now;
+        if (BULK) {
+            me.ring.wait();
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                sc[m][i] = scales[m][i][kb];
-        float part[kDownTiles][NT][4] = {}, inverse[NT][2];
+                now.q[0][i] = me.ring.codes(0, i * 8 + lane / 4);
+            __syncwarp();
+            ++me.ring.used;
+            me.fetch(a, c);
+        } else {
+            const uint32_t k = kb * 128 + lane % 4 * 32;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                now.q[0][i].lo = load_codes(rows[i], k, a.F);
+                now.q[0][i].hi = load_codes(rows[i], k + 16, a.F);
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             uint4 hi[4], lo[4];
-            const float inv = load_hidden<DT, kLo>(a, columns[nt], kb, nt * 8 + lane / 4 < n, hi,
-                                                   lo);
-            inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
-            inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
-            float one[kDownTiles][1][4] = {};
-            block_product<kDownTiles, 1>(
-                one, now, [&](int, int piece) { return hi[piece]; });
+            const float inv = now_h[nt].convert(hi, lo);
+            const float inverse[2] = {__shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8),
+                                      __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4)};
+            float part[1][1][4] = {};
+            block_product<1, 1>(part, now, [&](int, int piece) { return hi[piece]; });
             if (kLo)
-                block_product<kDownTiles, 1>(
-                    one, now, [&](int, int piece) { return lo[piece]; });
+                block_product<1, 1>(part, now, [&](int, int piece) { return lo[piece]; });
 #pragma unroll
-            for (int m = 0; m < kDownTiles; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    part[m][nt][i] = one[m][0][i];
+            for (int i = 0; i < 4; ++i)
+                sum[0][nt][i] += part[0][0][i] * (inverse[i & 1] * sc[i / 2]);
         }
-#pragma unroll
-        for (int m = 0; m < kDownTiles; ++m)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sum[m][nt][i] += part[m][nt][i] * (inverse[nt][i & 1] * sc[m][i / 2]);
     }
     // columns of different pairs may be one token's (its choices of one expert): one
     // column at a time
-    for (int c = 0; c < n; ++c) {
-        const int p = list[c];
+    for (int x = 0; x < n; ++x) {
+        const int p = list[x];
         const float g = a.w ? a.w[p] : 1.0f;
-        if (lane % 4 == c % 8 / 2) {
+        if (lane % 4 == x % 8 / 2) {
             float *token = sums + (uint32_t)p / a.K * kDownRows;
 #pragma unroll
-            for (int m = 0; m < kDownTiles; ++m)
+            for (int nt = 0; nt < NT; ++nt)
+                if (nt == x / 8)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    if (nt == c / 8)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            token[m * 16 + i * 8 + lane / 4] +=
-                                g * (c & 1 ? sum[m][nt][2 * i + 1] : sum[m][nt][2 * i]);
+                    for (int i = 0; i < 2; ++i)
+                        token[i * 8 + lane / 4] +=
+                            g * (x & 1 ? sum[0][nt][2 * i + 1] : sum[0][nt][2 * i]);
         }
         __syncwarp();
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(const __grid_constant__ MoeArgs a) {
-    extern __shared__ uint4 smem[];
-    DownShared &s = *reinterpret_cast<DownShared *>(smem);
-    float *sums = reinterpret_cast<float *>(&s + 1);      // [warp][token][row]
-    // before the wait: the choices, which were there before the first launch
-    choose(a, s.c);
+template <int DT, bool BULK>
+__global__ void __launch_bounds__(kDownThreads, 2)
+k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap map) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *rings = raw + (BULK ? (1024u - (smem_at(raw) & 1023u)) & 1023u : 0u);
+    DownShared &s = *reinterpret_cast<DownShared *>(
+        rings + (BULK ? (uint32_t)kDownWarps * 2 * Ring<1>::kStage : 0u));
     const int warp = threadIdx.x >> 5;
-    const uint32_t r0 = blockIdx.x * kDownRows, each = a.T * kDownRows;
-    float *mine = sums + (uint32_t)warp * each;
+    if (threadIdx.x == 0) {
+        s.failed = 0;
+        for (int w = 0; w < kDownWarps; ++w)
+            for (int i = 0; i < 2; ++i)
+                mbar_init((uint32_t)__cvta_generic_to_shared(&s.bars[w][i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // before the wait: the choices and the first weights, which were there before the first
+    // launch
+    choose(a, s.c);
+    const uint32_t each = a.T * kDownRows;
+    float *mine = s.sums + (uint32_t)warp * each;
     for (uint32_t i = threadIdx.x; i < each * kDownWarps; i += kDownThreads)
-        sums[i] = 0.0f;
+        s.sums[i] = 0.0f;
     __syncthreads();
-    kernel_prologue();
+    DownWarp me;
+    me.map = &map;
+    me.r0 = blockIdx.x * kDownRows;
+    me.ring.begin(rings + warp * 2 * Ring<1>::kStage, s.bars[warp], &s.failed);
     // this warp's run of (expert, block)
     const uint32_t steps = (uint32_t)s.c.count * a.fb;
-    uint32_t at = (uint32_t)((uint64_t)steps * warp / kDownWarps);
+    const uint32_t from = (uint32_t)((uint64_t)steps * warp / kDownWarps);
     const uint32_t end = (uint32_t)((uint64_t)steps * (warp + 1) / kDownWarps);
-    while (at < end) {
+    me.cursor.begin(a, from, end);
+    if (BULK) {
+        me.fetch(a, s.c);
+        me.fetch(a, s.c);
+    }
+    kernel_prologue();
+    int failed = 0;
+    for (uint32_t i = threadIdx.x; i < a.ups; i += kDownThreads)
+        failed |= a.failed[i];
+    for (uint32_t at = from; at < end;) {
         const uint32_t i = at / a.fb, kb0 = at - i * a.fb;
         const uint32_t kb1 = end - at < a.fb - kb0 ? kb0 + (end - at) : a.fb;
-        const int e = s.c.active[i];
-        for (int skip = 0;; skip += kColumns) {
-            const int all = list_pairs(a, s.c, e, skip, kColumns, s.list[warp]);
+        const int e = s.c.active[i], all = s.c.pairs[i];
+        for (int skip = 0; skip < all; skip += kColumns) {
+            list_pairs(a, s.c, e, skip, kColumns, s.list[warp]);
             const int n = all - skip < kColumns ? all - skip : kColumns;
             if (n <= 8)
-                down_part<DT, 1>(a, s.list[warp], mine, e, r0, kb0, kb1, n);
+                down_part<DT, BULK, 1>(a, s.c, me, s.list[warp], mine, e, kb0, kb1, n);
             else
-                down_part<DT, 2>(a, s.list[warp], mine, e, r0, kb0, kb1, n);
-            if (all - skip <= kColumns)
-                break;
+                down_part<DT, BULK, 2>(a, s.c, me, s.list[warp], mine, e, kb0, kb1, n);
         }
         at += kb1 - kb0;
     }
-    __syncthreads();
+    if (BULK && *me.ring.failed)
+        me.ring.drain();
+    failed = __syncthreads_or(failed | s.failed);
     for (uint32_t i = threadIdx.x; i < each; i += kDownThreads) {
         const uint32_t t = i / kDownRows, r = i % kDownRows;
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < kDownWarps; ++k)
-            v += sums[k * each + i];
-        if (r0 + r < a.H)
-            st_elem<DT>(a.out + t * a.sout, r0 + r, narrow1<DT>(v));
+            v += s.sums[k * each + i];
+        if (failed)
+            v = NAN;
+        if (me.r0 + r < a.H)
+            st_elem<DT>(a.out + t * a.sout, me.r0 + r, narrow1<DT>(v));
     }
 }
 
-template <int DT, int WARPS, bool STAGED>
-static cudaError_t launch_up(MoeArgs a, size_t room, int sms, cudaStream_t s) {
-    constexpr size_t base = (sizeof(UpShared<WARPS>) + 127) / 128 * 128;
-    constexpr auto kernel = k_moe_up<DT, WARPS, STAGED>;
-    const cudaError_t e = opt_in_smem<kernel>(kMoeSmem / (16 / WARPS));
+// The first launch; sets what the second needs to know of it.
+template <int DT, bool BULK>
+static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaStream_t s) {
+    constexpr size_t base = 1024 + (BULK ? kUpWarps * 2 * Ring<2>::kStage : 0) +
+                            (sizeof(UpShared) + 127) / 128 * 128;
+    const cudaError_t e = opt_in_smem<k_moe_up<DT, BULK>>(kMoeSmem);
     if (e != cudaSuccess)
         return e;
-    const size_t column = UpColumn<DT>::bytes(a.hb);
-    if (STAGED) {
-        const size_t held = room / column, pairs = (size_t)a.T * a.K;
-        a.columns = (uint32_t)(held < kColumns ? held : kColumns);
-        a.columns = a.columns < pairs ? a.columns : (uint32_t)pairs;
-    }
-    const uint64_t units = (uint64_t)((a.F + kUpRows - 1) / kUpRows) * a.T * a.K;
-    const uint64_t most = (uint64_t)(16 / WARPS) * sms;
-    return launch_kernel(kernel, (unsigned)(units < most ? units : most), 32 * WARPS,
-                         base + a.columns * column, s, true, a);
+    // columns that fit beside the rings, no more than there can be
+    const size_t column = UpColumn<DT>::bytes(a.hb), held = (kMoeSmem - base) / column;
+    const size_t pairs = (size_t)a.T * a.K, most = pairs < kColumns ? pairs : kColumns;
+    a.columns = (uint32_t)(held < most ? held : most);
+    const uint64_t units = (uint64_t)((a.F + kUpRows - 1) / kUpRows) * pairs;
+    a.ups = (uint32_t)(units < (uint64_t)sms ? units : (uint64_t)sms);
+    // The flags lie at the workspace's end, past the rows of h.  A pair has 4 F + 512 bytes
+    // there; rows of binary32 leave 500 of them.  Rows of binary16 leave 244 at least, and
+    // 480 from F = 60 on; below that a pair makes four CTAs at most.
+    if (a.ups > 480)
+        a.ups = 480;
+    a.failed -= a.ups;
+    return launch_kernel(k_moe_up<DT, BULK>, a.ups, kUpThreads, base + a.columns * column, s, true,
+                         a, map);
+}
+template <int DT, bool BULK>
+static cudaError_t launch_down(const MoeArgs &a, const CUtensorMap &map, cudaStream_t s) {
+    const cudaError_t e = opt_in_smem<k_moe_down<DT, BULK>>(down_smem(AR_MOE_LAYER_TOKENS, BULK));
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(k_moe_down<DT, BULK>, (a.H + kDownRows - 1) / kDownRows, kDownThreads,
+                         down_smem(a.T, BULK), s, true, a, map);
 }
 
-template <int DT> static cudaError_t moe_dt(MoeArgs a, cudaStream_t s) {
+template <int DT>
+static cudaError_t moe_dt(MoeArgs a, bool bulk_up, bool bulk_down, cudaStream_t s) {
     const int sms = sm_count();
     if (sms < 1)
         return cudaErrorUnknown;
-    cudaError_t e = opt_in_smem<k_moe_down<DT>>(down_smem(AR_MOE_LAYER_TOKENS));
-    if (e != cudaSuccess)
-        return e;
     a.sh = HiddenRow<DT>::bytes(a.F, a.fb);
-    // Two CTAs an SM of eight warps while each holds the columns of every token, so that one
-    // has its weights in flight while the other sums up; else one of sixteen.
-    constexpr size_t kTwo = kMoeSmem / 2 - (sizeof(UpShared<8>) + 127) / 128 * 128;
-    constexpr size_t kOne = kMoeSmem - (sizeof(UpShared<16>) + 127) / 128 * 128;
-    const size_t tokens = a.T < kColumns ? a.T : kColumns, column = UpColumn<DT>::bytes(a.hb);
-    e = tokens * column <= kTwo ? launch_up<DT, 8, true>(a, kTwo, sms, s)
-        : column <= kOne        ? launch_up<DT, 16, true>(a, kOne, sms, s)
-                                : launch_up<DT, 8, false>(a, 0, sms, s);
+    CUtensorMap up = {}, down = {};
+    if ((bulk_up || bulk_down) && !encoder())
+        return cudaErrorNotSupported;
+    if ((bulk_up && !encode(&up, a.up, a.H, 2 * (uint64_t)a.F, a.ldup, a.E, 16)) ||
+        (bulk_down && !encode(&down, a.down, a.F, a.H, a.lddown, a.E, 16)))
+        return cudaErrorInvalidValue;
+    const cudaError_t e =
+        bulk_up ? launch_up<DT, true>(a, up, sms, s) : launch_up<DT, false>(a, up, sms, s);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(k_moe_down<DT>, (a.H + kDownRows - 1) / kDownRows, kDownThreads,
-                         down_smem(a.T), s, true, a);
+    return bulk_down ? launch_down<DT, true>(a, down, s) : launch_down<DT, false>(a, down, s);
 }
 
 }  // namespace ar
@@ -834,15 +1108,15 @@ int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, cons
     a.hb = (uint32_t)hb;
     a.fb = (uint32_t)fb;
     a.ub = (uint32_t)ub;
-    a.columns = 0;
-    a.wide_up = wide(mu) + wide(mu, 32);
-    a.wide_down = wide(md) + wide(md, 32);
+    a.columns = a.ups = 0;
+    a.failed = reinterpret_cast<uint8_t *>(work) + mw.bytes;      // less a byte per CTA
     a.wide_x = wide(mx);
     a.ids8 = ids_bytes == 8;
+    const bool bu = wide(mu), bd = wide(md);
     switch (dtype) {
-    case AR_BF16: return launched(moe_dt<AR_BF16>(a, stream));
-    case AR_FP16: return launched(moe_dt<AR_FP16>(a, stream));
-    default: return launched(moe_dt<AR_FP32>(a, stream));
+    case AR_BF16: return launched(moe_dt<AR_BF16>(a, bu, bd, stream));
+    case AR_FP16: return launched(moe_dt<AR_FP16>(a, bu, bd, stream));
+    default: return launched(moe_dt<AR_FP32>(a, bu, bd, stream));
     }
 }
 
