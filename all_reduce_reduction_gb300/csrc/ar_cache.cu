@@ -21,6 +21,7 @@ struct MoveArgs {
     uint32_t slots;               // lanes of a row: 2 * heads << lane_bits
     uint32_t jobs_per_row;        // jobs that share one row (rows = 1 then)
     uint32_t lane_bits;
+    Divide by_lines;              // the lines of a row
 };
 
 constexpr int kMoveThreads = 256;
@@ -106,7 +107,7 @@ __device__ __forceinline__ SlotOf slot_of(const MoveArgs &a, uint32_t slot, uint
     SlotOf s;
     const uint32_t line = slot >> a.lane_bits;
     s.lane = slot & ((1u << a.lane_bits) - 1u);
-    s.row = line / (2u * a.g.heads);
+    s.row = a.by_lines(line);
     const uint32_t kv = line - s.row * 2u * a.g.heads;
     s.value = kv >= a.g.heads;
     s.head = s.value ? kv - a.g.heads : kv;
@@ -139,8 +140,11 @@ k_cache_move(const __grid_constant__ MoveArgs a) {
         if (!READ && at[i].on)
             line[i].load(row_line(at[i]), at[i].lane, a.lane_bits, D);
     }
-    if (threadIdx.x < rows)
-        places[threadIdx.x] = a.g.place(a.offsets, a.B, row0 + threadIdx.x);
+    for (uint32_t r = threadIdx.x / 32; r < rows; r += kMoveThreads / 32) {
+        const int2 at = a.g.place(a.offsets, a.B, row0 + r);
+        if (threadIdx.x % 32 == 0)
+            places[r] = at;
+    }
     __syncthreads();
     constexpr int kCell = CACHE8 ? 1 : L::kSize;          // bytes of a cached element
     if constexpr (READ) {
@@ -270,6 +274,7 @@ static cudaError_t move_form(MoveArgs a, cudaStream_t s) {
     while ((1u << a.lane_bits) < lanes)
         ++a.lane_bits;
     a.slots = 2u * a.g.heads << a.lane_bits;
+    a.by_lines = divide_by(2u * a.g.heads);
     a.jobs_per_row = (a.slots + kJob - 1) / kJob;
     a.rows = 1;
     if (a.jobs_per_row == 1) {

@@ -61,7 +61,8 @@ struct Pages {
     __host__ __device__ __forceinline__ uint64_t scale_at(int32_t p, uint32_t h, uint32_t s) const {
         return ((uint64_t)p * heads + h) * page + s;
     }
-    // The place of row t of a call's rows: its page (-1: none) and slot.
+    // The place of row t of a call's rows: its page (-1: none) and slot.  On the device by
+    // a whole warp, all lanes with one answer.
     __host__ __device__ __forceinline__ int2 place(const int32_t *offsets, uint32_t B,
                                                    uint32_t t) const {
         int2 none;
@@ -70,14 +71,14 @@ struct Pages {
         uint32_t b = t;
         int64_t back = 1;                     // tokens from the row to the sequence's end
         if (offsets) {
-            // the last b with offsets[b] <= t
+            // the last b with offsets[b] <= t, 32 words at a time: one wait for memory up to
+            // 32 sequences, two up to 1024
             uint32_t lo = 0, hi = B;
             while (hi - lo > 1) {
-                const uint32_t mid = lo + (hi - lo) / 2;
-                if ((int64_t)offsets[mid] <= (int64_t)t)
-                    lo = mid;
-                else
-                    hi = mid;
+                const uint32_t step = (hi - lo + 31) / 32;
+                const uint32_t n = count_up_to(offsets, lo, hi, step, t);
+                lo += (n > 0 ? n - 1 : 0) * step;
+                hi = hi - lo < step ? hi : lo + step;
             }
             b = lo;
             const int64_t end = offsets[b + 1];
@@ -93,6 +94,21 @@ struct Pages {
         at.x = page_of(b, (uint32_t)j);
         at.y = (int)slot_of((uint32_t)j);
         return at;
+    }
+    // How many of the words offsets[lo + i * step] below hi, i < 32, are at most t.
+    static __host__ __device__ __forceinline__ uint32_t count_up_to(const int32_t *offsets,
+                                                                    uint32_t lo, uint32_t hi,
+                                                                    uint32_t step, uint32_t t) {
+#ifdef __CUDA_ARCH__
+        const uint32_t at = (threadIdx.x & 31) * step;
+        const bool in = at < hi - lo && (int64_t)offsets[lo + at] <= (int64_t)t;
+        return __popc(__ballot_sync(0xFFFFFFFFu, in));
+#else
+        uint32_t n = 0;
+        for (uint32_t i = 0; i < 32 && i * step < hi - lo; ++i)
+            n += (int64_t)offsets[lo + i * step] <= (int64_t)t;
+        return n;
+#endif
     }
 };
 

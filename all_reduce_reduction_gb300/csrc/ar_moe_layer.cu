@@ -20,7 +20,7 @@
 //
 // First launch (up): a CTA takes 16 rows of both halves of one expert at a time, its
 // warps share the blocks along k.  The columns lie in shared memory, converted when the
-// expert changes, or, where they are too many for it, are converted on the way.  Second
+// expert changes (on the way they cost three times the weights' conversion).  Second
 // launch (down): a CTA takes rows of the output, its warps share the blocks along k of
 // all experts; each keeps its own sums of all tokens, which are added in order.
 //
@@ -53,6 +53,8 @@ struct MoeArgs {
     uint32_t T, K, H, F, E;
     uint32_t hb, fb, ub;              // blocks of 128 along H, F and 2F
     uint32_t columns;                 // pairs that the first launch's shared memory holds
+    uint32_t stages;                  // of its rings
+    uint32_t part_row;                // of its sums: floats between rows
     int wide_x;
     int ids8;
     uint8_t *failed;                  // of each CTA of the first launch: a wait ran out
@@ -184,7 +186,7 @@ template <int MT> struct Codes {
     Words8 q[MT][2];
 };
 
-// A warp's ring of two stages of `BOXES` tiles of 16 rows by 128 bytes, in 1024-byte
+// A warp's ring of 1, 2 or 4 stages of `BOXES` tiles of 16 rows by 128 bytes, in 1024-byte
 // units whose 16-byte pieces are exchanged by row (the map's 128-byte swizzle).
 constexpr uint64_t kMoeWaitNs = 2000000000ull;
 constexpr uint32_t kBox = 16 * 128;
@@ -193,9 +195,15 @@ template <int BOXES> struct Ring {
     uint32_t at, bars;                // this warp's stages and barriers
     const uint8_t *memory;
     volatile int *failed;             // of the CTA
-    uint32_t issued, used;
+    uint32_t issued, used, bits;      // 2^bits stages
 
-    __device__ __forceinline__ void begin(uint8_t *stages, uint64_t *barriers, int *flag) {
+    __device__ __forceinline__ uint32_t stage(uint32_t step) const {
+        return step & ((1u << bits) - 1u);
+    }
+    __device__ __forceinline__ uint32_t parity(uint32_t step) const { return step >> bits & 1; }
+    __device__ __forceinline__ void begin(uint8_t *stages, uint64_t *barriers, int *flag,
+                                          uint32_t stages_log2) {
+        bits = stages_log2;
         at = (uint32_t)__cvta_generic_to_shared(stages);
         bars = (uint32_t)__cvta_generic_to_shared(barriers);
         memory = stages;
@@ -205,7 +213,7 @@ template <int BOXES> struct Ring {
     // Boxes at (k, rows[b]) of matrix e to the next stage; by one lane.
     __device__ __forceinline__ void issue(const CUtensorMap *map, uint32_t k,
                                           const uint32_t *rows, int e) {
-        const uint32_t s = issued & 1, bar = bars + 8 * s;
+        const uint32_t s = stage(issued), bar = bars + 8 * s;
         mbar_expect(bar, kStage);
 #pragma unroll
         for (int b = 0; b < BOXES; ++b)
@@ -213,20 +221,20 @@ template <int BOXES> struct Ring {
     }
     // Until the oldest stage is there; after a failure at once.
     __device__ __forceinline__ void wait() {
-        const uint32_t bar = bars + 8 * (used & 1), parity = used >> 1 & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))
-            wait_slow(bar, parity);
+        const uint32_t bar = bars + 8 * stage(used), phase = parity(used);
+        if (!__all_sync(0xFFFFFFFFu, mbar_test(bar, phase)))
+            wait_slow(bar, phase);
     }
-    __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t parity) {
+    __device__ __noinline__ void wait_slow(uint32_t bar, uint32_t phase) {
         const uint64_t deadline = globaltimer_ns() + kMoeWaitNs;
-        while (!*failed && !mbar_test(bar, parity))
+        while (!*failed && !mbar_test(bar, phase))
             if (globaltimer_ns() > deadline)
                 *failed = 1;
         __syncwarp();
     }
     // This lane's codes of row r of box b.
     __device__ __forceinline__ Words8 codes(int b, uint32_t r) const {
-        const uint8_t *row = memory + (used & 1) * kStage + b * kBox + r * 128;
+        const uint8_t *row = memory + stage(used) * kStage + b * kBox + r * 128;
         const uint32_t c = (threadIdx.x & 3) * 2;
         Words8 w;
         w.lo = *reinterpret_cast<const uint4 *>(row + ((c ^ (r & 7)) << 4));
@@ -238,7 +246,7 @@ template <int BOXES> struct Ring {
     __device__ __forceinline__ void drain() {
         for (; used < issued; ++used) {
             const uint64_t deadline = globaltimer_ns() + kMoeWaitNs;
-            while (!mbar_test(bars + 8 * (used & 1), used >> 1 & 1) &&
+            while (!mbar_test(bars + 8 * stage(used), parity(used)) &&
                    globaltimer_ns() < deadline) {
             }
         }
@@ -302,21 +310,37 @@ __device__ __forceinline__ float convert_column(const float *v, uint4 *hi, uint4
     return inverse;
 }
 
-// 16 elements of a row of type DT from k on as binary32; zeros past K.
-template <int DT>
-__device__ __forceinline__ void load_column(const uint8_t *row, uint32_t k, uint32_t K, bool wide,
-                                            bool on, float *v) {
-    constexpr int E = 16 / Elem<DT>::kSize;
-    if (on && wide && k + 16 <= K) {
+// The lane's 32 elements of a row of type DT, as they lie in memory; zeros past K.
+template <int DT> struct RawColumn {
+    static constexpr int kSize = Elem<DT>::kSize, E = 16 / kSize;     // elements of a vector
+    uint4 v[2 * kSize];
+    __device__ __forceinline__ void load(const uint8_t *row, uint32_t kb, uint32_t K, bool wide,
+                                         bool on) {
+        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 32;
 #pragma unroll
-        for (int i = 0; i < 16; i += E)
-            Rows<DT, true>::widen(ld_v4_l1(row + (uint64_t)(k + i) * Elem<DT>::kSize), v + i);
-        return;
+        for (int i = 0; i < 2 * kSize; ++i) {
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && wide && k + i * E + E <= K) {
+                v[i] = ld_v4_l1(row + (uint64_t)(k + i * E) * kSize);
+            } else if (on) {
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (k + i * E + e < K)
+                        w[e * kSize / 4] |= ld_elem<DT>(row, k + i * E + e) << (8 * (e * kSize % 4));
+                v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
     }
+    // to binary16 in one part or two; returns the inverse of their scale
+    template <bool LO> __device__ __forceinline__ float convert(uint4 *hi, uint4 *lo) const {
+        float f[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] = on && k + i < K ? widen1<DT>(ld_elem<DT>(row, k + i)) : 0.0f;
-}
+        for (int i = 0; i < 2 * kSize; ++i)
+            Rows<DT, true>::widen(v[i], f + i * E);
+        return convert_column<LO>(f, hi, lo);
+    }
+};
 
 // ---- h between the launches ----------------------------------------------------------
 
@@ -340,10 +364,14 @@ static_assert(kUpRows == 16, "a box of each half; and what shares an exponent of
 struct UpShared {
     Chosen c;
     int16_t list[kUpWarps][kColumns];
-    float part[kUpWarps][2][kUpRows][kColumns + 1];
     uint64_t bars[kUpWarps][2];
     int failed;
 };
+// Bytes of it with the sums of half of the warps.
+static __host__ __device__ __forceinline__ uint32_t up_fixed(uint32_t part_row) {
+    return (uint32_t)(sizeof(UpShared) + kUpWarps / 2 * 2 * kUpRows * part_row * 4 + 127) / 128 *
+           128;
+}
 // A column in shared memory: blocks of 256 bytes, in one part or two, and an inverse
 // scale each.  Columns start 64 bytes apart in the banks.
 template <int DT> struct UpColumn {
@@ -431,7 +459,7 @@ struct UpCursor {
         if (++tile < last)
             return;
         tile = first;
-        if (++pass * kColumns < (uint32_t)c.pairs[i])
+        if (++pass * a.columns < (uint32_t)c.pairs[i])
             return;
         pass = 0;
         ++i;
@@ -463,10 +491,10 @@ struct UpWarp {
 };
 
 // Rows f0.. of both halves of expert e times n listed pairs.  BULK: the weights come
-// through the ring.  STAGED: the columns lie in shared memory at xs; otherwise they are
-// read and converted on the way.
-template <int DT, bool BULK, bool STAGED, int NT>
-__device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &me,
+// through the ring and the columns lie in shared memory at xs; otherwise both are read
+// on the way.  parts: where half of the warps leave their sums.
+template <int DT, bool BULK, int NT>
+__device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &me, float *parts,
                                         const uint8_t *xs, int e, uint32_t f0, int n) {
     using C = UpColumn<DT>;
     constexpr bool kLo = C::kParts == 2;
@@ -531,7 +559,7 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
                 }
         }
         float part[kUpTiles][NT][4] = {}, inverse[NT][2];   // of this lane's columns
-        if constexpr (STAGED) {
+        if constexpr (BULK) {
 #pragma unroll
             for (int lo = 0; lo < C::kParts; ++lo)
                 block_product<kUpTiles, NT>(part, now, [&](int nt, int piece) {
@@ -551,13 +579,11 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int c = nt * 8 + (int)lane / 4;
-                const uint8_t *row = a.x + (uint64_t)(c < n ? list[c] / a.K : 0u) * a.sx;
-                const uint32_t k = kb * 128 + lane % 4 * 32;
-                float v[32];
-                load_column<DT>(row, k, a.H, a.wide_x, c < n, v);
-                load_column<DT>(row, k + 16, a.H, a.wide_x, c < n, v + 16);
+                RawColumn<DT> raw;
+                raw.load(a.x + (uint64_t)(c < n ? list[c] / a.K : 0u) * a.sx, kb, a.H, a.wide_x,
+                         c < n);
                 uint4 hi[4], lo[4];
-                const float inv = convert_column<kLo>(v, hi, lo);
+                const float inv = raw.template convert<kLo>(hi, lo);
                 inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
                 inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
                 float one[kUpTiles][1][4] = {};
@@ -580,14 +606,26 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
                 for (int i = 0; i < 4; ++i)
                     sum[m][nt][i] += part[m][nt][i] * (inverse[nt][i & 1] * sc[m][i / 2]);
     }
+    // the upper half of the warps hands its sums to the lower
+    constexpr uint32_t kHalf = kUpWarps / 2;
+    auto slot = [&](uint32_t w, int half, uint32_t r, uint32_t c) -> float & {
+        return parts[((w * 2 + half) * kUpRows + r) * a.part_row + c];
+    };
+    auto each = [&](auto f) {
 #pragma unroll
-    for (int m = 0; m < kUpTiles; ++m)
+        for (int m = 0; m < kUpTiles; ++m)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s.part[warp][i / 2][m * 8 + lane / 4][nt * 8 + lane % 4 * 2 + i % 2] =
-                    sum[m][nt][i];
+                for (int i = 0; i < 4; ++i)
+                    f(slot(warp % kHalf, i / 2, m * 8 + lane / 4, nt * 8 + lane % 4 * 2 + i % 2),
+                      sum[m][nt][i]);
+    };
+    if (warp >= kHalf)
+        each([](float &x, float v) { x = v; });
+    __syncthreads();
+    if (warp < kHalf)
+        each([](float &x, float v) { x += v; });
     __syncthreads();
     // 16 lanes have the rows of one pair
     for (int c0 = (int)warp * 2; c0 < n; c0 += 2 * kUpWarps) {
@@ -596,9 +634,9 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
         if (c < n && f0 + r < a.F) {
             float g = 0.0f, u = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kUpWarps; ++k) {
-                g += s.part[k][0][r][c];
-                u += s.part[k][1][r][c];
+            for (uint32_t k = 0; k < kHalf; ++k) {
+                g += slot(k, 0, r, c);
+                u += slot(k, 1, r, c);
             }
             h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
         }
@@ -636,8 +674,9 @@ k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap 
     // the rings first: their swizzle wants 1024-byte boundaries
     uint8_t *rings = raw + ((1024u - (smem_at(raw) & 1023u)) & 1023u);
     UpShared &s = *reinterpret_cast<UpShared *>(
-        rings + (BULK ? (uint32_t)kUpWarps * 2 * Ring<2>::kStage : 0u));
-    uint8_t *xs = reinterpret_cast<uint8_t *>(&s) + (sizeof(s) + 127) / 128 * 128;
+        rings + (BULK ? (uint32_t)kUpWarps * a.stages * Ring<2>::kStage : 0u));
+    float *parts = reinterpret_cast<float *>(&s + 1);
+    uint8_t *xs = reinterpret_cast<uint8_t *>(&s) + up_fixed(a.part_row);
     const uint32_t warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         s.failed = 0;
@@ -659,34 +698,28 @@ k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap 
     UpWarp me;
     me.map = &map;
     me.tiles = tiles;
-    me.ring.begin(rings + warp * 2 * Ring<2>::kStage, s.bars[warp], &s.failed);
+    me.ring.begin(rings + warp * a.stages * Ring<2>::kStage, s.bars[warp], &s.failed, a.stages - 1);
     me.cursor.begin(a, tiles, unit, end);
-    if (BULK) {
-        me.fetch(a, s.c);
-        me.fetch(a, s.c);
-    }
+    if (BULK)
+        for (uint32_t i = 0; i < a.stages; ++i)
+            me.fetch(a, s.c);
     while (unit < end) {
         const uint32_t i = (uint32_t)(unit / tiles), tile = (uint32_t)(unit - (uint64_t)i * tiles);
         const uint32_t last = end - unit < tiles - tile ? tile + (uint32_t)(end - unit) : tiles;
         const int e = s.c.active[i], all = s.c.pairs[i];
-        for (int skip = 0; skip < all; skip += kColumns) {
+        for (int skip = 0; skip < all; skip += (int)a.columns) {
             int16_t *list = s.list[warp];
-            list_pairs(a, s.c, e, skip, kColumns, list);
-            const int n = all - skip < kColumns ? all - skip : kColumns;
-            const bool staged = n <= (int)a.columns;
-            if (staged) {
+            list_pairs(a, s.c, e, skip, (int)a.columns, list);
+            const int n = all - skip < (int)a.columns ? all - skip : (int)a.columns;
+            if (BULK) {
                 stage_columns<DT>(a, list, n, xs);
                 __syncthreads();
             }
             for (uint32_t t = tile; t < last; ++t) {
-                if (staged && n <= 8)
-                    up_unit<DT, BULK, true, 1>(a, s, me, xs, e, t * kUpRows, n);
-                else if (staged)
-                    up_unit<DT, BULK, true, 2>(a, s, me, xs, e, t * kUpRows, n);
-                else if (n <= 8)
-                    up_unit<DT, BULK, false, 1>(a, s, me, xs, e, t * kUpRows, n);
+                if (n <= 8)
+                    up_unit<DT, BULK, 1>(a, s, me, parts, xs, e, t * kUpRows, n);
                 else
-                    up_unit<DT, BULK, false, 2>(a, s, me, xs, e, t * kUpRows, n);
+                    up_unit<DT, BULK, 2>(a, s, me, parts, xs, e, t * kUpRows, n);
             }
         }
         unit += last - tile;
@@ -702,16 +735,19 @@ k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap 
 
 constexpr int kDownWarps = 8, kDownThreads = 32 * kDownWarps;
 constexpr int kDownRows = 16;
+// (four stages: the same; three CTAs an SM with registers for two: 114 us for one token
+// of 8192 x 2048, not 80)
+constexpr int kDownStagesLog2 = 1, kDownStages = 1 << kDownStagesLog2;
 
 struct DownShared {
     Chosen c;
     int16_t list[kDownWarps][kColumns];
-    uint64_t bars[kDownWarps][2];
+    uint64_t bars[kDownWarps][kDownStages];
     int failed;
     alignas(16) float sums[1];        // [warp][token][row]
 };
 static size_t down_smem(uint32_t T, bool bulk) {
-    return (bulk ? 1024 + kDownWarps * 2 * Ring<1>::kStage : 0) + sizeof(DownShared) +
+    return (bulk ? 1024 + kDownWarps * kDownStages * Ring<1>::kStage : 0) + sizeof(DownShared) +
            sizeof(float) * kDownWarps * kDownRows * T;
 }
 
@@ -765,16 +801,13 @@ struct DownWarp {
 // The lane's elements of a row of h, block kb: as they lie in memory.
 template <int DT> struct Hidden;
 template <> struct Hidden<AR_FP32> {
-    float v[32];
+    RawColumn<AR_FP32> v;
     __device__ __forceinline__ void load(const MoeArgs &a, const uint8_t *row, uint32_t kb,
                                          bool on) {
-        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 32;
-        load_column<AR_FP32>(row, k, a.F, true, on, v);
-        load_column<AR_FP32>(row, k + 16, a.F, true, on, v + 16);
+        v.load(row, kb, a.F, true, on);
     }
-    // in two parts; returns the inverse of their scale
     __device__ __forceinline__ float convert(uint4 *hi, uint4 *lo) const {
-        return convert_column<true>(v, hi, lo);
+        return v.convert<true>(hi, lo);
     }
 };
 template <int DT> struct Hidden {
@@ -931,12 +964,12 @@ k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMa
     extern __shared__ uint8_t raw[];
     uint8_t *rings = raw + (BULK ? (1024u - (smem_at(raw) & 1023u)) & 1023u : 0u);
     DownShared &s = *reinterpret_cast<DownShared *>(
-        rings + (BULK ? (uint32_t)kDownWarps * 2 * Ring<1>::kStage : 0u));
+        rings + (BULK ? (uint32_t)kDownWarps * kDownStages * Ring<1>::kStage : 0u));
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         s.failed = 0;
         for (int w = 0; w < kDownWarps; ++w)
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < kDownStages; ++i)
                 mbar_init((uint32_t)__cvta_generic_to_shared(&s.bars[w][i]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -951,16 +984,16 @@ k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMa
     DownWarp me;
     me.map = &map;
     me.r0 = blockIdx.x * kDownRows;
-    me.ring.begin(rings + warp * 2 * Ring<1>::kStage, s.bars[warp], &s.failed);
+    me.ring.begin(rings + warp * kDownStages * Ring<1>::kStage, s.bars[warp], &s.failed,
+                  kDownStagesLog2);
     // this warp's run of (expert, block)
     const uint32_t steps = (uint32_t)s.c.count * a.fb;
     const uint32_t from = (uint32_t)((uint64_t)steps * warp / kDownWarps);
     const uint32_t end = (uint32_t)((uint64_t)steps * (warp + 1) / kDownWarps);
     me.cursor.begin(a, from, end);
-    if (BULK) {
-        me.fetch(a, s.c);
-        me.fetch(a, s.c);
-    }
+    if (BULK)
+        for (int i = 0; i < kDownStages; ++i)
+            me.fetch(a, s.c);
     kernel_prologue();
     int failed = 0;
     for (uint32_t i = threadIdx.x; i < a.ups; i += kDownThreads)
@@ -995,18 +1028,44 @@ k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMa
     }
 }
 
+// Columns of an expert that fit beside rings of this many stages, no more than there can
+// be.
+template <int DT> static uint32_t up_columns(const MoeArgs &a, uint32_t stages) {
+    const size_t column = UpColumn<DT>::bytes(a.hb), pairs = (size_t)a.T * a.K;
+    const size_t rings = 1024 + kUpWarps * stages * Ring<2>::kStage;
+    size_t n = (kMoeSmem - rings - up_fixed(9)) / column;
+    if (n > 8) {
+        n = (kMoeSmem - rings - up_fixed(kColumns + 1)) / column;
+        n = n < 8 ? 8 : n;
+    }
+    n = n < kColumns ? n : kColumns;
+    return (uint32_t)(n < pairs ? n : pairs);
+}
+
 // The first launch; sets what the second needs to know of it.
 template <int DT, bool BULK>
 static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaStream_t s) {
-    constexpr size_t base = 1024 + (BULK ? kUpWarps * 2 * Ring<2>::kStage : 0) +
-                            (sizeof(UpShared) + 127) / 128 * 128;
     const cudaError_t e = opt_in_smem<k_moe_up<DT, BULK>>(kMoeSmem);
     if (e != cudaSuccess)
         return e;
-    // columns that fit beside the rings, no more than there can be
-    const size_t column = UpColumn<DT>::bytes(a.hb), held = (kMoeSmem - base) / column;
-    const size_t pairs = (size_t)a.T * a.K, most = pairs < kColumns ? pairs : kColumns;
-    a.columns = (uint32_t)(held < most ? held : most);
+    const uint64_t pairs = (uint64_t)a.T * a.K;
+    size_t smem;
+    if (BULK) {
+        // Rings of two stages where the columns of nearly every expert fit beside them (8
+        // tokens, top 8 of 64 experts of 8192 x 1024: 208 us; one stage 216), else of one
+        // (16 tokens: 284; two stages, and a second pass over the weights for more than four
+        // columns, 379).
+        const uint32_t mean = (uint32_t)((pairs + a.E - 1) / a.E), likely = 2 * mean + 2;
+        a.stages = up_columns<DT>(a, 2) >= (likely < a.T ? likely : a.T) ? 2 : 1;
+        a.columns = up_columns<DT>(a, a.stages);
+        a.part_row = a.columns <= 8 ? 9 : kColumns + 1;
+        smem = 1024 + kUpWarps * a.stages * Ring<2>::kStage + up_fixed(a.part_row) +
+               a.columns * UpColumn<DT>::bytes(a.hb);
+    } else {
+        a.columns = pairs < kColumns ? (uint32_t)pairs : kColumns;
+        a.part_row = kColumns + 1;
+        smem = 1024 + up_fixed(a.part_row);
+    }
     const uint64_t units = (uint64_t)((a.F + kUpRows - 1) / kUpRows) * pairs;
     a.ups = (uint32_t)(units < (uint64_t)sms ? units : (uint64_t)sms);
     // The flags lie at the workspace's end, past the rows of h.  A pair has 4 F + 512 bytes
@@ -1015,8 +1074,7 @@ static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaSt
     if (a.ups > 480)
         a.ups = 480;
     a.failed -= a.ups;
-    return launch_kernel(k_moe_up<DT, BULK>, a.ups, kUpThreads, base + a.columns * column, s, true,
-                         a, map);
+    return launch_kernel(k_moe_up<DT, BULK>, a.ups, kUpThreads, smem, s, true, a, map);
 }
 template <int DT, bool BULK>
 static cudaError_t launch_down(const MoeArgs &a, const CUtensorMap &map, cudaStream_t s) {
@@ -1034,6 +1092,8 @@ static cudaError_t moe_dt(MoeArgs a, bool bulk_up, bool bulk_down, cudaStream_t 
         return cudaErrorUnknown;
     a.sh = HiddenRow<DT>::bytes(a.F, a.fb);
     CUtensorMap up = {}, down = {};
+    // without room for a column the first launch reads them on the way
+    bulk_up = bulk_up && up_columns<DT>(a, 1) > 0;
     if ((bulk_up || bulk_down) && !encoder())
         return cudaErrorNotSupported;
     if ((bulk_up && !encode(&up, a.up, a.H, 2 * (uint64_t)a.F, a.ldup, a.E, 16)) ||
@@ -1108,7 +1168,7 @@ int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, cons
     a.hb = (uint32_t)hb;
     a.fb = (uint32_t)fb;
     a.ub = (uint32_t)ub;
-    a.columns = a.ups = 0;
+    a.columns = a.ups = a.stages = a.part_row = 0;
     a.failed = reinterpret_cast<uint8_t *>(work) + mw.bytes;      // less a byte per CTA
     a.wide_x = wide(mx);
     a.ids8 = ids_bytes == 8;

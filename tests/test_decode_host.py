@@ -81,6 +81,30 @@ int main() {
                 return printf("row %u at (%d, %d), not (%d, %d)\n", t, at.x, at.y, want, slot), 1;
         }
     }
+    // many sequences, empty ones among them: the search against a walk
+    for (uint32_t B : {1u, 2u, 31u, 32u, 33u, 34u, 64u, 65u, 1023u, 1024u, 1025u, 1057u, 5000u}) {
+        std::vector<int32_t> offsets(B + 1), lens(B, 9), table(B, 0);
+        offsets[0] = B % 3;
+        for (uint32_t b = 0; b < B; ++b)
+            offsets[b + 1] = offsets[b] + (b * 7919u + B) % 4;
+        Pages g = {};
+        g.table = table.data();
+        g.lens = lens.data();
+        g.ldtable = 1;
+        g.count = 1;
+        g.page = 9;
+        g.by_page = divide_by(9);
+        g.width = 1;
+        uint32_t b = 0;
+        for (uint32_t t = 0; t < (uint32_t)offsets[B] + 3; ++t) {
+            while (b < B && offsets[b + 1] <= (int32_t)t)
+                ++b;
+            const bool in = b < B && offsets[b] <= (int32_t)t;
+            const int2 at = g.place(offsets.data(), B, t);
+            if ((at.x == 0) != in || (in && at.y != 9 - (offsets[b + 1] - (int32_t)t)))
+                return printf("row %u of %u sequences\n", t, B), 1;
+        }
+    }
     // the division, at both ends of each quotient's range
     for (uint32_t d = 1; d < 5000; ++d)
         for (uint64_t n = 0; n < 1ull << 31; n = n * 2 + d) {
