@@ -2,8 +2,10 @@
 //
 //   as they are, or  scale = max(max |x|, 2^-96) / 448,  code = e4m3(x / scale)
 //
-// Bound by memory: every row is read once and written once.  A CTA takes a few
-// rows of all heads; a line (one head's D elements of k or of v) belongs to a
+// Bound by memory: every row is read once and written once (65536 rows of 8 heads of 128
+// bf16 from 8 bits: 64.2 us, 6.3 TB/s; 8192 rows to 8 bits 11.2, about 3 of it launch and
+// lookup).  Rows that are not 16-byte vectors go by elements (30000 rows of 7 x 101 bf16
+// to 8 bits: 119 us, 1.1 TB/s).  A CTA takes a few rows of all heads; a line (one head's D elements of k or of v) belongs to a
 // power of two of consecutive lanes, so that its largest magnitude is found by
 // shuffles.  Writing, the rows' loads are issued before their places are looked
 // up (offsets, length and page table depend on one another), reading after.
@@ -25,7 +27,7 @@ struct MoveArgs {
 };
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveSlots = 4;     // slots of a thread in flight
+constexpr int kMoveSlots = 2;     // slots of a thread in flight
 constexpr int kMoveRows = 64;     // most rows of a job
 
 // One lane's share of a line.  WIDE: N vectors of 16 bytes, vector i at unit
@@ -92,10 +94,62 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(b), "f"(a));
     return q;
 }
+__device__ __forceinline__ uint32_t to_e4m3x4(const float t[4]) {
+    uint32_t q;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(q) : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]));
+    return q;
+}
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t q) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)q));
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// The larger magnitudes of two words of two elements; a NaN gives way to a number.
+template <int DT> __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+    if (DT == AR_BF16) {
+        const __nv_bfloat162 m = __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162 *>(&a)),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&b)));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    }
+    const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2 *>(&a)),
+                              __habs2(*reinterpret_cast<const __half2 *>(&b)));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+// The same, whole lines: the largest magnitude among 1 << bits lanes' elements.
+template <int DT, bool WIDE, int N>
+__device__ __forceinline__ float largest(const Line<DT, WIDE, N> &line, bool on, uint32_t bits) {
+    using L = Line<DT, WIDE, N>;
+    if constexpr (WIDE && L::kSize == 2) {
+        uint32_t top = 0u;
+        if (on)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint4 w = line.w[n];
+                top = max_abs2<DT>(max_abs2<DT>(top, max_abs2<DT>(w.x, w.y)),
+                                   max_abs2<DT>(w.z, w.w));
+            }
+        for (int d = (1 << bits) / 2; d > 0; d >>= 1)
+            top = max_abs2<DT>(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const float2 f = widen2<DT>(top);
+        return fmaxf(f.x, fmaxf(f.y, 0.0f));          // 0 where all are NaN
+    } else {
+        float top = 0.0f;
+        if (on)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                float v[8];
+                line.widen(n, v);
+#pragma unroll
+                for (int e = 0; e < L::E; ++e)
+                    top = fmaxf(top, fabsf(v[e]));
+            }
+        for (int d = (1 << bits) / 2; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        return top;
+    }
 }
 
 // What one slot works on.
@@ -212,21 +266,8 @@ k_cache_move(const __grid_constant__ MoveArgs a) {
     } else {
 #pragma unroll
         for (int i = 0; i < kMoveSlots; ++i) {
-            float top = 0.0f;
-            if (CACHE8) {
-                // lines of no row take part with what they have: a warp's lanes stay together
-                if (at[i].on)
-#pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        float v[8];
-                        line[i].widen(n, v);
-#pragma unroll
-                        for (int e = 0; e < L::E; ++e)
-                            top = fmaxf(top, fabsf(v[e]));
-                    }
-                for (int d = (1 << a.lane_bits) / 2; d > 0; d >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            }
+            // lines of no row take part with nothing: a warp's lanes stay together
+            const float top = CACHE8 ? largest(line[i], at[i].on, a.lane_bits) : 0.0f;
             const int2 p = at[i].on ? places[at[i].row] : make_int2(-1, 0);
             if (p.x < 0)
                 continue;
@@ -248,18 +289,22 @@ k_cache_move(const __grid_constant__ MoveArgs a) {
                     continue;
                 float v[8];
                 line[i].widen(n, v);
-                if (!WIDE) {
-                    cells[e] = (uint8_t)to_e4m3x2(v[0] * inv, 0.0f);
-                    continue;
-                }
-                uint32_t q[2] = {0u, 0u};
+                if constexpr (WIDE) {
+                    uint32_t q[2];
 #pragma unroll
-                for (int x = 0; x < L::E; x += 2)
-                    q[x / 4] |= to_e4m3x2(v[x] * inv, v[(x + 1) % 8] * inv) << (8 * (x & 2));
-                if (L::E == 8)
-                    *reinterpret_cast<uint2 *>(cells + e) = make_uint2(q[0], q[1]);
-                else
-                    *reinterpret_cast<uint32_t *>(cells + e) = q[0];
+                    for (int x = 0; x < L::E; x += 4) {
+                        float t[4] = {v[x], v[x + 1], v[x + 2], v[x + 3]};
+                        mul2(t, inv, inv);
+                        mul2(t + 2, inv, inv);
+                        q[x / 4] = to_e4m3x4(t);
+                    }
+                    if (L::E == 8)
+                        *reinterpret_cast<uint2 *>(cells + e) = make_uint2(q[0], q[L::E / 4 - 1]);
+                    else
+                        *reinterpret_cast<uint32_t *>(cells + e) = q[0];
+                } else {
+                    cells[e] = (uint8_t)to_e4m3x2(v[0] * inv, 0.0f);
+                }
             }
         }
     }
@@ -299,7 +344,10 @@ static cudaError_t move_dt(const MoveArgs &a, bool w, bool e4m3, cudaStream_t s)
     if (!w)
         return e4m3 ? move_form<DT, false, 8, true, READ>(a, s)
                     : move_form<DT, false, 8, false, READ>(a, s);
-    constexpr int N = Elem<DT>::kSize == 4 ? 2 : 1;      // D <= 256 within 32 lanes
+    // 32 bytes of codes and twice or four times that of rows a lane: with half of it, every
+    // line's address, scale and shuffles are paid for by fewer bytes (65536 rows of 8 x 128
+    // bf16 from 8 bits 77.7 us, to 8 bits 99; so 64.2 and 70.4)
+    constexpr int N = Elem<DT>::kSize == 4 ? 4 : 2;
     return e4m3 ? move_form<DT, true, N, true, READ>(a, s)
                 : move_form<DT, true, N, false, READ>(a, s);
 }
