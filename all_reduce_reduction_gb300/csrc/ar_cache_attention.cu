@@ -19,164 +19,360 @@ namespace ar {
 
 // ---- any type and alignment -----------------------------------------------------
 
-// A tile of keys, then of values, in shared memory as binary32; a thread has one
-// key and four rows of the scores, then one or two columns of the outputs and half
-// of the rows.
-constexpr int kRows = 16;             // query heads of a unit
-constexpr int kAnyThreads = 256;
-constexpr uint32_t kAnyTile = 64;
+// Keys and values of binary32, or that are not 16-byte vectors.  Eight query heads are a
+// unit; a warp has eight positions of every tile of 32 in shared memory as binary32,
+// copied some tiles ahead where they are binary32 vectors and loaded by elements
+// otherwise.  Scores: a lane has one key and every fourth 16 bytes of it, for all eight
+// heads; the four lanes of a key then share the heads out.  Outputs: a lane has 4 columns
+// (8 past D = 128) of all heads.  Bound by shared-memory reads and multiply-adds for many
+// heads, by the copies' wait for few.
+constexpr int kTeams = 4, kAnyThreads = 32 * kTeams;
+constexpr uint32_t kAnyKeys = 8, kAnyHeads = 8, kAnyTile = kAnyKeys * kTeams;
 
-static size_t any_smem(uint32_t D) {
-    return sizeof(float) * ((size_t)kRows * D + kAnyTile * (D | 1) + kRows * (kAnyTile + 1));
+template <int DC, bool ASYNC> struct AnyForm {
+    static constexpr uint32_t kRow = DC * 4;
+    static constexpr uint32_t kMask = 2 * kAnyKeys * kRow, kStage = kMask + 16;
+    static constexpr int kStages = ASYNC ? 3 : 1;
+    static constexpr uint32_t kRing = kTeams * kStages * kStage;
+    static constexpr uint32_t kQ = kAnyHeads * kRow;
+    static constexpr uint32_t kWeights = kAnyKeys * kAnyHeads * 4;           // of a warp
+    static constexpr uint32_t kJoin = kTeams * 4 * kRow;                     // four heads
+    static constexpr uint32_t kSmem = kRing + kQ + kTeams * kWeights + kJoin;
+    static constexpr int kCtas = ASYNC ? (DC == 128 ? 2 : 1) : (DC == 128 ? 4 : 2);
+    // 16 bytes c of row r; odd rows are exchanged so that two rows' reads share no bank
+    static __device__ __forceinline__ uint32_t chunk(uint32_t r, uint32_t c) {
+        return r * kRow + ((c ^ ((r & 1) << 2)) << 4);
+    }
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
-template <int DT, bool CACHE8>
-__global__ void __launch_bounds__(kAnyThreads)
+template <int DT, bool CACHE8, int DC, bool ASYNC>
+__global__ void __launch_bounds__(kAnyThreads, AnyForm<DC, ASYNC>::kCtas)
 k_attention_any(const __grid_constant__ AttnArgs a) {
-    extern __shared__ float smem[];
-    __shared__ uint64_t scan[33];
-    __shared__ float m_[kRows], l_[kRows], alpha_[kRows];
-    __shared__ int2 place[kAnyTile];
+    using F = AnyForm<DC, ASYNC>;
+    constexpr int J = DC / 128;                   // vectors of a row that a lane has
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t scan[32];
+    __shared__ float team_m[kTeams][kAnyHeads], team_l[kTeams][kAnyHeads];
+    const uint32_t D = a.g.D, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t vectors = (D + 15) / 16 * 4;   // of a row, whole groups of four
+    uint8_t *ring = smem + warp * (F::kStages * F::kStage), *qs = smem + F::kRing;
+    float *weights = reinterpret_cast<float *>(qs + F::kQ + warp * F::kWeights);
+    float *join = reinterpret_cast<float *>(qs + F::kQ + kTeams * F::kWeights);
+    const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
     kernel_prologue();
-    const uint32_t D = a.g.D, stride = D | 1, tid = threadIdx.x;
-    float *qs = smem, *kv = qs + kRows * D, *sc = kv + kAnyTile * stride;
     if (tid == 0)
         WorkSpace(a.work).meta[blockIdx.x] = make_int4(0, 0, -1, 0);
     empty_rows<DT, kAnyTile>(a);
     uint64_t per;
     Cursor<kAnyTile> c = find_run<kAnyTile>(a, scan, &per);
-    for (; !c.done(); c.next_unit(a)) {
-        const UnitRows u = unit_rows(a, c.unit);
-        const uint32_t b = c.b;
-        __syncthreads();
-        const uint8_t *q = a.q + (uint64_t)b * a.sq + (uint64_t)u.head * D * Elem<DT>::kSize;
-        for (uint32_t i = tid; i < kRows * D; i += kAnyThreads)
-            qs[i] = i < u.rows * D ? widen1<DT>(ld_elem<DT>(q, i)) : 0.0f;
-        if (tid < kRows) {
-            m_[tid] = -INFINITY;
-            l_[tid] = 0.0f;
+
+    // ---- the positions of a step to shared memory
+    Cursor<kAnyTile> f = c;
+    uint32_t slot = 0;
+    int32_t page = -1;
+    auto look_up = [&] {                          // lane r: of row r of the next step
+        if (f.done())
+            return;
+        const uint32_t j = f.span.origin + f.t * kAnyTile + warp * kAnyKeys + (lane & 7);
+        page = -1;
+        if (j < f.span.n && j >= f.span.lo) {
+            page = a.g.page_of(f.b, j);
+            slot = a.g.slot_of(j);
         }
-        float acc[2][kRows / 2];          // columns tid % 128 (+ 128), rows of one half
+    };
+    auto fetch = [&](uint32_t stage) {
+        if (!f.done()) {
+            const uint32_t kv = f.unit / a.head_tiles;
+            constexpr uint32_t kCell = CACHE8 ? 1 : Elem<DT>::kSize;
+            const uint64_t mine = page >= 0 ? (uint64_t)page * a.g.stride +
+                                                  (uint64_t)a.g.in_page(kv, slot) * kCell
+                                            : ~0ull;
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, page >= 0) & 255u;
+            uint8_t *to = ring + stage * F::kStage;
+            if constexpr (ASYNC) {
+                const uint32_t at = ring_addr + stage * F::kStage;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+                for (uint32_t r = 0; r < kAnyKeys; ++r) {
+                    const uint64_t row = __shfl_sync(0xFFFFFFFFu, mine, r);
 #pragma unroll
-            for (int r = 0; r < kRows / 2; ++r)
-                acc[i][r] = 0.0f;
-        for (uint32_t t = c.t; t < c.t1; ++t) {
-            const uint32_t j0 = c.span.origin + t * kAnyTile;
-            __syncthreads();              // the last tile is done with
-            if (tid < kAnyTile) {
-                const uint32_t j = j0 + tid;
-                place[tid] = j < c.span.n ? make_int2(a.g.page_of(b, j), (int)a.g.slot_of(j))
-                                          : make_int2(-1, 0);
-            }
-            __syncthreads();
-            auto load = [&](const uint8_t *pool, const float *scales) {
-                for (uint32_t i = tid; i < kAnyTile * D; i += kAnyThreads) {
-                    const uint32_t r = i / D, d = i - r * D;
-                    const int2 p = place[r];
-                    float v = 0.0f;
-                    if (p.x >= 0) {
-                        const uint8_t *page = pool + (uint64_t)p.x * a.g.stride;
-                        const uint32_t e = a.g.in_page(u.kv, p.y) + d;
+                    for (uint32_t j = 0; j < J; ++j) {
+                        const uint32_t v = lane + 32 * j;
+                        const bool on = row != ~0ull && v * 4 < D;
+                        const uint64_t x = on ? row + v * 16 : 0;
+                        if (v < vectors) {
+                            copy16(at + F::chunk(r, v), a.g.k + x, on ? 16 : 0);
+                            copy16(at + kAnyKeys * F::kRow + F::chunk(r, v), a.g.v + x,
+                                   on ? 16 : 0);
+                        }
+                    }
+                }
+            } else {
+                float ks = 1.0f, vs = 1.0f;
+                if (CACHE8 && page >= 0) {
+                    ks = a.g.ks[a.g.scale_at(page, kv, slot)];
+                    vs = a.g.vs[a.g.scale_at(page, kv, slot)];
+                }
+                // eight rows' loads in flight, of 32 columns each
+                for (uint32_t d0 = 0; d0 < 4 * vectors; d0 += 32) {
+                    const uint32_t d = d0 + lane;
+                    uint32_t k[kAnyKeys], v[kAnyKeys];
+#pragma unroll
+                    for (uint32_t r = 0; r < kAnyKeys; ++r) {
+                        const uint64_t row = __shfl_sync(0xFFFFFFFFu, mine, r);
+                        k[r] = v[r] = 0u;
+                        if (row != ~0ull && d < D) {
+                            if (CACHE8) {
+                                k[r] = a.g.k[row + d];
+                                v[r] = a.g.v[row + d];
+                            } else {
+                                k[r] = ld_elem<DT>(a.g.k + row, d);
+                                v[r] = ld_elem<DT>(a.g.v + row, d);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (uint32_t r = 0; r < kAnyKeys; ++r) {
+                        float x, y;
                         if (CACHE8) {
-                            uint32_t h;
-                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)page[e]));
-                            v = __half2float(__ushort_as_half((unsigned short)h)) *
-                                scales[a.g.scale_at(p.x, u.kv, p.y)];
+                            uint32_t h, g;
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)k[r]));
+                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(g) : "h"((uint16_t)v[r]));
+                            x = __half2float(__ushort_as_half((unsigned short)h)) *
+                                __shfl_sync(0xFFFFFFFFu, ks, r);
+                            y = __half2float(__ushort_as_half((unsigned short)g)) *
+                                __shfl_sync(0xFFFFFFFFu, vs, r);
+                            // a row that is not there: zeros, whatever its lane's scales
+                            x = mask >> r & 1u ? x : 0.0f;
+                            y = mask >> r & 1u ? y : 0.0f;
                         } else {
-                            v = widen1<DT>(ld_elem<DT>(page, e));
+                            x = widen1<DT>(k[r]);
+                            y = widen1<DT>(v[r]);
+                        }
+                        if (d < 4 * vectors) {
+                            const uint32_t at = F::chunk(r, d / 4) + d % 4 * 4;
+                            *reinterpret_cast<float *>(to + at) = x;
+                            *reinterpret_cast<float *>(to + kAnyKeys * F::kRow + at) = y;
                         }
                     }
-                    kv[r * stride + d] = v;
-                }
-            };
-            load(a.g.k, a.g.ks);
-            __syncthreads();
-            {
-                const uint32_t key = tid % kAnyTile, r0 = tid / kAnyTile * 4;
-                float s[4] = {};
-                if (r0 < u.rows)
-                    for (uint32_t d = 0; d < D; ++d) {
-                        const float k = kv[key * stride + d];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            s[r] += qs[(r0 + r) * D + d] * k;
-                    }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    sc[(r0 + r) * (kAnyTile + 1) + key] =
-                        place[key].x >= 0 ? s[r] * a.scale2 : -INFINITY;
-            }
-            __syncthreads();
-            load(a.g.v, a.g.vs);
-            for (uint32_t r = tid / 32; r < u.rows; r += kAnyThreads / 32) {
-                float *row = sc + r * (kAnyTile + 1);
-                const uint32_t lane = tid & 31;
-                const float x = row[lane], y = row[lane + 32];
-                // a NaN score makes its row NaN: the maximum must not drop it
-                float top = fmaxf(x, y);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                const float was = m_[r], now = fmaxf(was, top), base = finite_max(now);
-                const float p0 = exp2f(x - base), p1 = exp2f(y - base);
-                const float sum = warp_sum(p0 + p1), al = exp2f(was - base);
-                row[lane] = p0;
-                row[lane + 32] = p1;
-                __syncwarp();
-                if (lane == 0) {
-                    m_[r] = now;
-                    l_[r] = l_[r] * al + sum;
-                    alpha_[r] = al;
                 }
             }
-            __syncthreads();
-            {
-                const uint32_t d0 = tid % 128, r0 = tid / 128 * (kRows / 2);
-                const uint32_t keys = c.span.n - j0 < kAnyTile ? c.span.n - j0 : kAnyTile;
-                if (r0 < u.rows)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t d = d0 + 128 * i;
-                        if (d >= D)
-                            break;
-#pragma unroll
-                        for (int r = 0; r < kRows / 2; ++r)
-                            if (r0 + r < u.rows)
-                                acc[i][r] *= alpha_[r0 + r];
-                        for (uint32_t k = 0; k < keys; ++k) {
-                            const float v = kv[k * stride + d];
-#pragma unroll
-                            for (int r = 0; r < kRows / 2; ++r)
-                                acc[i][r] += sc[(r0 + r) * (kAnyTile + 1) + k] * v;
-                        }
-                    }
-            }
+            if (lane == 0)
+                *reinterpret_cast<uint32_t *>(to + F::kMask) = mask;
+            f.next(a);
+            look_up();
         }
-        const int part = segment_part(a, c, per);
-        const uint32_t r0 = tid / 128 * (kRows / 2);
+        if (ASYNC)
+            asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up();
+    if (ASYNC)
+#pragma unroll
+        for (int i = 0; i < F::kStages - 1; ++i)
+            fetch(i);
+    uint32_t stage = 0;
+    const uint32_t key = lane / 4, quarter = lane % 4;
+
+    while (!c.done()) {
+        const UnitRows u = unit_rows(a, c.unit);
+        const uint8_t *q = a.q + (uint64_t)c.b * a.sq + (uint64_t)u.head * D * Elem<DT>::kSize;
+        for (uint32_t i = tid; i < kAnyHeads * DC; i += kAnyThreads) {
+            const uint32_t r = i / DC, d = i % DC;
+            reinterpret_cast<float *>(qs)[i] =
+                r < u.rows && d < D ? widen1<DT>(ld_elem<DT>(q, r * D + d)) : 0.0f;
+        }
+        __syncthreads();
+        // of this lane's heads 2 * quarter + {0, 1}: the running maximum, what scores are
+        // compared with and taken relative to, the sum
+        float m[2], bound[2], base[2], l[2];
+        float o[J][kAnyHeads][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t d = tid % 128 + 128 * i;
+            m[i] = bound[i] = -INFINITY;
+            base[i] = l[i] = 0.0f;
+        }
 #pragma unroll
-            for (int r = 0; r < kRows / 2; ++r) {
-                if (d >= D || r0 + r >= u.rows)
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (uint32_t h = 0; h < kAnyHeads; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[j][h][i] = 0.0f;
+        for (uint32_t t = c.t; t < c.t1; ++t) {
+            if (ASYNC) {
+                asm volatile("cp.async.wait_group %0;" :: "n"(F::kStages - 2) : "memory");
+                __syncwarp();
+                fetch((stage + F::kStages - 1) % F::kStages);
+            } else {
+                __syncwarp();                     // the step before is done with
+                fetch(0);
+                __syncwarp();
+            }
+            const uint8_t *here = ring + stage * F::kStage;
+            const uint32_t mask = *reinterpret_cast<const uint32_t *>(here + F::kMask);
+            float s[kAnyHeads][2];
+#pragma unroll
+            for (uint32_t h = 0; h < kAnyHeads; ++h)
+                s[h][0] = s[h][1] = 0.0f;
+#pragma unroll 2
+            for (uint32_t v = quarter; v < vectors; v += 4) {
+                const float4 k = *reinterpret_cast<const float4 *>(here + F::chunk(key, v));
+#pragma unroll
+                for (uint32_t h = 0; h < kAnyHeads; ++h) {
+                    const float4 x = *reinterpret_cast<const float4 *>(qs + h * F::kRow + v * 16);
+                    fma2(s[h], x.x, x.y, k.x, k.y);
+                    fma2(s[h], x.z, x.w, k.z, k.w);
+                }
+            }
+            // the four lanes of a key: half of the heads change hands, then a quarter
+            float e[2];
+            {
+                float x[4], y[2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float lo = s[j][0] + s[j][1], hi = s[4 + j][0] + s[4 + j][1];
+                    x[j] = quarter & 2 ? hi : lo;
+                    x[j] += __shfl_xor_sync(0xFFFFFFFFu, quarter & 2 ? lo : hi, 2);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    y[j] = quarter & 1 ? x[2 + j] : x[j];
+                    y[j] += __shfl_xor_sync(0xFFFFFFFFu, quarter & 1 ? x[j] : x[2 + j], 1);
+                    e[j] = mask >> key & 1u ? y[j] * a.scale2 : -INFINITY;
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, e[0] > bound[0] || e[1] > bound[1])) {
+                float al[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float now = fmaxf(m[i], e[i]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, d));
+                    al[i] = exp2f(m[i] - finite_max(now));
+                    m[i] = now;
+                    bound[i] = now + kSlack;
+                    base[i] = finite_max(now);
+                    l[i] *= al[i];
+                }
+#pragma unroll
+                for (uint32_t h = 0; h < kAnyHeads; ++h) {
+                    const float by = __shfl_sync(0xFFFFFFFFu, al[h & 1], h / 2);
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        mul2(o[j][h], by, by);
+                        mul2(o[j][h] + 2, by, by);
+                    }
+                }
+            }
+            const float2 p = make_float2(exp2f(e[0] - base[0]), exp2f(e[1] - base[1]));
+            l[0] += p.x;
+            l[1] += p.y;
+            *reinterpret_cast<float2 *>(weights + key * kAnyHeads + 2 * quarter) = p;
+            __syncwarp();
+#pragma unroll 2
+            for (uint32_t k = 0; k < kAnyKeys; ++k) {
+                const float4 x = *reinterpret_cast<const float4 *>(weights + k * kAnyHeads);
+                const float4 y = *reinterpret_cast<const float4 *>(weights + k * kAnyHeads + 4);
+                const float w[kAnyHeads] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const uint32_t v = lane + 32 * j;
+                    if (v >= vectors)
+                        continue;
+                    const float4 g = *reinterpret_cast<const float4 *>(
+                        here + kAnyKeys * F::kRow + F::chunk(k, v));
+#pragma unroll
+                    for (uint32_t h = 0; h < kAnyHeads; ++h) {
+                        fma2(o[j][h], w[h], w[h], g.x, g.y);
+                        fma2(o[j][h] + 2, w[h], w[h], g.z, g.w);
+                    }
+                }
+            }
+            stage = ASYNC ? (stage + 1) % F::kStages : 0;
+        }
+        const Cursor<kAnyTile> done = c;
+        c.next_unit(a);
+
+        // the teams' parts, in their order
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+                l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], d);
+            if (key == 0) {
+                team_m[warp][2 * quarter + i] = m[i];
+                team_l[warp][2 * quarter + i] = l[i];
+            }
+        }
+        __syncthreads();
+        const int part = segment_part(a, done, per);
+        auto total = [&](uint32_t h, float &sum) {        // of head h over the teams
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kTeams; ++w)
+                top = fmaxf(top, team_m[w][h]);
+            sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kTeams; ++w)
+                sum += team_l[w][h] * exp2f(team_m[w][h] - finite_max(top));
+            return top;
+        };
+#pragma unroll
+        for (uint32_t h0 = 0; h0 < kAnyHeads; h0 += 4) {
+            if (h0 >= u.rows)
+                break;
+            if (h0 > 0)
+                __syncthreads();
+#pragma unroll
+            for (uint32_t h = 0; h < 4; ++h) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kTeams; ++w)
+                    top = fmaxf(top, team_m[w][h0 + h]);
+                const float own = exp2f(team_m[warp][h0 + h] - finite_max(top));
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const float *x = o[j][h0 + h];
+                    *reinterpret_cast<float4 *>(join + (warp * 4 + h) * DC + (lane + 32 * j) * 4) =
+                        make_float4(x[0] * own, x[1] * own, x[2] * own, x[3] * own);
+                }
+            }
+            __syncthreads();
+            for (uint32_t i = tid; i < 4 * DC; i += kAnyThreads) {
+                const uint32_t h = h0 + i / DC, d = i % DC;
+                if (h >= u.rows || d >= D)
                     continue;
-                if (part < 0)
-                    store_row<DT>(a.out + (uint64_t)b * a.sout, (u.head + r0 + r) * D + d,
-                                  output_of(acc[i][r], l_[r0 + r]));
-                else
-                    WorkSpace(a.work).o[((uint64_t)part * a.unit_rows + r0 + r) * D + d] = acc[i][r];
+                float v = join[i];
+#pragma unroll
+                for (int w = 1; w < kTeams; ++w)
+                    v += join[w * 4 * DC + i];
+                if (part < 0) {
+                    float sum;
+                    total(h, sum);
+                    store_row<DT>(a.out + (uint64_t)done.b * a.sout, (u.head + h) * D + d,
+                                  output_of(v, sum));
+                } else {
+                    WorkSpace(a.work).o[((uint64_t)part * kAnyHeads + h) * D + d] = v;
+                }
             }
         }
         if (tid < u.rows) {
+            float sum;
+            const float top = total(tid, sum);
             if (part >= 0)
-                WorkSpace(a.work).ml[part * a.unit_rows + tid] = make_float2(m_[tid], l_[tid]);
+                WorkSpace(a.work).ml[part * kAnyHeads + tid] = make_float2(top, sum);
             else if (a.lse)
-                a.lse[(uint64_t)b * a.heads + u.head + tid] = lse_of(m_[tid], l_[tid]);
+                a.lse[(uint64_t)done.b * a.heads + u.head + tid] = lse_of(top, sum);
         }
+        __syncthreads();                          // before the next unit's q and sums
     }
+    if (ASYNC)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ---- the join ---------------------------------------------------------------------
@@ -289,27 +485,40 @@ template <int DT> static cudaError_t launch_join(const AttnArgs &a, int grid, cu
     return a.g.D % 4 == 0 ? join_form<DT, 4>(a, grid, s) : join_form<DT, 1>(a, grid, s);
 }
 
-template <int DT, bool CACHE8> static cudaError_t attention_any(const AttnArgs &a, cudaStream_t s) {
-    const size_t smem = any_smem(a.g.D);
-    cudaError_t e = opt_in_smem<k_attention_any<DT, CACHE8>>(any_smem(AR_CACHE_MAX_DIM));
+template <int DT, bool CACHE8, int DC, bool ASYNC>
+static cudaError_t any_form(AttnArgs &a, cudaStream_t s) {
+    using F = AnyForm<DC, ASYNC>;
+    cudaError_t e = opt_in_smem<k_attention_any<DT, CACHE8, DC, ASYNC>>(F::kSmem);
     if (e != cudaSuccess)
         return e;
     const int sms = sm_count();
     if (sms < 1)
         return cudaErrorUnknown;
-    const int grid = cta_limit(a.unit_rows, 2 * sms);
-    e = launch_kernel(k_attention_any<DT, CACHE8>, grid, kAnyThreads, smem, s, true, a);
+    a.unit_rows = kAnyHeads;
+    a.head_tiles = (a.group + kAnyHeads - 1) / kAnyHeads;
+    a.runs = 0;
+    const int grid = cta_limit(a.unit_rows, F::kCtas * sms);
+    e = launch_kernel(k_attention_any<DT, CACHE8, DC, ASYNC>, grid, kAnyThreads, F::kSmem, s, true,
+                      a);
     return e != cudaSuccess ? e : launch_join<DT>(a, grid, s);
 }
 
-template <int DT>
-static cudaError_t attention_dt(AttnArgs &a, bool e4m3, bool w, cudaStream_t s) {
-    if (DT != AR_FP32 && w) {
+// w: keys and values are whole 16-byte vectors on 16-byte boundaries.
+template <int DT> static cudaError_t attention_dt(AttnArgs &a, bool e4m3, bool w, cudaStream_t s) {
+    if (w && (DT != AR_FP32 || e4m3)) {
         int grid = 0;
         const cudaError_t e = launch_attention_mma(a, DT, e4m3, &grid, s);
         return e != cudaSuccess ? e : launch_join<DT>(a, grid, s);
     }
-    return e4m3 ? attention_any<DT, true>(a, s) : attention_any<DT, false>(a, s);
+    if constexpr (DT == AR_FP32)
+        if (w)
+            return a.g.D <= 128 ? any_form<DT, false, 128, true>(a, s)
+                                : any_form<DT, false, 256, true>(a, s);
+    if (e4m3)
+        return a.g.D <= 128 ? any_form<DT, true, 128, false>(a, s)
+                            : any_form<DT, true, 256, false>(a, s);
+    return a.g.D <= 128 ? any_form<DT, false, 128, false>(a, s)
+                        : any_form<DT, false, 256, false>(a, s);
 }
 
 }  // namespace ar
@@ -360,8 +569,7 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
     a.B = (uint32_t)B;
     a.heads = (uint32_t)heads;
     a.group = (uint32_t)(heads / kv_heads);
-    a.unit_rows = kRows;
-    a.head_tiles = (a.group + kRows - 1) / kRows;
+    a.unit_rows = a.head_tiles = 0;                       // by the form
     a.runs = 0;
     a.window = window < ((size_t)1 << 31) ? (uint32_t)window : 0u;
     const bool e4m3 = cache_dtype == AR_E4M3;

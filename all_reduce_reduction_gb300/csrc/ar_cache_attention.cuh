@@ -200,6 +200,10 @@ __device__ __forceinline__ float output_of(float o, float l) {
 // What the running maximum subtracts: a row of -inf alone keeps weights of 0.
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// The running maximum follows a row's scores only when one is this far above it
+// (as exponents of two): weights up to 2^4 cost nothing, new factors for all of o do.
+constexpr float kSlack = 4.0f;
+
 // Where a unit's rows go: first query head, rows.
 struct UnitRows {
     uint32_t kv, head, rows;
@@ -229,9 +233,9 @@ __device__ __forceinline__ int segment_part(const AttnArgs &a, const Cursor<TILE
     return 2 * blockIdx.x + 1;
 }
 
-// ar_cache_attention_mma.cu: the tensor-core form, for q of two bytes and a cache whose
-// rows are whole 16-byte vectors on 16-byte boundaries.  Sets the units of `a`;
-// *grid: its CTAs.
+// ar_cache_attention_mma.cu: the tensor-core form, for keys and values of one or two
+// bytes whose rows are whole 16-byte vectors on 16-byte boundaries.  Sets the units of
+// `a`; *grid: its CTAs.
 cudaError_t launch_attention_mma(AttnArgs &a, int dtype, bool e4m3, int *grid, cudaStream_t s);
 
 }  // namespace ar

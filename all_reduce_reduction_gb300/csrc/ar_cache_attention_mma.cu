@@ -1,5 +1,6 @@
 // Attention over the paged cache on the tensor cores, for keys and values of two
-// bytes (in the type of q) or one (E4M3, in binary16).
+// bytes (in the type of q) or one (E4M3, in binary16; q then too, in two parts where it
+// is binary32).
 //
 // A warp's products have 16 positions by 8 query heads that share a key-value head:
 // s' = k q', then o' += v' p', so that keys and values are the operand of 16 rows and
@@ -16,13 +17,25 @@ namespace ar {
 constexpr int kTeams = 4;                     // of warps, 16 positions of a tile each
 constexpr uint32_t kMmaTile = 16 * kTeams;
 
-// The running maximum follows a row's scores only when one is this far above it
-// (as exponents of two): weights up to 2^4 cost nothing, new factors for all of o do.
-constexpr float kSlack = 4.0f;
 // E4M3 values: a weight times its value's scale is held in binary16, so the maximum
 // is that of score + log2 scale (whole exponents, -96 at least: the sum of the weights
-// alone stays finite), and 2^8 times as much fits.
+// alone stays finite), and 2^8 times as much fits.  Scales that ar_cache_write gives are
+// 2^-105 at least; where the output is binary32, smaller ones count in full too: the
+// sum of the weights alone then has a maximum of its own.
 constexpr float kWeightBits = 8.0f, kLeastScale = -96.0f;
+
+// A scale as f * 2^e with f in [1, 2); e is -inf for 0, f what is not finite.
+__device__ __forceinline__ void split_scale(float v, float &e, float &f) {
+    const bool tiny = v < 0x1p-100f;
+    const uint32_t bits = __float_as_uint(tiny ? v * 0x1p100f : v);
+    const int exponent = (int)(bits >> 23);
+    e = v == 0.0f ? -INFINITY : (float)(exponent - 127 - (tiny ? 100 : 0));
+    f = __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u);
+    if (exponent == 255) {
+        e = 0.0f;
+        f = v;
+    }
+}
 
 __device__ __forceinline__ uint32_t shared_addr(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -83,7 +96,8 @@ template <int DT, bool CACHE8, int DC, int HG> struct MmaForm {
     static constexpr uint32_t kStage = kMask + 16;
     static constexpr int kStages = HG == 4 && DC < 256 ? 5 : 3;
     static constexpr uint32_t kRing = kTeams * kStages * kStage;
-    static constexpr uint32_t kQ = kHeads * DC * 2;
+    static constexpr int kQParts = DT == AR_FP32 ? 2 : 1;
+    static constexpr uint32_t kQPart = kHeads * DC * 2, kQ = kQParts * kQPart;
     // columns of the output that the warps join at a time
     static constexpr int kJoin = DC == 256 || (CACHE8 && DC == 128) ? 16 : 32;
     static constexpr uint32_t kJoinRow = kJoin + 2;
@@ -92,7 +106,7 @@ template <int DT, bool CACHE8, int DC, int HG> struct MmaForm {
     // the workspace)
     static constexpr int kCtas = HG == 4     ? 1
                                  : DC == 256 ? (CACHE8 && HG == 1 ? 2 : 1)
-                                 : DC == 128 ? (!CACHE8 ? 2 : HG == 1 ? 4 : 2)
+                                 : DC == 128 ? (!CACHE8 ? 2 : HG == 1 ? (kQParts == 1 ? 4 : 3) : 2)
                                              : (CACHE8 && HG == 1 ? 4 : HG == 1 ? 3 : 2);
 
     // chunk c of row r: the rows of a group of eight lie in different banks
@@ -117,7 +131,8 @@ __global__ void __launch_bounds__(MmaForm<DT, CACHE8, DC, HG>::kThreads, MmaForm
 k_attention_mma(const __grid_constant__ AttnArgs a) {
     using M = MmaForm<DT, CACHE8, DC, HG>;
     constexpr uint32_t H = M::kHeads;
-    constexpr bool kKeepQ = DC <= 128;   // q's operands stay in registers
+    constexpr bool kKeepQ = DC <= 128 && M::kQParts == 1;   // q's operands stay in registers
+    constexpr bool kApart = CACHE8 && DT == AR_FP32;        // scores have a maximum of their own
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t scan[33];
     __shared__ float group_m[kTeams][H], group_l[kTeams][H], head_scale[H];
@@ -136,25 +151,29 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
 
     // ---- q of a unit, two elements a word, a warp to a row: loaded a unit ahead
     constexpr int kWarps = kTeams * HG, kQRows = H / kWarps, kQWords = DC / 64;
+    constexpr uint32_t kQSize = Elem<DT>::kSize;
     const bool q_words = ((uintptr_t)a.q | a.sq) % 4 == 0;
-    uint32_t qw[kQRows][kQWords];
+    uint32_t qw[kQRows][kQWords][kQSize / 2];
     auto load_q_rows = [&] {
         if (c.done())
             return;
         const UnitRows u = unit_rows(a, c.unit);
-        const uint8_t *q = a.q + (uint64_t)c.b * a.sq + (uint64_t)u.head * D * 2;
+        const uint8_t *q = a.q + (uint64_t)c.b * a.sq + (uint64_t)u.head * D * kQSize;
 #pragma unroll
         for (int k = 0; k < kQRows; ++k)
 #pragma unroll
             for (int i = 0; i < kQWords; ++i) {
                 const uint32_t r = warp + k * kWarps, d = 2 * lane + 64 * i;
-                qw[k][i] = 0u;
-                if (r < u.rows && d < D) {
-                    const uint8_t *x = q + (uint64_t)(r * D + d) * 2;
-                    if (q_words)
-                        qw[k][i] = *reinterpret_cast<const uint32_t *>(x);
-                    else
-                        qw[k][i] = ld_elem<DT>(x, 0) | ld_elem<DT>(x, 1) << 16;
+#pragma unroll
+                for (uint32_t w = 0; w < kQSize / 2; ++w) {
+                    qw[k][i][w] = 0u;
+                    if (r < u.rows && d < D) {
+                        const uint8_t *x = q + (uint64_t)(r * D + d) * kQSize + 4 * w;
+                        if (kQSize == 4 || q_words)
+                            qw[k][i][w] = *reinterpret_cast<const uint32_t *>(x);
+                        else
+                            qw[k][i][w] = ld_elem<AR_BF16>(x, 0) | ld_elem<AR_BF16>(x, 1) << 16;
+                    }
                 }
             }
     };
@@ -260,9 +279,9 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
     const uint32_t v_chunk = CACHE8 ? lane / 16 : lane / 8 & 1;
     const uint32_t q_row = part8 * 8 + lane % 8, q_part = lane / 8;
     // q's operands of steps k, k + 1 of 16 columns: two words for each
-    auto load_q = [&](uint32_t (*q)[2], int k) {
+    auto load_q = [&](uint32_t (*q)[2], int k, uint32_t part) {
         uint32_t w[4];
-        ldmatrix4(w, q_addr + M::q_chunk(q_row, 2 * k + q_part));
+        ldmatrix4(w, q_addr + part * M::kQPart + M::q_chunk(q_row, 2 * k + q_part));
         q[0][0] = w[0];
         q[0][1] = w[1];
         q[1][0] = w[2];
@@ -281,11 +300,17 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
         for (int k = 0; k < kQRows; ++k) {
             const uint32_t r = warp + k * kWarps;
             float up = 1.0f, back = 1.0f;
+            auto pair = [&](int i) {
+                if constexpr (kQSize == 4)
+                    return make_float2(__uint_as_float(qw[k][i][0]), __uint_as_float(qw[k][i][1]));
+                else
+                    return widen2<DT>(qw[k][i][0]);
+            };
             if (CACHE8) {
                 float top = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kQWords; ++i) {
-                    const float2 x = widen2<DT>(qw[k][i]);
+                    const float2 x = pair(i);
                     top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
                 }
 #pragma unroll
@@ -296,12 +321,16 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
 #pragma unroll
             for (int i = 0; i < kQWords; ++i) {
                 const uint32_t e = M::q_column(2 * lane + 64 * i);
-                uint32_t w = qw[k][i];
+                uint8_t *at = qs + M::q_chunk(r, e / 8) + e % 8 * 2;
+                uint32_t w = qw[k][i][0];
                 if (CACHE8) {
-                    const float2 x = widen2<DT>(w);
+                    const float2 x = pair(i);
                     w = half2_of(x.x * up, x.y * up);
+                    if (M::kQParts == 2)
+                        *reinterpret_cast<uint32_t *>(at + M::kQPart) =
+                            rest_of(w, x.x * up, x.y * up);
                 }
-                *reinterpret_cast<uint32_t *>(qs + M::q_chunk(r, e / 8) + e % 8 * 2) = w;
+                *reinterpret_cast<uint32_t *>(at) = w;
             }
             if (lane == 0)
                 head_scale[r] = a.scale2 * back;
@@ -311,16 +340,18 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
         if (kKeepQ)
 #pragma unroll
             for (int k = 0; k < DC / 16; k += 2)
-                load_q(qf + (kKeepQ ? k : 0), k);
+                load_q(qf + (kKeepQ ? k : 0), k, 0);
         // of a lane's columns: heads first + {0, 1}
         const uint32_t first = part8 * 8 + lane % 4 * 2;
         // m, and what a score is compared with and taken relative to
         float scale[2], m[2], bound[2], base[2], l[2], o[DC / 16][4];
+        float score_m[2], score_bound[2], score_base[2];       // kApart: those of l
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             scale[i] = head_scale[first + i];
             m[i] = bound[i] = -INFINITY;
-            base[i] = l[i] = 0.0f;
+            base[i] = l[i] = score_base[i] = 0.0f;
+            score_m[i] = score_bound[i] = -INFINITY;
         }
 #pragma unroll
         for (int d = 0; d < DC / 16; ++d)
@@ -355,11 +386,14 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     ldmatrix4(ka[0], at + M::chunk(k_row, 2 * k + k_chunk));
                     ldmatrix4(ka[1], at + M::chunk(k_row, 2 * k + 2 + k_chunk));
                 }
-                if (!kKeepQ)
-                    load_q(qf, k);
-                const uint32_t(*q)[2] = qf + (kKeepQ ? k : 0);
-                mma16<M::kType>(s, ka[0], q[0][0], q[0][1]);
-                mma16<M::kType>(s2, ka[1], q[1][0], q[1][1]);
+#pragma unroll
+                for (int part = 0; part < M::kQParts; ++part) {
+                    if (!kKeepQ)
+                        load_q(qf, k, part);
+                    const uint32_t(*q)[2] = qf + (kKeepQ ? k : 0);
+                    mma16<M::kType>(s, ka[0], q[0][0], q[0][1]);
+                    mma16<M::kType>(s2, ka[1], q[1][0], q[1][1]);
+                }
             }
             // scales of the two positions; what they add to the maximum's exponent
             float ks[2], vs[2], lead[2];
@@ -369,8 +403,11 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 for (int j = 0; j < 2; ++j) {
                     ks[j] = scales[8 * j];
                     vs[j] = scales[16 + 8 * j];
-                    lead[j] = fmaxf((float)((int)(__float_as_uint(vs[j]) >> 23) - 127),
-                                    kLeastScale);
+                    if (kApart)
+                        split_scale(vs[j], lead[j], vs[j]);
+                    else
+                        lead[j] = fmaxf((float)((int)(__float_as_uint(vs[j]) >> 23) - 127),
+                                        kLeastScale);
                 }
             }
             bool above = false;
@@ -381,6 +418,8 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     s[i] = -INFINITY;
                 s2[i] = CACHE8 ? s[i] + lead[i / 2] : s[i];
                 above |= s2[i] > bound[i & 1];
+                if (kApart)
+                    above |= s[i] > score_bound[i & 1];
             }
             if (__any_sync(0xFFFFFFFFu, above)) {
                 float al[2];
@@ -394,7 +433,18 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     m[i] = now;
                     bound[i] = now + kSlack;
                     base[i] = finite_max(now) - (CACHE8 ? kWeightBits : 0.0f);
-                    l[i] *= al[i];
+                    if (kApart) {
+                        float top = fmaxf(score_m[i], fmaxf(s[i], s[2 + i]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        l[i] *= exp2_approx(score_m[i] - finite_max(top));
+                        score_m[i] = top;
+                        score_bound[i] = top + kSlack;
+                        score_base[i] = finite_max(top);
+                    } else {
+                        l[i] *= al[i];
+                    }
                 }
 #pragma unroll
                 for (int d = 0; d < DC / 16; ++d) {
@@ -408,6 +458,11 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                if (kApart) {
+                    l[i & 1] += exp2_approx(s[i] - score_base[i & 1]);
+                    p[i] = exp2_approx(s2[i] - base[i & 1]) * vs[i / 2];
+                    continue;
+                }
                 p[i] = exp2_approx(s[i] - base[i & 1]);
                 l[i & 1] += p[i];
                 if (CACHE8)
@@ -452,7 +507,8 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
         c.next_unit(a);
         load_q_rows();
 
-        // the groups' parts, in their order; what they are relative to
+        // the teams' parts, in their order; what they are relative to
+        float half_way[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -460,6 +516,12 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], d);
             if (CACHE8)
                 m[i] = m[i] == -INFINITY ? m[i] : m[i] - kWeightBits;
+            if (kApart) {
+                // o relative to the scores' maximum, as l: by halves, since the factor itself
+                // may have lost bits below 2^-126
+                half_way[i] = m[i] == -INFINITY ? 0.0f : exp2f(0.5f * (m[i] - score_m[i]));
+                m[i] = score_m[i];
+            }
             if (lane < 4) {
                 group_m[group][first + i] = m[i];
                 group_l[group][first + i] = l[i];
@@ -500,8 +562,10 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t column = 16 * d + (CACHE8 ? lane / 4 * 2 + i / 2
                                                              : lane / 4 + i / 2 * 8);
-                    mine[(first + (i & 1)) * M::kJoinRow + column] =
-                        o[d0 / 16 + d][i] * own[i & 1];
+                    float x = o[d0 / 16 + d][i];
+                    if (kApart)
+                        x = x * half_way[i & 1] * half_way[i & 1];
+                    mine[(first + (i & 1)) * M::kJoinRow + column] = x * own[i & 1];
                 }
             __syncthreads();
 #pragma unroll
@@ -563,6 +627,8 @@ static cudaError_t mma_dim(AttnArgs &a, int *grid, cudaStream_t s) {
 }
 
 cudaError_t launch_attention_mma(AttnArgs &a, int dtype, bool e4m3, int *grid, cudaStream_t s) {
+    if (dtype == AR_FP32)
+        return mma_dim<AR_FP32, true>(a, grid, s);
     if (dtype == AR_BF16)
         return e4m3 ? mma_dim<AR_BF16, true>(a, grid, s) : mma_dim<AR_BF16, false>(a, grid, s);
     return e4m3 ? mma_dim<AR_FP16, true>(a, grid, s) : mma_dim<AR_FP16, false>(a, grid, s);
