@@ -383,6 +383,29 @@ k_attention_any(const __grid_constant__ AttnArgs a) {
 // three times for memory.
 constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
+// This lane's columns of a row of D; zeros past it.
+template <int STEPS, int VEC>
+__device__ __forceinline__ void load_part(float (&x)[STEPS][VEC], const float *row, uint32_t D) {
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        const uint32_t d = (uint32_t)(k * 32 + (threadIdx.x & 31)) * VEC;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+            x[k][v] = 0.0f;
+        if (d >= D)
+            continue;
+        if constexpr (VEC == 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(row + d);
+            x[k][0] = f.x;
+            x[k][1] = f.y;
+            x[k][2] = f.z;
+            x[k][3] = f.w;
+        } else {
+            x[k][0] = row[d];
+        }
+    }
+}
+
 template <int DT, int VEC> __global__ void __launch_bounds__(kJoinThreads)
 k_attention_join(const __grid_constant__ AttnArgs a) {
     constexpr int kSteps = AR_CACHE_MAX_DIM / (32 * VEC);
@@ -390,6 +413,18 @@ k_attention_join(const __grid_constant__ AttnArgs a) {
     wait_for_input();
     const WorkSpace w(a.work);
     const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t D = a.g.D;
+    auto slot = [&](int i) {
+        return (uint32_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.unit_rows + r;
+    };
+    // what this warp adds first, before it is known whether there is that much: the place
+    // is one of the workspace's, and most units have two parts
+    float ahead[kSteps][VEC] = {};
+    float2 ahead_ml = make_float2(0.0f, 0.0f);
+    if (warp < 2 && c + warp < (int)gridDim.x)
+        load_part(ahead, w.o + (uint64_t)slot(warp) * D, D);
+    if (c + tid < (int)gridDim.x)
+        ahead_ml = w.ml[slot(tid)];
     const int4 meta = w.meta[c];
     if (meta.z < 0)
         return;
@@ -397,13 +432,9 @@ k_attention_join(const __grid_constant__ AttnArgs a) {
     if (r >= (int)u.rows)
         return;
     const int parts = meta.z - c + 1;
-    const uint32_t D = a.g.D;
-    auto slot = [&](int i) {
-        return (uint32_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.unit_rows + r;
-    };
     float top = -INFINITY;
     for (int i = tid; i < parts; i += kJoinThreads)
-        top = fmaxf(top, weight[i] = w.ml[slot(i)].x);
+        top = fmaxf(top, weight[i] = (i == tid ? ahead_ml : w.ml[slot(i)]).x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
@@ -416,7 +447,7 @@ k_attention_join(const __grid_constant__ AttnArgs a) {
     float l = 0.0f;
     for (int i = tid; i < parts; i += kJoinThreads) {
         weight[i] = exp2f(weight[i] - finite_max(top));
-        l += w.ml[slot(i)].y * weight[i];
+        l += (i == tid ? ahead_ml : w.ml[slot(i)]).y * weight[i];
     }
     l = warp_sum(l);
     __syncthreads();
@@ -428,24 +459,20 @@ k_attention_join(const __grid_constant__ AttnArgs a) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
             o[k][v] = 0.0f;
-#pragma unroll 8
-    for (int i = warp; i < parts; i += kJoinWarps) {
-        const float *row = w.o + (uint64_t)slot(i) * D;
+    auto add = [&](const float (*x)[VEC], float by) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            const uint32_t d = (uint32_t)(k * 32 + lane) * VEC;
-            if (d >= D)
-                continue;
-            if (VEC == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(row + d);
-                o[k][0] += x.x * weight[i];
-                o[k][1 % VEC] += x.y * weight[i];
-                o[k][2 % VEC] += x.z * weight[i];
-                o[k][3 % VEC] += x.w * weight[i];
-            } else {
-                o[k][0] += row[d] * weight[i];
-            }
-        }
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+                o[k][v] += x[k][v] * by;
+    };
+    if (warp < 2 && warp < parts)
+        add(ahead, weight[warp]);
+#pragma unroll 4
+    for (int i = warp < 2 ? warp + kJoinWarps : warp; i < parts; i += kJoinWarps) {
+        float x[kSteps][VEC];
+        load_part(x, w.o + (uint64_t)slot(i) * D, D);
+        add(x, weight[i]);
     }
     if (warp > 0)
 #pragma unroll
@@ -497,6 +524,7 @@ static cudaError_t any_form(AttnArgs &a, cudaStream_t s) {
     a.unit_rows = kAnyHeads;
     a.head_tiles = (a.group + kAnyHeads - 1) / kAnyHeads;
     a.runs = 0;
+    a.cluster = 0;
     const int grid = cta_limit(a.unit_rows, F::kCtas * sms);
     e = launch_kernel(k_attention_any<DT, CACHE8, DC, ASYNC>, grid, kAnyThreads, F::kSmem, s, true,
                       a);
@@ -508,7 +536,7 @@ template <int DT> static cudaError_t attention_dt(AttnArgs &a, bool e4m3, bool w
     if (w && (DT != AR_FP32 || e4m3)) {
         int grid = 0;
         const cudaError_t e = launch_attention_mma(a, DT, e4m3, &grid, s);
-        return e != cudaSuccess ? e : launch_join<DT>(a, grid, s);
+        return e != cudaSuccess || grid == 0 ? e : launch_join<DT>(a, grid, s);
     }
     if constexpr (DT == AR_FP32)
         if (w)
@@ -569,7 +597,7 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
     a.B = (uint32_t)B;
     a.heads = (uint32_t)heads;
     a.group = (uint32_t)(heads / kv_heads);
-    a.unit_rows = a.head_tiles = 0;                       // by the form
+    a.unit_rows = a.head_tiles = a.cluster = 0;           // by the form
     a.runs = 0;
     a.window = window < ((size_t)1 << 31) ? (uint32_t)window : 0u;
     const bool e4m3 = cache_dtype == AR_E4M3;

@@ -23,6 +23,7 @@ struct AttnArgs {
     uint32_t head_tiles;              // units of one key-value head
     uint32_t window;                  // 0: none
     int runs;                         // tiles begin at multiples of 16 positions
+    uint32_t cluster;                 // CTAs of a unit that share it by rank; 0: runs of tiles
 };
 
 // The CTAs that a launch of `most` may have: parts for all of them fit.
@@ -83,6 +84,18 @@ template <uint32_t TILE> struct Cursor {
         if (t >= t1 && left > 0)      // places for no tile only
             next_unit(a);
     }
+    // Share `rank` of `parts` of one unit, counted over all sequences.
+    __device__ __forceinline__ void share(const AttnArgs &a, uint32_t index, uint32_t rank,
+                                          uint32_t parts) {
+        const uint32_t units = a.g.heads * a.head_tiles;
+        b = index / units;
+        unit = index - b * units;
+        span = span_of(a, b);
+        tiles = tiles_of<TILE>(span);
+        t = (uint32_t)((uint64_t)tiles * rank / parts);
+        t1 = (uint32_t)((uint64_t)tiles * (rank + 1) / parts);
+        left = 0;
+    }
     __device__ __forceinline__ void next_unit(const AttnArgs &a) {
         t = t1 = 0;
         if (left == 0)
@@ -104,6 +117,11 @@ template <uint32_t TILE> struct Cursor {
             next_unit(a);
     }
 };
+
+// a / b; in 32 bits where that does, for a fraction of the time.
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
+    return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
+}
 
 // This CTA's run.  `part` is shared memory of 32 words.  *per: places of a run.
 template <uint32_t TILE>
@@ -142,7 +160,7 @@ __device__ __forceinline__ Cursor<TILE> find_run(const AttnArgs &a, uint64_t *pa
             sum += part[w];
         total += part[w];
     }
-    *per = (total + gridDim.x - 1) / gridDim.x;
+    *per = divide(total + gridDim.x - 1, gridDim.x);
     const uint64_t start = *per * blockIdx.x;
     if (start >= sum - mine && start < sum) {
         uint64_t base = sum - mine;
@@ -165,10 +183,10 @@ __device__ __forceinline__ Cursor<TILE> find_run(const AttnArgs &a, uint64_t *pa
     c.span = span_of(a, c.b);
     c.tiles = tiles_of<TILE>(c.span);
     const uint64_t all = kUnitCost + c.tiles, in = start - before;
-    c.unit = (uint32_t)(in / all);
+    c.unit = (uint32_t)divide(in, all);
     c.base = before + c.unit * all;
     c.left = total - start < *per ? total - start : *per;
-    c.begin(a, in % all);
+    c.begin(a, in - c.unit * all);
     return c;
 }
 
@@ -235,7 +253,11 @@ __device__ __forceinline__ int segment_part(const AttnArgs &a, const Cursor<TILE
 
 // ar_cache_attention_mma.cu: the tensor-core form, for keys and values of one or two
 // bytes whose rows are whole 16-byte vectors on 16-byte boundaries.  Sets the units of
-// `a`; *grid: its CTAs.
+// `a`; *grid: the CTAs whose parts a join has to look at, 0 if there are none.
 cudaError_t launch_attention_mma(AttnArgs &a, int dtype, bool e4m3, int *grid, cudaStream_t s);
+// ar_cache_attention_units.cu: its other form, without a join.  The first says whether it
+// serves `a` where `room` CTAs run at a time, and sets a.cluster.
+bool attention_units(AttnArgs &a, int room);
+cudaError_t launch_attention_units(const AttnArgs &a, int dtype, bool e4m3, cudaStream_t s);
 
 }  // namespace ar

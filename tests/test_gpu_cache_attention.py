@@ -80,13 +80,34 @@ def _check(lens, heads, kv, D, page, dtype, cache, window=0, scale=None, qpad=0,
                           **c.strides())
     torch.cuda.synchronize()
     want, wlse, err, lerr = _exact(c, f64(q).reshape(c.B, heads, D), np.float32(scale), window)
-    assert untouched(buf, c.B, cols, qpad, shift)
-    assert_within(f64(out).reshape(want.shape), want, err + half(want, dtype) * (1 + 1e-6), "out")
-    if with_lse:
-        got = lse.double().cpu().numpy()
-        empty = np.isinf(wlse)
-        assert (got[empty] == -np.inf).all()
-        assert_within(got[~empty], wlse[~empty], lerr[~empty], "lse")
+
+    def compare(what):
+        assert untouched(buf, c.B, cols, qpad, shift)
+        assert_within(f64(out).reshape(want.shape), want, err + half(want, dtype) * (1 + 1e-6),
+                      what)
+        if with_lse:
+            got = lse.double().cpu().numpy()
+            empty = np.isinf(wlse)
+            assert (got[empty] == -np.inf).all()
+            assert_within(got[~empty], wlse[~empty], lerr[~empty], what + ", lse")
+    compare("out")
+    # a table with room for far more, of which the lengths use as much: how units are shared
+    # out goes by what the host knows, the table's width; the result holds either way.  (A
+    # length past the table means another one then.)
+    if all(n <= c.width * c.page for n in c.lens_host):
+        first = out.clone()
+        width = c.width + 20000 // c.page + 1
+        table = torch.full((c.B, width), -1, dtype=torch.int32, device="cuda")
+        table[:, :c.width] = c.table[:, :c.width]
+        args = list(c.args())
+        args[6], args[7] = table, width
+        out.fill_(float("nan"))
+        ar.ar_cache_attention(q, *args, scale, out, lse, work, 4 * work.numel(), c.B, heads, kv, D,
+                              dtype, cache, window=window, ldq=cols + qpad, ldout=cols + qpad,
+                              ldpage=c.ldpage)
+        torch.cuda.synchronize()
+        compare("out, wide table")
+        return c, first
     return c, out
 
 
