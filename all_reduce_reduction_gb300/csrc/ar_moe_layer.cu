@@ -734,10 +734,11 @@ k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap 
 // ---- second launch --------------------------------------------------------------
 
 constexpr int kDownWarps = 8, kDownThreads = 32 * kDownWarps;
-constexpr int kDownRows = 16;
 // (four stages: the same; three CTAs an SM with registers for two: 114 us for one token
 // of 8192 x 2048, not 80)
 constexpr int kDownStagesLog2 = 1, kDownStages = 1 << kDownStagesLog2;
+// Most tokens whose sums leave room for a second CTA beside tiles of 32 rows.
+constexpr uint32_t kDownTokens = 32;
 
 struct DownShared {
     Chosen c;
@@ -746,9 +747,9 @@ struct DownShared {
     int failed;
     alignas(16) float sums[1];        // [warp][token][row]
 };
-static size_t down_smem(uint32_t T, bool bulk) {
-    return (bulk ? 1024 + kDownWarps * kDownStages * Ring<1>::kStage : 0) + sizeof(DownShared) +
-           sizeof(float) * kDownWarps * kDownRows * T;
+template <int MT> static size_t down_smem(uint32_t T, bool bulk) {
+    return (bulk ? 1024 + kDownWarps * kDownStages * Ring<MT>::kStage : 0) + sizeof(DownShared) +
+           sizeof(float) * kDownWarps * 16 * MT * T;
 }
 
 // The steps of a warp of the second launch: its blocks of (expert, k), a run of them, and
@@ -782,8 +783,8 @@ struct DownCursor {
     }
 };
 
-struct DownWarp {
-    Ring<1> ring;
+template <int MT> struct DownWarp {
+    Ring<MT> ring;
     DownCursor cursor;
     const CUtensorMap *map;
     uint32_t r0;
@@ -791,8 +792,13 @@ struct DownWarp {
     __device__ __forceinline__ void fetch(const MoeArgs &a, const Chosen &c) {
         if (cursor.done)
             return;
-        if ((threadIdx.x & 31) == 0 && !*ring.failed)
-            ring.issue(map, cursor.kb * 128, &r0, c.active[cursor.i]);
+        if ((threadIdx.x & 31) == 0 && !*ring.failed) {
+            uint32_t rows[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                rows[m] = r0 + 16 * m;
+            ring.issue(map, cursor.kb * 128, rows, c.active[cursor.i]);
+        }
         ++ring.issued;
         cursor.next(a, c);
     }
@@ -858,42 +864,46 @@ template <int DT> struct Hidden {
 
 // Blocks [kb0, kb1) along k of expert e times the listed pairs, added to this warp's
 // sums of their tokens.
-template <int DT, bool BULK, int NT>
-__device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, DownWarp &me,
+template <int DT, bool BULK, int MT, int NT>
+__device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, DownWarp<MT> &me,
                                           const int16_t *list, float *sums, int e, uint32_t kb0,
                                           uint32_t kb1, int n) {
     constexpr bool kLo = !HiddenRow<DT>::kHalf;
     const int lane = threadIdx.x & 31;
     const uint8_t *w = a.down + (uint64_t)e * a.H * a.lddown;
     const float *ws = a.down_scale + (uint64_t)e * a.hb * a.fb;
-    const uint8_t *rows[2];
-    const float *scales[2];
+    const uint8_t *rows[MT][2];
+    const float *scales[MT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t r = me.r0 + i * 8 + lane / 4;
-        r = r < a.H ? r : a.H - 1;        // past the last: their sums go nowhere
-        rows[i] = w + (uint64_t)r * a.lddown;
-        scales[i] = ws + (uint64_t)(r / 128) * a.fb;
-    }
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t r = me.r0 + 16 * m + i * 8 + lane / 4;
+            r = r < a.H ? r : a.H - 1;    // past the last: their sums go nowhere
+            rows[m][i] = w + (uint64_t)r * a.lddown;
+            scales[m][i] = ws + (uint64_t)(r / 128) * a.fb;
+        }
     const uint8_t *columns[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int x = nt * 8 + lane / 4;
         columns[nt] = a.h + (uint64_t)(x < n ? list[x] : 0) * a.sh;
     }
-    float sum[1][NT][4] = {};
+    float sum[MT][NT][4] = {};
     // what the next block needs besides its weights is loaded a block ahead, while
     // registers hold it
     constexpr bool kAhead = NT == 1 && !kLo;
     Hidden<DT> next_h[NT];
-    float next_scale[2];
+    float next_scale[MT][2];
     auto load = [&](uint32_t kb) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             next_h[nt].load(a, columns[nt], kb, nt * 8 + lane / 4 < n);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            next_scale[i] = scales[i][kb];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                next_scale[m][i] = scales[m][i][kb];
     };
     if (kAhead)
         load(kb0);
@@ -904,25 +914,34 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             now_h[nt] = next_h[nt];
-        const float sc[2] = {next_scale[0], next_scale[1]};
+        float sc[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                sc[m][i] = next_scale[m][i];
         if (kAhead && kb + 1 < kb1)
             load(kb + 1);
-        Codes<1> now;
+        Codes<MT> now;
         if (BULK) {
             me.ring.wait();
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                now.q[0][i] = me.ring.codes(0, i * 8 + lane / 4);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    now.q[m][i] = me.ring.codes(m, i * 8 + lane / 4);
             __syncwarp();
             ++me.ring.used;
             me.fetch(a, c);
         } else {
             const uint32_t k = kb * 128 + lane % 4 * 32;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                now.q[0][i].lo = load_codes(rows[i], k, a.F);
-                now.q[0][i].hi = load_codes(rows[i], k + 16, a.F);
-            }
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    now.q[m][i].lo = load_codes(rows[m][i], k, a.F);
+                    now.q[m][i].hi = load_codes(rows[m][i], k + 16, a.F);
+                }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -930,13 +949,15 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
             const float inv = now_h[nt].convert(hi, lo);
             const float inverse[2] = {__shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8),
                                       __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4)};
-            float part[1][1][4] = {};
-            block_product<1, 1>(part, now, [&](int, int piece) { return hi[piece]; });
+            float part[MT][1][4] = {};
+            block_product<MT, 1>(part, now, [&](int, int piece) { return hi[piece]; });
             if (kLo)
-                block_product<1, 1>(part, now, [&](int, int piece) { return lo[piece]; });
+                block_product<MT, 1>(part, now, [&](int, int piece) { return lo[piece]; });
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sum[0][nt][i] += part[0][0][i] * (inverse[i & 1] * sc[i / 2]);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum[m][nt][i] += part[m][0][i] * (inverse[i & 1] * sc[m][i / 2]);
         }
     }
     // columns of different pairs may be one token's (its choices of one expert): one
@@ -945,26 +966,30 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
         const int p = list[x];
         const float g = a.w ? a.w[p] : 1.0f;
         if (lane % 4 == x % 8 / 2) {
-            float *token = sums + (uint32_t)p / a.K * kDownRows;
+            float *token = sums + (uint32_t)p / a.K * (16 * MT);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (nt == x / 8)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        token[i * 8 + lane / 4] +=
-                            g * (x & 1 ? sum[0][nt][2 * i + 1] : sum[0][nt][2 * i]);
+                for (int nt = 0; nt < NT; ++nt)
+                    if (nt == x / 8)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            token[16 * m + i * 8 + lane / 4] +=
+                                g * (x & 1 ? sum[m][nt][2 * i + 1] : sum[m][nt][2 * i]);
         }
         __syncwarp();
     }
 }
 
-template <int DT, bool BULK>
+// MT: tiles of 16 rows of the output.
+template <int DT, bool BULK, int MT>
 __global__ void __launch_bounds__(kDownThreads, 2)
 k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap map) {
     extern __shared__ uint8_t raw[];
     uint8_t *rings = raw + (BULK ? (1024u - (smem_at(raw) & 1023u)) & 1023u : 0u);
     DownShared &s = *reinterpret_cast<DownShared *>(
-        rings + (BULK ? (uint32_t)kDownWarps * kDownStages * Ring<1>::kStage : 0u));
+        rings + (BULK ? (uint32_t)kDownWarps * kDownStages * Ring<MT>::kStage : 0u));
+    constexpr uint32_t kDownRows = 16 * MT;
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         s.failed = 0;
@@ -981,10 +1006,10 @@ k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMa
     for (uint32_t i = threadIdx.x; i < each * kDownWarps; i += kDownThreads)
         s.sums[i] = 0.0f;
     __syncthreads();
-    DownWarp me;
+    DownWarp<MT> me;
     me.map = &map;
     me.r0 = blockIdx.x * kDownRows;
-    me.ring.begin(rings + warp * kDownStages * Ring<1>::kStage, s.bars[warp], &s.failed,
+    me.ring.begin(rings + warp * kDownStages * Ring<MT>::kStage, s.bars[warp], &s.failed,
                   kDownStagesLog2);
     // this warp's run of (expert, block)
     const uint32_t steps = (uint32_t)s.c.count * a.fb;
@@ -1006,9 +1031,9 @@ k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMa
             list_pairs(a, s.c, e, skip, kColumns, s.list[warp]);
             const int n = all - skip < kColumns ? all - skip : kColumns;
             if (n <= 8)
-                down_part<DT, BULK, 1>(a, s.c, me, s.list[warp], mine, e, kb0, kb1, n);
+                down_part<DT, BULK, MT, 1>(a, s.c, me, s.list[warp], mine, e, kb0, kb1, n);
             else
-                down_part<DT, BULK, 2>(a, s.c, me, s.list[warp], mine, e, kb0, kb1, n);
+                down_part<DT, BULK, MT, 2>(a, s.c, me, s.list[warp], mine, e, kb0, kb1, n);
         }
         at += kb1 - kb0;
     }
@@ -1076,13 +1101,14 @@ static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaSt
     a.failed -= a.ups;
     return launch_kernel(k_moe_up<DT, BULK>, a.ups, kUpThreads, smem, s, true, a, map);
 }
-template <int DT, bool BULK>
+template <int DT, bool BULK, int MT>
 static cudaError_t launch_down(const MoeArgs &a, const CUtensorMap &map, cudaStream_t s) {
-    const cudaError_t e = opt_in_smem<k_moe_down<DT, BULK>>(down_smem(AR_MOE_LAYER_TOKENS, BULK));
+    constexpr uint32_t most = MT == 1 ? AR_MOE_LAYER_TOKENS : kDownTokens;
+    const cudaError_t e = opt_in_smem<k_moe_down<DT, BULK, MT>>(down_smem<MT>(most, BULK));
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(k_moe_down<DT, BULK>, (a.H + kDownRows - 1) / kDownRows, kDownThreads,
-                         down_smem(a.T, BULK), s, true, a, map);
+    return launch_kernel(k_moe_down<DT, BULK, MT>, (a.H + 16 * MT - 1) / (16 * MT), kDownThreads,
+                         down_smem<MT>(a.T, BULK), s, true, a, map);
 }
 
 template <int DT>
@@ -1103,7 +1129,10 @@ static cudaError_t moe_dt(MoeArgs a, bool bulk_up, bool bulk_down, cudaStream_t 
         bulk_up ? launch_up<DT, true>(a, up, sms, s) : launch_up<DT, false>(a, up, sms, s);
     if (e != cudaSuccess)
         return e;
-    return bulk_down ? launch_down<DT, true>(a, down, s) : launch_down<DT, false>(a, down, s);
+    if (!bulk_down)
+        return launch_down<DT, false, 1>(a, down, s);
+    return a.H / 32 >= (uint32_t)sms && a.T <= kDownTokens ? launch_down<DT, true, 2>(a, down, s)
+                                                          : launch_down<DT, true, 1>(a, down, s);
 }
 
 }  // namespace ar
