@@ -24,6 +24,9 @@
 // launch (down): a CTA takes rows of the output, its warps share the blocks along k of
 // all experts; each keeps its own sums of all tokens, which are added in order.
 //
+// One token, 8 of 64 experts of 8192 x 2048: 80.5 us (5.0 TB/s); 16 tokens, 8192 x 1024,
+// 279 (5.1; the first launch 172, the second 99).
+//
 // Every wait is bounded; after one that ran out the output is NaN.
 #include "ar_mma.cuh"
 #include "ar_rows.cuh"
@@ -1131,6 +1134,8 @@ static cudaError_t moe_dt(MoeArgs a, bool bulk_up, bool bulk_down, cudaStream_t 
         return e;
     if (!bulk_down)
         return launch_down<DT, false, 1>(a, down, s);
+    // 32 rows a CTA where that leaves no SM without one (16 tokens of 8192: 99 us for the
+    // second launch; 16 rows 117)
     return a.H / 32 >= (uint32_t)sms && a.T <= kDownTokens ? launch_down<DT, true, 2>(a, down, s)
                                                           : launch_down<DT, true, 1>(a, down, s);
 }

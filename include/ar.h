@@ -795,7 +795,9 @@ int ar_cache_read(const void *kcache, const void *vcache, size_t ldpage, const f
  * The sums over j are taken in parts that depend on lens, window, B, the heads
  * and the device, never on the order in which CTAs run.  exp is within a few
  * units in the last place; where keys and values have two bytes or one, the
- * weights exp(s_j - m) enter the second product with 16 bits or more.
+ * weights exp(s_j - m) enter the second product with 16 bits or more.  Where
+ * the output has two bytes, a vscale below 2^-105, which ar_cache_write does not
+ * give, may count as 0.
  *   q, out: dtype, B rows of heads * D elements, row strides ldq and ldout.
  *   kv_heads divides heads.   lse: B x heads binary32; may be NULL.
  *   kscale, vscale: not negative.
@@ -818,7 +820,9 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
  *   h = g / (1 + exp(-g)) * u
  *   out[t] = round( sum_k w[t*K + k] * down[e] h )
  * Choices whose id is outside [0, E) (another rank's, or dropped) add nothing.
- * The sums are binary32.
+ * The sums are binary32; where the output has two bytes, h is held with 11 bits
+ * between the launches.  Every wait inside is bounded; after one that ran out
+ * (none is known to) all of out is NaN.
  *   x, out: dtype, T x H.   ids: T x K words of ids_bytes (4 or 8) bytes, signed.
  *   w:    T x K binary32; NULL stands for ones.
  *   up:   E matrices of 2F x H E4M3, row stride ldup bytes, 2F * ldup apart;
