@@ -11,7 +11,7 @@
 // another only where a unit ends.
 //
 // One sequence of 131072, 64 / 8 heads of 128 bf16: 96 us with the join (5.6 TB/s); 64
-// sequences of 256 to 16384 in 8 bits 112 (5.3; bound by issue beside the stream: 370
+// sequences of 256 to 16384 in 8 bits 112 (5.3; bound by issue beside the stream: 470
 // instructions for 16 positions); 32 query heads of 256 on one of keys 44 (1.7; the join of
 // the teams' outputs).  With the heads as rows of the products 220 and 92 for the last two.
 #pragma once
