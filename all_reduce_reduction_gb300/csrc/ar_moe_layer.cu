@@ -5,9 +5,9 @@
 //
 // Bound by memory: the weights of every expert that a token chose are read once.
 // They are the 16-row operand of warp-wide products (E4M3 is exact in binary16), the
-// pairs (token, choice) of the expert the 8 or 16 columns: x and h are scaled by a
-// power of two for each 128 of a row so that binary16 holds them, in two parts where
-// one would round x.  A block of 128 along k gets its scales in binary32 when it is
+// pairs (token, choice) of the expert the 8 or 16 columns: x is scaled by a power of two
+// for each 128 of a row so that binary16 holds it, in two parts where one would round it;
+// h has two parts always.  A block of 128 along k gets its scales in binary32 when it is
 // summed.
 //
 // Weights come by TMA, a warp's own tiles of 16 rows by 128 bytes, through a ring of two
@@ -24,8 +24,8 @@
 // launch (down): a CTA takes rows of the output, its warps share the blocks along k of
 // all experts; each keeps its own sums of all tokens, which are added in order.
 //
-// One token, 8 of 64 experts of 8192 x 2048: 80.5 us (5.0 TB/s); 16 tokens, 8192 x 1024,
-// 279 (5.1; the first launch 172, the second 99).
+// One token, 8 of 64 experts of 8192 x 2048: 87 us (4.6 TB/s); 16 tokens, 8192 x 1024, 300
+// (4.7).
 //
 // Every wait is bounded; after one that ran out the output is NaN.
 #include "ar_mma.cuh"
@@ -260,17 +260,19 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// part += codes * columns.  column(nt, piece): eight of the lane's elements of column
-// l / 4 of tile nt, two steps' worth.
-template <int MT, int NT, typename Column>
+// part += codes * columns, which have PARTS parts.  column(nt, p, piece): eight of the lane's
+// elements of part p of column l / 4 of tile nt, two steps' worth.
+template <int MT, int NT, int PARTS, typename Column>
 __device__ __forceinline__ void block_product(float (*part)[NT][4], const Codes<MT> &w,
                                               Column column) {
 #pragma unroll
     for (int piece = 0; piece < 4; ++piece) {
-        uint4 b[NT];
+        uint4 b[NT][PARTS];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            b[n] = column(n, piece);
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p)
+                b[n][p] = column(n, p, piece);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -280,7 +282,10 @@ __device__ __forceinline__ void block_product(float (*part)[NT][4], const Codes<
                 from_e4m3x4(w.q[m][1][2 * piece + k], r[1], r[3]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    mma16<AR_FP16>(part[m][n], r, word_of(b[n], 2 * k), word_of(b[n], 2 * k + 1));
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+                        mma16<AR_FP16>(part[m][n], r, word_of(b[n][p], 2 * k),
+                                       word_of(b[n][p], 2 * k + 1));
             }
     }
 }
@@ -347,16 +352,57 @@ template <int DT> struct RawColumn {
 
 // ---- h between the launches ----------------------------------------------------------
 
-// Where the output has two bytes, h is held in binary16: 16 neighbours share a power of
-// two (its biased exponent in a byte), 11 bits of the largest, an eighth of the output's
-// own rounding in bf16 and of its size in fp16.  Otherwise it is binary32.
+// Where the output is binary32, so is h.  Otherwise h is held as two binary16 numbers (21
+// bits; one alone, 11 bits, took 81 and 282 us for one token and sixteen, not 87 and 300, but
+// was a second rounding that showed: fp16 outputs were 1.5 times as far from exact, of four
+// small experts) that 16 neighbours, a tile, have scaled by one power of two.  Its exponent goes in
+// steps of 16, so that the tiles of a block nearly always have the same one and enter a
+// product as they lie in memory: step j stands for 2^(120 - 16 j), which brings the tile's
+// largest magnitude between 2^-1 and 2^15.  The four bits of j are the lowest ones of the
+// second numbers of the tile's first four elements.  A block has 64 bytes for eight elements
+// of each of its four lanes: first numbers, then second numbers; the last block has as many
+// lanes as it has elements for.
 template <int DT> struct HiddenRow {
-    static constexpr bool kHalf = DT != AR_FP32;
-    static __host__ __device__ __forceinline__ uint64_t bytes(uint32_t F, uint32_t fb) {
+    static constexpr bool kParts = DT != AR_FP32;
+    static __host__ __device__ __forceinline__ uint64_t bytes(uint32_t F) {
         // rows are read by 16-byte vectors
-        return kHalf ? ((uint64_t)fb * (128 * 2 + 8) + 15) / 16 * 16 : (uint64_t)(F + 3) / 4 * 16;
+        return kParts ? (uint64_t)(F + 31) / 32 * 128 : (uint64_t)(F + 3) / 4 * 16;
+    }
+    // bytes of eight elements of the lanes of the block that element f is in
+    static __device__ __forceinline__ uint32_t piece(uint32_t f, uint32_t F) {
+        const uint32_t left = (F - f / 128 * 128 + 31) / 32;
+        return (left < 4 ? left : 4) * 16;
     }
 };
+// The step of a tile whose largest magnitude is `top`; 0 for one of zeros.
+__device__ __forceinline__ uint32_t tile_step(float top) {
+    const uint32_t e = __float_as_uint(top) >> 23;
+    return e < 6u ? 0u : (e - 6u) / 16;
+}
+__device__ __forceinline__ float step_scale(uint32_t j) {
+    return __uint_as_float((247u - 16u * j) << 23);
+}
+__device__ __forceinline__ float step_inverse(uint32_t j) {
+    return __uint_as_float((7u + 16u * j) << 23);
+}
+// The bit of a step that element r < 4 of a tile carries, and the step from the tile's
+// first two words.
+__device__ __forceinline__ uint32_t step_bit(uint32_t j, uint32_t r) {
+    return j >> ((r & 1) * 2 + r / 2) & 1u;
+}
+__device__ __forceinline__ uint32_t step_of(uint32_t w0, uint32_t w1) {
+    const uint32_t x = (w0 & 0x10001u) | (w1 & 0x10001u) << 1;
+    return (x | x >> 14) & 15u;
+}
+// v in binary16 with this lowest bit: the nearest such number, or next to it.
+__device__ __forceinline__ uint32_t half_with_bit(float v, uint32_t bit) {
+    const __half h = __float2half_rn(v);
+    const uint32_t q = __half_as_ushort(h);
+    if ((q & 1u) == bit)
+        return q;
+    const bool away = fabsf(v) >= fabsf(__half2float(h));     // and NaN stays one: q - 1
+    return away ? q + 1 : q - 1;
+}
 
 // ---- first launch -------------------------------------------------------------
 
@@ -563,14 +609,12 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
         }
         float part[kUpTiles][NT][4] = {}, inverse[NT][2];   // of this lane's columns
         if constexpr (BULK) {
-#pragma unroll
-            for (int lo = 0; lo < C::kParts; ++lo)
-                block_product<kUpTiles, NT>(part, now, [&](int nt, int piece) {
-                    return nt * 8 + (int)lane / 4 < n
-                               ? *reinterpret_cast<const uint4 *>(
-                                     mine + nt * 8 * bytes + (lo * a.hb + kb) * 256 + piece * 64)
-                               : make_uint4(0u, 0u, 0u, 0u);
-                });
+            block_product<kUpTiles, NT, C::kParts>(part, now, [&](int nt, int p, int piece) {
+                return nt * 8 + (int)lane / 4 < n
+                           ? *reinterpret_cast<const uint4 *>(
+                                 mine + nt * 8 * bytes + (p * a.hb + kb) * 256 + piece * 64)
+                           : make_uint4(0u, 0u, 0u, 0u);
+            });
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -590,10 +634,9 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
                 inverse[nt][0] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8);
                 inverse[nt][1] = __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4);
                 float one[kUpTiles][1][4] = {};
-                block_product<kUpTiles, 1>(one, now, [&](int, int piece) { return hi[piece]; });
-                if (kLo)
-                    block_product<kUpTiles, 1>(one, now,
-                                               [&](int, int piece) { return lo[piece]; });
+                block_product<kUpTiles, 1, C::kParts>(one, now, [&](int, int p, int piece) {
+                    return p ? lo[piece] : hi[piece];
+                });
 #pragma unroll
                 for (int m = 0; m < kUpTiles; ++m)
 #pragma unroll
@@ -644,7 +687,7 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
             h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
         }
         uint8_t *row = a.h + (uint64_t)(c < n ? list[c] : 0) * a.sh;
-        if (!HiddenRow<DT>::kHalf) {
+        if (!HiddenRow<DT>::kParts) {
             if (c < n && f0 + r < a.F)
                 reinterpret_cast<float *>(row)[f0 + r] = h;
             continue;
@@ -653,19 +696,18 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
 #pragma unroll
         for (int d = kUpRows / 2; d > 0; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        float scale, inverse;
-        half_range(top, scale, inverse);
         if (c >= n)
             continue;
-        const uint32_t f = f0 + r, tile = f0 / 16;
-        reinterpret_cast<uint16_t *>(row)[f / 128 * 128 + place_of(f % 128)] =
-            (uint16_t)narrow1<AR_FP16>(h * scale);
-        // and the exponents of what is left of the row's last block
-        uint8_t *exponents = row + (uint64_t)a.fb * 256;
-        if (r == 0)
-            exponents[tile] = (uint8_t)(__float_as_uint(scale) >> 23);
-        else if (tile + 1 == (a.F + 15) / 16 && tile + r < a.fb * 8)
-            exponents[tile + r] = 255;
+        const uint32_t step = tile_step(top), f = f0 + r, piece = HiddenRow<DT>::piece(f, a.F);
+        const float v = h * step_scale(step);
+        const uint32_t hi = __half_as_ushort(__float2half_rn(v));
+        const float left = isinf(h) ? 0.0f : v - __half2float(__ushort_as_half(hi));
+        uint8_t *at = row + (uint64_t)(f / 128) * 512 + f / 8 % 4 * piece + f / 32 % 4 * 16 +
+                      f % 8 * 2;
+        *reinterpret_cast<uint16_t *>(at) = (uint16_t)hi;
+        *reinterpret_cast<uint16_t *>(at + 4 * piece) =
+            (uint16_t)(r < 4 ? half_with_bit(left, step_bit(step, r))
+                             : __half_as_ushort(__float2half_rn(left)));
     }
     __syncthreads();
 }
@@ -807,63 +849,69 @@ template <int MT> struct DownWarp {
     }
 };
 
-// The lane's elements of a row of h, block kb: as they lie in memory.
+// The lane's elements of a row of h, block kb, in two parts.
 template <int DT> struct Hidden;
 template <> struct Hidden<AR_FP32> {
     RawColumn<AR_FP32> v;
+    uint4 parts[2][4];
     __device__ __forceinline__ void load(const MoeArgs &a, const uint8_t *row, uint32_t kb,
                                          bool on) {
         v.load(row, kb, a.F, true, on);
     }
-    __device__ __forceinline__ float convert(uint4 *hi, uint4 *lo) const {
-        return v.convert<true>(hi, lo);
+    // the inverse of the block's scale
+    __device__ __forceinline__ float convert(const MoeArgs &, uint32_t) {
+        return v.convert<true>(parts[0], parts[1]);
     }
 };
 template <int DT> struct Hidden {
-    uint4 v[4];
-    uint2 exponents;
+    uint4 parts[2][4];
     __device__ __forceinline__ void load(const MoeArgs &a, const uint8_t *row, uint32_t kb,
                                          bool on) {
         const uint32_t c = threadIdx.x & 3, k = kb * 128 + c * 32;
+        const uint32_t piece = HiddenRow<DT>::piece(kb * 128, a.F);
+        row += (uint64_t)kb * 512 + c * 16;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (on && k + 16 * (j / 2) < a.F)
-                v[j] = ld_v4_l1(row + kb * 256 + j * 64 + c * 16);
-        }
-        exponents = make_uint2(~0u, ~0u);
-        if (on)
-            exponents = *reinterpret_cast<const uint2 *>(row + a.fb * 256ull + kb * 8);
-    }
-    // The largest magnitude has the least exponent of scale; the others come down to it.
-    __device__ __forceinline__ float convert(uint4 *hi, uint4 *) const {
-        const uint32_t lane = threadIdx.x & 31;
-        uint32_t least = __vminu4(exponents.x, exponents.y);
-        least = __vminu4(least, least >> 16);
-        least = min(least & 255u, least >> 8 & 255u);
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // tiles 2 c and 2 c + 1
-            const uint32_t mine = (lane & 2 ? exponents.y : exponents.x) >>
-                                      (16 * (lane & 1) + 8 * half) & 255u;
-            const uint32_t down = mine - least;              // at most 241
-            const float f = __uint_as_float(down < 126u ? (127u - down) << 23 : 0u);
-            const __half2 by = __float2half2_rn(f);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint4 &x = v[2 * half + j];
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(w + i), by);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&y);
-                }
-                hi[2 * half + j] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j) {
+                parts[p][j] = make_uint4(0u, 0u, 0u, 0u);
+                if (on && k + 16 * (j / 2) < a.F)
+                    parts[p][j] = ld_v4_l1(row + (4 * p + j) * piece);
             }
+    }
+    // The inverse of the block's scale.  Tiles of several steps are brought to one scale in
+    // binary32, as in Hidden<AR_FP32>.
+    __device__ __forceinline__ float convert(const MoeArgs &a, uint32_t kb) {
+        uint32_t step[2], most;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            step[t] = step_of(parts[1][2 * t].x, parts[1][2 * t].y);
+        most = max(step[0], step[1]);
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+        const float inverse = step_inverse(most);
+        const uint32_t k = kb * 128 + (threadIdx.x & 3) * 32;
+        if (__all_sync(0xFFFFFFFFu, (step[0] == most || k >= a.F) &&
+                                        (step[1] == most || k + 16 >= a.F)))
+            return inverse;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t down = 16 * (most - step[i / 8]);      // 240 at most
+            const float by = down < 120 ? __uint_as_float((127 - down) << 23) : 0.0f;
+            const float2 hi = widen2<AR_FP16>(word_of(parts[0][i / 4], i % 4));
+            const float2 lo = widen2<AR_FP16>(word_of(parts[1][i / 4], i % 4));
+            v[2 * i] = (hi.x + lo.x) * by;
+            v[2 * i + 1] = (hi.y + lo.y) * by;
         }
-        return least >= 254u ? 0x1p-127f : __uint_as_float((254u - least) << 23);
+        return inverse * convert_column<true>(v, parts[0], parts[1]);
     }
 };
+// The line that p is in to L1: a load that nothing waits for (prefetch.global.L1 did not
+// bring it there).
+__device__ __forceinline__ void touch_l1(const void *p) {
+    asm volatile("{\n\t.reg .b32 unused;\n\tld.global.u32 unused, [%0];\n\t}" :: "l"(p));
+}
 
 // Blocks [kb0, kb1) along k of expert e times the listed pairs, added to this warp's
 // sums of their tokens.
@@ -871,60 +919,49 @@ template <int DT, bool BULK, int MT, int NT>
 __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, DownWarp<MT> &me,
                                           const int16_t *list, float *sums, int e, uint32_t kb0,
                                           uint32_t kb1, int n) {
-    constexpr bool kLo = !HiddenRow<DT>::kHalf;
     const int lane = threadIdx.x & 31;
     const uint8_t *w = a.down + (uint64_t)e * a.H * a.lddown;
     const float *ws = a.down_scale + (uint64_t)e * a.hb * a.fb;
-    const uint8_t *rows[MT][2];
-    const float *scales[MT][2];
+    // rows past the last stand in for it: their sums go nowhere
+    auto row_of = [&](int m, int i) {
+        const uint32_t r = me.r0 + 16 * m + i * 8 + lane / 4;
+        return r < a.H ? r : a.H - 1;
+    };
+    // a tile's 16 rows lie in one block of 128
+    const float *scales[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t r = me.r0 + 16 * m + i * 8 + lane / 4;
-            r = r < a.H ? r : a.H - 1;    // past the last: their sums go nowhere
-            rows[m][i] = w + (uint64_t)r * a.lddown;
-            scales[m][i] = ws + (uint64_t)(r / 128) * a.fb;
-        }
+        scales[m] = ws + (uint64_t)(row_of(m, 0) / 128) * a.fb;
     const uint8_t *columns[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int x = nt * 8 + lane / 4;
         columns[nt] = a.h + (uint64_t)(x < n ? list[x] : 0) * a.sh;
     }
-    float sum[MT][NT][4] = {};
-    // what the next block needs besides its weights is loaded a block ahead, while
-    // registers hold it
-    constexpr bool kAhead = NT == 1 && !kLo;
-    Hidden<DT> next_h[NT];
-    float next_scale[MT][2];
-    auto load = [&](uint32_t kb) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            next_h[nt].load(a, columns[nt], kb, nt * 8 + lane / 4 < n);
+    float sum[MT][NT][4] = {}, next_scale[MT];
+    auto load_scales = [&](uint32_t kb) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                next_scale[m][i] = scales[m][i][kb];
+            next_scale[m] = scales[m][kb];
     };
-    if (kAhead)
-        load(kb0);
+    load_scales(kb0);
     for (uint32_t kb = kb0; kb < kb1; ++kb) {
-        if (!kAhead)
-            load(kb);
-        Hidden<DT> now_h[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            now_h[nt] = next_h[nt];
-        float sc[MT][2];
+        float sc[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
+            sc[m] = next_scale[m];
+        Hidden<DT> h;
+        auto load_h = [&](int nt) { h.load(a, columns[nt], kb, nt * 8 + lane / 4 < n); };
+        load_h(0);                    // on its way while the weights are waited for
+        if (kb + 1 < kb1) {
+            load_scales(kb + 1);
+            // the next block's columns, a line of 128 bytes a lane: registers have no room
+            // for them (one token: 85 us; loaded when they are needed 90)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                sc[m][i] = next_scale[m][i];
-        if (kAhead && kb + 1 < kb1)
-            load(kb + 1);
+            for (int nt = 0; nt < NT; ++nt)
+                if ((kb + 1) * 128 + lane % 4 * 32 < a.F)
+                    touch_l1(columns[nt] + (uint64_t)(kb + 1) * 512 + lane % 4 * 128);
+        }
         Codes<MT> now;
         if (BULK) {
             me.ring.wait();
@@ -942,25 +979,29 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    now.q[m][i].lo = load_codes(rows[m][i], k, a.F);
-                    now.q[m][i].hi = load_codes(rows[m][i], k + 16, a.F);
+                    const uint8_t *row = w + (uint64_t)row_of(m, i) * a.lddown;
+                    now.q[m][i].lo = load_codes(row, k, a.F);
+                    now.q[m][i].hi = load_codes(row, k + 16, a.F);
                 }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            uint4 hi[4], lo[4];
-            const float inv = now_h[nt].convert(hi, lo);
+            if (nt > 0)
+                load_h(nt);
+            const float inv = h.convert(a, kb);
             const float inverse[2] = {__shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8),
                                       __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4)};
-            float part[MT][1][4] = {};
-            block_product<MT, 1>(part, now, [&](int, int piece) { return hi[piece]; });
-            if (kLo)
-                block_product<MT, 1>(part, now, [&](int, int piece) { return lo[piece]; });
+            // the two parts' sums apart: one chain of products would be twice as long
+            float part[MT][2][4] = {};
+            block_product<MT, 2, 1>(part, now, [&](int p, int, int piece) {
+                return h.parts[p][piece];
+            });
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[m][nt][i] += part[m][0][i] * (inverse[i & 1] * sc[m][i / 2]);
+                    sum[m][nt][i] += (part[m][0][i] + part[m][1][i]) *
+                                     (inverse[i & 1] * sc[m]);
         }
     }
     // columns of different pairs may be one token's (its choices of one expert): one
@@ -1097,10 +1138,9 @@ static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaSt
     const uint64_t units = (uint64_t)((a.F + kUpRows - 1) / kUpRows) * pairs;
     a.ups = (uint32_t)(units < (uint64_t)sms ? units : (uint64_t)sms);
     // The flags lie at the workspace's end, past the rows of h.  A pair has 4 F + 512 bytes
-    // there; rows of binary32 leave 500 of them.  Rows of binary16 leave 244 at least, and
-    // 480 from F = 60 on; below that a pair makes four CTAs at most.
-    if (a.ups > 480)
-        a.ups = 480;
+    // there, of which its row leaves 388 at least.
+    if (a.ups > 384)
+        a.ups = 384;
     a.failed -= a.ups;
     return launch_kernel(k_moe_up<DT, BULK>, a.ups, kUpThreads, smem, s, true, a, map);
 }
@@ -1119,7 +1159,7 @@ static cudaError_t moe_dt(MoeArgs a, bool bulk_up, bool bulk_down, cudaStream_t 
     const int sms = sm_count();
     if (sms < 1)
         return cudaErrorUnknown;
-    a.sh = HiddenRow<DT>::bytes(a.F, a.fb);
+    a.sh = HiddenRow<DT>::bytes(a.F);
     CUtensorMap up = {}, down = {};
     // without room for a column the first launch reads them on the way
     bulk_up = bulk_up && up_columns<DT>(a, 1) > 0;

@@ -820,8 +820,10 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
  *   h = g / (1 + exp(-g)) * u
  *   out[t] = round( sum_k w[t*K + k] * down[e] h )
  * Choices whose id is outside [0, E) (another rank's, or dropped) add nothing.
- * The sums are binary32; where the output has two bytes, h is held with 11 bits
- * between the launches.  Every wait inside is bounded; after one that ran out
+ * The sums are binary32.  x and h enter the products with 21 bits or more (x of
+ * two bytes as it is), but for what is 2^-39 of the largest of their 128
+ * neighbours or less, and where the output has two bytes 2^-23 of the largest of
+ * 16 neighbours of h.  Every wait inside is bounded; after one that ran out
  * (none is known to) all of out is NaN.
  *   x, out: dtype, T x H.   ids: T x K words of ids_bytes (4 or 8) bytes, signed.
  *   w:    T x K binary32; NULL stands for ones.
