@@ -11,7 +11,7 @@
 // another only where a unit ends.
 //
 // One sequence of 131072, 64 / 8 heads of 128 bf16: 96 us with the join (5.6 TB/s); 64
-// sequences of 256 to 16384 in 8 bits 112 (5.3; bound by issue beside the stream: 470
+// sequences of 256 to 16384 in 8 bits 117 (5.1; bound by issue beside the stream: 470
 // instructions for 16 positions); 32 query heads of 256 on one of keys 44 (1.7; the join of
 // the teams' outputs).  With the heads as rows of the products 220 and 92 for the last two.
 #pragma once
@@ -25,12 +25,21 @@ namespace ar {
 constexpr int kTeams = 4;                     // of warps, 16 positions of a tile each
 constexpr uint32_t kMmaTile = 16 * kTeams;
 
-// E4M3 values: a weight times its value's scale is held in binary16, so the maximum
-// is that of score + log2 scale (whole exponents, -96 at least: the sum of the weights
-// alone stays finite), and 2^8 times as much fits.  Scales that ar_cache_write gives are
-// 2^-105 at least; where the output is binary32, smaller ones count in full too: the
-// sum of the weights alone then has a maximum of its own.
-constexpr float kWeightBits = 8.0f, kLeastScale = -96.0f;
+// Products in binary16 (caches of binary16 and E4M3): a weight is held as two such numbers,
+// which end at 2^-25, so weights are 2^kBits times what they are relative to the maximum
+// (2^15 at most, with the slack).  A weight below kSmall would then have fewer than 12 bits
+// where the output is bf16, 14 where it is binary16, 16 where it is binary32.  Where a warp
+// has one among its 16 positions, what the two numbers leave of weights below 1 is added in
+// a product of its own, 2^24 times as large: they end at 2^-49 then.  (Batch in 8 bits as
+// above, scores of standard deviation 2.2: 117 us; with 14 bits 120, without any of it 113.)
+constexpr float kRestScale = 0x1p24f;
+
+// E4M3 values: a weight times its value's scale is what is held, so the maximum is that of
+// score + log2 scale (whole exponents, -96 at least: the sum of the weights alone stays
+// finite).  Scales that ar_cache_write gives are 2^-105 at least; where the output is
+// binary32, smaller ones count in full too: the sum of the weights alone then has a maximum
+// of its own.
+constexpr float kLeastScale = -96.0f;
 
 // A scale as f * 2^e with f in [1, 2); e is -inf for 0, f what is not finite.
 __device__ __forceinline__ void split_scale(float v, float &e, float &f) {
@@ -93,6 +102,9 @@ template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 template <int DT, bool CACHE8, int DC, int HG> struct MmaForm {
     static constexpr int kType = CACHE8 ? (int)AR_FP16 : DT;      // of the products
+    // powers of two above the maximum's weight; below which weights need a third part
+    static constexpr float kBits = CACHE8 ? 10.0f : DT == AR_FP16 ? 11.0f : 0.0f;
+    static constexpr float kSmall = DT == AR_FP32 ? 0x1p-9f : DT == AR_FP16 ? 0x1p-11f : 0x1p-13f;
     static constexpr uint32_t kCell = CACHE8 ? 1 : 2;
     static constexpr uint32_t kHeads = 8 * HG;                     // of a unit
     static constexpr int kThreads = 32 * kTeams * HG;
@@ -496,7 +508,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     al[i] = exp2_approx(m[i] - finite_max(now));
                     m[i] = now;
                     bound[i] = now + kSlack;
-                    base[i] = finite_max(now) - (CACHE8 ? kWeightBits : 0.0f);
+                    base[i] = finite_max(now) - M::kBits;
                     if (kApart) {
                         float top = fmaxf(score_m[i], fmaxf(s[i], s[2 + i]));
 #pragma unroll
@@ -518,6 +530,7 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             }
             // weights, in two parts: one would keep 8 (bf16) or 11 bits of them.  Transposed,
             // they are the second operand.
+            const uint32_t v_at = at + 16 * M::kRow;
             float p[4];
             uint32_t hi[2], lo[2];
 #pragma unroll
@@ -539,12 +552,8 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                 hi[j] = transpose8(w);
                 lo[j] = transpose8(pack2<M::kType>(p[2 * j] - x.x, p[2 * j + 1] - x.y));
             }
-            const uint32_t v_at = at + 16 * M::kRow;
-#pragma unroll
-            for (int d = 0; d < DC / 16; d += 2) {
-                if (d * 16 >= (int)D)
-                    break;
-                uint32_t va[2][4];
+            // columns 16 d .. 16 d + 31 of the values, the first operand of two products
+            auto load_v = [&](uint32_t (*va)[4], int d) {
                 if (CACHE8) {
                     // a word holds two columns of two positions: to two positions of each; the
                     // rows of a product are the even columns, then the odd ones
@@ -559,6 +568,44 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
                     ldmatrix4_trans(va[0], v_at + M::chunk(v_row, 2 * d + v_chunk));
                     ldmatrix4_trans(va[1], v_at + M::chunk(v_row, 2 * d + 2 + v_chunk));
                 }
+            };
+            if constexpr (M::kType == AR_FP16) {
+                const float least = fminf(fminf(p[0], p[1]), fminf(p[2], p[3]));
+                if (__any_sync(0xFFFFFFFFu, least < M::kSmall)) {
+                    uint32_t rest[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float r[2];
+                        const float2 x = widen2<AR_FP16>(pack2<AR_FP16>(p[2 * j], p[2 * j + 1]));
+                        r[0] = p[2 * j] - x.x;
+                        r[1] = p[2 * j + 1] - x.y;
+                        const float2 y = widen2<AR_FP16>(pack2<AR_FP16>(r[0], r[1]));
+                        r[0] = p[2 * j] < 1.0f ? (r[0] - y.x) * kRestScale : 0.0f;
+                        r[1] = p[2 * j + 1] < 1.0f ? (r[1] - y.y) * kRestScale : 0.0f;
+                        rest[j] = transpose8(pack2<AR_FP16>(r[0], r[1]));
+                    }
+#pragma unroll
+                    for (int d = 0; d < DC / 16; d += 2) {
+                        if (d * 16 >= (int)D)
+                            break;
+                        uint32_t va[2][4];
+                        load_v(va, d);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float sum[4] = {};
+                            mma16<AR_FP16>(sum, va[i], rest[0], rest[1]);
+                            fma2(o[d + i], sum[0], sum[1], 1 / kRestScale, 1 / kRestScale);
+                            fma2(o[d + i] + 2, sum[2], sum[3], 1 / kRestScale, 1 / kRestScale);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < DC / 16; d += 2) {
+                if (d * 16 >= (int)D)
+                    break;
+                uint32_t va[2][4];
+                load_v(va, d);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     mma16<M::kType>(o[d + i], va[i], hi[0], hi[1]);
@@ -579,8 +626,8 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)
                 l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], d);
-            if (CACHE8)
-                m[i] = m[i] == -INFINITY ? m[i] : m[i] - kWeightBits;
+            if (M::kBits != 0.0f)
+                m[i] = m[i] == -INFINITY ? m[i] : m[i] - M::kBits;
             if (kApart) {
                 // o relative to the scores' maximum, as l: by halves, since the factor itself
                 // may have lost bits below 2^-126
