@@ -99,12 +99,56 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
 template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return DT == AR_BF16 ? narrow2<AR_BF16>(a, b) : narrow2<AR_FP16>(a, b);
 }
+// The same, rounded toward zero.
+template <int DT> __device__ __forceinline__ uint32_t pack2_down(float a, float b) {
+    uint32_t w;
+    if (DT == AR_BF16)
+        asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    else
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+// Two weights in two parts.  E4M3 values are finite, and both parts rounded to the nearest.
+// Otherwise an infinity among the values has to remain one times either part: the first is
+// rounded down, and the second is more than what is left, by 2^-23 of the weight (bf16) or so
+// that it is 2^-24 at least (binary16; a weight that is 0 or less than 2^-24 needs
+// positive_parts).
+template <int TYPE, bool CACHE8>
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = CACHE8 ? pack2<TYPE>(a, b) : pack2_down<TYPE>(a, b);
+    const float2 x = widen2<TYPE>(hi);
+    if (CACHE8)
+        lo = pack2<TYPE>(a - x.x, b - x.y);
+    else if (TYPE == AR_BF16)
+        lo = pack2<TYPE>(fmaf(a, 1.0f + 0x1p-23f, -x.x), fmaf(b, 1.0f + 0x1p-23f, -x.y));
+    else
+        lo = pack2<TYPE>(fmaxf(a - x.x, 0x1p-24f), fmaxf(b - x.y, 0x1p-24f));
+}
+// Both parts of two weights in binary16: 0 for weights of 0, else 2^-24 at least.
+__device__ __forceinline__ void positive_parts(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const uint32_t none = (a == 0.0f ? 0xFFFFu : 0u) | (b == 0.0f ? 0xFFFF0000u : 0u);
+    hi |= ((hi & 0xFFFFu) == 0u ? 1u : 0u) | ((hi & 0xFFFF0000u) == 0u ? 0x10000u : 0u);
+    const float2 x = widen2<AR_FP16>(hi);
+    lo = pack2<AR_FP16>(fmaxf(a - x.x, 0x1p-24f), fmaxf(b - x.y, 0x1p-24f));
+    hi &= ~none;
+    lo &= ~none;
+}
+// Two binary16 numbers, those that are not finite as 0.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+    const uint32_t keep = ((w & 0x7C00u) == 0x7C00u ? 0u : 0xFFFFu) |
+                          ((w & 0x7C000000u) == 0x7C000000u ? 0u : 0xFFFF0000u);
+    return w & keep;
+}
 
 template <int DT, bool CACHE8, int DC, int HG> struct MmaForm {
     static constexpr int kType = CACHE8 ? (int)AR_FP16 : DT;      // of the products
     // powers of two above the maximum's weight; below which weights need a third part
     static constexpr float kBits = CACHE8 ? 10.0f : DT == AR_FP16 ? 11.0f : 0.0f;
-    static constexpr float kSmall = DT == AR_FP32 ? 0x1p-9f : DT == AR_FP16 ? 0x1p-11f : 0x1p-13f;
+    // (over binary16 the second number is 2^-24 off, not 2^-25)
+    static constexpr float kSmall = !CACHE8         ? 0x1p-10f
+                                    : DT == AR_FP32 ? 0x1p-9f
+                                    : DT == AR_FP16 ? 0x1p-11f
+                                                    : 0x1p-13f;
     static constexpr uint32_t kCell = CACHE8 ? 1 : 2;
     static constexpr uint32_t kHeads = 8 * HG;                     // of a unit
     static constexpr int kThreads = 32 * kTeams * HG;
@@ -547,10 +591,10 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t w = pack2<M::kType>(p[2 * j], p[2 * j + 1]);
-                const float2 x = widen2<M::kType>(w);
-                hi[j] = transpose8(w);
-                lo[j] = transpose8(pack2<M::kType>(p[2 * j] - x.x, p[2 * j + 1] - x.y));
+                uint32_t a, b;
+                split_weights<M::kType, CACHE8>(p[2 * j], p[2 * j + 1], a, b);
+                hi[j] = transpose8(a);
+                lo[j] = transpose8(b);
             }
             // columns 16 d .. 16 d + 31 of the values, the first operand of two products
             auto load_v = [&](uint32_t (*va)[4], int d) {
@@ -572,17 +616,25 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
             if constexpr (M::kType == AR_FP16) {
                 const float least = fminf(fminf(p[0], p[1]), fminf(p[2], p[3]));
                 if (__any_sync(0xFFFFFFFFu, least < M::kSmall)) {
-                    uint32_t rest[2];
+                    // (two parts of it over binary16: it takes back what positive_parts added)
+                    uint32_t rest[2], last[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float r[2];
-                        const float2 x = widen2<AR_FP16>(pack2<AR_FP16>(p[2 * j], p[2 * j + 1]));
-                        r[0] = p[2 * j] - x.x;
-                        r[1] = p[2 * j + 1] - x.y;
-                        const float2 y = widen2<AR_FP16>(pack2<AR_FP16>(r[0], r[1]));
-                        r[0] = p[2 * j] < 1.0f ? (r[0] - y.x) * kRestScale : 0.0f;
-                        r[1] = p[2 * j + 1] < 1.0f ? (r[1] - y.y) * kRestScale : 0.0f;
-                        rest[j] = transpose8(pack2<AR_FP16>(r[0], r[1]));
+                        uint32_t a, b;
+                        split_weights<M::kType, CACHE8>(p[2 * j], p[2 * j + 1], a, b);
+                        if (!CACHE8) {
+                            positive_parts(p[2 * j], p[2 * j + 1], a, b);
+                            hi[j] = transpose8(a);
+                            lo[j] = transpose8(b);
+                        }
+                        const float2 x = widen2<AR_FP16>(a), y = widen2<AR_FP16>(b);
+                        float r[2] = {p[2 * j] - x.x - y.x, p[2 * j + 1] - x.y - y.y};
+                        r[0] = p[2 * j] < 1.0f ? r[0] * kRestScale : 0.0f;
+                        r[1] = p[2 * j + 1] < 1.0f ? r[1] * kRestScale : 0.0f;
+                        const uint32_t w = pack2<AR_FP16>(r[0], r[1]);
+                        rest[j] = transpose8(w);
+                        if (!CACHE8)
+                            last[j] = transpose8(rest_of(w, r[0], r[1]));
                     }
 #pragma unroll
                     for (int d = 0; d < DC / 16; d += 2) {
@@ -593,7 +645,13 @@ k_attention_mma(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float sum[4] = {};
+                            if (!CACHE8)       // the first parts' products have them
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    va[i][k] = finite2(va[i][k]);
                             mma16<AR_FP16>(sum, va[i], rest[0], rest[1]);
+                            if (!CACHE8)
+                                mma16<AR_FP16>(sum, va[i], last[0], last[1]);
                             fma2(o[d + i], sum[0], sum[1], 1 / kRestScale, 1 / kRestScale);
                             fma2(o[d + i] + 2, sum[2], sum[3], 1 / kRestScale, 1 / kRestScale);
                         }
