@@ -29,6 +29,7 @@
 //
 // Every wait is bounded; after one that ran out the output is NaN.
 #include "ar_mma.cuh"
+#include "ar_ring.cuh"
 #include "ar_rows.cuh"
 #include "ar_tensor_map.cuh"
 
@@ -198,25 +199,20 @@ template <int BOXES> struct Ring {
     uint32_t at, bars;                // this warp's stages and barriers
     const uint8_t *memory;
     volatile int *failed;             // of the CTA
-    uint32_t issued, used, bits;      // 2^bits stages
+    RingSteps steps;
 
-    __device__ __forceinline__ uint32_t stage(uint32_t step) const {
-        return step & ((1u << bits) - 1u);
-    }
-    __device__ __forceinline__ uint32_t parity(uint32_t step) const { return step >> bits & 1; }
     __device__ __forceinline__ void begin(uint8_t *stages, uint64_t *barriers, int *flag,
                                           uint32_t stages_log2) {
-        bits = stages_log2;
         at = (uint32_t)__cvta_generic_to_shared(stages);
         bars = (uint32_t)__cvta_generic_to_shared(barriers);
         memory = stages;
         failed = flag;
-        issued = used = 0;
+        steps = {stages_log2, 0u, 0u};
     }
     // Boxes at (k, rows[b]) of matrix e to the next stage; by one lane.
     __device__ __forceinline__ void issue(const CUtensorMap *map, uint32_t k,
                                           const uint32_t *rows, int e) {
-        const uint32_t s = stage(issued), bar = bars + 8 * s;
+        const uint32_t s = steps.stage(steps.sent++), bar = bars + 8 * s;
         mbar_expect(bar, kStage);
 #pragma unroll
         for (int b = 0; b < BOXES; ++b)
@@ -224,7 +220,8 @@ template <int BOXES> struct Ring {
     }
     // Until the oldest stage is there; after a failure at once.
     __device__ __forceinline__ void wait() {
-        const uint32_t bar = bars + 8 * stage(used), phase = parity(used);
+        const uint32_t bar = bars + 8 * steps.stage(steps.used);
+        const uint32_t phase = steps.parity(steps.used);
         if (!__all_sync(0xFFFFFFFFu, mbar_test(bar, phase)))
             wait_slow(bar, phase);
     }
@@ -237,19 +234,19 @@ template <int BOXES> struct Ring {
     }
     // This lane's codes of row r of box b.
     __device__ __forceinline__ Words8 codes(int b, uint32_t r) const {
-        const uint8_t *row = memory + stage(used) * kStage + b * kBox + r * 128;
+        const uint8_t *row = memory + steps.stage(steps.used) * kStage + b * kBox + r * 128;
         const uint32_t c = (threadIdx.x & 3) * 2;
         Words8 w;
         w.lo = *reinterpret_cast<const uint4 *>(row + ((c ^ (r & 7)) << 4));
         w.hi = *reinterpret_cast<const uint4 *>(row + (((c + 1) ^ (r & 7)) << 4));
         return w;
     }
-    // After a failure: until what is in flight has landed, so that nothing comes to the
-    // CTA's memory once it has left.
-    __device__ __forceinline__ void drain() {
-        for (; used < issued; ++used) {
+    // After a failure, by the lane that sends: until what is in flight has landed, so that
+    // nothing comes to the CTA's memory once it has left.
+    __device__ __forceinline__ void drain() const {
+        for (uint32_t step = steps.oldest_open(); step != steps.sent; ++step) {
             const uint64_t deadline = globaltimer_ns() + kMoeWaitNs;
-            while (!mbar_test(bars + 8 * stage(used), parity(used)) &&
+            while (!mbar_test(bars + 8 * steps.stage(step), steps.parity(step)) &&
                    globaltimer_ns() < deadline) {
             }
         }
@@ -534,7 +531,6 @@ struct UpWarp {
             const uint32_t rows[2] = {cursor.tile * kUpRows, a.F + cursor.tile * kUpRows};
             ring.issue(map, cursor.kb * 128, rows, c.active[cursor.i]);
         }
-        ++ring.issued;
         cursor.next(a, c, tiles);
     }
 };
@@ -595,7 +591,7 @@ __device__ __forceinline__ void up_unit(const MoeArgs &a, UpShared &s, UpWarp &m
                 for (int i = 0; i < 2; ++i)
                     now.q[m][i] = me.ring.codes(i, m * 8 + lane / 4);
             __syncwarp();
-            ++me.ring.used;
+            ++me.ring.steps.used;
             me.fetch(a, s.c);
         } else {
             const uint32_t k = kb * 128 + lane % 4 * 32;
@@ -770,7 +766,7 @@ k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap 
         unit += last - tile;
     }
     __syncthreads();
-    if (BULK && s.failed)
+    if (BULK && s.failed && threadIdx.x % 32 == 0)
         me.ring.drain();
     if (threadIdx.x == 0)
         a.failed[blockIdx.x] = s.failed != 0;
@@ -844,7 +840,6 @@ template <int MT> struct DownWarp {
                 rows[m] = r0 + 16 * m;
             ring.issue(map, cursor.kb * 128, rows, c.active[cursor.i]);
         }
-        ++ring.issued;
         cursor.next(a, c);
     }
 };
@@ -971,7 +966,7 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
                 for (int i = 0; i < 2; ++i)
                     now.q[m][i] = me.ring.codes(m, i * 8 + lane / 4);
             __syncwarp();
-            ++me.ring.used;
+            ++me.ring.steps.used;
             me.fetch(a, c);
         } else {
             const uint32_t k = kb * 128 + lane % 4 * 32;
@@ -1081,7 +1076,7 @@ k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMa
         }
         at += kb1 - kb0;
     }
-    if (BULK && *me.ring.failed)
+    if (BULK && *me.ring.failed && threadIdx.x % 32 == 0)
         me.ring.drain();
     failed = __syncthreads_or(failed | s.failed);
     for (uint32_t i = threadIdx.x; i < each; i += kDownThreads) {
