@@ -636,7 +636,8 @@ def ar_moe_layer(x, ids, w, up, up_scale, down, down_scale, out, work, work_byte
                  lddown: int = 0, ldout: int = 0, ids_bytes=None, stream=None) -> None:
     """A mixture-of-experts layer for a few tokens (T * K <= AR_MOE_LAYER_PAIRS): gated
     first product, second product and the weighted sum over a token's choices.
-    ``ids_bytes`` as for ar_moe_route; ``work``: T * K * (F + 128) floats."""
+    ``ids_bytes`` as for ar_moe_route; ``work``: T * K * (F + 128) floats, of which
+    the last one's bits are AR_OK afterwards, AR_ERR_TIMEOUT if a wait ran out."""
     if ids_bytes is None:
         ids_bytes = ids.element_size() if hasattr(ids, "element_size") else 4
     calls = _calls or _layer_calls()

@@ -27,7 +27,8 @@
 // One token, 8 of 64 experts of 8192 x 2048: 87 us (4.6 TB/s); 16 tokens, 8192 x 1024, 300
 // (4.7).
 //
-// Every wait is bounded; after one that ran out the output is NaN.
+// Every wait is bounded; after one that ran out the output is NaN, all of it (first launch) or
+// the rows of a CTA (second), and the status word says so.
 #include "ar_mma.cuh"
 #include "ar_ring.cuh"
 #include "ar_rows.cuh"
@@ -61,6 +62,7 @@ struct MoeArgs {
     uint32_t part_row;                // of its sums: floats between rows
     int wide_x;
     int ids8;
+    int *status;                      // the workspace's last word
     uint8_t *failed;                  // of each CTA of the first launch: a wait ran out
     uint32_t ups;                     // those CTAs
 };
@@ -730,6 +732,8 @@ k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap 
     // only once what was before this one is done
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *a.status = AR_OK;
     choose(a, s.c);
     const uint32_t tiles = (a.F + kUpRows - 1) / kUpRows;
     // this CTA's run of (expert, rows)
@@ -1079,6 +1083,8 @@ k_moe_down(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMa
     if (BULK && *me.ring.failed && threadIdx.x % 32 == 0)
         me.ring.drain();
     failed = __syncthreads_or(failed | s.failed);
+    if (failed && threadIdx.x == 0)
+        *a.status = AR_ERR_TIMEOUT;
     for (uint32_t i = threadIdx.x; i < each; i += kDownThreads) {
         const uint32_t t = i / kDownRows, r = i % kDownRows;
         float v = 0.0f;
@@ -1132,8 +1138,8 @@ static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaSt
     }
     const uint64_t units = (uint64_t)((a.F + kUpRows - 1) / kUpRows) * pairs;
     a.ups = (uint32_t)(units < (uint64_t)sms ? units : (uint64_t)sms);
-    // The flags lie at the workspace's end, past the rows of h.  A pair has 4 F + 512 bytes
-    // there, of which its row leaves 388 at least.
+    // The flags lie at the workspace's end, past the rows of h and before the status word.  A
+    // pair has 4 F + 512 bytes there, of which its row leaves 388 at least.
     if (a.ups > 384)
         a.ups = 384;
     a.failed -= a.ups;
@@ -1238,7 +1244,8 @@ int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, cons
     a.fb = (uint32_t)fb;
     a.ub = (uint32_t)ub;
     a.columns = a.ups = a.stages = a.part_row = 0;
-    a.failed = reinterpret_cast<uint8_t *>(work) + mw.bytes;      // less a byte per CTA
+    a.status = reinterpret_cast<int *>(work) + mw.bytes / 4 - 1;
+    a.failed = reinterpret_cast<uint8_t *>(a.status);             // less a byte per CTA
     a.wide_x = wide(mx);
     a.ids8 = ids_bytes == 8;
     const bool bu = wide(mu), bd = wide(md);

@@ -828,15 +828,17 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
  * two bytes as it is), but for what is 2^-39 of the largest of their 128
  * neighbours or less, and where the output has two bytes 2^-23 of the largest of
  * 16 neighbours of h.  Every wait inside is bounded; after one that ran out
- * (none is known to) all of out is NaN.
+ * (none is known to) what it kept from being computed is NaN in out, and the
+ * workspace's last word, 4 bytes, is AR_ERR_TIMEOUT.  It is AR_OK otherwise.
  *   x, out: dtype, T x H.   ids: T x K words of ids_bytes (4 or 8) bytes, signed.
  *   w:    T x K binary32; NULL stands for ones.
  *   up:   E matrices of 2F x H E4M3, row stride ldup bytes, 2F * ldup apart;
  *         up_scale: E x ceil(2F/128) x ceil(H/128) binary32.
  *   down: E matrices of H x F E4M3, row stride lddown bytes, H * lddown apart;
  *         down_scale: E x ceil(H/128) x ceil(F/128) binary32.
- *   work: device memory, 16-byte aligned, of at least T * K * (F + 128) * 4 bytes.
- *         Calls that may run at the same time (graphs too) need one each.
+ *   work: device memory, 16-byte aligned, of at least T * K * (F + 128) * 4 bytes;
+ *         the last four of these are the status word.  Calls that may run at the
+ *         same time (graphs too) need one each.
  * T <= AR_MOE_LAYER_TOKENS, T * K <= AR_MOE_LAYER_PAIRS, K <= AR_MOE_MAX_CHOICES;
  * E <= AR_MOE_MAX_EXPERTS, H and F < 2^24 (AR_ERR_UNSUPPORTED beyond).  Weights whose rows are multiples of
  * 16 bytes at 16-byte boundaries take the vector path. */
