@@ -1,6 +1,7 @@
 // Attention on the tensor cores for few units of few tiles: each has a CTA, or a cluster
 // that joins its shares through its shared memory, in one launch (one sequence of 500
-// positions: 6.5 us; dealt and joined by a second launch 8.6).
+// positions: 5.8 us; dealt and joined by a second launch, as under a table with room for more
+// than 4096 of them, 8.6).
 #include "ar_cache_attention_mma.cuh"
 
 namespace ar {

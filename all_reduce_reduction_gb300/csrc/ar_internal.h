@@ -62,7 +62,9 @@ class DeviceScope {
 // programmatic dependent launch: it may start while the previous kernel in
 // the stream drains, and every kernel of this library waits (griddepcontrol
 // .wait) before its first global-memory access, so only the launch latency
-// overlaps, never the data.
+// overlaps, never the data.  One exception: k_moe_down reads the choices and
+// weights before its wait.  The kernel before it is always k_moe_up, which has
+// itself waited, for all that wrote them, before it lets k_moe_down come.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                                  cudaStream_t s, bool pdl, Args &&...args) {

@@ -811,20 +811,18 @@ struct DownCursor {
         pass = 0;
         done = at >= end;
     }
-    // true if the expert or the pass changes
-    __device__ __forceinline__ bool next(const MoeArgs &a, const Chosen &c) {
+    __device__ __forceinline__ void next(const MoeArgs &a, const Chosen &c) {
         if (++kb < kb1)
-            return false;
+            return;
         kb = kb0;
         if (++pass * kColumns < (uint32_t)c.pairs[i])
-            return true;
+            return;
         pass = 0;
         ++i;
         kb = kb0 = 0;
         kb1 = left < a.fb ? left : a.fb;
         left -= kb1;
         done = kb1 == 0;
-        return true;
     }
 };
 

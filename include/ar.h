@@ -792,8 +792,10 @@ int ar_cache_read(const void *kcache, const void *vcache, size_t ldpage, const f
  *   out = round( sum_j exp(s_j - m) * v_j / sum_j exp(s_j - m) )
  *   lse = m + ln sum_j exp(s_j - m)
  * Without any position (or with scores of -inf alone) out is 0 and lse -inf.
- * The sums over j are taken in parts that depend on lens, window, B, the heads
- * and the device, never on the order in which CTAs run.  exp is within a few
+ * The sums over j are taken in parts that depend on lens, window, B, the heads,
+ * width and page (how long a sequence may be, of which the host knows no more), D,
+ * the types, alignment and the device, never on the order in which CTAs run: who
+ * wants the same bits for the same sequence keeps the table's width.  exp is within a few
  * units in the last place.  Where keys and values have two bytes or one, the
  * weights exp(s_j - m) enter the second product (over E4M3 times their vscale)
  * with 15 bits or more; those far below the row's largest, over binary16 and E4M3
@@ -840,8 +842,10 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
  *         the last four of these are the status word.  Calls that may run at the
  *         same time (graphs too) need one each.
  * T <= AR_MOE_LAYER_TOKENS, T * K <= AR_MOE_LAYER_PAIRS, K <= AR_MOE_MAX_CHOICES;
- * E <= AR_MOE_MAX_EXPERTS, H and F < 2^24 (AR_ERR_UNSUPPORTED beyond).  Weights whose rows are multiples of
- * 16 bytes at 16-byte boundaries take the vector path. */
+ * E <= AR_MOE_MAX_EXPERTS, H and F < 2^24 (AR_ERR_UNSUPPORTED beyond).  Weights
+ * whose rows are multiples of 16 bytes at 16-byte boundaries take the vector path;
+ * those of up only where shared memory has room for a row of x beside them, H up to
+ * about 69000 (34000 in binary32): past that they are read byte by byte. */
 int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, const float *w,
                  const void *up, size_t ldup, const float *up_scale, const void *down,
                  size_t lddown, const float *down_scale, void *out, size_t ldout, float *work,
