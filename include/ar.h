@@ -845,7 +845,7 @@ int ar_cache_attention(const void *q, size_t ldq, const void *kcache, const void
  * E <= AR_MOE_MAX_EXPERTS, H and F < 2^24 (AR_ERR_UNSUPPORTED beyond).  Weights
  * whose rows are multiples of 16 bytes at 16-byte boundaries take the vector path;
  * those of up only where shared memory has room for a row of x beside them, H up to
- * about 69000 (34000 in binary32): past that they are read byte by byte. */
+ * 72576 (36480 in binary32): past that they are read byte by byte. */
 int ar_moe_layer(const void *x, size_t ldx, const void *ids, int ids_bytes, const float *w,
                  const void *up, size_t ldup, const float *up_scale, const void *down,
                  size_t lddown, const float *down_scale, void *out, size_t ldout, float *work,

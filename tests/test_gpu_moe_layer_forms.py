@@ -32,9 +32,11 @@ def test_every_number_of_columns(dtype, H):
     _check(24, 1, 1, H, 16, dtype, ids=[[0]] * 24, seed=H)
 
 
-@pytest.mark.parametrize("dtype,H", [("fp32", 36000), ("bf16", 72000)])
+@pytest.mark.parametrize("dtype,H", [("fp32", 36480), ("fp32", 36496), ("bf16", 72576),
+                                     ("bf16", 72592)])
 def test_rows_of_x_beyond_shared_memory(dtype, H):
-    """The first launch reads x and its weights on the way, the second has its rings."""
+    """Room for one column, and for none: the first launch then reads x and its weights on the
+    way, the second has its rings."""
     _check(10, 1, 2, H, 16, dtype, seed=3)
     _check(3, 2, 2, H, 48, dtype, seed=4)
 
