@@ -24,8 +24,8 @@
 // launch (down): a CTA takes rows of the output, its warps share the blocks along k of
 // all experts; each keeps its own sums of all tokens, which are added in order.
 //
-// One token, 8 of 64 experts of 8192 x 2048: 87 us (4.6 TB/s); 16 tokens, 8192 x 1024, 300
-// (4.7).
+// One token, 8 of 64 experts of 8192 x 2048: 87 us (4.6 TB/s); 16 tokens, 8192 x 1024, 297 to
+// 310 by box (4.6 to 4.8; the first launch 172, the second 114).
 //
 // Every wait is bounded; after one that ran out the output is NaN, all of it (first launch) or
 // the rows of a CTA (second), and the status word says so.
@@ -780,7 +780,7 @@ k_moe_up(const __grid_constant__ MoeArgs a, const __grid_constant__ CUtensorMap 
 
 constexpr int kDownWarps = 8, kDownThreads = 32 * kDownWarps;
 // (four stages: the same; three CTAs an SM with registers for two: 114 us for one token
-// of 8192 x 2048, not 80)
+// of 8192 x 2048, not 80, both with h in one binary16 number)
 constexpr int kDownStagesLog2 = 1, kDownStages = 1 << kDownStagesLog2;
 // Most tokens whose sums leave room for a second CTA beside tiles of 32 rows.
 constexpr uint32_t kDownTokens = 32;
@@ -953,7 +953,7 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
         if (kb + 1 < kb1) {
             load_scales(kb + 1);
             // the next block's columns, a line of 128 bytes a lane: registers have no room
-            // for them (one token: 85 us; loaded when they are needed 90)
+            // for them (one token: 85 us; without this 90; in registers a block ahead 97)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 if ((kb + 1) * 128 + lane % 4 * 32 < a.F)
@@ -1120,9 +1120,9 @@ static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaSt
     size_t smem;
     if (BULK) {
         // Rings of two stages where the columns of nearly every expert fit beside them (8
-        // tokens, top 8 of 64 experts of 8192 x 1024: 208 us; one stage 216), else of one
-        // (16 tokens: 284; two stages, and a second pass over the weights for more than four
-        // columns, 379).
+        // tokens, top 8 of 64 experts of 8192 x 1024: 220 us; one stage 227), else of one
+        // (16 tokens: 298; two stages, and a second pass over the weights for more than four
+        // columns, 391).
         const uint32_t mean = (uint32_t)((pairs + a.E - 1) / a.E), likely = 2 * mean + 2;
         a.stages = up_columns<DT>(a, 2) >= (likely < a.T ? likely : a.T) ? 2 : 1;
         a.columns = up_columns<DT>(a, a.stages);
@@ -1173,8 +1173,8 @@ static cudaError_t moe_dt(MoeArgs a, bool bulk_up, bool bulk_down, cudaStream_t 
         return e;
     if (!bulk_down)
         return launch_down<DT, false, 1>(a, down, s);
-    // 32 rows a CTA where that leaves no SM without one (16 tokens of 8192: 99 us for the
-    // second launch; 16 rows 117)
+    // 32 rows a CTA where that leaves no SM without one (8 and 16 tokens of 8192 x 1024: 220
+    // and 298 us; 16 rows 227 and 311; one token of 8192 x 2048 88.6, so 86.6)
     return a.H / 32 >= (uint32_t)sms && a.T <= kDownTokens ? launch_down<DT, true, 2>(a, down, s)
                                                           : launch_down<DT, true, 1>(a, down, s);
 }

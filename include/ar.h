@@ -803,7 +803,8 @@ int ar_cache_read(const void *kcache, const void *vcache, size_t ldpage, const f
  * is below 2^-57 of it may count as 0.  An infinity among the values is one in out,
  * if its weight is 2^-100 of the row's largest or more (NaN may come of it below).
  * Where the output has two bytes, a vscale below 2^-105, which ar_cache_write does
- * not give, may count as 0.  An infinite vscale may give NaN.
+ * not give, may count as 0.  An infinite vscale may give NaN.  Over E4M3, elements
+ * of q below 2^-39 of their head's largest count as 0, and binary32 ones have 22 bits.
  *   q, out: dtype, B rows of heads * D elements, row strides ldq and ldout.
  *   kv_heads divides heads.   lse: B x heads binary32; may be NULL.
  *   kscale, vscale: not negative.
