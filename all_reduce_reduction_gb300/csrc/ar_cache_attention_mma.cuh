@@ -11,7 +11,7 @@
 // another only where a unit ends.
 //
 // One sequence of 131072, 64 / 8 heads of 128 bf16: 96 us with the join (5.6 TB/s); 64
-// sequences of 256 to 16384 in 8 bits 117 (5.1; bound by issue beside the stream: 470
+// sequences of 256 to 16384 in 8 bits 117 (5.1; bound by issue beside the stream: 484
 // instructions for 16 positions); 32 query heads of 256 on one of keys 44 (1.7; the join of
 // the teams' outputs).  With the heads as rows of the products 220 and 92 for the last two.
 #pragma once
@@ -142,7 +142,7 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 
 template <int DT, bool CACHE8, int DC, int HG> struct MmaForm {
     static constexpr int kType = CACHE8 ? (int)AR_FP16 : DT;      // of the products
-    // powers of two above the maximum's weight; below which weights need a third part
+    // the maximum's weight is 2^kBits; weights below kSmall have a third part
     static constexpr float kBits = CACHE8 ? 10.0f : DT == AR_FP16 ? 11.0f : 0.0f;
     // (over binary16 the second number is 2^-24 off, not 2^-25)
     static constexpr float kSmall = !CACHE8         ? 0x1p-10f
