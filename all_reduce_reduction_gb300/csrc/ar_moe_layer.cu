@@ -24,8 +24,8 @@
 // launch (down): a CTA takes rows of the output, its warps share the blocks along k of
 // all experts; each keeps its own sums of all tokens, which are added in order.
 //
-// One token, 8 of 64 experts of 8192 x 2048: 87 us (4.6 TB/s); 16 tokens, 8192 x 1024, 297 to
-// 310 by box (4.6 to 4.8; the first launch 172, the second 114).
+// One token, 8 of 64 experts of 8192 x 2048: 85 us (4.7 TB/s); 16 tokens, 8192 x 1024, 293 to
+// 304 by box (4.7 to 4.8; the first launch 172, the second 112).
 //
 // Every wait is bounded; after one that ran out the output is NaN, all of it (first launch) or
 // the rows of a CTA (second), and the status word says so.
@@ -352,7 +352,7 @@ template <int DT> struct RawColumn {
 // ---- h between the launches ----------------------------------------------------------
 
 // Where the output is binary32, so is h.  Otherwise h is held as two binary16 numbers (21
-// bits; one alone, 11 bits, took 81 and 282 us for one token and sixteen, not 87 and 300, but
+// bits; one alone, 11 bits, took 81 and 282 us for one token and sixteen, not 85 and 293, but
 // was a second rounding that showed: fp16 outputs were 1.5 times as far from exact, of four
 // small experts) that 16 neighbours, a tile, have scaled by one power of two.  Its exponent goes in
 // steps of 16, so that the tiles of a block nearly always have the same one and enter a
@@ -953,7 +953,7 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
         if (kb + 1 < kb1) {
             load_scales(kb + 1);
             // the next block's columns, a line of 128 bytes a lane: registers have no room
-            // for them (one token: 85 us; without this 90; in registers a block ahead 97)
+            // for them (one token: 85 us; without this 87.5; in registers a block ahead 97)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 if ((kb + 1) * 128 + lane % 4 * 32 < a.F)
@@ -988,16 +988,16 @@ __device__ __forceinline__ void down_part(const MoeArgs &a, const Chosen &c, Dow
             const float inv = h.convert(a, kb);
             const float inverse[2] = {__shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8),
                                       __shfl_sync(0xFFFFFFFFu, inv, lane % 4 * 8 + 4)};
-            // the two parts' sums apart: one chain of products would be twice as long
-            float part[MT][2][4] = {};
-            block_product<MT, 2, 1>(part, now, [&](int p, int, int piece) {
+            // (the parts' sums apart, two chains of half the length: 88 us for one token, not 85)
+            float part[MT][1][4] = {};
+            block_product<MT, 1, 2>(part, now, [&](int, int p, int piece) {
                 return h.parts[p][piece];
             });
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[m][nt][i] += (part[m][0][i] + part[m][1][i]) *
+                    sum[m][nt][i] += part[m][0][i] *
                                      (inverse[i & 1] * sc[m]);
         }
     }
@@ -1120,9 +1120,9 @@ static cudaError_t launch_up(MoeArgs &a, const CUtensorMap &map, int sms, cudaSt
     size_t smem;
     if (BULK) {
         // Rings of two stages where the columns of nearly every expert fit beside them (8
-        // tokens, top 8 of 64 experts of 8192 x 1024: 220 us; one stage 227), else of one
-        // (16 tokens: 298; two stages, and a second pass over the weights for more than four
-        // columns, 391).
+        // tokens, top 8 of 64 experts of 8192 x 1024: 215 us; one stage 221), else of one
+        // (16 tokens: 293; two stages, and a second pass over the weights for more than four
+        // columns, 387).
         const uint32_t mean = (uint32_t)((pairs + a.E - 1) / a.E), likely = 2 * mean + 2;
         a.stages = up_columns<DT>(a, 2) >= (likely < a.T ? likely : a.T) ? 2 : 1;
         a.columns = up_columns<DT>(a, a.stages);
@@ -1173,8 +1173,8 @@ static cudaError_t moe_dt(MoeArgs a, bool bulk_up, bool bulk_down, cudaStream_t 
         return e;
     if (!bulk_down)
         return launch_down<DT, false, 1>(a, down, s);
-    // 32 rows a CTA where that leaves no SM without one (8 and 16 tokens of 8192 x 1024: 220
-    // and 298 us; 16 rows 227 and 311; one token of 8192 x 2048 88.6, so 86.6)
+    // 32 rows a CTA where that leaves no SM without one (8 and 16 tokens of 8192 x 1024: 215
+    // and 293 us; 16 rows 225 and 308; one token of 8192 x 2048 85, so 86)
     return a.H / 32 >= (uint32_t)sms && a.T <= kDownTokens ? launch_down<DT, true, 2>(a, down, s)
                                                           : launch_down<DT, true, 1>(a, down, s);
 }
