@@ -793,18 +793,19 @@ int ar_cache_read(const void *kcache, const void *vcache, size_t ldpage, const f
  *   lse = m + ln sum_j exp(s_j - m)
  * Without any position (or with scores of -inf alone) out is 0 and lse -inf.
  * The sums over j are taken in parts that depend on lens, window, B, the heads,
- * width and page (how long a sequence may be, of which the host knows no more), D,
- * the types, alignment and the device, never on the order in which CTAs run: who
- * wants the same bits for the same sequence keeps the table's width.  exp is within a few
- * units in the last place.  Where keys and values have two bytes or one, the
- * weights exp(s_j - m) enter the second product (over E4M3 times their vscale)
- * with 15 bits or more; those far below the row's largest, over binary16 and E4M3
- * with 12 (bf16 outputs) or 14 (binary16 outputs), down to 2^-43 of it, and what
- * is below 2^-57 of it may count as 0.  An infinity among the values is one in out,
- * if its weight is 2^-100 of the row's largest or more (NaN may come of it below).
- * Where the output has two bytes, a vscale below 2^-105, which ar_cache_write does
- * not give, may count as 0.  An infinite vscale may give NaN.  Over E4M3, elements
- * of q below 2^-39 of their head's largest count as 0, and binary32 ones have 22 bits.
+ * width and page (how long a sequence may be, of which the host knows no more),
+ * D, the types, alignment and the device, never on the order in which CTAs run:
+ * who wants the same bits for the same sequence keeps the table's width.  exp
+ * is within a few units in the last place.  Where keys and values have two
+ * bytes or one, the weights exp(s_j - m) enter the second product (over E4M3
+ * times their vscale) with 15 bits or more; those far below the row's largest,
+ * over binary16 and E4M3 with 12 (bf16 outputs) or 14 (binary16 outputs), down
+ * to 2^-43 of it, and what is below 2^-57 of it may count as 0.  An infinity
+ * among the values is one in out, if its weight is 2^-100 of the row's largest
+ * or more (NaN may come of it below). Where the output has two bytes, a vscale
+ * below 2^-105, which ar_cache_write does not give, may count as 0.  An
+ * infinite vscale may give NaN.  Over E4M3, elements of q below 2^-39 of their
+ * head's largest count as 0, and binary32 ones have 22 bits.
  *   q, out: dtype, B rows of heads * D elements, row strides ldq and ldout.
  *   kv_heads divides heads.   lse: B x heads binary32; may be NULL.
  *   kscale, vscale: not negative.
